@@ -26,7 +26,7 @@ __all__ = [
     "sparse_attn_fwd", "validate_indices", "device_error", "debug_wait_timeout", "pipeline",
     "coarse_attn", "coarse_attn_workspace_bytes", "pair_cubes", "pair_workspace_bytes", "kernel_launches",
     "table_from_csr", "block_select", "block_select_workspace_bytes", "sparse_attn_fwd_peak", "all_cubes",
-    "PipelineGraph",
+    "PipelineGraph", "cache_pool", "cache_append", "cache_attn", "cache_attn_workspace_bytes", "cache_read",
 ]
 
 _STATUS = {0: "VSA_OK", 1: "VSA_ERR_INVALID_ARG", 2: "VSA_ERR_UNSUPPORTED", 3: "VSA_ERR_ALIGNMENT",
@@ -42,6 +42,12 @@ class VsaError(RuntimeError):
 class VsaGrid(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("W", ctypes.c_int32), ("heads", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
+class VsaCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("width", ctypes.c_int32), ("pool", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -107,6 +113,18 @@ def _declare(lib):
     lib.vsa_block_select_workspace_bytes.argtypes = [_i32] * 4
     lib.vsa_block_select.restype = ctypes.c_int
     lib.vsa_block_select.argtypes = [_p, _p, _i32, _i32, _i32, _i32, ctypes.c_float, ctypes.c_float, _p, _p, _p, _p]
+    lib.vsa_cache_pool_bytes.restype = ctypes.c_size_t
+    lib.vsa_cache_pool_bytes.argtypes = [_i32] * 3
+    lib.vsa_cache_append.restype = ctypes.c_int
+    lib.vsa_cache_append.argtypes = [ctypes.POINTER(VsaCache), _p, _p, _p, _i32, _i32, _p, _p, _i32, _i32, _i32, _p,
+                                     _p, _p]
+    lib.vsa_cache_read.restype = ctypes.c_int
+    lib.vsa_cache_read.argtypes = [ctypes.POINTER(VsaCache), _i32, _p, _p, _p]
+    lib.vsa_cache_attn_workspace_bytes.restype = ctypes.c_size_t
+    lib.vsa_cache_attn_workspace_bytes.argtypes = [_i32] * 4
+    lib.vsa_cache_attn.restype = ctypes.c_int
+    lib.vsa_cache_attn.argtypes = [ctypes.POINTER(VsaCache), _p, _i32, _i32, _p, _i32, _p, _i32, ctypes.c_float, _p,
+                                   _p, _p, _p]
     lib.vsa_kernel_launches.restype = ctypes.c_uint64
     lib.vsa_kernel_launches.argtypes = []
     return lib
@@ -581,6 +599,164 @@ def table_from_csr(lut_ptr, kv_idx, width: int, ncubes: int, shape=None):
         table = table.reshape(tuple(shape) + (width,))
         counts = counts.reshape(tuple(shape))
     return table, counts
+
+
+def cache_pool(pages: int, kv_heads: int, D: int, device="cuda"):
+    """A pool of 4-bit pages: uint8 [pages, kv_heads, 72 * D], zeros (see vsa_cache for its layout)."""
+    torch = _torch()
+    if pages <= 0 or kv_heads <= 0 or D not in (64, 128):
+        raise ValueError("pages and kv_heads must be positive and D 64 or 128")
+    return torch.zeros((int(pages), int(kv_heads), 72 * int(D)), dtype=torch.uint8, device=device)
+
+
+def _cache(pool, table, kv_lens, kv_scale, others=()):
+    """Checks a cache's tensors (and that `others` are on its device) -> VsaCache."""
+    torch = _torch()
+    _need(pool, torch.uint8, "pool")
+    _need(table, torch.int32, "table")
+    _need(kv_lens, torch.int32, "kv_lens")
+    if pool.dim() != 3 or pool.shape[2] not in (72 * 64, 72 * 128):
+        raise ValueError("pool must be [pages, kv_heads, 72 * D] with D 64 or 128")
+    if table.dim() != 2 or tuple(kv_lens.shape) != (table.shape[0],):
+        raise ValueError("table must be [B, width] and kv_lens [B]")
+    if kv_scale is not None:
+        _need(kv_scale, torch.float32, "kv_scale")
+        if tuple(kv_scale.shape) != (2, pool.shape[1]):
+            raise ValueError("kv_scale must be [2, kv_heads]")
+    for t in (table, kv_lens, kv_scale, *others):
+        if t is not None and t.device != pool.device:
+            raise ValueError("all tensors of a cache call must be on the pool's device")
+    return VsaCache(pool.shape[0], pool.shape[1], pool.shape[2] // 72, table.shape[0], table.shape[1],
+                    pool.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
+                    None if kv_scale is None else kv_scale.data_ptr())
+
+
+def _rows(t, cache, heads, name):
+    torch = _torch()
+    _need(t, torch.bfloat16, name)
+    if t.dim() != 4 or t.shape[0] != cache.B or t.shape[3] != cache.D or (heads and t.shape[2] != heads):
+        raise ValueError(f"{name} must be [B, S, {'kv_heads' if heads else 'heads'}, D]")
+
+
+def _lens(t, cache, name):
+    if t is not None:
+        _need(t, _torch().int32, name)
+        if tuple(t.shape) != (cache.B,):
+            raise ValueError(f"{name} must be [B]")
+
+
+def cache_append(pool, k, v, table, kv_lens, new_lens=None, rope=None, positions=None, interleaved: bool = False,
+                 q=None, q_out=None, kv_scale=None, stream=None):
+    """Writes a step's k, v (bf16 [B, S, kv_heads, D]) to their 4-bit pages, k rotated by `rope`
+    (fp32 [rows, R]: cosines, then sines) on the way; with q (bf16 [B, S, heads, D]) returns the
+    queries rotated alike, else None (vsa_cache_append).
+
+    kv_lens (int32 [B]) counts the step's tokens already; new_lens says how many each sequence
+    has (None: S).  positions int32 [B, S] are rows of rope (None: places in the sequence)."""
+    torch = _torch()
+    c = _cache(pool, table, kv_lens, kv_scale, (k, v, new_lens, rope, positions, q, q_out))
+    _rows(k, c, c.kv_heads, "k")
+    _rows(v, c, c.kv_heads, "v")
+    if v.shape != k.shape:
+        raise ValueError("k and v must share a shape")
+    S = k.shape[1]
+    _lens(new_lens, c, "new_lens")
+    if rope is not None:
+        _need(rope, torch.float32, "rope")
+        if rope.dim() != 2 or not rope.shape[0] or not rope.shape[1]:
+            raise ValueError("rope must be [rows, R] with R > 0")
+    if positions is not None:
+        _need(positions, torch.int32, "positions")
+        if tuple(positions.shape) != (c.B, S):
+            raise ValueError("positions must be [B, S]")
+    if q is None and q_out is not None:
+        raise ValueError("q_out goes with q")
+    if q is not None:
+        _rows(q, c, 0, "q")
+        if q.shape[1] != S:
+            raise ValueError("q must have k's tokens")
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        _need(q_out, torch.bfloat16, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be shaped like q")
+    ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    with torch.cuda.device(pool.device):
+        _check(library().vsa_cache_append(ctypes.byref(c), ptr(q), k.data_ptr(), v.data_ptr(), S,
+                                          q.shape[2] if q is not None else 0, ptr(new_lens), ptr(rope),
+                                          rope.shape[0] if rope is not None else 0,
+                                          rope.shape[1] if rope is not None else 0, int(bool(interleaved)),
+                                          ptr(positions), ptr(q_out), _stream(stream)), "vsa_cache_append")
+    return q_out
+
+
+def cache_read(pool, table, kv_lens, S: int, kv_scale=None, k=None, v=None, stream=None):
+    """The first S cached tokens of every sequence -> (k, v) bf16 [B, S, kv_heads, D], zero past each
+    length; with S a multiple of 64 they are tiled tensors for sparse_attn_fwd (vsa_cache_read)."""
+    torch = _torch()
+    c = _cache(pool, table, kv_lens, kv_scale, (k, v))
+    shape = (c.B, int(S), c.kv_heads, c.D)
+    out = []
+    for t, n in ((k, "k"), (v, "v")):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
+        _need(t, torch.bfloat16, n)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{n} must be {shape}")
+        out.append(t)
+    with torch.cuda.device(pool.device):
+        _check(library().vsa_cache_read(ctypes.byref(c), int(S), out[0].data_ptr(), out[1].data_ptr(),
+                                        _stream(stream)), "vsa_cache_read")
+    return out[0], out[1]
+
+
+def cache_attn_workspace_bytes(kv_heads: int, D: int, Sq: int, heads: int) -> int:
+    return int(library().vsa_cache_attn_workspace_bytes(kv_heads, D, Sq, heads))
+
+
+def cache_attn(q, pool, table, kv_lens, q_lens=None, causal: bool = True, page_sel=None, kv_scale=None,
+               sm_scale: float = 0.0, workspace=None, out=None, lse=None, want_lse: bool = True, stream=None):
+    """Attention of q (bf16 [B, Sq, heads, D], rotated as the keys were) over the 4-bit cache ->
+    (out bf16 like q, lse fp32 [B, heads, Sq] or None) (vsa_cache_attn).
+
+    q_lens (int32 [B]) are each sequence's query rows (None: Sq), its last tokens when causal;
+    page_sel (int32 [B, kv_heads, n]) limits each kv head to n pages of its sequence (-1: none)."""
+    torch = _torch()
+    c = _cache(pool, table, kv_lens, kv_scale, (q, q_lens, page_sel, workspace, out, lse))
+    _rows(q, c, 0, "q")
+    B, Sq, heads, D = q.shape
+    if heads == 0 or heads % c.kv_heads:
+        raise ValueError("heads must be a multiple of kv_heads")
+    _lens(q_lens, c, "q_lens")
+    nsel = 0
+    if page_sel is not None:
+        _need(page_sel, torch.int32, "page_sel")
+        if page_sel.dim() != 3 or tuple(page_sel.shape[:2]) != (B, c.kv_heads) or not page_sel.shape[2]:
+            raise ValueError("page_sel must be [B, kv_heads, n] with n > 0")
+        nsel = page_sel.shape[2]
+    nbytes = cache_attn_workspace_bytes(c.kv_heads, D, Sq, heads)
+    if workspace is None:
+        workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=q.device)
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.numel() < nbytes:
+        raise ValueError(f"workspace needs {nbytes} bytes")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, torch.bfloat16, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must be shaped like q")
+    if want_lse and lse is None:
+        lse = torch.empty((B, heads, Sq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (B, heads, Sq):
+            raise ValueError("lse must be [B, heads, Sq]")
+    ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    with torch.cuda.device(pool.device):
+        _check(library().vsa_cache_attn(ctypes.byref(c), q.data_ptr(), Sq, heads, ptr(q_lens), int(bool(causal)),
+                                        ptr(page_sel), nsel, float(sm_scale), workspace.data_ptr(), out.data_ptr(),
+                                        ptr(lse), _stream(stream)), "vsa_cache_attn")
+    return out, lse
 
 
 def kernel_launches() -> int:

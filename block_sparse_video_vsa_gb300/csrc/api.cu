@@ -1,6 +1,6 @@
 // C ABI of the VSA library: argument validation on the host, then dispatch
-// to the kernels of tile.cu, coarse.cu, pair.cu, fine.cu, coarse_attn.cu and
-// block_select.cu
+// to the kernels of tile.cu, coarse.cu, pair.cu, fine.cu, coarse_attn.cu,
+// block_select.cu, cache_store.cu and cache_attn.cu
 // (coarse_noalloc.cu holds the allocation-free coarse entry point).  See
 // include/vsa.h for the contract of each entry point.
 #include <math.h>
@@ -9,7 +9,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "vsa_common.cuh"
+#include "cache.cuh"
 
 namespace vsa {
 
@@ -71,6 +71,37 @@ bool grid_ok(const vsa_grid* g) {
 
 int64_t cubes_of(const vsa_grid* g) {
     return (int64_t)((g->T + 3) / 4) * ((g->H + 3) / 4) * ((g->W + 3) / 4);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// What every vsa_cache_* call asks of the cache and of its rows a sequence.
+vsa_status cache_args(const vsa_cache* c, int32_t S) {
+    if (!c || !c->pool || !c->table || !c->kv_lens) return VSA_ERR_INVALID_ARG;
+    if (c->pages <= 0 || c->kv_heads <= 0 || c->B <= 0 || c->width <= 0 || S <= 0)
+        return VSA_ERR_INVALID_ARG;
+    const int64_t lim = (int64_t)1 << 31;
+    if (c->D != 64 && c->D != 128) return VSA_ERR_UNSUPPORTED;
+    if (c->B > 65535 || c->kv_heads > 65535 || (int64_t)c->pages * c->kv_heads >= lim ||
+        (int64_t)c->width * kPageTokens >= lim || (int64_t)c->B * S >= lim || S > (64 << 24))
+        return VSA_ERR_UNSUPPORTED;
+    if (!aligned16(c->pool) || !aligned4(c->table) || !aligned4(c->kv_lens) || !aligned4(c->kv_scale))
+        return VSA_ERR_ALIGNMENT;
+    return VSA_OK;
+}
+
+vsa_status cache_view(const vsa_cache* c, CacheView* v, DevCtx* ctx) {
+    if (get_dev_ctx(ctx) != cudaSuccess) return VSA_ERR_CUDA;
+    v->pool = static_cast<unsigned char*>(c->pool);
+    v->table = c->table;
+    v->kv_lens = c->kv_lens;
+    v->kv_scale = c->kv_scale;
+    v->err = ctx->err;
+    v->pages = c->pages;
+    v->kv_heads = c->kv_heads;
+    v->B = c->B;
+    v->width = c->width;
+    return VSA_OK;
 }
 
 }  // namespace
@@ -322,6 +353,71 @@ vsa_status vsa_block_select(const void* q, const void* k, int32_t B, int32_t S, 
     if (sm_scale <= 0.f) sm_scale = 1.0f / sqrtf((float)D);
     return from_cuda(launch_block_select(q, k, B, S, heads, D, tau, sm_scale, workspace, cube_idx, cube_counts,
                                          static_cast<cudaStream_t>(stream)));
+}
+
+size_t vsa_cache_pool_bytes(int32_t pages, int32_t kv_heads, int32_t D) {
+    if (pages <= 0 || kv_heads <= 0 || (D != 64 && D != 128)) return 0;
+    return (size_t)pages * kv_heads * 72 * D;
+}
+
+vsa_status vsa_cache_append(const vsa_cache* c, const void* q, const void* k, const void* v, int32_t S,
+                            int32_t heads, const int32_t* new_lens, const float* rope, int32_t rope_rows,
+                            int32_t rope_dim, int32_t interleaved, const int32_t* positions, void* q_out,
+                            vsa_stream_t stream) {
+    CacheView cv;
+    DevCtx ctx;
+    vsa_status st = cache_args(c, S);
+    if (st != VSA_OK) return st;
+    if (!k || !v || (q == nullptr) != (q_out == nullptr) || (q && heads <= 0)) return VSA_ERR_INVALID_ARG;
+    if (rope_dim < 0 || (rope_dim > 0) != (rope != nullptr) || (rope && rope_rows <= 0)) return VSA_ERR_INVALID_ARG;
+    if (rope_dim % 32 || rope_dim > c->D || (q && heads > 65535)) return VSA_ERR_UNSUPPORTED;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || !aligned16(rope) ||
+        !aligned4(new_lens) || !aligned4(positions))
+        return VSA_ERR_ALIGNMENT;
+    st = cache_view(c, &cv, &ctx);
+    if (st != VSA_OK) return st;
+    return from_cuda(launch_cache_append(cv, c->D, q, k, v, S, q ? heads : 0, new_lens, rope, rope_rows, rope_dim,
+                                         interleaved, positions, q_out, ctx.num_sms,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+vsa_status vsa_cache_read(const vsa_cache* c, int32_t S, void* k, void* v, vsa_stream_t stream) {
+    CacheView cv;
+    DevCtx ctx;
+    vsa_status st = cache_args(c, S);
+    if (st != VSA_OK) return st;
+    if (!k || !v) return VSA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v)) return VSA_ERR_ALIGNMENT;
+    st = cache_view(c, &cv, &ctx);
+    if (st != VSA_OK) return st;
+    return from_cuda(launch_cache_read(cv, c->D, S, k, v, static_cast<cudaStream_t>(stream)));
+}
+
+size_t vsa_cache_attn_workspace_bytes(int32_t kv_heads, int32_t D, int32_t Sq, int32_t heads) {
+    if (kv_heads <= 0 || heads <= 0 || heads % kv_heads || Sq <= 0 || (D != 64 && D != 128) ||
+        (int64_t)Sq * (heads / kv_heads) >= (1 << 24))
+        return 0;
+    return cache_attn_workspace_bytes(D, Sq, heads / kv_heads);
+}
+
+vsa_status vsa_cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t heads, const int32_t* q_lens,
+                          int32_t causal, const int32_t* page_sel, int32_t nsel, float sm_scale, void* workspace,
+                          void* out, float* lse, vsa_stream_t stream) {
+    CacheView cv;
+    DevCtx ctx;
+    vsa_status st = cache_args(c, Sq);
+    if (st != VSA_OK) return st;
+    if (!q || !workspace || !out || heads <= 0 || heads % c->kv_heads) return VSA_ERR_INVALID_ARG;
+    if (nsel < 0 || (nsel > 0) != (page_sel != nullptr) || !(sm_scale == sm_scale)) return VSA_ERR_INVALID_ARG;
+    if (heads > 65535 || (int64_t)Sq * (heads / c->kv_heads) >= (1 << 24)) return VSA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(workspace) || !aligned16(out) || !aligned4(q_lens) || !aligned4(page_sel) ||
+        !aligned4(lse))
+        return VSA_ERR_ALIGNMENT;
+    st = cache_view(c, &cv, &ctx);
+    if (st != VSA_OK) return st;
+    if (sm_scale <= 0.f) sm_scale = 1.0f / sqrtf((float)c->D);
+    return from_cuda(launch_cache_attn(cv, c->D, q, Sq, heads, q_lens, causal, page_sel, nsel, sm_scale, workspace,
+                                       out, lse, ctx.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t vsa_pair_workspace_bytes(int32_t B, int32_t heads, int32_t ncubes, int32_t topk) {

@@ -1,0 +1,251 @@
+// Shared pieces of the 4-bit paged cache: the page layout, conversions
+// between its codes and fp16, and the split of attention work over a grid.
+//
+// A page holds 64 tokens of one kv head in 72 * D contiguous bytes:
+//   K codes [64][D / 2] | V codes [64][D / 2] | K scales [64][D / 16] | V scales [64][D / 16]
+// A code is e2m1 (sign, two exponent bits, one mantissa bit), low nibble =
+// even channel; a scale is e4m3 and covers 16 channels.  code * scale has at
+// most 2 + 4 significant bits and lies in [2^-10, 2688], so the product is
+// exact in fp16 (and in bf16): the kernels multiply in fp16 without rounding.
+// The fp32 head scale stays outside (it joins sm_scale and the epilogue).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "vsa_common.cuh"
+
+namespace vsa {
+
+constexpr int kPageTokens = 64;
+
+// What every cache kernel knows of the cache (device pointers).
+struct CacheView {
+    unsigned char* pool;
+    const int32_t* table;    // [B][width]
+    const int32_t* kv_lens;  // [B]
+    const float* kv_scale;   // [2][kv_heads], or null: 1
+    unsigned int* err;
+    int pages, kv_heads, B, width;
+};
+
+#if defined(__CUDACC__)
+
+template <int kD>
+struct PageLayout {
+    static constexpr int kRow = kD / 2;     // code bytes of a token
+    static constexpr int kGroups = kD / 16;  // scale bytes of a token
+    static constexpr int kV = kPageTokens * kRow;
+    static constexpr int kKScale = 2 * kPageTokens * kRow;
+    static constexpr int kVScale = kKScale + kPageTokens * kGroups;
+    static constexpr int kBytes = kVScale + kPageTokens * kGroups;
+};
+static_assert(PageLayout<128>::kBytes == 72 * 128 && PageLayout<64>::kBytes == 72 * 64, "page size");
+
+// Tokens of sequence b in the cache; a length the page table cannot hold is
+// cut to what it holds (and noted in the error word by the caller's choice).
+__device__ __forceinline__ int cache_len(const CacheView& c, int b, bool note) {
+    const int n = __ldg(c.kv_lens + b);
+    const long long cap = (long long)c.width * kPageTokens;
+    if (n < 0 || n > cap) {
+        if (note) atomicOr(c.err, VSA_DEVERR_INDEX);
+        return n < 0 ? 0 : (int)cap;
+    }
+    return n;
+}
+
+// Four bytes of code pairs -> four fp16 pairs (byte j's low nibble in the low half).
+__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// Two e4m3 bytes (bits 0..15) -> fp16 pair.
+__device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t two) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(two));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Power-of-two factor that brings a query row of largest magnitude `amax`
+// near 2^14, so that its bf16 values (8 significant bits) convert to fp16 (11)
+// without rounding down to 2^-38 of the row's largest; 1 for a row of zeros,
+// infinities or NaN alone.  The inverse goes into the row's softmax scale.
+__device__ __forceinline__ int q_exponent(float amax) {
+    if (!(amax > 0.f) || amax > 3.4e38f) return 0;
+    const int e = (int)((__float_as_uint(amax) >> 23) & 0xFFu) - 127;  // below the normals: -127
+    return min(14 - e, 120);
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
+
+// Untiled bulk copy into shared memory (16-byte aligned, a multiple of 16 bytes), completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// ------------------------------------------------- split of attention work
+// A unit is (sequence b, kv head, tile of `tile` query rows); row r is head
+// kv_head * group + r % group of query r / group.  Units are laid end to end
+// in the order (b, kv head, tile), each as long as the pages it walks (one at
+// least, so that every unit has an owner that writes its rows), and the line
+// is cut into equal parts, one for each CTA: batches of ragged lengths and
+// single long sequences fill the grid alike.  A unit that lies in one part
+// is written by its CTA; the parts of a cut unit go to the workspace (two
+// slots a CTA: slot 0 for a unit begun by an earlier CTA, slot 1 for one it
+// begins itself and does not finish) and are joined by combine_kernel.
+struct AttnParams {
+    CacheView c;
+    const int32_t* q_lens;    // [B], or null: Sq
+    const int32_t* page_sel;  // [B][kv_heads][nsel], or null
+    const uint4* q;           // bf16 [B][Sq][heads][D]
+    uint4* out;
+    float* lse;               // [B][heads][Sq], or null
+    float* part_o;            // [2 * grid][tile][D]
+    float2* part_ml;          // [2 * grid][tile]: maximum (log2 units), sum
+    int Sq, heads, group, nsel, causal;
+    int tile, tiles;          // rows of a unit; units of a (b, kv head)
+    int grid;                 // CTAs of the attention kernel
+    int whole;                // units are not cut: a unit belongs to the CTA that holds its first page
+    float scale_log2;         // sm_scale * log2(e)
+};
+
+struct SeqLens {
+    int kv, q;
+};
+
+__device__ __forceinline__ SeqLens seq_lens(const AttnParams& p, int b, bool note = false) {
+    SeqLens s;
+    s.kv = cache_len(p.c, b, note);
+    s.q = p.q_lens ? min(max(__ldg(p.q_lens + b), 0), p.Sq) : p.Sq;
+    return s;
+}
+
+// Pages that tile t of a sequence walks (0: nothing to attend).
+__device__ __forceinline__ int tile_pages(const AttnParams& p, const SeqLens& s, int t) {
+    const int rows = s.q * p.group;
+    const int first = t * p.tile;
+    if (first >= rows) return 0;
+    if (p.page_sel) return p.nsel;
+    int lim = s.kv;
+    if (p.causal) lim = min(lim, s.kv - s.q + (min(rows, first + p.tile) - 1) / p.group + 1);
+    return lim > 0 ? (lim + kPageTokens - 1) / kPageTokens : 0;
+}
+__device__ __forceinline__ int tile_cost(const AttnParams& p, const SeqLens& s, int t) {
+    return max(1, tile_pages(p, s, t));
+}
+// Cost of one kv head of a sequence: the sum of its tiles.
+__device__ __forceinline__ long long head_cost(const AttnParams& p, const SeqLens& s) {
+    if (!p.causal || p.tiles == 1) {
+        const int live = min(p.tiles, (s.q * p.group + p.tile - 1) / p.tile);
+        return (long long)live * tile_cost(p, s, 0) + (p.tiles - live);
+    }
+    long long n = 0;
+    for (int t = 0; t < p.tiles; ++t) n += tile_cost(p, s, t);
+    return n;
+}
+
+// A place on the line: page `page` of unit (b, h, t).
+struct Place {
+    int b, h, t, page;
+};
+
+// Part `c` of `n` of a line of `total`: [part_begin(c), part_begin(c + 1)).
+__device__ __forceinline__ long long part_begin(long long total, int c, int n) {
+    return (long long)(((unsigned long long)total * (unsigned)c) / (unsigned)n);
+}
+__device__ __forceinline__ int part_of(long long total, long long pos, int n) {
+    int c = (int)(((unsigned long long)pos * (unsigned)n) / (unsigned long long)total);
+    while (c + 1 < n && part_begin(total, c + 1, n) <= pos) ++c;
+    while (c > 0 && part_begin(total, c, n) > pos) --c;
+    return c;
+}
+
+struct PlanScratch {
+    long long warp_sum[32];
+    Place place;
+};
+
+// Length of the whole line, and this thread's share of its prefix: sequences
+// [b0, b1) start at `before`.  Called by all threads of the block.
+__device__ __forceinline__ long long line_scan(const AttnParams& p, PlanScratch& sc, int& b0, int& b1,
+                                               long long& before) {
+    const int n = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (n + 31) >> 5;
+    const int per = (p.c.B + n - 1) / n;
+    b0 = min((int)threadIdx.x * per, p.c.B);
+    b1 = min(b0 + per, p.c.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += p.c.kv_heads * head_cost(p, seq_lens(p, b));
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sc.warp_sum[warp] = incl;
+    __syncthreads();
+    long long base = 0, total = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) base += sc.warp_sum[w];
+        total += sc.warp_sum[w];
+    }
+    before = base + incl - mine;
+    return total;
+}
+
+// The place of position `pos` of the line (pos < total; all threads of the
+// block call it with the same pos).
+__device__ __forceinline__ Place line_place(const AttnParams& p, PlanScratch& sc, int b0, int b1, long long before,
+                                            long long pos) {
+    for (int b = b0; b < b1; ++b) {
+        const SeqLens s = seq_lens(p, b);
+        const long long hc = head_cost(p, s);
+        const long long cost = p.c.kv_heads * hc;
+        if (pos >= before && pos < before + cost) {
+            Place x;
+            x.b = b;
+            x.h = (int)((pos - before) / hc);
+            long long at = (pos - before) - x.h * hc;
+            x.t = 0;
+            for (int n; at >= (n = tile_cost(p, s, x.t)); ++x.t) at -= n;
+            x.page = (int)at;
+            sc.place = x;
+        }
+        before += cost;
+    }
+    __syncthreads();
+    const Place x = sc.place;
+    __syncthreads();
+    return x;
+}
+
+// Pages each CTA takes at least (where there are fewer than grid * this, some CTAs take none).
+constexpr int kMinPart = 2;
+__device__ __forceinline__ int used_parts(const AttnParams& p, long long total) {
+    const long long n = (total + kMinPart - 1) / kMinPart;
+    return n < p.grid ? (int)n : p.grid;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace vsa

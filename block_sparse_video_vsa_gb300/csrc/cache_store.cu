@@ -1,0 +1,293 @@
+// Writing and reading the 4-bit paged cache.
+//
+// append_kernel: the keys and values of a step go to their pages, the keys
+// (and the step's queries, to an output of their own) rotated on the way:
+//   (x, y) -> (x c - y s, y c + x s) for the channel pairs (2i, 2i + 1) or
+//   (i, i + R / 2), with c, s the fp32 table row of the token's position.
+// Products and sums are rounded one by one (no fused multiply-add), so the
+// fp32 result, and with it every code, is the one the formula gives step by
+// step.  Then, for 16 channels with y = x / head scale:
+//   scale = e4m3(max|y| / 6),  code = e2m1(y / scale)   (nearest, ties to even)
+// where both divisions are multiplications by the fp32 reciprocal.
+// HBM bound: (heads + 2 kv_heads) * D * 2 bytes in, heads * D * 2 + kv_heads
+// * D * 9 / 8 out a token.  A thread takes 32 channels of one token (two
+// scale groups, the two halves of a rotated pair among them) and holds their
+// cosines and sines in registers over all heads it walks; a warp takes
+// neighbouring tokens of one head, whose codes are contiguous in the page.
+//
+// read_kernel: pages back to bf16 rows, [B, S, kv_heads, D], zero past each
+// sequence's length.  HBM bound (9/16 byte in, 2 bytes out an element): one
+// block a page and head, 16-byte stores.
+#include "cache.cuh"
+
+namespace vsa {
+
+namespace {
+
+struct AppendParams {
+    CacheView c;
+    const uint4* q;
+    const uint4* k;
+    const uint4* v;
+    uint4* q_out;
+    const int32_t* new_lens;   // [B], or null: S
+    const int32_t* positions;  // [B][S], or null: the token's place in its sequence
+    const float* rope;         // [rope_rows][R]: R / 2 cosines, R / 2 sines
+    int S, heads, rope_rows, R;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(u[i]);
+        x[2 * i + 1] = bf16_hi(u[i]);
+    }
+}
+
+// Codes (two words) and scale byte of 16 channels.  The cache holds finite
+// numbers only: NaN is stored as 0, and what is beyond 448 * 6 saturates.
+__device__ __forceinline__ uint32_t quantise16(const float* x, float inv_head, uint32_t (&code)[2]) {
+    float y[16];
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        y[i] = __fmul_rn(x[i], inv_head);
+        y[i] = y[i] == y[i] ? y[i] : 0.f;
+        a = fmaxf(a, fabsf(y[i]));
+    }
+    uint16_t s8;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(__fmul_rn(a, 1.f / 6.f)));
+    const float s = __half2float(__ushort_as_half((unsigned short)(e4m3_to_f16(s8) & 0xFFFFu)));
+    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // No NaN here: a zero scale has no infinity in its group (that scale is 448).
+            const float lo = __fmul_rn(y[8 * w + 2 * j], r), hi = __fmul_rn(y[8 * w + 2 * j + 1], r);
+            uint32_t b;
+            asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, 0, 0, 0};\n\t}"
+                : "=r"(b)
+                : "f"(hi), "f"(lo));
+            word |= b << (8 * j);
+        }
+        code[w] = word;
+    }
+    return s8 & 0xFFu;
+}
+
+constexpr int kAppendThreads = 256;
+
+// kTok tokens a block: 8 neighbouring tokens, or 1 for steps of few tokens
+// (then the block's threads spread over heads instead).
+template <int kD, int kTok, bool kPairs>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) {
+    using L = PageLayout<kD>;
+    constexpr int kSlices = kD / 32;                              // threads of a head row
+    constexpr int kHeadLanes = kAppendThreads / (kSlices * kTok);  // heads in flight
+    const int slice = threadIdx.x % kSlices;
+    const int b = blockIdx.z;
+    const int tok = blockIdx.x * kTok + (threadIdx.x / kSlices) % kTok;
+    const int n = cache_len(p.c, b, threadIdx.x == 0);
+    const int fresh = min(p.new_lens ? max(__ldg(p.new_lens + b), 0) : p.S, min(p.S, n));
+    const bool live = tok < fresh;
+    const int at = n - fresh + tok;  // place in the sequence
+    // Where the token goes.
+    unsigned char* page = nullptr;
+    if (live) {
+        const int id = __ldg(p.c.table + (size_t)b * p.c.width + at / kPageTokens);
+        if (id >= 0 && id < p.c.pages)
+            page = p.c.pool + (size_t)id * p.c.kv_heads * L::kBytes;
+        else if (slice == 0)
+            atomicOr(p.c.err, VSA_DEVERR_INDEX);
+    }
+    const int in_page = at % kPageTokens;
+    // The two groups of 16 channels: [g0, g0 + 16) and [g1, g1 + 16).
+    const bool turned = slice * 32 < p.R;
+    const int g0 = turned && !kPairs ? slice * 16 : slice * 32;
+    const int g1 = turned && !kPairs ? slice * 16 + p.R / 2 : slice * 32 + 16;
+    float cs[16], sn[16];
+    bool known = true;  // the position has a row
+    if (turned && live) {
+        const int pos = p.positions ? __ldg(p.positions + (size_t)b * p.S + tok) : at;
+        known = pos >= 0 && pos < p.rope_rows;
+        if (!known && slice == 0) atomicOr(p.c.err, VSA_DEVERR_INDEX);
+        const float4* row = reinterpret_cast<const float4*>(p.rope + (size_t)(known ? pos : 0) * p.R + slice * 16);
+        const float4* row_s = row + p.R / 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 a = __ldg(row + i), s = __ldg(row_s + i);
+            cs[4 * i] = a.x; cs[4 * i + 1] = a.y; cs[4 * i + 2] = a.z; cs[4 * i + 3] = a.w;
+            sn[4 * i] = s.x; sn[4 * i + 1] = s.y; sn[4 * i + 2] = s.z; sn[4 * i + 3] = s.w;
+        }
+    }
+    if (tok >= p.S) return;
+    const size_t token = (size_t)b * p.S + tok;
+    const int hq = p.q_out ? p.heads : 0;
+    const int all = hq + 2 * p.c.kv_heads;
+    for (int h = blockIdx.y * kHeadLanes + threadIdx.x / (kSlices * kTok); h < all; h += gridDim.y * kHeadLanes) {
+        const bool is_q = h < hq, is_k = !is_q && h < hq + p.c.kv_heads;
+        const int kh = is_q ? h : is_k ? h - hq : h - hq - p.c.kv_heads;
+        if (!live) {  // a padding row: nothing to keep, its query is zero
+            if (is_q) {
+                uint4* dst = p.q_out + (token * p.heads + kh) * (kD / 8);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    dst[g0 / 8 + i] = make_uint4(0, 0, 0, 0);
+                    dst[g1 / 8 + i] = make_uint4(0, 0, 0, 0);
+                }
+            }
+            continue;
+        }
+        const uint4* src = is_q ? p.q + (token * p.heads + kh) * (kD / 8)
+                                : (is_k ? p.k : p.v) + (token * p.c.kv_heads + kh) * (kD / 8);
+        float x[32];
+        unpack8(__ldg(src + g0 / 8), x);
+        unpack8(__ldg(src + g0 / 8 + 1), x + 8);
+        unpack8(__ldg(src + g1 / 8), x + 16);
+        unpack8(__ldg(src + g1 / 8 + 1), x + 24);
+        if (turned && (is_q || is_k)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                // Pair i: (2i, 2i + 1) of the 32 channels, or (i, 16 + i) of the two halves.
+                float& u = x[kPairs ? 2 * i : i];
+                float& w = x[kPairs ? 2 * i + 1 : 16 + i];
+                const float a = u, c = w;
+                u = known ? __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(c, sn[i])) : 0.f;
+                w = known ? __fadd_rn(__fmul_rn(c, cs[i]), __fmul_rn(a, sn[i])) : 0.f;
+            }
+        }
+        if (is_q) {
+            uint4* dst = p.q_out + (token * p.heads + kh) * (kD / 8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float* y = x + 8 * i;
+                dst[(i < 2 ? g0 / 8 : g1 / 8 - 2) + i] =
+                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                               pack_bf16x2(y[6], y[7]));
+            }
+        } else if (page) {
+            const float hs = p.c.kv_scale ? __ldg(p.c.kv_scale + (is_k ? 0 : p.c.kv_heads) + kh) : 1.f;
+            const float inv = __frcp_rn(hs);
+            uint32_t c0[2], c1[2];
+            const uint32_t s0 = quantise16(x, inv, c0), s1 = quantise16(x + 16, inv, c1);
+            unsigned char* head = page + (size_t)kh * L::kBytes;
+            unsigned char* codes = head + (is_k ? 0 : L::kV) + in_page * L::kRow;
+            unsigned char* scales = head + (is_k ? L::kKScale : L::kVScale) + in_page * L::kGroups;
+            *reinterpret_cast<uint2*>(codes + g0 / 2) = make_uint2(c0[0], c0[1]);
+            *reinterpret_cast<uint2*>(codes + g1 / 2) = make_uint2(c1[0], c1[1]);
+            scales[g0 / 16] = (unsigned char)s0;
+            scales[g1 / 16] = (unsigned char)s1;
+        }
+    }
+}
+
+struct ReadParams {
+    CacheView c;
+    uint4* k;
+    uint4* v;
+    int S;
+};
+
+constexpr int kReadThreads = 256;
+
+template <int kD>
+__global__ void __launch_bounds__(kReadThreads) read_kernel(ReadParams p) {
+    using L = PageLayout<kD>;
+    constexpr int kLanes = kD / 8;                  // threads of a token row (8 channels each)
+    constexpr int kStep = kReadThreads / kLanes;    // tokens a pass
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int first = blockIdx.x * kPageTokens;
+    const int lane = threadIdx.x % kLanes;
+    const int n = cache_len(p.c, b, threadIdx.x == 0);
+    const unsigned char* page = nullptr;
+    if (first < n) {
+        const int id = __ldg(p.c.table + (size_t)b * p.c.width + blockIdx.x);
+        if (id >= 0 && id < p.c.pages)
+            page = p.c.pool + ((size_t)id * p.c.kv_heads + h) * L::kBytes;
+        else if (threadIdx.x == 0)
+            atomicOr(p.c.err, VSA_DEVERR_INDEX);
+    }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const float hs = p.c.kv_scale ? __ldg(p.c.kv_scale + side * p.c.kv_heads + h) : 1.f;
+        uint32_t code[kPageTokens / kStep], scale[kPageTokens / kStep];
+#pragma unroll
+        for (int i = 0; i < kPageTokens / kStep; ++i) {
+            const int t = threadIdx.x / kLanes + i * kStep;
+            const bool held = page && first + t < n;
+            code[i] = held ? __ldg(reinterpret_cast<const uint32_t*>(page + side * L::kV + t * L::kRow) + lane) : 0u;
+            scale[i] = held ? (uint32_t)__ldg(page + (side ? L::kVScale : L::kKScale) + t * L::kGroups + lane / 2) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < kPageTokens / kStep; ++i) {
+            const int t = first + threadIdx.x / kLanes + i * kStep;
+            if (t >= p.S) continue;
+            uint32_t e[4], w[4];
+            e2m1_to_f16(code[i], e);
+            const uint32_t s = e4m3_to_f16(scale[i] * 0x101u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t y = mul_f16x2(e[j], s);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y));
+                w[j] = pack_bf16x2(f.x * hs, f.y * hs);
+            }
+            uint4* dst = (side ? p.v : p.k) + (((size_t)b * p.S + t) * p.c.kv_heads + h) * kLanes + lane;
+            __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheView& c, int D, const void* q, const void* k, const void* v, int S,
+                                int heads, const int32_t* new_lens, const float* rope, int rope_rows, int rope_dim,
+                                int interleaved, const int32_t* positions, void* q_out, int num_sms,
+                                cudaStream_t stream) {
+    AppendParams p;
+    p.c = c;
+    p.q = static_cast<const uint4*>(q);
+    p.k = static_cast<const uint4*>(k);
+    p.v = static_cast<const uint4*>(v);
+    p.q_out = static_cast<uint4*>(q_out);
+    p.new_lens = new_lens;
+    p.positions = positions;
+    p.rope = rope;
+    p.S = S;
+    p.heads = heads;
+    p.rope_rows = rope_rows;
+    p.R = rope_dim;
+    const int all = (q_out ? heads : 0) + 2 * c.kv_heads;
+    const int tok = S >= 8 ? 8 : 1;
+    const int lanes = kAppendThreads / (D / 32 * tok);
+    const int bx = (S + tok - 1) / tok;
+    // Heads are spread over blocks until there are some four for each SM, and not further.
+    const int most = (all + lanes - 1) / lanes;
+    const long long blocks = (long long)bx * c.B;
+    int by = (int)((4LL * num_sms + blocks - 1) / blocks);
+    by = by < 1 ? 1 : by > most ? most : by;
+    const dim3 grid((unsigned)bx, (unsigned)by, (unsigned)c.B);
+    auto of_d64 = interleaved ? (tok == 8 ? append_kernel<64, 8, true> : append_kernel<64, 1, true>)
+                              : (tok == 8 ? append_kernel<64, 8, false> : append_kernel<64, 1, false>);
+    auto of_d128 = interleaved ? (tok == 8 ? append_kernel<128, 8, true> : append_kernel<128, 1, true>)
+                               : (tok == 8 ? append_kernel<128, 8, false> : append_kernel<128, 1, false>);
+    (D == 64 ? of_d64 : of_d128)<<<grid, kAppendThreads, 0, stream>>>(p);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(const CacheView& c, int D, int S, void* k, void* v, cudaStream_t stream) {
+    ReadParams p;
+    p.c = c;
+    p.k = static_cast<uint4*>(k);
+    p.v = static_cast<uint4*>(v);
+    p.S = S;
+    const dim3 grid((unsigned)((S + kPageTokens - 1) / kPageTokens), (unsigned)c.kv_heads, (unsigned)c.B);
+    (D == 64 ? read_kernel<64> : read_kernel<128>)<<<grid, kReadThreads, 0, stream>>>(p);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace vsa

@@ -58,6 +58,20 @@ cudaError_t launch_block_select(const void* q, const void* k, int B, int S, int 
                                 float sm_scale, void* workspace, int32_t* cube_idx, int32_t* cube_counts,
                                 cudaStream_t stream);
 
+// cache_store.cu
+struct CacheView;
+cudaError_t launch_cache_append(const CacheView& c, int D, const void* q, const void* k, const void* v, int S,
+                                int heads, const int32_t* new_lens, const float* rope, int rope_rows, int rope_dim,
+                                int interleaved, const int32_t* positions, void* q_out, int num_sms,
+                                cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheView& c, int D, int S, void* k, void* v, cudaStream_t stream);
+
+// cache_attn.cu
+size_t cache_attn_workspace_bytes(int D, int Sq, int group);
+cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, int heads, const int32_t* q_lens,
+                              int causal, const int32_t* page_sel, int nsel, float sm_scale, void* workspace,
+                              void* out, float* lse, int num_sms, cudaStream_t stream);
+
 // pair.cu
 int pair_words(int ncubes);
 size_t pair_workspace_bytes(int B, int heads, int ncubes, int topk);

@@ -19,7 +19,9 @@
  * (vsa_coarse_attn) and its gated sum with the fine output
  * (vsa_sparse_attn_fwd_gated), and a mean-pool block selector with a
  * cumulative threshold for sequences in 128-token blocks
- * (vsa_block_select).
+ * (vsa_block_select).  For video generated chunk by chunk, a paged cache of
+ * earlier keys and values in 4 bits, one cube (64 tokens) a page:
+ * vsa_cache_append, vsa_cache_attn and vsa_cache_read.
  *
  * Sources (page title, section):
  *   [VSA-AMD] "VSA: Accelerating Video Diffusion Inference with Sparse
@@ -92,6 +94,7 @@ typedef struct {
 
 /* Device error word bits (vsa_device_error). */
 #define VSA_DEVERR_TIMEOUT 0x1u /* a bounded mbarrier wait in a kernel ran out */
+#define VSA_DEVERR_INDEX 0x2u   /* a vsa_cache_* call met a page, length or position out of range */
 
 /* Human-readable name of a status code.  Never NULL. */
 const char* vsa_status_string(vsa_status s);
@@ -421,6 +424,116 @@ size_t vsa_block_select_workspace_bytes(int32_t B, int32_t S, int32_t heads, int
 vsa_status vsa_block_select(const void* q, const void* k, int32_t B, int32_t S, int32_t heads, int32_t D,
                             float tau, float sm_scale, void* workspace, int32_t* cube_idx,
                             int32_t* cube_counts, vsa_stream_t stream);
+
+/*
+ * A paged cache of keys and values in 4 bits (no counterpart in the pages: it
+ * keeps a clip's earlier cubes for queries that come later).
+ *   pool     : uint8 [pages, kv_heads, 72 * D], 16-byte aligned; page p of kv
+ *              head h holds 64 tokens:
+ *                K codes [64][D / 2] | V codes [64][D / 2] |
+ *                K scales [64][D / 16] | V scales [64][D / 16]
+ *              A code is 4 bits (e2m1: sign, two exponent bits, one mantissa
+ *              bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), the low nibble the even
+ *              channel; a scale is an e4m3 byte for 16 channels.  The value is
+ *              code * scale * head scale; code * scale is exact in bf16.
+ *   table    : int32 [B, width]: page of tokens 64 w .. 64 w + 63 of sequence
+ *              b; entries past a sequence's last page are not read
+ *   kv_lens  : int32 [B]: tokens of each sequence, those of the present step
+ *              included, in [0, 64 * width]
+ *   kv_scale : fp32 [2, kv_heads] (keys, values), each positive and finite, or
+ *              NULL: 1.  Choose it so that |x| / head scale stays below 2688
+ *              and well above 2^-6 (e4m3 is coarse below that).
+ * Sequences may share pages that no call appends to.  A length, page or
+ * position outside its range never leads to an access out of range: it sets
+ * VSA_DEVERR_INDEX in the device error word (vsa_device_error) and the length
+ * is cut, the page passed over.
+ * Limits of the vsa_cache_* calls: D in {64, 128}; B, kv_heads <= 65535;
+ * pages * kv_heads < 2^31; 64 * width < 2^31.
+ */
+typedef struct {
+    int32_t pages, kv_heads, D; /* the pool */
+    int32_t B, width;           /* sequences; columns of the page table */
+    void* pool;
+    const int32_t* table;
+    const int32_t* kv_lens;
+    const float* kv_scale;
+} vsa_cache;
+
+/* Bytes of a pool: pages * kv_heads * 72 * D.  0 for bad sizes. */
+size_t vsa_cache_pool_bytes(int32_t pages, int32_t kv_heads, int32_t D);
+
+/*
+ * Appends a step's keys and values to the cache, rotating keys (and queries)
+ * by position on the way.  Token i < new_lens[b] of sequence b goes to place
+ * kv_lens[b] - new_lens[b] + i of the sequence; kv_lens already counts it, so
+ * one update of kv_lens serves the append and the attention of every layer.
+ *   rotation : for the channel pairs (x, y) = (2i, 2i + 1) when interleaved,
+ *              (i, i + rope_dim / 2) otherwise, i < rope_dim / 2:
+ *              (x c_i - y s_i, y c_i + x s_i) in fp32, each product and sum
+ *              rounded; channels from rope_dim on stay.  c, s: row `position`
+ *              of rope.  Three-axis rotations are tables indexed by raster
+ *              token.
+ *   storing  : with y = x * (1 / head scale), for each 16 channels: scale =
+ *              e4m3(max|y| * (1 / 6)), code = e2m1(y * (1 / scale)), to
+ *              nearest, ties to even, saturating (fp32 throughout).  NaN is
+ *              stored as 0.
+ *   q         : bf16 [B, S, heads, D] or NULL;  q_out likewise (written in
+ *               full: the rotated queries, zero rows from new_lens on).  Both
+ *               or neither; heads is not read without them.
+ *   k, v      : bf16 [B, S, kv_heads, D]
+ *   new_lens  : int32 [B], cut to [0, min(S, kv_lens[b])], or NULL: S
+ *   rope      : fp32 [rope_rows, rope_dim] (rope_dim / 2 cosines, then the
+ *               sines), or NULL with rope_dim = 0: no rotation
+ *   positions : int32 [B, S], or NULL: the token's place in its sequence.  A
+ *               token whose position has no row gets a zero rotation
+ *               (VSA_DEVERR_INDEX).
+ * Pages being appended to belong to one sequence.  Slots that no token goes
+ * to are left as they are.  rope_dim: a multiple of 32, at most D.  heads <=
+ * 65535.  B * S < 2^31.
+ */
+vsa_status vsa_cache_append(const vsa_cache* c, const void* q, const void* k, const void* v, int32_t S,
+                            int32_t heads, const int32_t* new_lens, const float* rope, int32_t rope_rows,
+                            int32_t rope_dim, int32_t interleaved, const int32_t* positions, void* q_out,
+                            vsa_stream_t stream);
+
+/*
+ * Reads the first S tokens of every sequence back:
+ *   k, v : bf16 [B, S, kv_heads, D] (written in full; rows from kv_lens[b] on
+ *          are zero).  code * scale * head scale, rounded to bf16 once (exact
+ *          for head scales that are powers of two).
+ * With S = 64 * ncubes these are tiled tensors for vsa_sparse_attn_fwd.
+ * B * S < 2^31, S <= 64 * 2^24.
+ */
+vsa_status vsa_cache_read(const vsa_cache* c, int32_t S, void* k, void* v, vsa_stream_t stream);
+
+/*
+ * Attention of Sq query rows a sequence over the cache.  Query i < q_lens[b]
+ * of head h attends, through kv head h / (heads / kv_heads), the keys
+ *   x < kv_lens[b], and with causal != 0  x <= kv_lens[b] - q_lens[b] + i,
+ *   and with page_sel only x in the pages listed for (b, kv head):
+ *   s_x = sm_scale * (q . k_x),  out = sum_x softmax(s)_x v_x,
+ *   lse = log(sum_x exp(s_x)).
+ * A row with no key, and rows from q_lens[b] on, get out = 0, lse = -inf.
+ *   q         : bf16 [B, Sq, heads, D], rotated as the keys were
+ *               (vsa_cache_append's q_out); heads a multiple of kv_heads
+ *   q_lens    : int32 [B], cut to [0, Sq], or NULL: Sq
+ *   page_sel  : int32 [B, kv_heads, nsel]: page numbers within the sequence
+ *               (columns of the table), distinct within a row, in any order;
+ *               numbers outside the sequence's pages (-1) are passed over.
+ *               Or NULL with nsel = 0: every page
+ *   sm_scale  : <= 0 selects 1 / sqrt(D)
+ *   workspace : vsa_cache_attn_workspace_bytes(...) bytes, 16-byte aligned,
+ *               overwritten; calls that may overlap (other streams, graphs
+ *               replayed at once) need workspaces of their own
+ *   out       : bf16 [B, Sq, heads, D] (written in full)
+ *   lse       : fp32 [B, heads, Sq] (written), or NULL
+ * Softmax statistics and sums are fp32, P is rounded to fp16.
+ * Limits: Sq * heads / kv_heads < 2^24, heads <= 65535, B * Sq < 2^31.
+ */
+size_t vsa_cache_attn_workspace_bytes(int32_t kv_heads, int32_t D, int32_t Sq, int32_t heads);
+vsa_status vsa_cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t heads, const int32_t* q_lens,
+                          int32_t causal, const int32_t* page_sel, int32_t nsel, float sm_scale, void* workspace,
+                          void* out, float* lse, vsa_stream_t stream);
 
 /*
  * Debug aid for the block-sparse encoding ([VSA-AMD] Block-Sparse Encoding):
