@@ -246,6 +246,86 @@ __device__ __forceinline__ int used_parts(const AttnParams& p, long long total) 
     return n < p.grid ? (int)n : p.grid;
 }
 
+// A CTA's walk along its part of the line, unit by unit.
+struct Segment {
+    int b, h, t;
+    SeqLens len;
+    int first, last;  // pages
+    bool whole;       // the unit from end to end: its rows are written at once
+};
+struct Walk {
+    Place at;
+    SeqLens len;
+    long long left;  // of the part
+
+    // All threads of the block call it; false: nothing for this CTA.
+    __device__ bool begin(const AttnParams& p, PlanScratch& sc) {
+        int b0, b1;
+        long long before;
+        const long long total = line_scan(p, sc, b0, b1, before);
+        const int parts = used_parts(p, total);
+        if ((int)blockIdx.x >= parts) return false;
+        const long long from = part_begin(total, blockIdx.x, parts);
+        left = part_begin(total, blockIdx.x + 1, parts) - from;
+        at = line_place(p, sc, b0, b1, before, from);
+        len = seq_lens(p, at.b, threadIdx.x == 0);
+        if (p.whole && at.page > 0) {  // units are not cut: the one begun earlier is its owner's
+            const int rest = tile_cost(p, len, at.t) - at.page;
+            left -= rest;
+            at.page += rest;
+        }
+        return true;
+    }
+    __device__ bool next(const AttnParams& p, Segment& s) {
+        if (left <= 0) return false;
+        int cost = tile_cost(p, len, at.t);
+        if (at.page >= cost) {  // the next unit
+            at.page = 0;
+            if (++at.t == p.tiles) {
+                at.t = 0;
+                if (++at.h == p.c.kv_heads) {
+                    at.h = 0;
+                    if (++at.b == p.c.B) return false;
+                    len = seq_lens(p, at.b, threadIdx.x == 0);
+                }
+            }
+            cost = tile_cost(p, len, at.t);
+        }
+        const int take = p.whole || cost - at.page < left ? cost - at.page : (int)left;
+        const int n = tile_pages(p, len, at.t);
+        s.b = at.b;
+        s.h = at.h;
+        s.t = at.t;
+        s.len = len;
+        s.first = min(at.page, n);
+        s.last = min(at.page + take, n);
+        s.whole = at.page == 0 && take == cost;
+        left -= take;
+        at.page += take;
+        return true;
+    }
+};
+
+// Looks up page `i` of a segment's walk: its page number within the sequence,
+// and its place in the pool (-1: passed over).
+__device__ __forceinline__ void look_up(const AttnParams& p, const Segment& s, int i, int& logical, int& id) {
+    logical = p.page_sel ? __ldg(p.page_sel + ((size_t)s.b * p.c.kv_heads + s.h) * p.nsel + i) : i;
+    id = -1;
+    if (logical < 0 || logical >= (s.len.kv + kPageTokens - 1) / kPageTokens) return;
+    id = __ldg(p.c.table + (size_t)s.b * p.c.width + logical);
+    if (id < 0 || id >= p.c.pages) {
+        atomicOr(p.c.err, VSA_DEVERR_INDEX);
+        id = -1;
+    }
+}
+
+constexpr int kMaxGrid = 160;                     // CTAs of an attention launch: one for each SM (152 on GB300)
+constexpr uint64_t kCacheWaitNs = 2000000000ull;  // 2 s
+constexpr float kCacheRescale = 8.0f;             // growth of the maximum (log2 units) that rescales the output
+
+// cache_chunk.cu
+cudaError_t launch_chunk(const AttnParams& p, int D, cudaStream_t stream);
+
 #endif  // __CUDACC__
 
 }  // namespace vsa

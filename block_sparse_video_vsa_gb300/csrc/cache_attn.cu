@@ -32,9 +32,6 @@ namespace vsa {
 
 namespace {
 
-constexpr float kTokenRescale = 8.0f;           // log2 units
-constexpr uint64_t kCacheWaitNs = 2000000000ull;  // 2 s
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -99,71 +96,21 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
     }
     // The joining kernel may be set up meanwhile (its blocks wait for this grid's end).
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // This CTA's part of the line.
-    int b0, b1;
-    long long before;
-    const long long total = line_scan(p, sm.plan, b0, b1, before);
-    const int parts = used_parts(p, total);
-    if ((int)blockIdx.x >= parts) return;
-    const long long begin = part_begin(total, blockIdx.x, parts);
-    long long left = part_begin(total, blockIdx.x + 1, parts) - begin;
-    Place at = line_place(p, sm.plan, b0, b1, before, begin);
-    SeqLens len = seq_lens(p, at.b, threadIdx.x == 0);
+    Walk walk;
+    if (!walk.begin(p, sm.plan)) return;
     volatile int* abort_flag = &sm.abort_flag;
-
-    // Walks the segments of the part: f(place, pages begin, pages end, whole unit).
-    auto walk = [&](auto&& f) {
-        // Units are not cut: the one begun earlier is its owner's.
-        if (p.whole && at.page > 0) {
-            const int rest = tile_cost(p, len, at.t) - at.page;
-            left -= rest;
-            at.page += rest;
-        }
-        while (true) {
-            int cost = tile_cost(p, len, at.t);
-            if (at.page >= cost) {  // next unit
-                at.page = 0;
-                if (++at.t == p.tiles) {
-                    at.t = 0;
-                    if (++at.h == p.c.kv_heads) {
-                        at.h = 0;
-                        if (++at.b == p.c.B) break;
-                        len = seq_lens(p, at.b, threadIdx.x == 0);
-                    }
-                }
-                cost = tile_cost(p, len, at.t);
-            }
-            if (left <= 0) break;
-            const int take = p.whole || cost - at.page < left ? cost - at.page : (int)left;
-            const int n = tile_pages(p, len, at.t);
-            if (!f(min(at.page, n), min(at.page + take, n), at.page == 0 && take == cost)) break;
-            left -= take;
-            at.page += take;
-        }
-    };
 
     if (warp == kWarps) {
         // =========================================================== producer
         uint32_t j = 0;
         bool ok = true;
-        walk([&](int first, int last, bool) {
-            const unsigned char* pool = p.c.pool + (size_t)at.h * L::kBytes;
-            const int held = (len.kv + kPageTokens - 1) / kPageTokens;
-            for (int base = first; base < last && ok; base += 32) {
+        for (Segment sg; ok && walk.next(p, sg);) {
+            const unsigned char* pool = p.c.pool + (size_t)sg.h * L::kBytes;
+            for (int base = sg.first; base < sg.last && ok; base += 32) {
                 // Lane i looks up page base + i.
-                int logical = base + lane, id = -1;
-                if (base + lane < last) {
-                    if (p.page_sel)
-                        logical = __ldg(p.page_sel + ((size_t)at.b * p.c.kv_heads + at.h) * p.nsel + base + lane);
-                    if (logical >= 0 && logical < held) {
-                        id = __ldg(p.c.table + (size_t)at.b * p.c.width + logical);
-                        if (id < 0 || id >= p.c.pages) {
-                            atomicOr(p.c.err, VSA_DEVERR_INDEX);
-                            id = -1;
-                        }
-                    }
-                }
-                const int n = min(32, last - base);
+                int logical = 0, id = -1;
+                if (base + lane < sg.last) look_up(p, sg, base + lane, logical, id);
+                const int n = min(32, sg.last - base);
                 for (int i = 0; i < n; ++i, ++j) {
                     const int slot = j % kSlots;
                     const int page = __shfl_sync(0xffffffffu, id, i), num = __shfl_sync(0xffffffffu, logical, i);
@@ -186,8 +133,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                     __syncwarp();
                 }
             }
-            return ok;
-        });
+        }
         // The copies in flight land before the CTA's shared memory is released.
         if (lane == 0) {
             for (int s = 0; s < kSlots && (uint32_t)s < j; ++s) {
@@ -207,13 +153,13 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
     const int R = p.Sq * p.group;
     uint32_t j = 0;      // pages of the part before the segment
     bool ok = true;
-    walk([&](int first, int last, bool whole) {
+    for (Segment at; walk.next(p, at);) {
         // ------------------------------------------------ the unit's queries
         uint32_t qf[kNT][2 * kWords][2];
         RowState<kNT> rs;
         const int row0 = at.t * p.tile;
-        const int live_rows = min(len.q * p.group, row0 + 8 * kNT);
-        int min_lim = len.kv;
+        const int live_rows = min(at.len.q * p.group, row0 + 8 * kNT);
+        int min_lim = at.len.kv;
         const float c_head = p.scale_log2 * (p.c.kv_scale ? __ldg(p.c.kv_scale + at.h) : 1.f);
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
@@ -248,8 +194,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                 rs.scale[nt][c] = c_head * pow2i(-er);
                 rs.m[nt][c] = -INFINITY;
                 rs.l[nt][c] = 0.f;
-                int lim = len.kv;
-                if (p.causal && r < live_rows) lim = min(lim, len.kv - len.q + r / p.group + 1);
+                int lim = at.len.kv;
+                if (p.causal && r < live_rows) lim = min(lim, at.len.kv - at.len.q + r / p.group + 1);
                 rs.lim[nt][c] = lim;
                 min_lim = min(min_lim, lim);
             }
@@ -265,7 +211,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                 for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
 
         // ------------------------------------------------------------- pages
-        const uint32_t j1 = j + (uint32_t)(last - first);
+        const uint32_t j1 = j + (uint32_t)(at.last - at.first);
         for (uint32_t jj = j + (warp + kWarps - j % kWarps) % kWarps; jj < j1; jj += kWarps) {
             const int slot = jj % kSlots;
             ok = mbar_wait_bounded(smem_u32(&sm.full[slot]), (jj / kSlots) & 1, abort_flag, p.c.err, kCacheWaitNs);
@@ -350,7 +296,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                     mx *= rs.scale[nt][c];
                     alpha[nt][c] = 1.f;
-                    if (mx > rs.m[nt][c] + kTokenRescale || (rs.m[nt][c] == -INFINITY && mx > -INFINITY)) {
+                    if (mx > rs.m[nt][c] + kCacheRescale || (rs.m[nt][c] == -INFINITY && mx > -INFINITY)) {
                         alpha[nt][c] = rs.m[nt][c] == -INFINITY ? 0.f : ex2_approx(rs.m[nt][c] - mx);
                         rs.m[nt][c] = mx;
                         rs.l[nt][c] *= alpha[nt][c];
@@ -383,7 +329,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                         for (int c = 0; c < 4; ++c) o[i][nt][c] *= alpha[nt][c & 1];
             }
             // O^T += V^T P^T
-            const bool ragged = key0 + kPageTokens > len.kv;  // slots past the length hold anything
+            const bool ragged = key0 + kPageTokens > at.len.kv;  // slots past the length hold anything
 #pragma unroll
             for (int m = 0; m < kTiles; ++m) {
                 int tok[4] = {16 * m + v_row0, 16 * m + v_row1, 16 * m + 8 + v_row0, 16 * m + 8 + v_row1};
@@ -398,7 +344,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                         vw[i][0] = *reinterpret_cast<const uint32_t*>(src);
                     }
                     sc[i] = page[L::kVScale + tok[i] * L::kGroups + g * kChan / 16];
-                    if (ragged && key0 + tok[i] >= len.kv) sc[i] = 0u;
+                    if (ragged && key0 + tok[i] >= at.len.kv) sc[i] = 0u;
                 }
                 const uint32_t s01 = e4m3_to_f16(sc[0] | (sc[1] << 8)), s23 = e4m3_to_f16(sc[2] | (sc[3] << 8));
 #pragma unroll
@@ -462,7 +408,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                 sum.z = fmaf(a, x.z, sum.z);
                 sum.w = fmaf(a, x.w, sum.w);
             }
-            if (whole) {
+            if (at.whole) {
                 const int qi = (row0 + r) / p.group, head = at.h * p.group + (row0 + r) - qi * p.group;
                 const bool live = row0 + r < live_rows && l != 0.f;
                 const float inv = live ? v_head / l : 0.f;
@@ -473,7 +419,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                     p.lse[((size_t)at.b * p.heads + head) * p.Sq + qi] =
                         live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
             } else {
-                const size_t slot = 2 * (size_t)blockIdx.x + (first > 0 ? 0 : 1);
+                const size_t slot = 2 * (size_t)blockIdx.x + (at.first > 0 ? 0 : 1);
                 reinterpret_cast<float4*>(p.part_o)[(slot * p.tile + r) * kQuads + c4] = sum;
                 if (c4 == 0) p.part_ml[slot * p.tile + r] = make_float2(m, l);
             }
@@ -481,8 +427,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
         // Every warp goes on or leaves with the others: they read one thread's view of the flag.
         if (threadIdx.x == 0) sm.stop = *abort_flag;
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-        return *reinterpret_cast<volatile int*>(&sm.stop) == 0;
-    });
+        if (*reinterpret_cast<volatile int*>(&sm.stop)) break;
+    }
 }
 
 // Joins the parts of the units that were cut: one warp a row.
@@ -563,9 +509,8 @@ cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-constexpr int kMaxGrid = 160;  // CTAs, one for each SM (152 on GB300)
-
-int tile_rows(int rows) { return rows <= 8 ? 8 : 16; }
+// Rows of a unit: up to 16 rows a kv head go to token_kernel, more to chunk_kernel.
+int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
 
 }  // namespace
 
@@ -601,7 +546,9 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     const int most = page_sel ? nsel : c.width;
     p.whole = most <= kWholePages;
     cudaError_t e;
-    if (D == 64)
+    if (p.tile == 128)
+        e = launch_chunk(p, D, stream);
+    else if (D == 64)
         e = p.tile == 8 ? launch_token<64, 1, 11, 22>(p, stream) : launch_token<64, 2, 7, 21>(p, stream);
     else
         e = p.tile == 8 ? launch_token<128, 1, 7, 21>(p, stream) : launch_token<128, 2, 7, 14>(p, stream);

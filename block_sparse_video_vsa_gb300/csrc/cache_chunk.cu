@@ -1,0 +1,663 @@
+// Attention over the 4-bit paged cache, many query rows a kv head (chunks of
+// tokens): the same function as token_kernel (cache_attn.cu), on tcgen05.
+//
+// Tensor bound for long chunks (4 * D flops for each row and key), so the
+// structure is the fine stage's: 128 query rows a unit, one TMEM lane each,
+// 128 keys (two pages) a step, Q and P as A operands in TMEM, two softmax
+// groups that take the steps of a unit in turn with a maximum, sum and output
+// of their own, joined at the unit's end.  What differs is where K and V come
+// from: a producer warp copies pages whole (4-bit codes and scales, 72 * D
+// contiguous bytes) into a ring, and a warpgroup converts each step's two
+// pages into fp16 K and V tiles (exact, see cache.cuh) in the 128-byte
+// swizzled layout the tensor core reads.  So a page crosses HBM and L2 in 9
+// bits a K and V element pair instead of 32, and is converted once for 128
+// rows: about 1.5 instructions an element, next to some 2.7 of softmax a
+// logit.
+//  * Warp roles (512 threads): warp 0 looks pages up and copies them; warp 1
+//    owns TMEM and issues Q K^T, warp 3 P V; warps 4..7 convert; warps 8..11
+//    and 12..15 are the softmax groups (group 0 the CTA's even steps).
+//  * TMEM (512 columns): S [0,128); P (fp16 pairs) [128,192); Q [192,256);
+//    O_0 [256,384); O_1 [384,512).
+//  * A query row is scaled by a power of two on its way to fp16 (its bf16
+//    values keep all their bits) and the inverse joins its softmax scale.
+//  * Every wait is bounded; one that runs out raises the CTA's abort flag and
+//    the device error word, and each role winds down.
+#include "cache.cuh"
+
+namespace vsa {
+
+namespace {
+
+constexpr int kChunkThreads = 512;
+constexpr int kKStages = 2, kVStages = 3;
+constexpr int kRawPages = 6;  // at least 2 * kKStages + 2: see the parity note at the convert role
+static_assert(kRawPages >= 2 * kKStages + 2, "raw ring");
+constexpr int kMetaSteps = 16;
+// Registers: 4 warpgroups launched with 128 each; the shares add up to 512.
+constexpr int kIssueRegs = 64, kConvertRegs = 80, kSoftRegs = 184;
+static_assert(kIssueRegs + kConvertRegs + 2 * kSoftRegs <= 512, "register split exceeds the launch");
+
+constexpr int kTmemS = 0, kTmemP = 128, kTmemQ = 192, kTmemO0 = 256, kTmemO1 = 384;
+
+template <int kD>
+struct ChunkSmem {
+    static constexpr int kHalf = 128 * 128;          // 128 keys x 64 channels of fp16, swizzled
+    static constexpr int kTile = kHalf * (kD / 64);  // K or V of a step
+    static constexpr int kOffK = 0;
+    static constexpr int kOffV = kOffK + kKStages * kTile;
+    static constexpr int kOffRaw = kOffV + kVStages * kTile;
+    static constexpr int kOffMisc = kOffRaw + kRawPages * PageLayout<kD>::kBytes;
+};
+
+// A softmax warp's walk and its present and next unit: kept in shared memory,
+// the steps need the registers.
+struct SoftWalk {
+    Walk walk;
+    Segment unit[2];
+};
+
+struct __align__(16) ChunkMisc {
+    uint64_t raw_full[kRawPages], raw_empty[kRawPages];
+    uint64_t k_full[kKStages], k_empty[kKStages];
+    uint64_t v_full[kVStages], v_empty[kVStages];
+    uint64_t s_full[2];  // per softmax group: S of its next step is ready
+    uint64_t s_free;     // S has been loaded into registers
+    uint64_t p_full;     // P of the step (and any rescaling of O) is in TMEM
+    uint64_t pv_grp[2];  // per group: P V of its step has completed
+    uint64_t unit_done;  // every P V of the unit has completed
+    uint64_t q_full, q_empty;
+    uint64_t o_free;     // O_0 and O_1 have been read by the unit's epilogue
+    uint64_t drain[2];
+    int2 key0[kMetaSteps];   // first key of a step's pages (kNoKey: none)
+    float xm[2][2][128];     // [unit parity][group][row]: maximum, sum at the unit's end
+    float xl[2][2][128];
+    float scale[2][128];     // [unit parity][row]: logit -> log2 units
+    SoftWalk soft[8];
+    PlanScratch plan;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+constexpr int kNoKey = 0x7FFFFFFF;  // beyond every row's limit
+
+template <int kD>
+constexpr int chunk_smem() {
+    return ChunkSmem<kD>::kOffMisc + (int)sizeof(ChunkMisc) + 1024;  // slack for 1024-byte alignment
+}
+static_assert(chunk_smem<128>() <= 232448, "shared memory of the chunk kernel");
+
+// As idesc_bf16_f32, fp16 inputs.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+    return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
+__device__ __forceinline__ float max3f(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Maximum of x[0..63], as four running chains.
+__device__ __forceinline__ float chunk_max64(const float* x) {
+    float a[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int c = 4; c < 60; c += 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = max3f(a[j], x[c + j], x[c + 4 + j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = fmaxf(a[j], x[60 + j]);
+    return fmaxf(max3f(a[0], a[1], a[2]), a[3]);
+}
+
+// exp2(x * c2 - mb) of 64 logits as 32 fp16 pairs; adds the fp32 values to l.
+__device__ __forceinline__ void chunk_exp64(const float* x, float c2, float mb, uint32_t* pk, float& l) {
+    const float2 c2v = make_float2(c2, c2), nmb = make_float2(-mb, -mb);
+    float2 s01 = make_float2(0.f, 0.f), s23 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < 64; c += 4) {
+        const float2 a01 = __ffma2_rn(make_float2(x[c], x[c + 1]), c2v, nmb);
+        const float2 a23 = __ffma2_rn(make_float2(x[c + 2], x[c + 3]), c2v, nmb);
+        const float p0 = ex2_approx(a01.x), p1 = ex2_approx(a01.y);
+        const float p2 = ex2_approx(a23.x), p3 = ex2_approx(a23.y);
+        s01 = __fadd2_rn(s01, make_float2(p0, p1));
+        s23 = __fadd2_rn(s23, make_float2(p2, p3));
+        pk[c >> 1] = pack_f16x2(p0, p1);
+        pk[(c >> 1) + 1] = pack_f16x2(p2, p3);
+    }
+    l += (s01.x + s01.y) + (s23.x + s23.y);
+}
+
+__device__ __forceinline__ int steps_of(const Segment& s) { return (s.last - s.first + 1) >> 1; }
+
+// Softmax thread of row r: puts its query row of unit s into the TMEM Q
+// columns of its lane as fp16, scaled by a power of two, and returns the row's
+// factor from logits to log2 units.
+template <int kD>
+__device__ __forceinline__ float stage_query(const AttnParams& p, const Segment& s, int r, uint32_t t_lane) {
+    const int row = s.t * 128 + r;
+    const bool real = row < p.Sq * p.group;
+    const int qi = real ? row / p.group : 0;
+    const int head = s.h * p.group + (real ? row - qi * p.group : 0);
+    const uint4* src = p.q + (((size_t)s.b * p.Sq + qi) * p.heads + head) * (kD / 8);
+    float amax = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < kD / 8; ++i) {
+        const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+    }
+    const int e = q_exponent(amax);
+    const float f = pow2i(e);
+#pragma unroll 1
+    for (int c0 = 0; c0 < kD / 2; c0 += 32) {
+        uint32_t w[32];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            const uint4 x = real ? __ldg(src + c0 / 4 + v) : make_uint4(0, 0, 0, 0);
+            w[4 * v] = x.x; w[4 * v + 1] = x.y; w[4 * v + 2] = x.z; w[4 * v + 3] = x.w;
+        }
+#pragma unroll
+        for (int v = 0; v < 32; ++v) w[v] = pack_f16x2(bf16_lo(w[v]) * f, bf16_hi(w[v]) * f);
+        tmem_st32(t_lane + kTmemQ + c0, w);
+    }
+    tmem_wait_st();
+    return p.scale_log2 * (p.c.kv_scale ? __ldg(p.c.kv_scale + s.h) : 1.f) * pow2i(-e);
+}
+
+// One key's codes of K or V (kD / 2 bytes at `codes`) and scales to a row of a
+// fp16 tile.  Lanes of neighbouring rows start at different 16-byte pieces, so
+// that neither the loads nor the swizzled stores meet in a bank.
+template <int kD>
+__device__ __forceinline__ void convert_row(const unsigned char* codes, const unsigned char* scales, int row, bool zero,
+                                            unsigned char* tile) {
+    constexpr int kPieces = kD / 32;  // of 32 channels
+    uint32_t sc[kD / 64];             // scale bytes, two for each piece
+    if constexpr (kD == 128) {
+        const uint2 x = *reinterpret_cast<const uint2*>(scales);
+        sc[0] = zero ? 0u : x.x;
+        sc[1] = zero ? 0u : x.y;
+    } else {
+        sc[0] = zero ? 0u : *reinterpret_cast<const uint32_t*>(scales);
+    }
+    const int r7 = row & 7;
+    unsigned char* base = tile + row * 128;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const int c = (i + (kD == 128 ? row >> 1 : row >> 2)) & (kPieces - 1);
+        const uint4 w = *reinterpret_cast<const uint4*>(codes + c * 16);
+        uint32_t two;
+        if constexpr (kD == 128)
+            two = (c & 2 ? sc[1] : sc[0]) >> (16 * (c & 1));
+        else
+            two = sc[0] >> (16 * c);
+        two = e4m3_to_f16(two);
+        const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        unsigned char* half = base + (c >> 1) * ChunkSmem<kD>::kHalf;
+        const int bit2 = (c & 1) * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
+            e2m1_to_f16(ws[k], h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = mul_f16x2(h[j], k < 2 ? s0 : s1);
+            *reinterpret_cast<uint4*>(half + (((bit2 + k) ^ r7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+}
+
+template <int kD>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
+    using L = PageLayout<kD>;
+    using Sm = ChunkSmem<kD>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    ChunkMisc& ms = *reinterpret_cast<ChunkMisc*>(smem + Sm::kOffMisc);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = &ms.abort_flag;
+    unsigned int* err = p.c.err;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRawPages; ++s) {
+            mbar_init(smem_u32(&ms.raw_full[s]), 1);
+            mbar_init(smem_u32(&ms.raw_empty[s]), 2);  // the two warps that convert the page
+        }
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(smem_u32(&ms.k_full[s]), 4);
+            mbar_init(smem_u32(&ms.k_empty[s]), 1);
+        }
+        for (int s = 0; s < kVStages; ++s) {
+            mbar_init(smem_u32(&ms.v_full[s]), 4);
+            mbar_init(smem_u32(&ms.v_empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&ms.s_full[s]), 1);
+            mbar_init(smem_u32(&ms.pv_grp[s]), 1);
+            mbar_init(smem_u32(&ms.drain[s]), 1);
+        }
+        mbar_init(smem_u32(&ms.s_free), 4);
+        mbar_init(smem_u32(&ms.p_full), 4);
+        mbar_init(smem_u32(&ms.unit_done), 1);
+        mbar_init(smem_u32(&ms.q_full), 4);
+        mbar_init(smem_u32(&ms.q_empty), 1);
+        mbar_init(smem_u32(&ms.o_free), 8);
+        ms.abort_flag = 0;
+        fence_barrier_init();
+    }
+    // The tiles start as zeros: the tensor core multiplies rows that no page
+    // filled (an odd last page, pages passed over) by probabilities of zero.
+    {
+        int4* z = reinterpret_cast<int4*>(smem);
+        for (int e = threadIdx.x; e < Sm::kOffRaw / 16; e += kChunkThreads) z[e] = make_int4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Walk walk;
+    if (!walk.begin(p, ms.plan)) return;  // the whole CTA: TMEM is not allocated yet
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&ms.tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem_base;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == 0) {
+            // ================================================= page producer
+            uint32_t j = 0, g = 0;  // pages and steps so far
+            bool ok = true;
+            for (Segment sg; ok && walk.next(p, sg);) {
+                const unsigned char* pool = p.c.pool + (size_t)sg.h * L::kBytes;
+                for (int base = sg.first; base < sg.last && ok; base += 32) {
+                    int logical = 0, id = -1;
+                    if (base + lane < sg.last) look_up(p, sg, base + lane, logical, id);
+                    const int n = min(32, sg.last - base);
+                    for (int i = 0; i < n; ++i, ++j) {
+                        const int slot = j % kRawPages;
+                        const int page = __shfl_sync(0xffffffffu, id, i);
+                        const int num = __shfl_sync(0xffffffffu, logical, i);
+                        if (j >= (uint32_t)kRawPages) {
+                            ok = mbar_wait_bounded(smem_u32(&ms.raw_empty[slot]), (j / kRawPages + 1) & 1, abort_flag,
+                                                   err, kCacheWaitNs);
+                            if (!ok) break;
+                        }
+                        if (lane == 0) {
+                            // Steps start at even pages of the segment (32 is even).
+                            int* key0 = &ms.key0[g % kMetaSteps].x;
+                            key0[i & 1] = page < 0 ? kNoKey : num * kPageTokens;
+                            if (!(i & 1)) key0[1] = kNoKey;
+                            const uint32_t bar = smem_u32(&ms.raw_full[slot]);
+                            if (page < 0) {
+                                mbar_arrive(bar);
+                            } else {
+                                mbar_arrive_expect_tx(bar, L::kBytes);
+                                bulk_load(sbase + Sm::kOffRaw + slot * L::kBytes,
+                                          pool + (size_t)page * p.c.kv_heads * L::kBytes, L::kBytes, bar);
+                            }
+                        }
+                        if ((i & 1) || base + i + 1 == sg.last) ++g;
+                        __syncwarp();
+                    }
+                }
+            }
+            if (lane == 0) {
+                for (int s = 0; s < kRawPages && (uint32_t)s < j; ++s) {
+                    const uint32_t last = j - 1 - ((j - 1 - s) % kRawPages);
+                    mbar_wait_drain_1(smem_u32(&ms.raw_full[s]), (last / kRawPages) & 1, err, kCacheWaitNs);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ========================================================= Q K^T
+            const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);
+            const uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
+            const uint32_t lo_k = (uint32_t)smem_desc_sw128(sbase + Sm::kOffK, 16, 1024);
+            uint32_t g = 0, ul = 0;
+            bool ok = true;
+            for (Segment sg; ok && walk.next(p, sg); ++ul) {
+                const int nst = steps_of(sg);
+                ok = mbar_wait_bounded(smem_u32(&ms.q_full), ul & 1, abort_flag, err, kCacheWaitNs);
+                for (int t = 0; t < nst && ok; ++t, ++g) {
+                    if (g >= 1)
+                        ok = mbar_wait_bounded(smem_u32(&ms.s_free), (g - 1) & 1, abort_flag, err, kCacheWaitNs);
+                    const int slot = g % kKStages;
+                    if (ok)
+                        ok = mbar_wait_bounded(smem_u32(&ms.k_full[slot]), (g / kKStages) & 1, abort_flag, err,
+                                               kCacheWaitNs);
+                    if (!ok) break;
+                    const uint32_t b0 = lo_k + ((uint32_t)(slot * Sm::kTile) >> 4);
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kD / 16; ++kk)
+                        mma_ts_warp(tmem + kTmemS, tmem + kTmemQ + kk * 8,
+                                    b0 + (((kk >> 2) * Sm::kHalf + (kk & 3) * 32) >> 4), hi, idesc, kk > 0);
+                    mma_commit_warp(smem_u32(&ms.s_full[g & 1]));
+                    mma_commit_warp(smem_u32(&ms.k_empty[slot]));
+                }
+                if (!ok) break;
+                mma_commit_warp(smem_u32(&ms.q_empty));
+            }
+            mma_commit_warp(smem_u32(&ms.drain[0]));
+            if (lane == 0) mbar_wait_drain_1(smem_u32(&ms.drain[0]), 0, err, kCacheWaitNs);
+            __syncwarp();
+        } else if (warp == 3) {
+            // =========================================================== P V
+            const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);
+            const uint32_t idesc = idesc_f16_f32(128, kD, 0, 1);
+            const uint32_t lo_v = (uint32_t)smem_desc_sw128(sbase + Sm::kOffV, Sm::kHalf, 1024);
+            uint32_t g = 0, ul = 0;
+            bool ok = true;
+            for (Segment sg; ok && walk.next(p, sg); ++ul) {
+                const int nst = steps_of(sg);
+                // O_0 and O_1 start over once the last epilogue has read them (a
+                // unit without steps waits too: unit_done stays one phase ahead).
+                if (ul >= 1) ok = mbar_wait_bounded(smem_u32(&ms.o_free), (ul - 1) & 1, abort_flag, err, kCacheWaitNs);
+                for (int t = 0; t < nst && ok; ++t, ++g) {
+                    const int slot = g % kVStages;
+                    ok = mbar_wait_bounded(smem_u32(&ms.p_full), g & 1, abort_flag, err, kCacheWaitNs) &&
+                         mbar_wait_bounded(smem_u32(&ms.v_full[slot]), (g / kVStages) & 1, abort_flag, err,
+                                           kCacheWaitNs);
+                    if (!ok) break;
+                    const uint32_t b0 = lo_v + ((uint32_t)(slot * Sm::kTile) >> 4);
+                    const uint32_t d = tmem + ((g & 1) ? kTmemO1 : kTmemO0);
+                    const uint32_t acc = t >= 2 ? 1u : 0u;  // a group's first step of the unit overwrites its O
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts_warp(d, tmem + kTmemP + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc,
+                                    acc | (kk > 0 ? 1u : 0u));
+                    if (sg.first + 2 * t + 1 < sg.last) {
+#pragma unroll
+                        for (int kk = 4; kk < 8; ++kk)
+                            mma_ts_warp(d, tmem + kTmemP + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc, 1u);
+                    }
+                    mma_commit_warp(smem_u32(&ms.pv_grp[g & 1]));
+                    mma_commit_warp(smem_u32(&ms.v_empty[slot]));
+                }
+                if (!ok) break;
+                mma_commit_warp(smem_u32(&ms.unit_done));
+            }
+            mma_commit_warp(smem_u32(&ms.drain[1]));
+            if (lane == 0) mbar_wait_drain_1(smem_u32(&ms.drain[1]), 0, err, kCacheWaitNs);
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        // ============================================================ convert
+        // Thread = key row of the step's tile; warps 4, 5 the first page, warps
+        // 6, 7 the second.  A raw slot may pass from one pair to the other: a
+        // pair is at most kKStages steps ahead (K tiles wait for Q K^T, which
+        // waits for both pairs), so with kRawPages >= 2 * kKStages + 2 the
+        // slot's former phase has completed before the next is waited for.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+        const int row = (warp - 4) * 32 + lane;
+        const int which = row >> 6, slot_row = row & 63;
+        uint32_t j = 0, g = 0;
+        bool ok = true;
+        for (Segment sg; ok && walk.next(p, sg);) {
+            for (int i = sg.first; i < sg.last && ok; i += 2, ++g) {
+                const int held = min(2, sg.last - i);
+                const bool mine = which < held;
+                const uint32_t page = j + which;
+                const int rs = page % kRawPages;
+                const unsigned char* raw = smem + Sm::kOffRaw + rs * L::kBytes;
+                if (mine)
+                    ok = mbar_wait_bounded(smem_u32(&ms.raw_full[rs]), (page / kRawPages) & 1, abort_flag, err,
+                                           kCacheWaitNs);
+                if (!ok) break;
+                const int2 k0 = ms.key0[g % kMetaSteps];
+                const int key0 = which ? k0.y : k0.x;
+                const bool none = key0 == kNoKey;  // passed over: no key counts, V rows of zeros
+                const int ks = g % kKStages, vs = g % kVStages;
+                if (g >= (uint32_t)kKStages)
+                    ok = mbar_wait_bounded(smem_u32(&ms.k_empty[ks]), (g / kKStages + 1) & 1, abort_flag, err,
+                                           kCacheWaitNs);
+                if (!ok) break;
+                if (mine && !none)
+                    convert_row<kD>(raw + slot_row * L::kRow, raw + L::kKScale + slot_row * L::kGroups, row, false,
+                                    smem + Sm::kOffK + ks * Sm::kTile);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.k_full[ks]));
+                if (g >= (uint32_t)kVStages)
+                    ok = mbar_wait_bounded(smem_u32(&ms.v_empty[vs]), (g / kVStages + 1) & 1, abort_flag, err,
+                                           kCacheWaitNs);
+                if (!ok) break;
+                // Slots past the sequence's end hold anything: their V is zero.
+                if (mine)
+                    convert_row<kD>(raw + L::kV + slot_row * L::kRow, raw + L::kVScale + slot_row * L::kGroups, row,
+                                    none || key0 + slot_row >= sg.len.kv, smem + Sm::kOffV + vs * Sm::kTile);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&ms.v_full[vs]));
+                    if (mine) mbar_arrive(smem_u32(&ms.raw_empty[rs]));
+                }
+                j += held;
+            }
+        }
+    } else {
+        // ============================================================ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        const int G = (warp - 8) >> 2;
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t o_mine = t_lane + (G ? kTmemO1 : kTmemO0);
+        constexpr int dh = kD / 2;  // output columns of this thread: [G * dh, G * dh + dh)
+        const float ninf = -INFINITY;
+        bool ok = true;
+        uint32_t g0 = 0, ul = 0;  // steps before the unit, units
+        SoftWalk& sw = ms.soft[warp - 8];
+        auto advance = [&](int to) -> bool {  // the walk's next unit into sw.unit[to]
+            Walk w = sw.walk;
+            Segment s;
+            const bool has = w.next(p, s);
+            __syncwarp();
+            if (lane == 0) {
+                sw.walk = w;
+                sw.unit[to] = s;
+            }
+            __syncwarp();
+            return has;
+        };
+        if (lane == 0) sw.walk = walk;
+        __syncwarp();
+        bool more = advance(0);
+        if (G == 0 && more) {
+            ms.scale[0][r] = stage_query<kD>(p, sw.unit[0], r, t_lane);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ms.q_full));
+        }
+#pragma unroll 1
+        for (; more; ++ul) {
+            const bool next = advance((ul + 1) & 1);
+            const Segment& sg = sw.unit[ul & 1];
+            const int nst = steps_of(sg);
+            const int row = sg.t * 128 + r;
+            const int live_rows = sg.len.q * p.group;
+            int lim = sg.len.kv;  // first key the row does not see
+            if (p.causal && row < live_rows) lim = max(0, min(lim, sg.len.kv - sg.len.q + row / p.group + 1));
+            // The group that takes the next unit's first step stages its queries.
+            const bool stager = next && ((g0 + nst) & 1) == (uint32_t)G;
+            float c2 = 0.f, m = ninf, l = 0.f;
+            bool first = true;
+#pragma unroll 1
+            for (int t = (int)((g0 + G) & 1); t < nst; t += 2) {
+                const uint32_t gs = g0 + t;
+                if (ok) ok = mbar_wait_bounded(smem_u32(&ms.s_full[G]), (gs >> 1) & 1, abort_flag, err, kCacheWaitNs);
+                tc_fence_after();
+                c2 = ms.scale[ul & 1][r];
+                const int2 k0 = ms.key0[gs % kMetaSteps];
+                // Keys of the two pages that this row sees (none where no page is).
+                const int va = lim - k0.x, vb = lim - k0.y;
+                float x[128];
+#pragma unroll
+                for (int c = 0; c < 128; c += 32)
+                    tmem_ld32(t_lane + kTmemS + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
+                tmem_wait_ld();
+                // S is in registers: its columns may take the next step's.
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.s_free));
+                if (__any_sync(0xffffffffu, va < kPageTokens || vb < kPageTokens)) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) {
+                        x[c] = c < va ? x[c] : ninf;
+                        x[64 + c] = c < vb ? x[64 + c] : ninf;
+                    }
+                }
+                const float mx = fmaxf(chunk_max64(x), chunk_max64(x + 64)) * c2;
+                // Lazy maximum: O and l are rescaled on a jump only.
+                float alpha = 1.f;
+                if (mx > m + kCacheRescale) {
+                    alpha = m == ninf ? 0.f : ex2_approx(m - mx);
+                    m = mx;
+                    l *= alpha;
+                }
+                const float mb = m == ninf ? 0.f : m;
+                uint32_t pk[64];
+                chunk_exp64(x, c2, mb, pk, l);
+                chunk_exp64(x + 64, c2, mb, pk + 32, l);
+                // P V of the step before (the other group's) has read P.
+                if (gs > 0 && ok)
+                    ok = mbar_wait_bounded(smem_u32(&ms.pv_grp[G ^ 1]), ((gs - 1) >> 1) & 1, abort_flag, err,
+                                           kCacheWaitNs);
+                tc_fence_after();
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 16)
+                        tmem_st16(t_lane + kTmemP + c, *reinterpret_cast<uint32_t(*)[16]>(&pk[c]));
+                }
+                if (ok && !first && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // The last P V into this group's O has completed.
+                    ok = mbar_wait_bounded(smem_u32(&ms.pv_grp[G]), ((gs - 2) >> 1) & 1, abort_flag, err,
+                                           kCacheWaitNs);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kD; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_mine + c0, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+                        tmem_st32(o_mine + c0, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.p_full));
+                first = false;
+            }
+            if (stager) {
+                // The unit's Q K^T have completed: Q may be overwritten.
+                if (ok) ok = mbar_wait_bounded(smem_u32(&ms.q_empty), ul & 1, abort_flag, err, kCacheWaitNs);
+                if (ok) {
+                    tc_fence_after();
+                    ms.scale[(ul + 1) & 1][r] = stage_query<kD>(p, sw.unit[(ul + 1) & 1], r, t_lane);
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.q_full));
+            }
+            // ------------------------------------------------ unit epilogue
+            //   m = max(m_0, m_1), a_k = 2^(m_k - m), l = a_0 l_0 + a_1 l_1, O = a_0 O_0 + a_1 O_1
+            ms.xm[ul & 1][G][r] = m;
+            ms.xl[ul & 1][G][r] = l;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+            // The group of the unit's even steps comes first, whatever it is:
+            // the sums do not depend on what the CTA did before the unit.
+            const int ge = (int)(g0 & 1u);
+            const float m_e = ms.xm[ul & 1][ge][r], l_e = ms.xl[ul & 1][ge][r];
+            const float m_o = ms.xm[ul & 1][ge ^ 1][r], l_o = ms.xl[ul & 1][ge ^ 1][r];
+            const float mt = fmaxf(m_e, m_o);
+            float a_e = m_e == ninf ? 0.f : ex2_approx(m_e - mt);
+            float a_o = m_o == ninf ? 0.f : ex2_approx(m_o - mt);
+            const float lt = __fmaf_rn(a_e, l_e, __fmul_rn(a_o, l_o));
+            const uint32_t o_e = ge ? kTmemO1 : kTmemO0, o_o = ge ? kTmemO0 : kTmemO1;
+            const bool has_e = nst > 0, has_o = nst > 1;  // a group without a step holds no O of the unit
+            const bool real = ok && row < p.Sq * p.group;
+            const int qi = real ? row / p.group : 0;
+            const int head = sg.h * p.group + (real ? row - qi * p.group : 0);
+            const bool live = row < live_rows && lt != 0.f;
+            const size_t part = (2 * (size_t)blockIdx.x + (sg.first > 0 ? 0 : 1)) * 128 + r;
+            if (sg.whole) {
+                const float inv =
+                    live ? (p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + sg.h) : 1.f) / lt : 0.f;
+                a_e *= inv;
+                a_o *= inv;
+            }
+            if (ok) ok = mbar_wait_bounded(smem_u32(&ms.unit_done), ul & 1, abort_flag, err, kCacheWaitNs);
+            tc_fence_after();
+            uint4* dst = p.out + (((size_t)sg.b * p.Sq + qi) * p.heads + head) * (kD / 8) + G * (dh / 8);
+            float4* dst_part = reinterpret_cast<float4*>(p.part_o + part * kD + G * dh);
+#pragma unroll 1
+            for (int c0 = 0; c0 < dh; c0 += 32) {
+                uint32_t oa[32], ob[32];
+                tmem_ld32(t_lane + o_e + G * dh + c0, oa);
+                tmem_ld32(t_lane + o_o + G * dh + c0, ob);
+                tmem_wait_ld();
+                float f[32];
+#pragma unroll
+                for (int q = 0; q < 32; ++q)
+                    f[q] = __fmaf_rn(a_e, has_e ? __uint_as_float(oa[q]) : 0.f,
+                                     __fmul_rn(a_o, has_o ? __uint_as_float(ob[q]) : 0.f));
+                if (!real || !ok) continue;
+                if (sg.whole) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) w[q] = live ? pack_bf16x2(f[8 * v + 2 * q], f[8 * v + 2 * q + 1]) : 0u;
+                        __stcs(dst + c0 / 8 + v, make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        dst_part[c0 / 4 + v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
+                }
+            }
+            // O_0 and O_1 have been read: the next unit may start them over.
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ms.o_free));
+            if (real && ok && G == 0) {
+                if (!sg.whole)
+                    p.part_ml[part] = make_float2(mt, lt);
+                else if (p.lse)
+                    p.lse[((size_t)sg.b * p.heads + head) * p.Sq + qi] =
+                        live ? (mt + __log2f(lt)) * 0.69314718055994531f : ninf;
+            }
+            g0 += nst;
+            more = next;
+        }
+    }
+
+    // ------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk(const AttnParams& p, int D, cudaStream_t stream) {
+    auto kernel = D == 64 ? chunk_kernel<64> : chunk_kernel<128>;
+    const int smem = D == 64 ? chunk_smem<64>() : chunk_smem<128>();
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    // The register split draws on the launch's 128 registers a thread; with
+    // fewer, setmaxnreg would wait forever, so such a build is refused.
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != 128) return cudaErrorInvalidKernelImage;
+    kernel<<<p.grid, kChunkThreads, smem, stream>>>(p);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace vsa
