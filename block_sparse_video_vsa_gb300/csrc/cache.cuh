@@ -113,7 +113,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // single long sequences fill the grid alike.  A unit that lies in one part
 // is written by its CTA; the parts of a cut unit go to the workspace (two
 // slots a CTA: slot 0 for a unit begun by an earlier CTA, slot 1 for one it
-// begins itself and does not finish) and are joined by combine_kernel.
+// begins itself and does not finish) and are joined by combine_kernel, a block
+// for each cut: there are fewer cuts than CTAs, whatever the batch.
 struct AttnParams {
     CacheView c;
     const int32_t* q_lens;    // [B], or null: Sq
@@ -123,6 +124,7 @@ struct AttnParams {
     float* lse;               // [B][heads][Sq], or null
     float* part_o;            // [2 * grid][tile][D]
     float2* part_ml;          // [2 * grid][tile]: maximum (log2 units), sum
+    int4* places;             // [grid]: where each CTA's part begins (b, h, t, page); b = -1: no part
     int Sq, heads, group, nsel, causal;
     int tile, tiles;          // rows of a unit; units of a (b, kv head)
     int grid;                 // CTAs of the attention kernel
@@ -154,15 +156,41 @@ __device__ __forceinline__ int tile_pages(const AttnParams& p, const SeqLens& s,
 __device__ __forceinline__ int tile_cost(const AttnParams& p, const SeqLens& s, int t) {
     return max(1, tile_pages(p, s, t));
 }
+// sum of floor((a i + b) / m) for i < n (a, b >= 0, m > 0), by Euclid's steps on (a, m).
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+    long long sum = 0;
+    while (n > 0) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const long long y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
 // Cost of one kv head of a sequence: the sum of its tiles.
 __device__ __forceinline__ long long head_cost(const AttnParams& p, const SeqLens& s) {
-    if (!p.causal || p.tiles == 1) {
-        const int live = min(p.tiles, (s.q * p.group + p.tile - 1) / p.tile);
-        return (long long)live * tile_cost(p, s, 0) + (p.tiles - live);
-    }
-    long long n = 0;
-    for (int t = 0; t < p.tiles; ++t) n += tile_cost(p, s, t);
-    return n;
+    const int live = min(p.tiles, (s.q * p.group + p.tile - 1) / p.tile);
+    if (!p.causal || p.page_sel || live <= 1) return (long long)live * tile_cost(p, s, 0) + (p.tiles - live);
+    // Tile t but the last sees keys up to its last row's place,
+    //   pages = ceil((kv - q + 1 + floor(((t + 1) tile - 1) / group)) / 64)
+    //         = floor((tile t + tile - 1 + group (kv - q + 64)) / (64 group)),
+    // one at least: tiles before `none` have no key at all (a sequence shorter than its queries).
+    const long long lead = (long long)p.group * (s.kv - s.q + kPageTokens) + p.tile - 1, per = 64LL * p.group;
+    long long none = 0;
+    if (lead < per) none = min((long long)live - 1, (per - lead + p.tile - 1) / p.tile);
+    return (p.tiles - live) + tile_cost(p, s, live - 1) + none +
+           floor_sum(live - 1 - none, per, p.tile, lead + none * p.tile);
 }
 
 // A place on the line: page `page` of unit (b, h, t).
@@ -174,15 +202,9 @@ struct Place {
 __device__ __forceinline__ long long part_begin(long long total, int c, int n) {
     return (long long)(((unsigned long long)total * (unsigned)c) / (unsigned)n);
 }
-__device__ __forceinline__ int part_of(long long total, long long pos, int n) {
-    int c = (int)(((unsigned long long)pos * (unsigned)n) / (unsigned long long)total);
-    while (c + 1 < n && part_begin(total, c + 1, n) <= pos) ++c;
-    while (c > 0 && part_begin(total, c, n) > pos) --c;
-    return c;
-}
-
 struct PlanScratch {
     long long warp_sum[32];
+    long long within;  // position within the kv head
     Place place;
 };
 
@@ -218,25 +240,41 @@ __device__ __forceinline__ long long line_scan(const AttnParams& p, PlanScratch&
 __device__ __forceinline__ Place line_place(const AttnParams& p, PlanScratch& sc, int b0, int b1, long long before,
                                             long long pos) {
     for (int b = b0; b < b1; ++b) {
-        const SeqLens s = seq_lens(p, b);
-        const long long hc = head_cost(p, s);
+        const long long hc = head_cost(p, seq_lens(p, b));
         const long long cost = p.c.kv_heads * hc;
         if (pos >= before && pos < before + cost) {
-            Place x;
-            x.b = b;
-            x.h = (int)((pos - before) / hc);
-            long long at = (pos - before) - x.h * hc;
-            x.t = 0;
-            for (int n; at >= (n = tile_cost(p, s, x.t)); ++x.t) at -= n;
-            x.page = (int)at;
-            sc.place = x;
+            sc.place.b = b;
+            sc.place.h = (int)((pos - before) / hc);
+            sc.within = (pos - before) - sc.place.h * hc;
         }
         before += cost;
     }
     __syncthreads();
-    const Place x = sc.place;
+    if (threadIdx.x < 32) {  // the tile: 32 at a time
+        const int lane = threadIdx.x;
+        const SeqLens s = seq_lens(p, sc.place.b);
+        long long at = sc.within;
+        for (int t0 = 0; t0 < p.tiles; t0 += 32) {
+            const int n = t0 + lane < p.tiles ? tile_cost(p, s, t0 + lane) : 0;
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const int all = __shfl_sync(0xffffffffu, incl, 31);
+            if (at < all) {
+                if (at >= incl - n && at < incl) {
+                    sc.place.t = t0 + lane;
+                    sc.place.page = (int)at - (incl - n);
+                }
+                break;
+            }
+            at -= all;
+        }
+    }
     __syncthreads();
-    return x;
+    return sc.place;
 }
 
 // Pages each CTA takes at least (where there are fewer than grid * this, some CTAs take none).
@@ -264,11 +302,15 @@ struct Walk {
         long long before;
         const long long total = line_scan(p, sc, b0, b1, before);
         const int parts = used_parts(p, total);
-        if ((int)blockIdx.x >= parts) return false;
+        if ((int)blockIdx.x >= parts) {
+            if (threadIdx.x == 0) p.places[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            return false;
+        }
         const long long from = part_begin(total, blockIdx.x, parts);
         left = part_begin(total, blockIdx.x + 1, parts) - from;
         at = line_place(p, sc, b0, b1, before, from);
         len = seq_lens(p, at.b, threadIdx.x == 0);
+        if (threadIdx.x == 0) p.places[blockIdx.x] = make_int4(at.b, at.h, at.t, at.page);
         if (p.whole && at.page > 0) {  // units are not cut: the one begun earlier is its owner's
             const int rest = tile_cost(p, len, at.t) - at.page;
             left -= rest;

@@ -431,67 +431,69 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
     }
 }
 
-// Joins the parts of the units that were cut: one warp a row.
+// Joins the parts of the units that were cut.  Block y looks at the cut before
+// CTA y + 1's part; the unit's first cut does the work, one warp a row:
 //   m = max m_i, out = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i
+constexpr int kJoinWarps = 4;
+
 template <int kD>
-__global__ void __launch_bounds__(128) combine_kernel(AttnParams p) {
-    __shared__ PlanScratch sc;
-    __shared__ long long s_before;
-    const int unit = blockIdx.y;  // kv head * tiles + tile
-    const int b = blockIdx.z, h = unit / p.tiles, t = unit % p.tiles;
-    int b0, b1;
-    long long before;
-    const long long total = line_scan(p, sc, b0, b1, before);
-    if (b >= b0 && b < b1) {
-        for (int x = b0; x < b; ++x) before += p.c.kv_heads * head_cost(p, seq_lens(p, x));
-        s_before = before;
-    }
-    __syncthreads();
-    const SeqLens len = seq_lens(p, b);
-    long long pos = s_before + h * head_cost(p, len);
-    for (int x = 0; x < t; ++x) pos += tile_cost(p, len, x);
-    const int parts = used_parts(p, total);
-    const int c0 = part_of(total, pos, parts), c1 = part_of(total, pos + tile_cost(p, len, t) - 1, parts);
-    // What is above reads the lengths alone and overlaps the attention kernel's
-    // end; every block waits for it, so this grid never ends before it.
+__global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (c0 == c1) return;  // the CTA wrote the rows itself
+    const int c0 = blockIdx.y;  // the CTA that begins the unit, if this is its first cut
+    const int4 u = p.places[c0 + 1];
+    if (u.x < 0 || u.w == 0) return;
+    const int4 prev = p.places[c0];
+    if (prev.w > 0 && prev.x == u.x && prev.y == u.y && prev.z == u.z) return;
     const int lane = threadIdx.x & 31;
-    const int R = p.Sq * p.group, live_rows = len.q * p.group;
-    const float v_head = p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + h) : 1.f;
-    for (int r = blockIdx.x * 4 + (threadIdx.x >> 5); r < p.tile; r += gridDim.x * 4) {
-        const int row = t * p.tile + r;
-        if (row >= R) break;
-        // Slot 1 of the unit's first CTA, slot 0 of the others.
-        float m = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[(2 * (size_t)c + (c == c0)) * p.tile + r].x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        constexpr int kPer = kD / 32;
-        float l = 0.f, sum[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) sum[i] = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const size_t at = (2 * (size_t)c + (c == c0)) * p.tile + r;
-            const float2 ml = p.part_ml[at];
-            const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-            l = fmaf(a, ml.y, l);
-            const float* o = p.part_o + at * kD + lane * kPer;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) sum[i] = fmaf(a, o[i], sum[i]);
-        }
-        const int qi = row / p.group, head = h * p.group + row - qi * p.group;
-        const bool live = row < live_rows && l != 0.f;
-        const float inv = live ? v_head / l : 0.f;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)b * p.Sq + qi) * p.heads + head) * (kD / 8)) +
-                        lane * (kPer / 2);
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) dst[i / 2] = live ? pack_bf16x2(sum[i] * inv, sum[i + 1] * inv) : 0u;
-        if (lane == 0 && p.lse)
-            p.lse[((size_t)b * p.heads + head) * p.Sq + qi] =
-                live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    int c1 = c0 + 1;  // the unit's last CTA
+    for (bool in = true; in;) {
+        const int c = c1 + 1 + lane;
+        int4 x = make_int4(-1, 0, 0, 0);
+        if (c < p.grid) x = p.places[c];
+        const unsigned same = __ballot_sync(0xffffffffu, x.x == u.x && x.y == u.y && x.z == u.z && x.w > 0);
+        const int n = __ffs(~same) - 1;  // -1: all 32
+        c1 += n < 0 ? 32 : n;
+        in = n < 0;
     }
+    const SeqLens len = seq_lens(p, u.x);
+    const int R = p.Sq * p.group, live_rows = len.q * p.group;
+    const float v_head = p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + u.y) : 1.f;
+    const int r = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    const int row = u.z * p.tile + r;
+    if (row >= R) return;
+    // Slot 1 of the unit's first CTA, slot 0 of the others.
+    float m = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[(2 * (size_t)c + (c == c0)) * p.tile + r].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    constexpr int kPer = kD / 32;
+    float l = 0.f, sum[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum[i] = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+        const size_t at = (2 * (size_t)c + (c == c0)) * p.tile + r;
+        const float2 ml = p.part_ml[at];
+        const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        l = fmaf(a, ml.y, l);
+        float o[kPer];
+        if constexpr (kPer == 4)
+            *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(p.part_o + at * kD + lane * kPer);
+        else
+            *reinterpret_cast<float2*>(o) = *reinterpret_cast<const float2*>(p.part_o + at * kD + lane * kPer);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sum[i] = fmaf(a, o[i], sum[i]);
+    }
+    const int qi = row / p.group, head = u.y * p.group + row - qi * p.group;
+    const bool live = row < live_rows && l != 0.f;
+    const float inv = live ? v_head / l : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)u.x * p.Sq + qi) * p.heads + head) * (kD / 8)) +
+                    lane * (kPer / 2);
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) dst[i / 2] = live ? pack_bf16x2(sum[i] * inv, sum[i + 1] * inv) : 0u;
+    if (lane == 0 && p.lse)
+        p.lse[((size_t)u.x * p.heads + head) * p.Sq + qi] =
+            live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int kD, int kNT, int kWarps, int kSlots>
@@ -516,7 +518,7 @@ int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
 
 size_t cache_attn_workspace_bytes(int D, int Sq, int group) {
     const int tile = tile_rows(Sq * group);
-    return (size_t)2 * kMaxGrid * tile * ((size_t)D * 4 + 8);
+    return (size_t)kMaxGrid * 16 + (size_t)2 * kMaxGrid * tile * ((size_t)D * 4 + 8);
 }
 
 cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, int heads, const int32_t* q_lens,
@@ -538,7 +540,8 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     p.tile = tile_rows(rows);
     p.tiles = (rows + p.tile - 1) / p.tile;
     p.grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
-    p.part_ml = static_cast<float2*>(workspace);
+    p.places = static_cast<int4*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.places + kMaxGrid);
     p.part_o = reinterpret_cast<float*>(p.part_ml + (size_t)2 * kMaxGrid * p.tile);
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     // Short walks are not worth joining: a unit of up to kWholePages pages stays in one CTA.
@@ -553,11 +556,11 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     else
         e = p.tile == 8 ? launch_token<128, 1, 7, 21>(p, stream) : launch_token<128, 2, 7, 14>(p, stream);
     if (e != cudaSuccess || p.whole) return e;
-    // One warp a row of a unit; launched early (it reads the parts after the
-    // attention kernel has ended).
+    // Launched early (it waits for the attention kernel's end by itself).
+    if (p.grid < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.tile + 3) / 4), (unsigned)(c.kv_heads * p.tiles), (unsigned)c.B);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)((p.tile + kJoinWarps - 1) / kJoinWarps), (unsigned)(p.grid - 1));
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
