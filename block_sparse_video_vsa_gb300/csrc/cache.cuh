@@ -107,8 +107,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // ------------------------------------------------- split of attention work
 // A unit is (sequence b, kv head, tile of `tile` query rows); row r is head
 // kv_head * group + r % group of query r / group.  Units are laid end to end
-// in the order (b, kv head, tile), each as long as the pages it walks (one at
-// least, so that every unit has an owner that writes its rows), and the line
+// in the order (b, kv head, tile), each as long as the pages it walks plus
+// unit_cost (what starting and ending a unit costs, in pages), and the line
 // is cut into equal parts, one for each CTA: batches of ragged lengths and
 // single long sequences fill the grid alike.  A unit that lies in one part
 // is written by its CTA; the parts of a cut unit go to the workspace (two
@@ -124,10 +124,13 @@ struct AttnParams {
     float* lse;               // [B][heads][Sq], or null
     float* part_o;            // [2 * grid][tile][D]
     float2* part_ml;          // [2 * grid][tile]: maximum (log2 units), sum
-    int4* places;             // [grid]: where each CTA's part begins (b, h, t, page); b = -1: no part
+    void* scratch;            // token_kernel: [grid][warps][2] states
+    int4* places;             // [grid]: where each CTA's part begins (b, h, t, page); b = -1: between units
     int Sq, heads, group, nsel, causal;
     int tile, tiles;          // rows of a unit; units of a (b, kv head)
     int grid;                 // CTAs of the attention kernel
+    int unit_cost;
+    int brief;                // up to 32 sequences, one tile each, a line shorter than 2^31
     int whole;                // units are not cut: a unit belongs to the CTA that holds its first page
     float scale_log2;         // sm_scale * log2(e)
 };
@@ -145,6 +148,7 @@ __device__ __forceinline__ SeqLens seq_lens(const AttnParams& p, int b, bool not
 
 // Pages that tile t of a sequence walks (0: nothing to attend).
 __device__ __forceinline__ int tile_pages(const AttnParams& p, const SeqLens& s, int t) {
+    if (p.tiles == 1) return s.q == 0 ? 0 : p.page_sel ? p.nsel : (s.kv + kPageTokens - 1) / kPageTokens;
     const int rows = s.q * p.group;
     const int first = t * p.tile;
     if (first >= rows) return 0;
@@ -154,10 +158,10 @@ __device__ __forceinline__ int tile_pages(const AttnParams& p, const SeqLens& s,
     return lim > 0 ? (lim + kPageTokens - 1) / kPageTokens : 0;
 }
 __device__ __forceinline__ int tile_cost(const AttnParams& p, const SeqLens& s, int t) {
-    return max(1, tile_pages(p, s, t));
+    return tile_pages(p, s, t) + p.unit_cost;
 }
 // sum of floor((a i + b) / m) for i < n (a, b >= 0, m > 0), by Euclid's steps on (a, m).
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+static __device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
     long long sum = 0;
     while (n > 0) {
         if (a >= m) {
@@ -180,101 +184,77 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
 }
 // Cost of one kv head of a sequence: the sum of its tiles.
 __device__ __forceinline__ long long head_cost(const AttnParams& p, const SeqLens& s) {
+    if (p.tiles == 1) return tile_cost(p, s, 0);
     const int live = min(p.tiles, (s.q * p.group + p.tile - 1) / p.tile);
-    if (!p.causal || p.page_sel || live <= 1) return (long long)live * tile_cost(p, s, 0) + (p.tiles - live);
+    const long long ends = (long long)p.tiles * p.unit_cost;
+    if (!p.causal || p.page_sel || live <= 1) return ends + (long long)live * tile_pages(p, s, 0);
     // Tile t but the last sees keys up to its last row's place,
     //   pages = ceil((kv - q + 1 + floor(((t + 1) tile - 1) / group)) / 64)
     //         = floor((tile t + tile - 1 + group (kv - q + 64)) / (64 group)),
-    // one at least: tiles before `none` have no key at all (a sequence shorter than its queries).
+    // from the first tile with a key on (a sequence may be shorter than its queries).
     const long long lead = (long long)p.group * (s.kv - s.q + kPageTokens) + p.tile - 1, per = 64LL * p.group;
     long long none = 0;
     if (lead < per) none = min((long long)live - 1, (per - lead + p.tile - 1) / p.tile);
-    return (p.tiles - live) + tile_cost(p, s, live - 1) + none +
-           floor_sum(live - 1 - none, per, p.tile, lead + none * p.tile);
+    return ends + tile_pages(p, s, live - 1) + floor_sum(live - 1 - none, per, p.tile, lead + none * p.tile);
 }
 
-// A place on the line: page `page` of unit (b, h, t).
+// A place on the line: page `page` of unit (b, h, t) (from the unit's number of pages on: its end).
 struct Place {
     int b, h, t, page;
 };
 
-// Part `c` of `n` of a line of `total`: [part_begin(c), part_begin(c + 1)).
+// Where part `c` of `n` of a line of `total` begins (parts of equal length, the first total % n one longer).
 __device__ __forceinline__ long long part_begin(long long total, int c, int n) {
-    return (long long)(((unsigned long long)total * (unsigned)c) / (unsigned)n);
+    long long q, r;
+    if (total < (1LL << 31)) {
+        q = (int)total / n;
+        r = (int)total - (int)q * n;
+    } else {
+        q = total / n;
+        r = total - q * n;
+    }
+    return q * c + min((long long)c, r);
 }
+
 struct PlanScratch {
     long long warp_sum[32];
-    long long within;  // position within the kv head
-    Place place;
+    long long within;  // where the part begins: sequence, position in it
+    int b;
 };
 
-// Length of the whole line, and this thread's share of its prefix: sequences
-// [b0, b1) start at `before`.  Called by all threads of the block.
-__device__ __forceinline__ long long line_scan(const AttnParams& p, PlanScratch& sc, int& b0, int& b1,
-                                               long long& before) {
-    const int n = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (n + 31) >> 5;
-    const int per = (p.c.B + n - 1) / n;
-    b0 = min((int)threadIdx.x * per, p.c.B);
-    b1 = min(b0 + per, p.c.B);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += p.c.kv_heads * head_cost(p, seq_lens(p, b));
-    long long incl = mine;
+// Tile and page at position `at` of a kv head of sequence s (a whole warp calls it).
+__device__ __forceinline__ void tile_at(const AttnParams& p, const SeqLens& s, long long at, Place& x) {
+    x.t = 0;
+    x.page = (int)at;
+    if (p.tiles == 1) return;
+    const int lane = threadIdx.x & 31;
+    for (int t0 = 0; t0 < p.tiles; t0 += 32) {
+        const int n = t0 + lane < p.tiles ? tile_cost(p, s, t0 + lane) : 0;
+        int incl = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, at < incl);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            x.t = t0 + l;
+            x.page = (int)at - __shfl_sync(0xffffffffu, incl - n, l);
+            return;
+        }
+        at -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 31) sc.warp_sum[warp] = incl;
-    __syncthreads();
-    long long base = 0, total = 0;
-    for (int w = 0; w < warps; ++w) {
-        if (w < warp) base += sc.warp_sum[w];
-        total += sc.warp_sum[w];
-    }
-    before = base + incl - mine;
-    return total;
 }
 
-// The place of position `pos` of the line (pos < total; all threads of the
-// block call it with the same pos).
-__device__ __forceinline__ Place line_place(const AttnParams& p, PlanScratch& sc, int b0, int b1, long long before,
-                                            long long pos) {
-    for (int b = b0; b < b1; ++b) {
-        const long long hc = head_cost(p, seq_lens(p, b));
-        const long long cost = p.c.kv_heads * hc;
-        if (pos >= before && pos < before + cost) {
-            sc.place.b = b;
-            sc.place.h = (int)((pos - before) / hc);
-            sc.within = (pos - before) - sc.place.h * hc;
-        }
-        before += cost;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {  // the tile: 32 at a time
-        const int lane = threadIdx.x;
-        const SeqLens s = seq_lens(p, sc.place.b);
-        long long at = sc.within;
-        for (int t0 = 0; t0 < p.tiles; t0 += 32) {
-            const int n = t0 + lane < p.tiles ? tile_cost(p, s, t0 + lane) : 0;
-            int incl = n;
+__device__ __forceinline__ long long scan_warp(long long x) {  // inclusive
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            const int all = __shfl_sync(0xffffffffu, incl, 31);
-            if (at < all) {
-                if (at >= incl - n && at < incl) {
-                    sc.place.t = t0 + lane;
-                    sc.place.page = (int)at - (incl - n);
-                }
-                break;
-            }
-            at -= all;
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += v;
     }
-    __syncthreads();
-    return sc.place;
+    return x;
 }
 
 // Pages each CTA takes at least (where there are fewer than grid * this, some CTAs take none).
@@ -289,6 +269,7 @@ struct Segment {
     int b, h, t;
     SeqLens len;
     int first, last;  // pages
+    int length;       // on the line
     bool whole;       // the unit from end to end: its rows are written at once
 };
 struct Walk {
@@ -296,11 +277,76 @@ struct Walk {
     SeqLens len;
     long long left;  // of the part
 
+    // The start where calls are small: every warp by itself, lane b sequence b, 32 bits.
+    __device__ bool begin_brief(const AttnParams& p) {
+        const int lane = threadIdx.x & 31;
+        SeqLens s = {0, 0};
+        if (lane < p.c.B) s = seq_lens(p, lane, threadIdx.x < 32 && blockIdx.x == 0);
+        const int hc = tile_cost(p, s, 0);
+        const int mine = lane < p.c.B ? p.c.kv_heads * hc : 0;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const unsigned total = (unsigned)__shfl_sync(0xffffffffu, incl, 31);
+        const unsigned parts = min((total + kMinPart - 1) / kMinPart, (unsigned)p.grid), c = blockIdx.x;
+        if (c >= parts) {
+            if (threadIdx.x == 0) p.places[c] = make_int4(-1, 0, 0, 0);
+            return false;
+        }
+        const unsigned q = total / parts, r = total - q * parts;
+        const int from = (int)(q * c + min(c, r));
+        left = q + (c < r ? 1 : 0);
+        const int l = __ffs(__ballot_sync(0xffffffffu, from < incl)) - 1;
+        at.b = l;
+        len.kv = __shfl_sync(0xffffffffu, s.kv, l);
+        len.q = __shfl_sync(0xffffffffu, s.q, l);
+        const int within = from - __shfl_sync(0xffffffffu, incl - mine, l);
+        const int cost = __shfl_sync(0xffffffffu, hc, l);
+        at.h = (int)((unsigned)within / (unsigned)cost);
+        at.t = 0;
+        at.page = within - at.h * cost;
+        return true;
+    }
     // All threads of the block call it; false: nothing for this CTA.
     __device__ bool begin(const AttnParams& p, PlanScratch& sc) {
-        int b0, b1;
-        long long before;
-        const long long total = line_scan(p, sc, b0, b1, before);
+        if (!(p.brief ? begin_brief(p) : begin_any(p, sc))) return false;
+        // A unit's end is its owner's, and so is the rest of a unit that is not cut.
+        const bool cut = at.page > 0 && at.page < tile_pages(p, len, at.t) && !p.whole;
+        if (threadIdx.x == 0)
+            p.places[blockIdx.x] = cut ? make_int4(at.b, at.h, at.t, at.page) : make_int4(-1, 0, 0, 0);
+        if (at.page > 0 && !cut) {
+            const int rest = tile_cost(p, len, at.t) - at.page;
+            left -= rest;
+            at.page += rest;
+        }
+        return true;
+    }
+    __device__ bool begin_any(const AttnParams& p, PlanScratch& sc) {
+        const int lane = threadIdx.x & 31;
+        // Sequences [b0, b1) are this thread's: up to 32 of them are dealt to
+        // the lanes of every warp, more to the threads of the block.
+        const bool few = p.c.B <= 32;
+        const int who = few ? lane : (int)threadIdx.x, n = few ? 32 : (int)blockDim.x;
+        const int per = few ? 1 : (p.c.B + n - 1) / n;
+        const int b0 = min(who * per, p.c.B), b1 = min(b0 + per, p.c.B);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += p.c.kv_heads * head_cost(p, seq_lens(p, b));
+        long long incl = scan_warp(mine);
+        long long total = __shfl_sync(0xffffffffu, incl, 31);
+        if (!few) {
+            if (lane == 0) sc.warp_sum[threadIdx.x >> 5] = total;
+            __syncthreads();
+            total = 0;
+            long long base = 0;
+            for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+                if (w < (int)threadIdx.x >> 5) base += sc.warp_sum[w];
+                total += sc.warp_sum[w];
+            }
+            incl += base;
+        }
         const int parts = used_parts(p, total);
         if ((int)blockIdx.x >= parts) {
             if (threadIdx.x == 0) p.places[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -308,14 +354,34 @@ struct Walk {
         }
         const long long from = part_begin(total, blockIdx.x, parts);
         left = part_begin(total, blockIdx.x + 1, parts) - from;
-        at = line_place(p, sc, b0, b1, before, from);
-        len = seq_lens(p, at.b, threadIdx.x == 0);
-        if (threadIdx.x == 0) p.places[blockIdx.x] = make_int4(at.b, at.h, at.t, at.page);
-        if (p.whole && at.page > 0) {  // units are not cut: the one begun earlier is its owner's
-            const int rest = tile_cost(p, len, at.t) - at.page;
-            left -= rest;
-            at.page += rest;
+        // The thread whose sequences hold `from` finds the sequence.
+        long long within = from - (incl - mine);
+        int b = -1;
+        if (within >= 0 && within < mine) {
+            for (b = b0;; ++b) {
+                const long long cost = p.c.kv_heads * head_cost(p, seq_lens(p, b));
+                if (within < cost) break;
+                within -= cost;
+            }
         }
+        if (few) {
+            const int l = __ffs(__ballot_sync(0xffffffffu, b >= 0)) - 1;
+            b = __shfl_sync(0xffffffffu, b, l);
+            within = __shfl_sync(0xffffffffu, within, l);
+        } else {
+            if (b >= 0) {
+                sc.b = b;
+                sc.within = within;
+            }
+            __syncthreads();
+            b = sc.b;
+            within = sc.within;
+        }
+        at.b = b;
+        len = seq_lens(p, b, threadIdx.x == 0);
+        const long long hc = head_cost(p, len);
+        at.h = within < (1LL << 31) ? (int)within / (int)min(hc, 0x7FFFFFFFLL) : (int)(within / hc);
+        tile_at(p, len, within - at.h * hc, at);
         return true;
     }
     __device__ bool next(const AttnParams& p, Segment& s) {
@@ -341,7 +407,8 @@ struct Walk {
         s.len = len;
         s.first = min(at.page, n);
         s.last = min(at.page + take, n);
-        s.whole = at.page == 0 && take == cost;
+        s.length = take;
+        s.whole = at.page == 0 && take >= n;
         left -= take;
         at.page += take;
         return true;

@@ -10,9 +10,11 @@
 // kernel is built to keep bulk copies in flight and to spend few instructions
 // on an element.
 //  * A producer warp looks pages up and copies them whole (72 * D contiguous
-//    bytes) into a ring; consumer warp w takes every kWarps-th page of the
-//    CTA's part of the line (see cache.cuh) with a softmax state of its own,
-//    and the warps' states are joined once a unit through shared memory.
+//    bytes) into slots, two or more for each consumer warp; warp w takes every kWarps-th page of the
+//    CTA's part of the line (see cache.cuh) with a softmax state of its own.
+//    At a unit's end each leaves its state in the slot of its last page, and
+//    the warp that comes last joins them and writes the rows, while the others
+//    are at the next unit: no barrier among the warps.
 //  * S^T = K Q^T and O^T = V^T P^T (m16n8k16, fp16 in, fp32 out): the matrix
 //    instructions' 16-row side holds tokens, then channels, so 8 query rows
 //    fill them.  tcgen05 is no help here: its smallest tile has 64 rows and
@@ -50,113 +52,192 @@ __device__ __forceinline__ uint32_t bit_select(uint32_t m, uint32_t a, uint32_t 
     return d;
 }
 
-// Shared memory of the kernel: kSlots pages, then the warps' states.
-template <int kD, int kNT, int kWarps, int kSlots>
-struct TokenSmem {
+// A page is walked in two pieces of 32 tokens.
+constexpr int kPieceTokens = 32;
+
+// The CTA's part of the line is cut again, into equal stretches for its warps
+// (in half pages): a warp meets few units, and a unit's warps are neighbours.
+template <int kWarps>
+struct Tasks {
+    int width;                // of a warp's stretch
+    long long base;           // where the next segment begins
+    int first_warp, count;    // of the segment: its warps
+    __device__ void begin_part(const AttnParams& p, const Walk& walk) {
+        long long n = walk.left;
+        if (p.whole) {  // the last unit may reach over the part's end
+            Walk w = walk;
+            n = 0;
+            for (Segment s; w.next(p, s);) n += s.length;
+        }
+        width = (int)max(1LL, (2 * n + kWarps - 1) / kWarps);
+        base = 0;
+    }
+    // This warp's pieces [first, end) of the segment; false: it has no part in it.
+    __device__ bool take(const Segment& s, int warp, int& first, int& end) {
+        const int n = 2 * (s.last - s.first);
+        first_warp = (int)(base / width);
+        count = (int)((base + max(n, 1) - 1) / width) - first_warp + 1;
+        const long long lo = (long long)warp * width - base;  // the stretch, from the segment's first piece on
+        base += 2LL * s.length;
+        first = 2 * s.first + (int)max(0LL, min((long long)n, lo));
+        end = 2 * s.first + (int)max(0LL, min((long long)n, lo + width));
+        return warp >= first_warp && warp < first_warp + count;
+    }
+};
+
+// A warp's state at a unit's end: O [kRows][kRowPad], then (maximum in log2
+// units, sum) [kRows].
+template <int kD, int kNT>
+struct TokenState {
     static constexpr int kRows = 8 * kNT;
     static constexpr int kRowPad = kD + 4;  // floats: neighbouring rows start in other banks
-    unsigned char page[kSlots][PageLayout<kD>::kBytes];
-    float o[kWarps][kRows][kRowPad];
-    float2 ml[kWarps][kRows];
-    uint64_t full[kSlots];
-    uint64_t empty[kSlots];
-    int logical[kSlots];  // page number within the sequence, or -1: nothing to read
+    float o[kRows][kRowPad];
+    float2 ml[kRows];
+};
+
+// Shared memory of the kernel: kOwn page slots for each warp.
+template <int kD, int kNT, int kWarps, int kOwn>
+struct TokenSmem {
+    unsigned char page[kWarps][kOwn][PageLayout<kD>::kBytes];
+    uint64_t full[kWarps][kOwn];
+    int number[kWarps][kOwn];  // page number within the sequence, or -1: nothing to read
+    // Of the states that a warp leaves: the unit (from 1) and where it is (in
+    // the warp's first slot when the warp has no more pages to come, else in
+    // the workspace: the slots are better used for pages).  [0]: of the unit
+    // that an earlier warp begins, the first of the warp's stretch; [1]: of a
+    // unit that it begins itself.  Those that end in its stretch it joins at
+    // once, so neither is ever needed again before it has been read.
+    unsigned int left[kWarps][2];
+    TokenState<kD, kNT>* state[kWarps][2];
+    unsigned int claimed[kWarps];  // by a unit's first warp: the unit, once a warp joins it
+    // Each warp's walks of the part (of the pages it asks for, and of those it
+    // works on) and the 32 pages it has looked up last.
+    Walk ask_walk[kWarps], walk[kWarps];
+    Tasks<kWarps> ask_tasks[kWarps], tasks[kWarps];
+    Segment ask_unit[kWarps], unit[kWarps];
+    int2 pages[kWarps][32];  // place in the pool (-1: passed over), page number
     PlanScratch plan;
     int abort_flag;
-    int stop;  // abort_flag as one thread read it between the joining barriers
+    static_assert(sizeof(TokenState<kD, kNT>) <= kOwn * PageLayout<kD>::kBytes, "a state fits a warp's slots");
 };
 
-// One unit's rows as the consumer warps hold them.
-template <int kNT>
-struct RowState {
-    float m[kNT][2], l[kNT][2];   // rows nt * 8 + 2 t + e: maximum (log2 units), this lane's share of the sum
-    float scale[kNT][2];          // logit -> log2 units
-    int lim[kNT][2];              // first key the row does not see
-};
-
-template <int kD, int kNT, int kWarps, int kSlots>
-__global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams p) {
+template <int kD, int kNT, int kWarps, int kOwn>
+__global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
     using L = PageLayout<kD>;
-    using Smem = TokenSmem<kD, kNT, kWarps, kSlots>;
-    constexpr int kTiles = kPageTokens / 16;  // token tiles of a page
-    constexpr int kWords = kD / 32;           // code words a lane holds of a K row
-    constexpr int kChan = kD / 8;             // V channels of a lane
+    using Smem = TokenSmem<kD, kNT, kWarps, kOwn>;
+    using State = TokenState<kD, kNT>;
+    constexpr int kTiles = kPieceTokens / 16;  // token tiles of a piece
+    constexpr int kWords = kD / 32;            // code words a lane holds of a K row
+    constexpr int kChan = kD / 8;              // V channels of a lane
     extern __shared__ __align__(128) unsigned char smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(smem_u32(&sm.full[s]), 1);
-            mbar_init(smem_u32(&sm.empty[s]), 1);
-        }
-        sm.abort_flag = 0;
+    if (threadIdx.x < kWarps * kOwn) {
+        mbar_init(smem_u32(&sm.full[0][threadIdx.x]), 1);
+        if (threadIdx.x < kWarps) sm.left[threadIdx.x][0] = sm.left[threadIdx.x][1] = sm.claimed[threadIdx.x] = 0;
+        if (threadIdx.x == 0) sm.abort_flag = 0;
         fence_barrier_init();
     }
     // The joining kernel may be set up meanwhile (its blocks wait for this grid's end).
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    Walk walk;
-    if (!walk.begin(p, sm.plan)) return;
+    {
+        Walk w;
+        if (!w.begin(p, sm.plan)) return;
+        Tasks<kWarps> tk;
+        tk.begin_part(p, w);
+        if (lane == 0) {
+            sm.ask_walk[warp] = sm.walk[warp] = w;
+            sm.ask_tasks[warp] = sm.tasks[warp] = tk;
+        }
+        __syncwarp();
+    }
     volatile int* abort_flag = &sm.abort_flag;
 
-    if (warp == kWarps) {
-        // =========================================================== producer
-        uint32_t j = 0;
-        bool ok = true;
-        for (Segment sg; ok && walk.next(p, sg);) {
-            const unsigned char* pool = p.c.pool + (size_t)sg.h * L::kBytes;
-            for (int base = sg.first; base < sg.last && ok; base += 32) {
-                // Lane i looks up page base + i.
-                int logical = 0, id = -1;
-                if (base + lane < sg.last) look_up(p, sg, base + lane, logical, id);
-                const int n = min(32, sg.last - base);
-                for (int i = 0; i < n; ++i, ++j) {
-                    const int slot = j % kSlots;
-                    const int page = __shfl_sync(0xffffffffu, id, i), num = __shfl_sync(0xffffffffu, logical, i);
-                    if (j >= (uint32_t)kSlots) {
-                        ok = mbar_wait_bounded(smem_u32(&sm.empty[slot]), (j / kSlots + 1) & 1, abort_flag, p.c.err,
-                                               kCacheWaitNs);
-                        if (!ok) break;
-                    }
-                    if (lane == 0) {
-                        sm.logical[slot] = page < 0 ? -1 : num;
-                        const uint32_t bar = smem_u32(&sm.full[slot]);
-                        if (page < 0) {
-                            mbar_arrive(bar);
-                        } else {
-                            mbar_arrive_expect_tx(bar, L::kBytes);
-                            bulk_load(smem_u32(sm.page[slot]), pool + (size_t)page * p.c.kv_heads * L::kBytes,
-                                      L::kBytes, bar);
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
-        }
-        // The copies in flight land before the CTA's shared memory is released.
+    // Asks for the warp's next page, into its next slot (which it has done
+    // with): the pages of its tasks in order, kOwn ahead of its work.
+    uint32_t asked = 0;
+    int ask = 0, ask_end = 0, page0 = 0;  // the task's pages; first of those looked up
+    bool ask_more = true;
+    // The next unit of which this warp has pieces [first, end); counts the units on the way.
+    auto next_task = [&](Walk& walk, Tasks<kWarps>& tasks, Segment& unit, int& first, int& end, unsigned& units) {
+        Walk w = walk;
+        Tasks<kWarps> tk = tasks;
+        Segment s;
+        bool has;
+        do {
+            has = w.next(p, s);
+            ++units;
+        } while (has && !tk.take(s, warp, first, end));
+        __syncwarp();
         if (lane == 0) {
-            for (int s = 0; s < kSlots && (uint32_t)s < j; ++s) {
-                const uint32_t lastj = j - 1 - ((j - 1 - s) % kSlots);
-                mbar_wait_drain_1(smem_u32(&sm.full[s]), (lastj / kSlots) & 1, p.c.err, kCacheWaitNs);
+            walk = w;
+            tasks = tk;
+            unit = s;
+        }
+        __syncwarp();
+        return has;
+    };
+    auto look_up_32 = [&](int first) {  // of the unit asked for
+        const Segment& u = sm.ask_unit[warp];
+        int2 x = make_int2(-1, 0);
+        if (first + lane < u.last) look_up(p, u, first + lane, x.y, x.x);
+        __syncwarp();
+        sm.pages[warp][lane] = x;
+        page0 = first;
+        __syncwarp();
+    };
+    auto ask_next = [&]() {
+        while (ask == ask_end && ask_more) {
+            unsigned units = 0;
+            int first = 0, end = 0;
+            ask_more = next_task(sm.ask_walk[warp], sm.ask_tasks[warp], sm.ask_unit[warp], first, end, units);
+            if (!ask_more) return;
+            ask = first >> 1;
+            ask_end = (end + 1) >> 1;
+            if (ask < ask_end) look_up_32(ask);
+        }
+        if (!ask_more) return;
+        if (ask - page0 == 32) look_up_32(ask);
+        const int2 page = sm.pages[warp][ask - page0];
+        const int slot = asked % kOwn;
+        if (lane == 0) {
+            const uint32_t bar = smem_u32(&sm.full[warp][slot]);
+            sm.number[warp][slot] = page.x < 0 ? -1 : page.y;
+            if (page.x < 0) {
+                mbar_arrive(bar);
+            } else {
+                mbar_arrive_expect_tx(bar, L::kBytes);
+                bulk_load(smem_u32(sm.page[warp][slot]),
+                          p.c.pool + ((size_t)page.x * p.c.kv_heads + sm.ask_unit[warp].h) * L::kBytes, L::kBytes, bar);
             }
         }
-        return;
-    }
+        ++asked;
+        ++ask;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kOwn; ++i) ask_next();
 
-    // ============================================================= consumers
-    // Row r of a page tile sits at token f(r) = r ^ ((r >> 1) & 1) of its 8: of
+    // Row r of a token tile sits at token f(r) = r ^ ((r >> 1) & 1) of its 8: of
     // the four tokens that a V load's lanes t = 0..3 read, two are even and two
     // odd (64-byte rows: 2-way bank conflicts instead of 4-way).
     const int k_row = g ^ ((g >> 1) & 1);
     const int v_row0 = (2 * t) ^ (t & 1), v_row1 = (2 * t + 1) ^ (t & 1);
     const int R = p.Sq * p.group;
-    uint32_t j = 0;      // pages of the part before the segment
+    uint32_t j = 0;            // this warp's pages so far
+    unsigned int unit = 0;     // units so far
     bool ok = true;
-    for (Segment at; walk.next(p, at);) {
+    int piece_begin, piece_end;
+    const Segment& at = sm.unit[warp];
+    while (ok && next_task(sm.walk[warp], sm.tasks[warp], sm.unit[warp], piece_begin, piece_end, unit)) {
+        const int present = sm.tasks[warp].count, first_warp = sm.tasks[warp].first_warp;  // the unit's warps
+        const bool none = at.first == at.last;  // no pages: this warp writes the rows alone
         // ------------------------------------------------ the unit's queries
         uint32_t qf[kNT][2 * kWords][2];
-        RowState<kNT> rs;
+        float rs_m[kNT][2], rs_l[kNT][2];  // rows nt * 8 + 2 t + c: maximum (log2 units), this lane's share of the sum
+        float rs_scale[kNT][2];            // logit -> log2 units
+        int rs_lim[kNT][2];                // first key the row does not see
         const int row0 = at.t * p.tile;
         const int live_rows = min(at.len.q * p.group, row0 + 8 * kNT);
         int min_lim = at.len.kv;
@@ -191,12 +272,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
             for (int c = 0; c < 2; ++c) {
                 const int er = __shfl_sync(0xffffffffu, e, (2 * t + c) * 4);
                 const int r = row0 + nt * 8 + 2 * t + c;
-                rs.scale[nt][c] = c_head * pow2i(-er);
-                rs.m[nt][c] = -INFINITY;
-                rs.l[nt][c] = 0.f;
+                rs_scale[nt][c] = c_head * pow2i(-er);
+                rs_m[nt][c] = -INFINITY;
+                rs_l[nt][c] = 0.f;
                 int lim = at.len.kv;
                 if (p.causal && r < live_rows) lim = min(lim, at.len.kv - at.len.q + r / p.group + 1);
-                rs.lim[nt][c] = lim;
+                rs_lim[nt][c] = lim;
                 min_lim = min(min_lim, lim);
             }
         }
@@ -210,54 +291,63 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
 
-        // ------------------------------------------------------------- pages
-        const uint32_t j1 = j + (uint32_t)(at.last - at.first);
-        for (uint32_t jj = j + (warp + kWarps - j % kWarps) % kWarps; jj < j1; jj += kWarps) {
-            const int slot = jj % kSlots;
-            ok = mbar_wait_bounded(smem_u32(&sm.full[slot]), (jj / kSlots) & 1, abort_flag, p.c.err, kCacheWaitNs);
-            if (!ok) break;
-            const int logical = sm.logical[slot];
-            if (logical < 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
+        // ------------------------------------------------------------ pieces
+#pragma unroll 1
+        for (int pc = piece_begin; pc < piece_end; ++pc) {
+            const int slot = j % kOwn;
+            const int half = pc & 1;
+            if (!half || pc == piece_begin) {
+                ok = mbar_wait_bounded(smem_u32(&sm.full[warp][slot]), (j / kOwn) & 1, abort_flag, p.c.err,
+                                       kCacheWaitNs);
+                if (!ok) break;
+            }
+            const bool page_end = half || pc + 1 == piece_end;  // done with the page after this piece
+            const int number = sm.number[warp][slot];
+            const int key0 = number * kPageTokens + half * kPieceTokens;
+            if (number < 0 || key0 >= at.len.kv) {
+                if (page_end) {
+                    ++j;
+                    __syncwarp();
+                    ask_next();
+                }
                 continue;
             }
-            const unsigned char* page = sm.page[slot];
-            const int key0 = logical * kPageTokens;
-            // S^T
+            const unsigned char* page = sm.page[warp][slot];
+            const int tok0 = half * kPieceTokens;
+            // S^T: the two token tiles side by side (their sums do not wait for one another)
             float s[kTiles][kNT][4];
+            uint32_t kw[kTiles][2][kWords], ks[kTiles][2][kWords / 2];
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m) {
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[m][nt][c] = 0.f;
-                uint32_t kw[2][kWords], ks[2][kWords / 2];
+            for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int tok = 16 * m + 8 * half + k_row;
+                    const int tok = tok0 + 16 * m + 8 * half + k_row;
                     const unsigned char* src = page + tok * L::kRow + t * (kWords * 4);
                     const unsigned char* sc = page + L::kKScale + tok * L::kGroups + t * (kWords / 2);
                     if constexpr (kWords == 4) {
                         const uint4 x = *reinterpret_cast<const uint4*>(src);
-                        kw[half][0] = x.x; kw[half][1] = x.y; kw[half][2] = x.z; kw[half][3] = x.w;
+                        kw[m][half][0] = x.x; kw[m][half][1] = x.y; kw[m][half][2] = x.z; kw[m][half][3] = x.w;
                         const uint32_t two = e4m3_to_f16(*reinterpret_cast<const uint16_t*>(sc));
-                        ks[half][0] = __byte_perm(two, 0, 0x1010);
-                        ks[half][1] = __byte_perm(two, 0, 0x3232);
+                        ks[m][half][0] = __byte_perm(two, 0, 0x1010);
+                        ks[m][half][1] = __byte_perm(two, 0, 0x3232);
                     } else {
                         const uint2 x = *reinterpret_cast<const uint2*>(src);
-                        kw[half][0] = x.x; kw[half][1] = x.y;
-                        ks[half][0] = e4m3_to_f16((uint32_t)*sc * 0x101u);
+                        kw[m][half][0] = x.x; kw[m][half][1] = x.y;
+                        ks[m][half][0] = e4m3_to_f16((uint32_t)*sc * 0x101u);
                     }
+#pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt) s[m][nt][2 * half] = s[m][nt][2 * half + 1] = 0.f;
                 }
 #pragma unroll
-                for (int w = 0; w < kWords; ++w) {
+            for (int w = 0; w < kWords; ++w)
+#pragma unroll
+                for (int m = 0; m < kTiles; ++m) {
                     uint32_t a[2][4];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        e2m1_to_f16(kw[half][w], a[half]);
+                        e2m1_to_f16(kw[m][half][w], a[half]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) a[half][i] = mul_f16x2(a[half][i], ks[half][w / 2]);
+                        for (int i = 0; i < 4; ++i) a[half][i] = mul_f16x2(a[half][i], ks[m][half][w / 2]);
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
@@ -266,10 +356,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                             mma_f16(s[m][nt], a[0][2 * i], a[1][2 * i], a[0][2 * i + 1], a[1][2 * i + 1],
                                     qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
                 }
-            }
             // Keys past a row's limit (and scores of what lies there) do not count.
-            const bool masked = key0 + kPageTokens > min_lim;
-            if (masked) {
+            if (key0 + kPieceTokens > min_lim) {
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m)
 #pragma unroll
@@ -277,7 +365,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const int key = key0 + 16 * m + 8 * (c >> 1) + k_row;
-                            if (key >= rs.lim[nt][c & 1]) s[m][nt][c] = -INFINITY;
+                            if (key >= rs_lim[nt][c & 1]) s[m][nt][c] = -INFINITY;
                         }
             }
             // Online softmax; P^T as fp16 fragments.
@@ -286,33 +374,38 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
             bool rescale = false;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
+                float mx[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+                    mx[c] = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
 #pragma unroll
-                    for (int m = 1; m < kTiles; ++m) mx = fmaxf(mx, fmaxf(s[m][nt][c], s[m][nt][c + 2]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    mx *= rs.scale[nt][c];
+                    for (int m = 1; m < kTiles; ++m) mx[c] = fmaxf(mx[c], fmaxf(s[m][nt][c], s[m][nt][c + 2]));
+                }
+#pragma unroll
+                for (int x = 4; x < 32; x *= 2)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], x));
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float top = mx[c] * rs_scale[nt][c];
                     alpha[nt][c] = 1.f;
-                    if (mx > rs.m[nt][c] + kCacheRescale || (rs.m[nt][c] == -INFINITY && mx > -INFINITY)) {
-                        alpha[nt][c] = rs.m[nt][c] == -INFINITY ? 0.f : ex2_approx(rs.m[nt][c] - mx);
-                        rs.m[nt][c] = mx;
-                        rs.l[nt][c] *= alpha[nt][c];
+                    if (top > rs_m[nt][c] + kCacheRescale) {
+                        alpha[nt][c] = rs_m[nt][c] == -INFINITY ? 0.f : ex2_approx(rs_m[nt][c] - top);
+                        rs_m[nt][c] = top;
+                        rs_l[nt][c] *= alpha[nt][c];
                         rescale = true;
                     }
-                    const float mb = rs.m[nt][c] == -INFINITY ? 0.f : rs.m[nt][c];
+                    const float mb = rs_m[nt][c] == -INFINITY ? 0.f : rs_m[nt][c];
                     float sum = 0.f;
 #pragma unroll
                     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             float& x = s[m][nt][c + 2 * half];
-                            x = ex2_approx(fmaf(x, rs.scale[nt][c], -mb));
+                            x = ex2_approx(fmaf(x, rs_scale[nt][c], -mb));
                             sum += x;
                         }
-                    rs.l[nt][c] += sum;
+                    rs_l[nt][c] += sum;
                 }
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m) {
@@ -329,22 +422,26 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                         for (int c = 0; c < 4; ++c) o[i][nt][c] *= alpha[nt][c & 1];
             }
             // O^T += V^T P^T
-            const bool ragged = key0 + kPageTokens > at.len.kv;  // slots past the length hold anything
+            const bool ragged = key0 + kPieceTokens > at.len.kv;  // slots past the length hold anything
 #pragma unroll
             for (int m = 0; m < kTiles; ++m) {
-                int tok[4] = {16 * m + v_row0, 16 * m + v_row1, 16 * m + 8 + v_row0, 16 * m + 8 + v_row1};
+                const int tok[4] = {16 * m + v_row0, 16 * m + v_row1, 16 * m + 8 + v_row0, 16 * m + 8 + v_row1};
                 uint32_t vw[4][kChan / 8], sc[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const unsigned char* src = page + L::kV + tok[i] * L::kRow + g * (kChan / 2);
+                    const unsigned char* src = page + L::kV + (tok0 + tok[i]) * L::kRow + g * (kChan / 2);
                     if constexpr (kChan == 16) {
                         const uint2 x = *reinterpret_cast<const uint2*>(src);
                         vw[i][0] = x.x; vw[i][1] = x.y;
                     } else {
                         vw[i][0] = *reinterpret_cast<const uint32_t*>(src);
                     }
-                    sc[i] = page[L::kVScale + tok[i] * L::kGroups + g * kChan / 16];
-                    if (ragged && key0 + tok[i] >= at.len.kv) sc[i] = 0u;
+                    sc[i] = page[L::kVScale + (tok0 + tok[i]) * L::kGroups + g * kChan / 16];
+                }
+                if (ragged) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (key0 + tok[i] >= at.len.kv) sc[i] = 0u;
                 }
                 const uint32_t s01 = e4m3_to_f16(sc[0] | (sc[1] << 8)), s23 = e4m3_to_f16(sc[2] | (sc[3] << 8));
 #pragma unroll
@@ -364,152 +461,273 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) token_kernel(AttnParams 
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
+            if (page_end) {
+                ++j;
+                __syncwarp();
+                ask_next();
+            }
         }
-        j = j1;
+        if (!ok) break;
 
-        // ------------------------------------- join the warps, write the rows
+        // ----------------------------------------------- leave the state
+        const int R_tile = min(State::kRows, R - row0);
+        if (!none) {
+            const int begun = first_warp == warp;
+            State* st = j == asked
+                            ? reinterpret_cast<State*>(sm.page[warp][0])
+                            : static_cast<State*>(p.scratch) + ((size_t)blockIdx.x * kWarps + warp) * 2 + begun;
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+            for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float l = rs.l[nt][c];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                const int r = nt * 8 + 2 * t + c;
-                if (g == 0) sm.ml[warp][r] = make_float2(rs.m[nt][c], l);
-                float4* dst = reinterpret_cast<float4*>(&sm.o[warp][r][g * kChan]);
+                for (int c = 0; c < 2; ++c) {
+                    float l = rs_l[nt][c];
+                    l += __shfl_xor_sync(0xffffffffu, l, 4);
+                    l += __shfl_xor_sync(0xffffffffu, l, 8);
+                    l += __shfl_xor_sync(0xffffffffu, l, 16);
+                    const int r = nt * 8 + 2 * t + c;
+                    if (g == 0) st->ml[r] = make_float2(rs_m[nt][c], l);
+                    float4* dst = reinterpret_cast<float4*>(&st->o[r][g * kChan]);
 #pragma unroll
-                for (int i = 0; i < kChan / 4; ++i)
-                    dst[i] = make_float4(o[2 * i][nt][c], o[2 * i][nt][c + 2], o[2 * i + 1][nt][c],
-                                         o[2 * i + 1][nt][c + 2]);
+                    for (int i = 0; i < kChan / 4; ++i)
+                        dst[i] = make_float4(o[2 * i][nt][c], o[2 * i][nt][c + 2], o[2 * i + 1][nt][c],
+                                             o[2 * i + 1][nt][c + 2]);
+                }
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) {
+                sm.state[warp][begun] = st;
+                __threadfence_block();
+                *reinterpret_cast<volatile unsigned int*>(&sm.left[warp][begun]) = unit;
             }
-        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-        constexpr int kRows = Smem::kRows, kQuads = kD / 4;
+            __threadfence_block();
+            __syncwarp();
+            // All states are there for the last warp at least; one joins them.
+            bool there = true;
+            if (lane < present)
+                there = *reinterpret_cast<volatile unsigned int*>(&sm.left[first_warp + lane][lane == 0]) == unit;
+            if (!__all_sync(0xffffffffu, there)) continue;
+            unsigned int taken = 0;
+            if (lane == 0) taken = atomicMax(&sm.claimed[first_warp], unit);  // units count up
+            if (__shfl_sync(0xffffffffu, taken, 0) >= unit) continue;
+            __threadfence_block();
+        }
+        // ------------------------- the last warp: join the states, write the rows
+        // (in the order of their pieces: the sums do not depend on which came last).
+        constexpr int kPer = kD / 32;  // channels of a lane
         const float v_head = p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + at.h) : 1.f;
-        for (int e = threadIdx.x; e < kRows * kQuads; e += kWarps * 32) {
-            const int r = e / kQuads, c4 = e % kQuads;
-            if (row0 + r >= R) continue;
-            float m = -INFINITY;
+        const int n = none ? 0 : present;
+        // (Short loops: code that runs once a unit costs more to fetch than to run.)
+        constexpr int kRows = State::kRows, kLanes = 32 / kRows;  // lanes of a row
+        constexpr int kTurns = (kWarps + kLanes - 1) / kLanes;
+        const int r = lane / kLanes, q = lane % kLanes;  // states q, q + kLanes, ... of row r
+        float a[kTurns], row_l[kTurns], m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.ml[w][r].x);
-            float l = 0.f;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < kTurns; ++k) {
+            const int i = k * kLanes + q;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (i < n) ml = sm.state[first_warp + i][i == 0]->ml[r];
+            a[k] = ml.x;
+            row_l[k] = ml.y;
+            m = fmaxf(m, ml.x);
+        }
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 ml = sm.ml[w][r];
-                const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-                const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][4 * c4]);
-                l = fmaf(a, ml.y, l);
-                sum.x = fmaf(a, x.x, sum.x);
-                sum.y = fmaf(a, x.y, sum.y);
-                sum.z = fmaf(a, x.z, sum.z);
-                sum.w = fmaf(a, x.w, sum.w);
+        for (int x = 1; x < kLanes; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {
+            a[k] = a[k] == -INFINITY ? 0.f : ex2_approx(a[k] - m);
+            l = fmaf(a[k], row_l[k], l);
+        }
+#pragma unroll
+        for (int x = 1; x < kLanes; x *= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
+        // Where row r goes, and its factor.
+        const int qi = (row0 + r) / p.group, head = at.h * p.group + (row0 + r) - qi * p.group;
+        const bool live = row0 + r < live_rows && l != 0.f, whole = at.whole;
+        long long dst = ((long long)at.b * p.Sq + qi) * p.heads + head;
+        float factor = live ? v_head / l : 0.f;
+        if (!whole) {
+            dst = (2 * (long long)blockIdx.x + (at.first > 0 ? 0 : 1)) * p.tile + r;
+            factor = 1.f;
+        }
+        if (q == 0 && r < R_tile) {
+            if (!whole)
+                p.part_ml[dst] = make_float2(m, l);
+            else if (p.lse)
+                p.lse[((size_t)at.b * p.heads + head) * p.Sq + qi] =
+                    live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+        float sum[kRows][kPer];
+#pragma unroll
+        for (int x = 0; x < kRows; ++x)
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) sum[x][c] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k)
+#pragma unroll 1
+            for (int i = k * kLanes; i < min(n, (k + 1) * kLanes); ++i) {
+                const State* si = sm.state[first_warp + i][i == 0];
+                float y[kRows][kPer];
+#pragma unroll
+                for (int x = 0; x < kRows; ++x) {
+                    if constexpr (kPer == 4)
+                        *reinterpret_cast<float4*>(y[x]) = *reinterpret_cast<const float4*>(&si->o[x][lane * kPer]);
+                    else
+                        *reinterpret_cast<float2*>(y[x]) = *reinterpret_cast<const float2*>(&si->o[x][lane * kPer]);
+                }
+#pragma unroll
+                for (int x = 0; x < kRows; ++x) {
+                    const float ai = __shfl_sync(0xffffffffu, a[k], x * kLanes + i - k * kLanes);
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c) sum[x][c] = fmaf(ai, y[x][c], sum[x][c]);
+                }
             }
-            if (at.whole) {
-                const int qi = (row0 + r) / p.group, head = at.h * p.group + (row0 + r) - qi * p.group;
-                const bool live = row0 + r < live_rows && l != 0.f;
-                const float inv = live ? v_head / l : 0.f;
-                uint2* dst = reinterpret_cast<uint2*>(p.out + (((size_t)at.b * p.Sq + qi) * p.heads + head) * (kD / 8));
-                dst[c4] = live ? make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv))
-                               : make_uint2(0u, 0u);
-                if (c4 == 0 && p.lse)
-                    p.lse[((size_t)at.b * p.heads + head) * p.Sq + qi] =
-                        live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kRows; ++x) {
+            if (x >= R_tile) break;
+            const float f = __shfl_sync(0xffffffffu, factor, x * kLanes);
+            const bool any = __shfl_sync(0xffffffffu, (int)live, x * kLanes) != 0;
+            const long long to = __shfl_sync(0xffffffffu, dst, x * kLanes);
+            if (whole) {
+                uint32_t w[kPer / 2];
+#pragma unroll
+                for (int c = 0; c < kPer; c += 2) w[c / 2] = any ? pack_bf16x2(sum[x][c] * f, sum[x][c + 1] * f) : 0u;
+                uint32_t* out = reinterpret_cast<uint32_t*>(p.out + to * (kD / 8)) + lane * (kPer / 2);
+                if constexpr (kPer == 4)
+                    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+                else
+                    *out = w[0];
             } else {
-                const size_t slot = 2 * (size_t)blockIdx.x + (at.first > 0 ? 0 : 1);
-                reinterpret_cast<float4*>(p.part_o)[(slot * p.tile + r) * kQuads + c4] = sum;
-                if (c4 == 0) p.part_ml[slot * p.tile + r] = make_float2(m, l);
+                float* out = p.part_o + to * kD + lane * kPer;
+                if constexpr (kPer == 4)
+                    *reinterpret_cast<float4*>(out) = make_float4(sum[x][0], sum[x][1], sum[x][2], sum[x][3]);
+                else
+                    *reinterpret_cast<float2*>(out) = make_float2(sum[x][0], sum[x][1]);
             }
         }
-        // Every warp goes on or leaves with the others: they read one thread's view of the flag.
-        if (threadIdx.x == 0) sm.stop = *abort_flag;
-        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-        if (*reinterpret_cast<volatile int*>(&sm.stop)) break;
     }
+    // Copies still in flight (a walk that an abort cut short) land before the
+    // CTA's shared memory is released.
+    if (lane == 0)
+        for (; j < asked; ++j)
+            mbar_wait_drain_1(smem_u32(&sm.full[warp][j % kOwn]), (j / kOwn) & 1, p.c.err, kCacheWaitNs);
 }
 
-// Joins the parts of the units that were cut.  Block y looks at the cut before
-// CTA y + 1's part; the unit's first cut does the work, one warp a row:
+// Joins the parts of the units that were cut.  Block (r, y) looks at the cut
+// before CTA y + 1's part; the unit's first cut does the work, a block a row:
 //   m = max m_i, out = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i
+// The warps take the parts in turn and ask for eight at a time: a unit cut
+// into many parts is a matter of latency.
 constexpr int kJoinWarps = 4;
 
 template <int kD>
 __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) {
+    __shared__ float s_o[kJoinWarps][kD];
+    __shared__ float2 s_ml[kJoinWarps];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = blockIdx.y;  // the CTA that begins the unit, if this is its first cut
-    const int4 u = p.places[c0 + 1];
-    if (u.x < 0 || u.w == 0) return;
-    const int4 prev = p.places[c0];
-    if (prev.w > 0 && prev.x == u.x && prev.y == u.y && prev.z == u.z) return;
-    const int lane = threadIdx.x & 31;
-    int c1 = c0 + 1;  // the unit's last CTA
-    for (bool in = true; in;) {
-        const int c = c1 + 1 + lane;
-        int4 x = make_int4(-1, 0, 0, 0);
-        if (c < p.grid) x = p.places[c];
-        const unsigned same = __ballot_sync(0xffffffffu, x.x == u.x && x.y == u.y && x.z == u.z && x.w > 0);
-        const int n = __ffs(~same) - 1;  // -1: all 32
-        c1 += n < 0 ? 32 : n;
-        in = n < 0;
+    // Lane i: where CTA c0 + i's part begins (b < 0: not inside a unit).
+    int4 x = make_int4(-1, 0, 0, 0);
+    if (c0 + lane < p.grid) x = p.places[c0 + lane];
+    const int4 u = make_int4(__shfl_sync(0xffffffffu, x.x, 1), __shfl_sync(0xffffffffu, x.y, 1),
+                             __shfl_sync(0xffffffffu, x.z, 1), 0);
+    unsigned same = __ballot_sync(0xffffffffu, x.x == u.x && x.y == u.y && x.z == u.z);
+    if (u.x < 0 || (same & 1u)) return;
+    int c1 = c0 + __ffs(~(same >> 1)) - 1;  // the unit's last CTA
+    for (int c = c0 + 32; same >> 31 && c < p.grid; c += 32) {  // (more than 31 parts)
+        x = make_int4(-1, 0, 0, 0);
+        if (c + lane < p.grid) x = p.places[c + lane];
+        const unsigned more = __ballot_sync(0xffffffffu, x.x == u.x && x.y == u.y && x.z == u.z);
+        c1 = c - 1 + (more == 0xffffffffu ? 32 : __ffs(~more) - 1);
+        if (more != 0xffffffffu) break;
     }
-    const SeqLens len = seq_lens(p, u.x);
-    const int R = p.Sq * p.group, live_rows = len.q * p.group;
-    const float v_head = p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + u.y) : 1.f;
-    const int r = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    const int row = u.z * p.tile + r;
-    if (row >= R) return;
+    const int r = blockIdx.x, row = u.z * p.tile + r;
+    if (row >= p.Sq * p.group) return;
     // Slot 1 of the unit's first CTA, slot 0 of the others.
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[(2 * (size_t)c + (c == c0)) * p.tile + r].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    constexpr int kPer = kD / 32;
-    float l = 0.f, sum[kPer];
+    constexpr int kPer = kD / 32, kAhead = 8;
+    float m = -INFINITY, l = 0.f, sum[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) sum[i] = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const size_t at = (2 * (size_t)c + (c == c0)) * p.tile + r;
-        const float2 ml = p.part_ml[at];
-        const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-        l = fmaf(a, ml.y, l);
-        float o[kPer];
-        if constexpr (kPer == 4)
-            *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(p.part_o + at * kD + lane * kPer);
-        else
-            *reinterpret_cast<float2*>(o) = *reinterpret_cast<const float2*>(p.part_o + at * kD + lane * kPer);
+#pragma unroll 1
+    for (int c = c0 + warp; c <= c1; c += kJoinWarps * kAhead) {
+        float2 ml[kAhead];
+        float o[kAhead][kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) sum[i] = fmaf(a, o[i], sum[i]);
+        for (int k = 0; k < kAhead; ++k) {
+            const int ck = c + k * kJoinWarps;
+            const size_t at = (2 * (size_t)ck + (ck == c0)) * p.tile + r;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (ck > c1) continue;
+            ml[k] = p.part_ml[at];
+            if constexpr (kPer == 4)
+                *reinterpret_cast<float4*>(o[k]) = *reinterpret_cast<const float4*>(p.part_o + at * kD + lane * kPer);
+            else
+                *reinterpret_cast<float2*>(o[k]) = *reinterpret_cast<const float2*>(p.part_o + at * kD + lane * kPer);
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, ml[k].x);
+        if (top == -INFINITY) continue;
+        const float keep = ex2_approx(m - top);
+        m = top;
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sum[i] *= keep;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (ml[k].x == -INFINITY) continue;
+            const float a = ex2_approx(ml[k].x - m);
+            l = fmaf(a, ml[k].y, l);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) sum[i] = fmaf(a, o[k][i], sum[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = sum[i];
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (threadIdx.x >= kD / 2) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_ml[w].x);
+    l = 0.f;
+    float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float2 ml = s_ml[w];
+        const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        const float2 z = *reinterpret_cast<const float2*>(&s_o[w][2 * threadIdx.x]);
+        l = fmaf(a, ml.y, l);
+        y.x = fmaf(a, z.x, y.x);
+        y.y = fmaf(a, z.y, y.y);
     }
     const int qi = row / p.group, head = u.y * p.group + row - qi * p.group;
-    const bool live = row < live_rows && l != 0.f;
-    const float inv = live ? v_head / l : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)u.x * p.Sq + qi) * p.heads + head) * (kD / 8)) +
-                    lane * (kPer / 2);
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) dst[i / 2] = live ? pack_bf16x2(sum[i] * inv, sum[i + 1] * inv) : 0u;
-    if (lane == 0 && p.lse)
+    const bool live = row < seq_lens(p, u.x).q * p.group && l != 0.f;
+    const float inv = live ? (p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + u.y) : 1.f) / l : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)u.x * p.Sq + qi) * p.heads + head) * (kD / 8));
+    dst[threadIdx.x] = live ? pack_bf16x2(y.x * inv, y.y * inv) : 0u;
+    if (threadIdx.x == 0 && p.lse)
         p.lse[((size_t)u.x * p.heads + head) * p.Sq + qi] =
             live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-template <int kD, int kNT, int kWarps, int kSlots>
+constexpr int kTokenWarps = 12;  // at most: states in the workspace
+
+template <int kD, int kNT, int kWarps, int kOwn>
 cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
-    constexpr int smem = (int)sizeof(TokenSmem<kD, kNT, kWarps, kSlots>);
+    constexpr int smem = (int)sizeof(TokenSmem<kD, kNT, kWarps, kOwn>);
     static_assert(smem <= 232448, "shared memory of the token kernel");
-    // A slot is always read by the same warp, so no warp can look for a slot's
-    // next phase before the present one has completed.
-    static_assert(kSlots % kWarps == 0, "slots are dealt to warps");
-    auto kernel = token_kernel<kD, kNT, kWarps, kSlots>;
+    static_assert(kOwn >= 2 && kOwn <= 32, "a piece to come beside the present one");
+    auto kernel = token_kernel<kD, kNT, kWarps, kOwn>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<p.grid, (kWarps + 1) * 32, smem, stream>>>(p);
+    static_assert(kWarps <= kTokenWarps && kWarps <= 16, "states in the workspace");
+    kernel<<<p.grid, kWarps * 32, smem, stream>>>(p);
     note_launches(1);
     return cudaGetLastError();
 }
+
+// Starting and ending a unit, in pages.
+constexpr int kTokenUnitCost = 1, kChunkUnitCost = 6;
 
 // Rows of a unit: up to 16 rows a kv head go to token_kernel, more to chunk_kernel.
 int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
@@ -518,7 +736,9 @@ int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
 
 size_t cache_attn_workspace_bytes(int D, int Sq, int group) {
     const int tile = tile_rows(Sq * group);
-    return (size_t)kMaxGrid * 16 + (size_t)2 * kMaxGrid * tile * ((size_t)D * 4 + 8);
+    const size_t row = (size_t)D * 4 + 8;
+    return (size_t)kMaxGrid * 16 + (size_t)2 * kMaxGrid * tile * row +
+           (tile == 128 ? 0 : (size_t)kMaxGrid * kTokenWarps * 2 * tile * (row + 16));
 }
 
 cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, int heads, const int32_t* q_lens,
@@ -543,23 +763,27 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     p.places = static_cast<int4*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.places + kMaxGrid);
     p.part_o = reinterpret_cast<float*>(p.part_ml + (size_t)2 * kMaxGrid * p.tile);
+    p.scratch = p.part_o + (size_t)2 * kMaxGrid * p.tile * D;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
+    p.unit_cost = p.tile == 128 ? kChunkUnitCost : kTokenUnitCost;
+    const int most = page_sel ? nsel : c.width;
+    p.brief = c.B <= 32 && p.tiles == 1 &&
+              (long long)c.B * c.kv_heads * ((long long)most + p.unit_cost) < (1LL << 31);
     // Short walks are not worth joining: a unit of up to kWholePages pages stays in one CTA.
     constexpr int kWholePages = 8;
-    const int most = page_sel ? nsel : c.width;
     p.whole = most <= kWholePages;
     cudaError_t e;
     if (p.tile == 128)
         e = launch_chunk(p, D, stream);
     else if (D == 64)
-        e = p.tile == 8 ? launch_token<64, 1, 11, 22>(p, stream) : launch_token<64, 2, 7, 21>(p, stream);
+        e = p.tile == 8 ? launch_token<64, 1, 12, 4>(p, stream) : launch_token<64, 2, 12, 4>(p, stream);
     else
-        e = p.tile == 8 ? launch_token<128, 1, 7, 21>(p, stream) : launch_token<128, 2, 7, 14>(p, stream);
+        e = p.tile == 8 ? launch_token<128, 1, 12, 2>(p, stream) : launch_token<128, 2, 8, 3>(p, stream);
     if (e != cudaSuccess || p.whole) return e;
     // Launched early (it waits for the attention kernel's end by itself).
     if (p.grid < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.tile + kJoinWarps - 1) / kJoinWarps), (unsigned)(p.grid - 1));
+    cfg.gridDim = dim3((unsigned)(p.tiles == 1 ? rows : p.tile), (unsigned)(p.grid - 1));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
