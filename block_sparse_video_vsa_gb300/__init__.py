@@ -609,40 +609,49 @@ def cache_pool(pages: int, kv_heads: int, D: int, device="cuda"):
     return torch.zeros((int(pages), int(kv_heads), 72 * int(D)), dtype=torch.uint8, device=device)
 
 
-def _cache(pool, table, kv_lens, kv_scale, others=()):
-    """Checks a cache's tensors (and that `others` are on its device) -> VsaCache."""
+def _on(t, dtype, name, device):
+    """_need, and on `device`, with one pass over the tensor where all is well (a call takes ten of them)."""
+    if type(t) is _torch().Tensor and t.dtype is dtype and t.is_contiguous() and t.get_device() == device >= 0:
+        return t.data_ptr()
+    _need(t, dtype, name)
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the pool's device")
+    return t.data_ptr()
+
+
+def _cache(pool, table, kv_lens, kv_scale):
+    """Checks a cache's tensors -> (VsaCache, device index, B, kv_heads, D)."""
     torch = _torch()
-    _need(pool, torch.uint8, "pool")
-    _need(table, torch.int32, "table")
-    _need(kv_lens, torch.int32, "kv_lens")
-    if pool.dim() != 3 or pool.shape[2] not in (72 * 64, 72 * 128):
+    i32 = torch.int32
+    if not isinstance(pool, torch.Tensor):
+        raise TypeError("pool must be a torch.Tensor")
+    dev = pool.get_device()
+    ptrs = (_on(pool, torch.uint8, "pool", dev), _on(table, i32, "table", dev), _on(kv_lens, i32, "kv_lens", dev))
+    shape, rows = pool.shape, table.shape
+    if len(shape) != 3 or shape[2] not in (72 * 64, 72 * 128):
         raise ValueError("pool must be [pages, kv_heads, 72 * D] with D 64 or 128")
-    if table.dim() != 2 or tuple(kv_lens.shape) != (table.shape[0],):
+    if len(rows) != 2 or kv_lens.shape != rows[:1]:
         raise ValueError("table must be [B, width] and kv_lens [B]")
+    scale = None
     if kv_scale is not None:
-        _need(kv_scale, torch.float32, "kv_scale")
-        if tuple(kv_scale.shape) != (2, pool.shape[1]):
+        scale = _on(kv_scale, torch.float32, "kv_scale", dev)
+        if kv_scale.shape != (2, shape[1]):
             raise ValueError("kv_scale must be [2, kv_heads]")
-    for t in (table, kv_lens, kv_scale, *others):
-        if t is not None and t.device != pool.device:
-            raise ValueError("all tensors of a cache call must be on the pool's device")
-    return VsaCache(pool.shape[0], pool.shape[1], pool.shape[2] // 72, table.shape[0], table.shape[1],
-                    pool.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
-                    None if kv_scale is None else kv_scale.data_ptr())
+    D = shape[2] // 72
+    return VsaCache(shape[0], shape[1], D, rows[0], rows[1], *ptrs, scale), dev, rows[0], shape[1], D
 
 
-def _rows(t, cache, heads, name):
+def _cache_call(fn, dev, stream, *args):
+    """fn(*args, stream) with the cache's device current."""
     torch = _torch()
-    _need(t, torch.bfloat16, name)
-    if t.dim() != 4 or t.shape[0] != cache.B or t.shape[3] != cache.D or (heads and t.shape[2] != heads):
-        raise ValueError(f"{name} must be [B, S, {'kv_heads' if heads else 'heads'}, D]")
-
-
-def _lens(t, cache, name):
-    if t is not None:
-        _need(t, _torch().int32, name)
-        if tuple(t.shape) != (cache.B,):
-            raise ValueError(f"{name} must be [B]")
+    if dev == torch.cuda.current_device():
+        raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(stream))
+    if status:
+        raise VsaError(status, fn.__name__)
 
 
 def cache_append(pool, k, v, table, kv_lens, new_lens=None, rope=None, positions=None, interleaved: bool = False,
@@ -654,39 +663,42 @@ def cache_append(pool, k, v, table, kv_lens, new_lens=None, rope=None, positions
     kv_lens (int32 [B]) counts the step's tokens already; new_lens says how many each sequence
     has (None: S).  positions int32 [B, S] are rows of rope (None: places in the sequence)."""
     torch = _torch()
-    c = _cache(pool, table, kv_lens, kv_scale, (k, v, new_lens, rope, positions, q, q_out))
-    _rows(k, c, c.kv_heads, "k")
-    _rows(v, c, c.kv_heads, "v")
-    if v.shape != k.shape:
-        raise ValueError("k and v must share a shape")
-    S = k.shape[1]
-    _lens(new_lens, c, "new_lens")
+    bf16, i32 = torch.bfloat16, torch.int32
+    c, dev, B, kv, D = _cache(pool, table, kv_lens, kv_scale)
+    k_ptr, v_ptr = _on(k, bf16, "k", dev), _on(v, bf16, "v", dev)
+    shape = k.shape
+    if len(shape) != 4 or (shape[0], shape[2], shape[3]) != (B, kv, D) or v.shape != shape:
+        raise ValueError("k and v must be [B, S, kv_heads, D]")
+    S = shape[1]
+    new_ptr = pos_ptr = rope_ptr = q_ptr = out_ptr = None
+    rows = R = heads = 0
+    if new_lens is not None:
+        new_ptr = _on(new_lens, i32, "new_lens", dev)
+        if new_lens.shape != (B,):
+            raise ValueError("new_lens must be [B]")
     if rope is not None:
-        _need(rope, torch.float32, "rope")
+        rope_ptr = _on(rope, torch.float32, "rope", dev)
         if rope.dim() != 2 or not rope.shape[0] or not rope.shape[1]:
             raise ValueError("rope must be [rows, R] with R > 0")
+        rows, R = rope.shape
     if positions is not None:
-        _need(positions, torch.int32, "positions")
-        if tuple(positions.shape) != (c.B, S):
+        pos_ptr = _on(positions, i32, "positions", dev)
+        if positions.shape != (B, S):
             raise ValueError("positions must be [B, S]")
-    if q is None and q_out is not None:
-        raise ValueError("q_out goes with q")
     if q is not None:
-        _rows(q, c, 0, "q")
-        if q.shape[1] != S:
-            raise ValueError("q must have k's tokens")
+        q_ptr = _on(q, bf16, "q", dev)
+        if q.dim() != 4 or q.shape[:2] != shape[:2] or q.shape[3] != D:
+            raise ValueError("q must be [B, S, heads, D] with k's tokens")
+        heads = q.shape[2]
         if q_out is None:
             q_out = torch.empty_like(q)
-        _need(q_out, torch.bfloat16, "q_out")
+        out_ptr = _on(q_out, bf16, "q_out", dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must be shaped like q")
-    ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-    with torch.cuda.device(pool.device):
-        _check(library().vsa_cache_append(ctypes.byref(c), ptr(q), k.data_ptr(), v.data_ptr(), S,
-                                          q.shape[2] if q is not None else 0, ptr(new_lens), ptr(rope),
-                                          rope.shape[0] if rope is not None else 0,
-                                          rope.shape[1] if rope is not None else 0, int(bool(interleaved)),
-                                          ptr(positions), ptr(q_out), _stream(stream)), "vsa_cache_append")
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    _cache_call(library().vsa_cache_append, dev, stream, c, q_ptr, k_ptr, v_ptr, S, heads, new_ptr, rope_ptr, rows, R,
+                1 if interleaved else 0, pos_ptr, out_ptr)
     return q_out
 
 
@@ -694,20 +706,17 @@ def cache_read(pool, table, kv_lens, S: int, kv_scale=None, k=None, v=None, stre
     """The first S cached tokens of every sequence -> (k, v) bf16 [B, S, kv_heads, D], zero past each
     length; with S a multiple of 64 they are tiled tensors for sparse_attn_fwd (vsa_cache_read)."""
     torch = _torch()
-    c = _cache(pool, table, kv_lens, kv_scale, (k, v))
-    shape = (c.B, int(S), c.kv_heads, c.D)
-    out = []
-    for t, n in ((k, "k"), (v, "v")):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
-        _need(t, torch.bfloat16, n)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{n} must be {shape}")
-        out.append(t)
-    with torch.cuda.device(pool.device):
-        _check(library().vsa_cache_read(ctypes.byref(c), int(S), out[0].data_ptr(), out[1].data_ptr(),
-                                        _stream(stream)), "vsa_cache_read")
-    return out[0], out[1]
+    c, dev, B, kv, D = _cache(pool, table, kv_lens, kv_scale)
+    shape = (B, int(S), kv, D)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
+    k_ptr, v_ptr = _on(k, torch.bfloat16, "k", dev), _on(v, torch.bfloat16, "v", dev)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError(f"k and v must be {shape}")
+    _cache_call(library().vsa_cache_read, dev, stream, c, shape[1], k_ptr, v_ptr)
+    return k, v
 
 
 def cache_attn_workspace_bytes(kv_heads: int, D: int, Sq: int, heads: int) -> int:
@@ -722,40 +731,45 @@ def cache_attn(q, pool, table, kv_lens, q_lens=None, causal: bool = True, page_s
     q_lens (int32 [B]) are each sequence's query rows (None: Sq), its last tokens when causal;
     page_sel (int32 [B, kv_heads, n]) limits each kv head to n pages of its sequence (-1: none)."""
     torch = _torch()
-    c = _cache(pool, table, kv_lens, kv_scale, (q, q_lens, page_sel, workspace, out, lse))
-    _rows(q, c, 0, "q")
-    B, Sq, heads, D = q.shape
-    if heads == 0 or heads % c.kv_heads:
+    lib = library()
+    c, dev, B, kv, D = _cache(pool, table, kv_lens, kv_scale)
+    q_ptr = _on(q, torch.bfloat16, "q", dev)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != D:
+        raise ValueError("q must be [B, Sq, heads, D]")
+    Sq, heads = shape[1], shape[2]
+    if heads == 0 or heads % kv:
         raise ValueError("heads must be a multiple of kv_heads")
-    _lens(q_lens, c, "q_lens")
+    lens_ptr = sel_ptr = lse_ptr = None
     nsel = 0
+    if q_lens is not None:
+        lens_ptr = _on(q_lens, torch.int32, "q_lens", dev)
+        if q_lens.shape != (B,):
+            raise ValueError("q_lens must be [B]")
     if page_sel is not None:
-        _need(page_sel, torch.int32, "page_sel")
-        if page_sel.dim() != 3 or tuple(page_sel.shape[:2]) != (B, c.kv_heads) or not page_sel.shape[2]:
+        sel_ptr = _on(page_sel, torch.int32, "page_sel", dev)
+        if page_sel.dim() != 3 or page_sel.shape[:2] != (B, kv) or not page_sel.shape[2]:
             raise ValueError("page_sel must be [B, kv_heads, n] with n > 0")
         nsel = page_sel.shape[2]
-    nbytes = cache_attn_workspace_bytes(c.kv_heads, D, Sq, heads)
+    nbytes = lib.vsa_cache_attn_workspace_bytes(kv, D, Sq, heads)
     if workspace is None:
         workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=q.device)
-    _need(workspace, torch.uint8, "workspace")
+    work_ptr = _on(workspace, torch.uint8, "workspace", dev)
     if workspace.numel() < nbytes:
         raise ValueError(f"workspace needs {nbytes} bytes")
     if out is None:
         out = torch.empty_like(q)
-    _need(out, torch.bfloat16, "out")
-    if out.shape != q.shape:
+    out_ptr = _on(out, torch.bfloat16, "out", dev)
+    if out.shape != shape:
         raise ValueError("out must be shaped like q")
     if want_lse and lse is None:
         lse = torch.empty((B, heads, Sq), dtype=torch.float32, device=q.device)
     if lse is not None:
-        _need(lse, torch.float32, "lse")
-        if tuple(lse.shape) != (B, heads, Sq):
+        lse_ptr = _on(lse, torch.float32, "lse", dev)
+        if lse.shape != (B, heads, Sq):
             raise ValueError("lse must be [B, heads, Sq]")
-    ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-    with torch.cuda.device(pool.device):
-        _check(library().vsa_cache_attn(ctypes.byref(c), q.data_ptr(), Sq, heads, ptr(q_lens), int(bool(causal)),
-                                        ptr(page_sel), nsel, float(sm_scale), workspace.data_ptr(), out.data_ptr(),
-                                        ptr(lse), _stream(stream)), "vsa_cache_attn")
+    _cache_call(lib.vsa_cache_attn, dev, stream, c, q_ptr, Sq, heads, lens_ptr, 1 if causal else 0, sel_ptr, nsel,
+                sm_scale, work_ptr, out_ptr, lse_ptr)
     return out, lse
 
 

@@ -13,6 +13,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "vsa_common.cuh"
 
 namespace vsa {
@@ -28,6 +30,20 @@ struct CacheView {
     unsigned int* err;
     int pages, kv_heads, B, width;
 };
+
+// Lets `kernel` use `smem` bytes; `done` (one for each kernel) remembers the
+// devices, which saves small calls a driver call.
+template <class K>
+inline cudaError_t allow_smem(K kernel, int smem, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 #if defined(__CUDACC__)
 

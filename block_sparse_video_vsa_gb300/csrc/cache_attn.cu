@@ -718,7 +718,8 @@ cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
     static_assert(smem <= 232448, "shared memory of the token kernel");
     static_assert(kOwn >= 2 && kOwn <= 32, "a piece to come beside the present one");
     auto kernel = token_kernel<kD, kNT, kWarps, kOwn>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(kernel, smem, done);
     if (e != cudaSuccess) return e;
     static_assert(kWarps <= kTokenWarps && kWarps <= 16, "states in the workspace");
     kernel<<<p.grid, kWarps * 32, smem, stream>>>(p);

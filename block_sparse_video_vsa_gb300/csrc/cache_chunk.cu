@@ -644,20 +644,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
 
 }  // namespace
 
-cudaError_t launch_chunk(const AttnParams& p, int D, cudaStream_t stream) {
-    auto kernel = D == 64 ? chunk_kernel<64> : chunk_kernel<128>;
-    const int smem = D == 64 ? chunk_smem<64>() : chunk_smem<128>();
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+template <int kD>
+static cudaError_t launch_chunk_d(const AttnParams& p, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
     // The register split draws on the launch's 128 registers a thread; with
     // fewer, setmaxnreg would wait forever, so such a build is refused.
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kernel);
+    static const int regs = [] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, chunk_kernel<kD>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs != 128) return cudaErrorInvalidKernelImage;
+    const cudaError_t e = allow_smem(chunk_kernel<kD>, chunk_smem<kD>(), done);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs != 128) return cudaErrorInvalidKernelImage;
-    kernel<<<p.grid, kChunkThreads, smem, stream>>>(p);
+    chunk_kernel<kD><<<p.grid, kChunkThreads, chunk_smem<kD>(), stream>>>(p);
     note_launches(1);
     return cudaGetLastError();
+}
+
+cudaError_t launch_chunk(const AttnParams& p, int D, cudaStream_t stream) {
+    return D == 64 ? launch_chunk_d<64>(p, stream) : launch_chunk_d<128>(p, stream);
 }
 
 }  // namespace vsa
