@@ -28,6 +28,8 @@
 //  * P is rounded to fp16 (2^-11 relative; the sum keeps the fp32 values);
 //    maximum, sum and output are fp32.  The maximum is followed lazily: the
 //    output is rescaled when it grows by more than 2^8.
+#include <algorithm>
+
 #include "cache.cuh"
 
 namespace vsa {
@@ -640,74 +642,79 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) 
         c1 = c - 1 + (more == 0xffffffffu ? 32 : __ffs(~more) - 1);
         if (more != 0xffffffffu) break;
     }
-    const int r = blockIdx.x, row = u.z * p.tile + r;
-    if (row >= p.Sq * p.group) return;
-    // Slot 1 of the unit's first CTA, slot 0 of the others.
-    constexpr int kPer = kD / 32, kAhead = 8;
-    float m = -INFINITY, l = 0.f, sum[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) sum[i] = 0.f;
 #pragma unroll 1
-    for (int c = c0 + warp; c <= c1; c += kJoinWarps * kAhead) {
-        float2 ml[kAhead];
-        float o[kAhead][kPer];
+    for (int r = blockIdx.x; r < p.tile; r += gridDim.x) {
+        const int row = u.z * p.tile + r;
+        if (row >= p.Sq * p.group) return;
+        // Slot 1 of the unit's first CTA, slot 0 of the others.
+        constexpr int kPer = kD / 32, kAhead = 8;
+        float m = -INFINITY, l = 0.f, sum[kPer];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int ck = c + k * kJoinWarps;
-            const size_t at = (2 * (size_t)ck + (ck == c0)) * p.tile + r;
-            ml[k] = make_float2(-INFINITY, 0.f);
-            if (ck > c1) continue;
-            ml[k] = p.part_ml[at];
-            if constexpr (kPer == 4)
+        for (int i = 0; i < kPer; ++i) sum[i] = 0.f;
+#pragma unroll 1
+        for (int c = c0 + warp; c <= c1; c += kJoinWarps * kAhead) {
+            float2 ml[kAhead];
+            float o[kAhead][kPer];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int ck = c + k * kJoinWarps;
+                const size_t at = (2 * (size_t)ck + (ck == c0)) * p.tile + r;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (ck > c1) continue;
+                ml[k] = p.part_ml[at];
+                if constexpr (kPer == 4)
                 *reinterpret_cast<float4*>(o[k]) = *reinterpret_cast<const float4*>(p.part_o + at * kD + lane * kPer);
-            else
+                else
                 *reinterpret_cast<float2*>(o[k]) = *reinterpret_cast<const float2*>(p.part_o + at * kD + lane * kPer);
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) top = fmaxf(top, ml[k].x);
+            if (top == -INFINITY) continue;
+            const float keep = ex2_approx(m - top);
+            m = top;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) sum[i] *= keep;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (ml[k].x == -INFINITY) continue;
+                const float a = ex2_approx(ml[k].x - m);
+                l = fmaf(a, ml[k].y, l);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) sum[i] = fmaf(a, o[k][i], sum[i]);
+            }
         }
-        float top = m;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, ml[k].x);
-        if (top == -INFINITY) continue;
-        const float keep = ex2_approx(m - top);
-        m = top;
-        l *= keep;
+        for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = sum[i];
+        if (lane == 0) s_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        if (threadIdx.x < kD / 2) {
+            m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) sum[i] *= keep;
+            for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_ml[w].x);
+            l = 0.f;
+            float2 y = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (ml[k].x == -INFINITY) continue;
-            const float a = ex2_approx(ml[k].x - m);
-            l = fmaf(a, ml[k].y, l);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) sum[i] = fmaf(a, o[k][i], sum[i]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = sum[i];
-    if (lane == 0) s_ml[warp] = make_float2(m, l);
-    __syncthreads();
-    if (threadIdx.x >= kD / 2) return;
-    m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_ml[w].x);
-    l = 0.f;
-    float2 y = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        const float2 ml = s_ml[w];
-        const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-        const float2 z = *reinterpret_cast<const float2*>(&s_o[w][2 * threadIdx.x]);
-        l = fmaf(a, ml.y, l);
-        y.x = fmaf(a, z.x, y.x);
-        y.y = fmaf(a, z.y, y.y);
-    }
-    const int qi = row / p.group, head = u.y * p.group + row - qi * p.group;
-    const bool live = row < seq_lens(p, u.x).q * p.group && l != 0.f;
-    const float inv = live ? (p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + u.y) : 1.f) / l : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)u.x * p.Sq + qi) * p.heads + head) * (kD / 8));
-    dst[threadIdx.x] = live ? pack_bf16x2(y.x * inv, y.y * inv) : 0u;
-    if (threadIdx.x == 0 && p.lse)
-        p.lse[((size_t)u.x * p.heads + head) * p.Sq + qi] =
+            for (int w = 0; w < kJoinWarps; ++w) {
+                const float2 ml = s_ml[w];
+                const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+                const float2 z = *reinterpret_cast<const float2*>(&s_o[w][2 * threadIdx.x]);
+                l = fmaf(a, ml.y, l);
+                y.x = fmaf(a, z.x, y.x);
+                y.y = fmaf(a, z.y, y.y);
+            }
+            const int qi = row / p.group, head = u.y * p.group + row - qi * p.group;
+            const bool live = row < seq_lens(p, u.x).q * p.group && l != 0.f;
+            const float inv = live ? (p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + u.y) : 1.f) / l : 0.f;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)u.x * p.Sq + qi) * p.heads + head) * (kD / 8));
+            dst[threadIdx.x] = live ? pack_bf16x2(y.x * inv, y.y * inv) : 0u;
+            if (threadIdx.x == 0 && p.lse)
+            p.lse[((size_t)u.x * p.heads + head) * p.Sq + qi] =
             live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+        __syncthreads();
+    }
 }
 
 constexpr int kTokenWarps = 12;  // at most: states in the workspace
@@ -731,7 +738,7 @@ cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
 constexpr int kTokenUnitCost = 1, kChunkUnitCost = 6;
 
 // Rows of a unit: up to 16 rows a kv head go to token_kernel, more to chunk_kernel.
-int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
+int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256; }
 
 }  // namespace
 
@@ -739,7 +746,7 @@ size_t cache_attn_workspace_bytes(int D, int Sq, int group) {
     const int tile = tile_rows(Sq * group);
     const size_t row = (size_t)D * 4 + 8;
     return (size_t)kMaxGrid * 16 + (size_t)2 * kMaxGrid * tile * row +
-           (tile == 128 ? 0 : (size_t)kMaxGrid * kTokenWarps * 2 * tile * (row + 16));
+           (tile >= 128 ? 0 : (size_t)kMaxGrid * kTokenWarps * 2 * tile * (row + 16));
 }
 
 cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, int heads, const int32_t* q_lens,
@@ -766,7 +773,7 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     p.part_o = reinterpret_cast<float*>(p.part_ml + (size_t)2 * kMaxGrid * p.tile);
     p.scratch = p.part_o + (size_t)2 * kMaxGrid * p.tile * D;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
-    p.unit_cost = p.tile == 128 ? kChunkUnitCost : kTokenUnitCost;
+    p.unit_cost = p.tile >= 128 ? kChunkUnitCost : kTokenUnitCost;
     const int most = page_sel ? nsel : c.width;
     p.brief = c.B <= 32 && p.tiles == 1 &&
               (long long)c.B * c.kv_heads * ((long long)most + p.unit_cost) < (1LL << 31);
@@ -774,7 +781,7 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     constexpr int kWholePages = 8;
     p.whole = most <= kWholePages;
     cudaError_t e;
-    if (p.tile == 128)
+    if (p.tile >= 128)
         e = launch_chunk(p, D, stream);
     else if (D == 64)
         e = p.tile == 8 ? launch_token<64, 1, 12, 4>(p, stream) : launch_token<64, 2, 12, 4>(p, stream);
@@ -784,7 +791,7 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     // Launched early (it waits for the attention kernel's end by itself).
     if (p.grid < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.tiles == 1 ? rows : p.tile), (unsigned)(p.grid - 1));
+    cfg.gridDim = dim3((unsigned)std::min(p.tiles == 1 ? rows : p.tile, 16), (unsigned)(p.grid - 1));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];

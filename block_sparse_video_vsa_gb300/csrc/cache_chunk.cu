@@ -1,23 +1,26 @@
 // Attention over the 4-bit paged cache, many query rows a kv head (chunks of
 // tokens): the same function as token_kernel (cache_attn.cu), on tcgen05.
 //
-// Tensor bound for long chunks (4 * D flops for each row and key), so the
-// structure is the fine stage's: 128 query rows a unit, one TMEM lane each,
-// 128 keys (two pages) a step, Q and P as A operands in TMEM, two softmax
-// groups that take the steps of a unit in turn with a maximum, sum and output
-// of their own, joined at the unit's end.  What differs is where K and V come
-// from: a producer warp copies pages whole (4-bit codes and scales, 72 * D
-// contiguous bytes) into a ring, and a warpgroup converts each step's two
-// pages into fp16 K and V tiles (exact, see cache.cuh) in the 128-byte
-// swizzled layout the tensor core reads.  So a page crosses HBM and L2 in 9
-// bits a K and V element pair instead of 32, and is converted once for 128
-// rows: about 1.5 instructions an element, next to some 2.7 of softmax a
-// logit.
+// Tensor bound for long chunks (4 * D flops for each row and key).  A unit is
+// kQ tiles of 128 query rows, one TMEM lane each; a step is 128 keys (two
+// pages).  What stands between the cache and the tensor core is the conversion
+// of codes to fp16 operands, about 1.5 instructions an element and as many
+// bytes of shared-memory writes as the tensor core reads, so it is shared by
+// as many rows as TMEM has room for:
+//  * kQ = 2 (more than 128 rows): each softmax group has a tile of its own and
+//    takes every step; K and V are converted once for 256 rows.
+//  * kQ = 1: both groups have the same rows and take the steps in turn, each
+//    with a maximum, sum and output of its own, joined at the unit's end.
+// A producer warp copies pages (halves: K and V with their scales) into a
+// ring; a warpgroup converts them (exact, see cache.cuh) to K and V tiles in
+// the 128-byte swizzled layout the tensor core reads.  A page crosses HBM and
+// L2 in 9 bits a pair of K and V elements instead of 32.
 //  * Warp roles (512 threads): warp 0 looks pages up and copies them; warp 1
 //    owns TMEM and issues Q K^T, warp 3 P V; warps 4..7 convert; warps 8..11
-//    and 12..15 are the softmax groups (group 0 the CTA's even steps).
-//  * TMEM (512 columns): S [0,128); P (fp16 pairs) [128,192); Q [192,256);
-//    O_0 [256,384); O_1 [384,512).
+//    and 12..15 are the softmax groups.
+//  * TMEM (512 columns): S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1
+//    [384,512).  P (fp16 pairs) takes the first 64 columns of its S once the
+//    softmax has loaded that; Q is in shared memory.
 //  * A query row is scaled by a power of two on its way to fp16 (its bf16
 //    values keep all their bits) and the inverse joins its softmax scale.
 //  * Every wait is bounded; one that runs out raises the CTA's abort flag and
@@ -29,24 +32,27 @@ namespace vsa {
 namespace {
 
 constexpr int kChunkThreads = 512;
-constexpr int kKStages = 2, kVStages = 3;
-constexpr int kRawPages = 6;  // at least 2 * kKStages + 2: see the parity note at the convert role
-static_assert(kRawPages >= 2 * kKStages + 2, "raw ring");
 constexpr int kMetaSteps = 16;
 // Registers: 4 warpgroups launched with 128 each; the shares add up to 512.
 constexpr int kIssueRegs = 64, kConvertRegs = 80, kSoftRegs = 184;
 static_assert(kIssueRegs + kConvertRegs + 2 * kSoftRegs <= 512, "register split exceeds the launch");
 
-constexpr int kTmemS = 0, kTmemP = 128, kTmemQ = 192, kTmemO0 = 256, kTmemO1 = 384;
+constexpr int kTmemS = 0, kTmemO = 256, kTmemGroup = 128;  // of group G: + G * kTmemGroup
 
-template <int kD>
+template <int kD, int kQ>
 struct ChunkSmem {
-    static constexpr int kHalf = 128 * 128;          // 128 keys x 64 channels of fp16, swizzled
-    static constexpr int kTile = kHalf * (kD / 64);  // K or V of a step
-    static constexpr int kOffK = 0;
+    static constexpr int kKStages = 2;
+    static constexpr int kVStages = kD == 128 && kQ == 2 ? 2 : 3;
+    static constexpr int kRaw = kD == 128 ? 6 : 12;  // half pages
+    static constexpr int kHalf = 128 * 128;          // 128 rows x 64 channels of fp16, swizzled
+    static constexpr int kTile = kHalf * (kD / 64);  // Q of a tile, K or V of a step
+    static constexpr int kCodes = kPageTokens * kD / 2, kScales = kPageTokens * kD / 16;
+    static constexpr int kRawBytes = kCodes + kScales;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kQ * kTile;
     static constexpr int kOffV = kOffK + kKStages * kTile;
     static constexpr int kOffRaw = kOffV + kVStages * kTile;
-    static constexpr int kOffMisc = kOffRaw + kRawPages * PageLayout<kD>::kBytes;
+    static constexpr int kOffMisc = kOffRaw + kRaw * kRawBytes;
 };
 
 // A softmax warp's walk and its present and next unit: kept in shared memory,
@@ -57,21 +63,17 @@ struct SoftWalk {
 };
 
 struct __align__(16) ChunkMisc {
-    uint64_t raw_full[kRawPages], raw_empty[kRawPages];
-    uint64_t k_full[kKStages], k_empty[kKStages];
-    uint64_t v_full[kVStages], v_empty[kVStages];
-    uint64_t s_full[2];  // per softmax group: S of its next step is ready
-    uint64_t s_free;     // S has been loaded into registers
-    uint64_t p_full;     // P of the step (and any rescaling of O) is in TMEM
-    uint64_t pv_grp[2];  // per group: P V of its step has completed
-    uint64_t unit_done;  // every P V of the unit has completed
-    uint64_t q_full, q_empty;
-    uint64_t o_free;     // O_0 and O_1 have been read by the unit's epilogue
+    uint64_t raw_full[12], raw_empty[12];
+    uint64_t k_full[2], k_empty[2];
+    uint64_t v_full[3], v_empty[3];
+    // Per softmax group: S of its next step is ready; P of it (and any
+    // rescaling of O) is in TMEM; P V has completed (S may be overwritten).
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t q_full[2], q_empty[2];  // per tile
     uint64_t drain[2];
-    int2 key0[kMetaSteps];   // first key of a step's pages (kNoKey: none)
-    float xm[2][2][128];     // [unit parity][group][row]: maximum, sum at the unit's end
-    float xl[2][2][128];
-    float scale[2][128];     // [unit parity][row]: logit -> log2 units
+    int2 key0[kMetaSteps];  // first key of a step's pages (kNoKey: none)
+    float xm[2][128], xl[2][128];  // kQ = 1: the groups' maxima and sums at the unit's end
+    float scale[2][128];           // kQ = 1: [unit parity][row]: logit -> log2 units
     SoftWalk soft[8];
     PlanScratch plan;
     uint32_t tmem_base;
@@ -79,11 +81,11 @@ struct __align__(16) ChunkMisc {
 };
 constexpr int kNoKey = 0x7FFFFFFF;  // beyond every row's limit
 
-template <int kD>
+template <int kD, int kQ>
 constexpr int chunk_smem() {
-    return ChunkSmem<kD>::kOffMisc + (int)sizeof(ChunkMisc) + 1024;  // slack for 1024-byte alignment
+    return ChunkSmem<kD, kQ>::kOffMisc + (int)sizeof(ChunkMisc) + 1024;  // slack for 1024-byte alignment
 }
-static_assert(chunk_smem<128>() <= 232448, "shared memory of the chunk kernel");
+static_assert(chunk_smem<128, 1>() <= 232448 && chunk_smem<128, 2>() <= 232448, "shared memory of the chunk kernel");
 
 // As idesc_bf16_f32, fp16 inputs.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
@@ -124,91 +126,99 @@ __device__ __forceinline__ void chunk_exp64(const float* x, float c2, float mb, 
 
 __device__ __forceinline__ int steps_of(const Segment& s) { return (s.last - s.first + 1) >> 1; }
 
-// Softmax thread of row r: puts its query row of unit s into the TMEM Q
-// columns of its lane as fp16, scaled by a power of two, and returns the row's
-// factor from logits to log2 units.
-template <int kD>
-__device__ __forceinline__ float stage_query(const AttnParams& p, const Segment& s, int r, uint32_t t_lane) {
-    const int row = s.t * 128 + r;
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+    return x;
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Softmax thread of row r of a tile: puts query row `row` of unit s into the
+// tile's Q as fp16, scaled by a power of two, and returns the row's factor from
+// logits to log2 units.
+template <int kD, int kQ>
+__device__ __forceinline__ float stage_query(const AttnParams& p, const Segment& s, int row, int r, uint32_t tile) {
     const bool real = row < p.Sq * p.group;
     const int qi = real ? row / p.group : 0;
     const int head = s.h * p.group + (real ? row - qi * p.group : 0);
     const uint4* src = p.q + (((size_t)s.b * p.Sq + qi) * p.heads + head) * (kD / 8);
+    uint32_t w[kD / 2];
     float amax = 0.f;
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < kD / 8; ++i) {
         const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
     }
+#pragma unroll
+    for (int i = 0; i < kD / 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
     const int e = q_exponent(amax);
     const float f = pow2i(e);
-#pragma unroll 1
-    for (int c0 = 0; c0 < kD / 2; c0 += 32) {
-        uint32_t w[32];
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
-            const uint4 x = real ? __ldg(src + c0 / 4 + v) : make_uint4(0, 0, 0, 0);
-            w[4 * v] = x.x; w[4 * v + 1] = x.y; w[4 * v + 2] = x.z; w[4 * v + 3] = x.w;
-        }
+    for (int i = 0; i < kD / 8; ++i) {
+        uint32_t y[4];
 #pragma unroll
-        for (int v = 0; v < 32; ++v) w[v] = pack_f16x2(bf16_lo(w[v]) * f, bf16_hi(w[v]) * f);
-        tmem_st32(t_lane + kTmemQ + c0, w);
+        for (int j = 0; j < 4; ++j) y[j] = pack_f16x2(bf16_lo(w[4 * i + j]) * f, bf16_hi(w[4 * i + j]) * f);
+        sts128(tile + (i >> 3) * ChunkSmem<kD, kQ>::kHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
     }
-    tmem_wait_st();
+    fence_proxy_async_smem();
     return p.scale_log2 * (p.c.kv_scale ? __ldg(p.c.kv_scale + s.h) : 1.f) * pow2i(-e);
 }
 
-// One key's codes of K or V (kD / 2 bytes at `codes`) and scales to a row of a
-// fp16 tile.  Lanes of neighbouring rows start at different 16-byte pieces, so
-// that neither the loads nor the swizzled stores meet in a bank.
-template <int kD>
-__device__ __forceinline__ void convert_row(const unsigned char* codes, const unsigned char* scales, int row, bool zero,
-                                            unsigned char* tile) {
-    constexpr int kPieces = kD / 32;  // of 32 channels
-    uint32_t sc[kD / 64];             // scale bytes, two for each piece
-    if constexpr (kD == 128) {
-        const uint2 x = *reinterpret_cast<const uint2*>(scales);
-        sc[0] = zero ? 0u : x.x;
-        sc[1] = zero ? 0u : x.y;
-    } else {
-        sc[0] = zero ? 0u : *reinterpret_cast<const uint32_t*>(scales);
+// Half of one key's codes of K or V and their scales (`codes`, `scales`: the
+// key's, in shared memory) to row `row` of a fp16 tile: channels [h kD / 2,
+// (h + 1) kD / 2).  Two threads a key, neighbouring lanes, each starting at
+// another 16-byte piece (kD = 128) so that neither the loads nor the swizzled
+// stores of 8 lanes meet in a bank.
+template <int kD, int kQ>
+__device__ __forceinline__ void convert_half_row(uint32_t codes, uint32_t scales, int row, int h, bool zero,
+                                                 uint32_t tile) {
+    constexpr int kPieces = kD / 64;  // of 32 channels
+    const int flip = kPieces == 2 ? ((row >> 1) ^ h) & 1 : 0;
+    uint4 w[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) w[i] = lds128(codes + h * (kD / 4) + (i ^ flip) * 16);
+    uint32_t sc = 0u;  // scale bytes, two a piece
+    if (!zero) {
+        if constexpr (kD == 128)
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc) : "r"(scales + h * 4));
+        else
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc) : "r"(scales + h * 2));
     }
-    const int r7 = row & 7;
-    unsigned char* base = tile + row * 128;
+    // Unit u of 16 bytes (8 channels) of a 64-channel half goes to u ^ (row & 7).
+    const uint32_t base = tile + row * 128 + (kD == 128 ? h * ChunkSmem<kD, kQ>::kHalf : 0);
+    const uint32_t low = (row & 3) << 4, top = (row & 4) << 4;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        const int c = (i + (kD == 128 ? row >> 1 : row >> 2)) & (kPieces - 1);
-        const uint4 w = *reinterpret_cast<const uint4*>(codes + c * 16);
-        uint32_t two;
-        if constexpr (kD == 128)
-            two = (c & 2 ? sc[1] : sc[0]) >> (16 * (c & 1));
-        else
-            two = sc[0] >> (16 * c);
-        two = e4m3_to_f16(two);
+        const int c = kD == 128 ? i ^ flip : h;  // piece of the 64 channels
+        const uint32_t two = e4m3_to_f16(kD == 128 ? sc >> (16 * c) : sc);
         const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        unsigned char* half = base + (c >> 1) * ChunkSmem<kD>::kHalf;
-        const int bit2 = (c & 1) * 4;
+        const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        const uint32_t at = base + ((c << 6) ^ top);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            uint32_t h[4];
-            e2m1_to_f16(ws[k], h);
+            uint32_t y[4];
+            e2m1_to_f16(ws[k], y);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = mul_f16x2(h[j], k < 2 ? s0 : s1);
-            *reinterpret_cast<uint4*>(half + (((bit2 + k) ^ r7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int j = 0; j < 4; ++j) y[j] = mul_f16x2(y[j], k < 2 ? s0 : s1);
+            sts128(at + ((k << 4) ^ low), y[0], y[1], y[2], y[3]);
         }
     }
 }
 
-template <int kD>
+// Groups with rows of a unit.
+template <int kQ>
+__device__ __forceinline__ int groups_of(const AttnParams& p, const Segment& s) {
+    return kQ == 2 && s.t * 256 + 128 < p.Sq * p.group ? 2 : 1;
+}
+
+template <int kD, int kQ>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
     using L = PageLayout<kD>;
-    using Sm = ChunkSmem<kD>;
+    using Sm = ChunkSmem<kD, kQ>;
     extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     ChunkMisc& ms = *reinterpret_cast<ChunkMisc*>(smem + Sm::kOffMisc);
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -216,37 +226,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
     unsigned int* err = p.c.err;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kRawPages; ++s) {
+        for (int s = 0; s < Sm::kRaw; ++s) {
             mbar_init(smem_u32(&ms.raw_full[s]), 1);
-            mbar_init(smem_u32(&ms.raw_empty[s]), 2);  // the two warps that convert the page
+            mbar_init(smem_u32(&ms.raw_empty[s]), 4);
         }
-        for (int s = 0; s < kKStages; ++s) {
+        for (int s = 0; s < Sm::kKStages; ++s) {
             mbar_init(smem_u32(&ms.k_full[s]), 4);
             mbar_init(smem_u32(&ms.k_empty[s]), 1);
         }
-        for (int s = 0; s < kVStages; ++s) {
+        for (int s = 0; s < Sm::kVStages; ++s) {
             mbar_init(smem_u32(&ms.v_full[s]), 4);
             mbar_init(smem_u32(&ms.v_empty[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&ms.s_full[s]), 1);
-            mbar_init(smem_u32(&ms.pv_grp[s]), 1);
+            mbar_init(smem_u32(&ms.p_full[s]), 4);
+            mbar_init(smem_u32(&ms.pv_done[s]), 1);
+            mbar_init(smem_u32(&ms.q_full[s]), 4);
+            mbar_init(smem_u32(&ms.q_empty[s]), 1);
             mbar_init(smem_u32(&ms.drain[s]), 1);
         }
-        mbar_init(smem_u32(&ms.s_free), 4);
-        mbar_init(smem_u32(&ms.p_full), 4);
-        mbar_init(smem_u32(&ms.unit_done), 1);
-        mbar_init(smem_u32(&ms.q_full), 4);
-        mbar_init(smem_u32(&ms.q_empty), 1);
-        mbar_init(smem_u32(&ms.o_free), 8);
         ms.abort_flag = 0;
         fence_barrier_init();
     }
     // The tiles start as zeros: the tensor core multiplies rows that no page
     // filled (an odd last page, pages passed over) by probabilities of zero.
     {
-        int4* z = reinterpret_cast<int4*>(smem);
-        for (int e = threadIdx.x; e < Sm::kOffRaw / 16; e += kChunkThreads) z[e] = make_int4(0, 0, 0, 0);
+        int4* z = reinterpret_cast<int4*>(smem + Sm::kOffK);
+        for (int e = threadIdx.x; e < (Sm::kOffRaw - Sm::kOffK) / 16; e += kChunkThreads) z[e] = make_int4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -265,46 +272,56 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 0) {
             // ================================================= page producer
-            uint32_t j = 0, g = 0;  // pages and steps so far
+            // Half pages in the order of their conversion: K of the step's
+            // pages, then V of them.
+            uint32_t j = 0, g = 0;  // half pages and steps so far
             bool ok = true;
             for (Segment sg; ok && walk.next(p, sg);) {
                 const unsigned char* pool = p.c.pool + (size_t)sg.h * L::kBytes;
                 for (int base = sg.first; base < sg.last && ok; base += 32) {
                     int logical = 0, id = -1;
                     if (base + lane < sg.last) look_up(p, sg, base + lane, logical, id);
-                    const int n = min(32, sg.last - base);
-                    for (int i = 0; i < n; ++i, ++j) {
-                        const int slot = j % kRawPages;
-                        const int page = __shfl_sync(0xffffffffu, id, i);
-                        const int num = __shfl_sync(0xffffffffu, logical, i);
-                        if (j >= (uint32_t)kRawPages) {
-                            ok = mbar_wait_bounded(smem_u32(&ms.raw_empty[slot]), (j / kRawPages + 1) & 1, abort_flag,
-                                                   err, kCacheWaitNs);
-                            if (!ok) break;
-                        }
-                        if (lane == 0) {
-                            // Steps start at even pages of the segment (32 is even).
-                            int* key0 = &ms.key0[g % kMetaSteps].x;
-                            key0[i & 1] = page < 0 ? kNoKey : num * kPageTokens;
-                            if (!(i & 1)) key0[1] = kNoKey;
-                            const uint32_t bar = smem_u32(&ms.raw_full[slot]);
-                            if (page < 0) {
-                                mbar_arrive(bar);
-                            } else {
-                                mbar_arrive_expect_tx(bar, L::kBytes);
-                                bulk_load(sbase + Sm::kOffRaw + slot * L::kBytes,
-                                          pool + (size_t)page * p.c.kv_heads * L::kBytes, L::kBytes, bar);
+                    const int n = min(32, sg.last - base);  // (32 is even: steps do not straddle)
+                    for (int i = 0; i < n && ok; i += 2, ++g) {
+                        const int held = min(2, n - i);
+                        const int page0 = __shfl_sync(0xffffffffu, id, i);
+                        const int page1 = held == 2 ? __shfl_sync(0xffffffffu, id, i + 1) : -1;
+                        const int num0 = __shfl_sync(0xffffffffu, logical, i);
+                        const int num1 = held == 2 ? __shfl_sync(0xffffffffu, logical, i + 1) : 0;
+                        if (lane == 0)
+                            ms.key0[g % kMetaSteps] = make_int2(page0 < 0 ? kNoKey : num0 * kPageTokens,
+                                                                page1 < 0 ? kNoKey : num1 * kPageTokens);
+                        for (int k = 0; k < 2 * held; ++k, ++j) {
+                            const int side = k >= held;
+                            const int page = (k - side * held) ? page1 : page0;
+                            const int slot = j % Sm::kRaw;
+                            if (j >= (uint32_t)Sm::kRaw) {
+                                ok = mbar_wait_bounded(smem_u32(&ms.raw_empty[slot]), (j / Sm::kRaw + 1) & 1,
+                                                       abort_flag, err, kCacheWaitNs);
+                                if (!ok) break;
                             }
+                            if (lane == 0) {
+                                const uint32_t bar = smem_u32(&ms.raw_full[slot]);
+                                if (page < 0) {
+                                    mbar_arrive(bar);
+                                } else {
+                                    mbar_arrive_expect_tx(bar, Sm::kRawBytes);
+                                    const uint32_t dst = sbase + Sm::kOffRaw + slot * Sm::kRawBytes;
+                                    const unsigned char* src = pool + (size_t)page * p.c.kv_heads * L::kBytes;
+                                    bulk_load(dst, src + side * L::kV, Sm::kCodes, bar);
+                                    bulk_load(dst + Sm::kCodes, src + (side ? L::kVScale : L::kKScale), Sm::kScales,
+                                              bar);
+                                }
+                            }
+                            __syncwarp();
                         }
-                        if ((i & 1) || base + i + 1 == sg.last) ++g;
-                        __syncwarp();
                     }
                 }
             }
             if (lane == 0) {
-                for (int s = 0; s < kRawPages && (uint32_t)s < j; ++s) {
-                    const uint32_t last = j - 1 - ((j - 1 - s) % kRawPages);
-                    mbar_wait_drain_1(smem_u32(&ms.raw_full[s]), (last / kRawPages) & 1, err, kCacheWaitNs);
+                for (int s = 0; s < Sm::kRaw && (uint32_t)s < j; ++s) {
+                    const uint32_t last = j - 1 - ((j - 1 - s) % Sm::kRaw);
+                    mbar_wait_drain_1(smem_u32(&ms.raw_full[s]), (last / Sm::kRaw) & 1, err, kCacheWaitNs);
                 }
             }
             __syncwarp();
@@ -312,31 +329,52 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             // ========================================================= Q K^T
             const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);
             const uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
+            const uint32_t lo_q = (uint32_t)smem_desc_sw128(sbase + Sm::kOffQ, 16, 1024);
             const uint32_t lo_k = (uint32_t)smem_desc_sw128(sbase + Sm::kOffK, 16, 1024);
-            uint32_t g = 0, ul = 0;
+            uint32_t g = 0, n_s[2] = {0, 0}, n_q[2] = {0, 0};  // steps; S written, units staged, per group
             bool ok = true;
-            for (Segment sg; ok && walk.next(p, sg); ++ul) {
-                const int nst = steps_of(sg);
-                ok = mbar_wait_bounded(smem_u32(&ms.q_full), ul & 1, abort_flag, err, kCacheWaitNs);
+            for (Segment sg; ok && walk.next(p, sg);) {
+                const int nst = steps_of(sg), groups = groups_of<kQ>(p, sg);
                 for (int t = 0; t < nst && ok; ++t, ++g) {
-                    if (g >= 1)
-                        ok = mbar_wait_bounded(smem_u32(&ms.s_free), (g - 1) & 1, abort_flag, err, kCacheWaitNs);
-                    const int slot = g % kKStages;
-                    if (ok)
-                        ok = mbar_wait_bounded(smem_u32(&ms.k_full[slot]), (g / kKStages) & 1, abort_flag, err,
-                                               kCacheWaitNs);
-                    if (!ok) break;
+                    const int slot = g % Sm::kKStages;
+                    ok = mbar_wait_bounded(smem_u32(&ms.k_full[slot]), (g / Sm::kKStages) & 1, abort_flag, err,
+                                           kCacheWaitNs);
                     const uint32_t b0 = lo_k + ((uint32_t)(slot * Sm::kTile) >> 4);
-                    tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk)
-                        mma_ts_warp(tmem + kTmemS, tmem + kTmemQ + kk * 8,
-                                    b0 + (((kk >> 2) * Sm::kHalf + (kk & 3) * 32) >> 4), hi, idesc, kk > 0);
-                    mma_commit_warp(smem_u32(&ms.s_full[g & 1]));
+                    for (int G = 0; G < 2; ++G) {
+                        if (kQ == 1 ? (g & 1) != (uint32_t)G : G >= groups) continue;
+                        const int tile = kQ == 1 ? 0 : G;
+                        if (t == 0 && ok)
+                            ok = mbar_wait_bounded(smem_u32(&ms.q_full[tile]), n_q[tile] & 1, abort_flag, err,
+                                                   kCacheWaitNs);
+                        if (n_s[G] > 0 && ok)  // P V of the group's last step has read P, which lies in S
+                            ok = mbar_wait_bounded(smem_u32(&ms.pv_done[G]), (n_s[G] - 1) & 1, abort_flag, err,
+                                                   kCacheWaitNs);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a0 = lo_q + ((uint32_t)(tile * Sm::kTile) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kD / 16; ++kk) {
+                            const uint32_t step = ((kk >> 2) * Sm::kHalf + (kk & 3) * 32) >> 4;
+                            mma_ss_warp(tmem + kTmemS + G * kTmemGroup, a0 + step, hi, b0 + step, hi, idesc, kk > 0);
+                        }
+                        mma_commit_warp(smem_u32(&ms.s_full[G]));
+                        ++n_s[G];
+                    }
+                    if (!ok) break;
                     mma_commit_warp(smem_u32(&ms.k_empty[slot]));
                 }
                 if (!ok) break;
-                mma_commit_warp(smem_u32(&ms.q_empty));
+#pragma unroll
+                for (int tile = 0; tile < kQ; ++tile) {
+                    if (tile >= groups) continue;
+                    // (A unit without steps has its queries staged all the same.)
+                    if (nst == 0 && ok)
+                        ok = mbar_wait_bounded(smem_u32(&ms.q_full[tile]), n_q[tile] & 1, abort_flag, err,
+                                               kCacheWaitNs);
+                    mma_commit_warp(smem_u32(&ms.q_empty[tile]));
+                    ++n_q[tile];
+                }
             }
             mma_commit_warp(smem_u32(&ms.drain[0]));
             if (lane == 0) mbar_wait_drain_1(smem_u32(&ms.drain[0]), 0, err, kCacheWaitNs);
@@ -346,37 +384,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);
             const uint32_t idesc = idesc_f16_f32(128, kD, 0, 1);
             const uint32_t lo_v = (uint32_t)smem_desc_sw128(sbase + Sm::kOffV, Sm::kHalf, 1024);
-            uint32_t g = 0, ul = 0;
+            uint32_t g = 0, n_p[2] = {0, 0};
             bool ok = true;
-            for (Segment sg; ok && walk.next(p, sg); ++ul) {
-                const int nst = steps_of(sg);
-                // O_0 and O_1 start over once the last epilogue has read them (a
-                // unit without steps waits too: unit_done stays one phase ahead).
-                if (ul >= 1) ok = mbar_wait_bounded(smem_u32(&ms.o_free), (ul - 1) & 1, abort_flag, err, kCacheWaitNs);
+            for (Segment sg; ok && walk.next(p, sg);) {
+                const int nst = steps_of(sg), groups = groups_of<kQ>(p, sg);
                 for (int t = 0; t < nst && ok; ++t, ++g) {
-                    const int slot = g % kVStages;
-                    ok = mbar_wait_bounded(smem_u32(&ms.p_full), g & 1, abort_flag, err, kCacheWaitNs) &&
-                         mbar_wait_bounded(smem_u32(&ms.v_full[slot]), (g / kVStages) & 1, abort_flag, err,
+                    const int slot = g % Sm::kVStages;
+                    ok = mbar_wait_bounded(smem_u32(&ms.v_full[slot]), (g / Sm::kVStages) & 1, abort_flag, err,
                                            kCacheWaitNs);
-                    if (!ok) break;
                     const uint32_t b0 = lo_v + ((uint32_t)(slot * Sm::kTile) >> 4);
-                    const uint32_t d = tmem + ((g & 1) ? kTmemO1 : kTmemO0);
-                    const uint32_t acc = t >= 2 ? 1u : 0u;  // a group's first step of the unit overwrites its O
-                    tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts_warp(d, tmem + kTmemP + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc,
-                                    acc | (kk > 0 ? 1u : 0u));
-                    if (sg.first + 2 * t + 1 < sg.last) {
+                    for (int G = 0; G < 2; ++G) {
+                        if (kQ == 1 ? (g & 1) != (uint32_t)G : G >= groups) continue;
+                        if (ok)
+                            ok = mbar_wait_bounded(smem_u32(&ms.p_full[G]), n_p[G] & 1, abort_flag, err, kCacheWaitNs);
+                        if (!ok) break;
+                        // The unit's first step of the group starts its O over.
+                        const uint32_t acc = t >= (kQ == 1 ? 2 : 1) ? 1u : 0u;
+                        const uint32_t d = tmem + kTmemO + G * kTmemGroup, a = tmem + kTmemS + G * kTmemGroup;
+                        tc_fence_after();
 #pragma unroll
-                        for (int kk = 4; kk < 8; ++kk)
-                            mma_ts_warp(d, tmem + kTmemP + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc, 1u);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts_warp(d, a + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc, acc | (kk > 0 ? 1u : 0u));
+                        if (sg.first + 2 * t + 1 < sg.last) {
+#pragma unroll
+                            for (int kk = 4; kk < 8; ++kk)
+                                mma_ts_warp(d, a + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc, 1u);
+                        }
+                        mma_commit_warp(smem_u32(&ms.pv_done[G]));
+                        ++n_p[G];
                     }
-                    mma_commit_warp(smem_u32(&ms.pv_grp[g & 1]));
+                    if (!ok) break;
                     mma_commit_warp(smem_u32(&ms.v_empty[slot]));
                 }
-                if (!ok) break;
-                mma_commit_warp(smem_u32(&ms.unit_done));
             }
             mma_commit_warp(smem_u32(&ms.drain[1]));
             if (lane == 0) mbar_wait_drain_1(smem_u32(&ms.drain[1]), 0, err, kCacheWaitNs);
@@ -384,56 +424,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         }
     } else if (warp < 8) {
         // ============================================================ convert
-        // Thread = key row of the step's tile; warps 4, 5 the first page, warps
-        // 6, 7 the second.  A raw slot may pass from one pair to the other: a
-        // pair is at most kKStages steps ahead (K tiles wait for Q K^T, which
-        // waits for both pairs), so with kRawPages >= 2 * kKStages + 2 the
-        // slot's former phase has completed before the next is waited for.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
-        const int row = (warp - 4) * 32 + lane;
-        const int which = row >> 6, slot_row = row & 63;
+        const int th = threadIdx.x - 128, key = th >> 1, h = th & 1;  // two threads a key of a page
         uint32_t j = 0, g = 0;
         bool ok = true;
         for (Segment sg; ok && walk.next(p, sg);) {
             for (int i = sg.first; i < sg.last && ok; i += 2, ++g) {
                 const int held = min(2, sg.last - i);
-                const bool mine = which < held;
-                const uint32_t page = j + which;
-                const int rs = page % kRawPages;
-                const unsigned char* raw = smem + Sm::kOffRaw + rs * L::kBytes;
-                if (mine)
-                    ok = mbar_wait_bounded(smem_u32(&ms.raw_full[rs]), (page / kRawPages) & 1, abort_flag, err,
-                                           kCacheWaitNs);
-                if (!ok) break;
-                const int2 k0 = ms.key0[g % kMetaSteps];
-                const int key0 = which ? k0.y : k0.x;
-                const bool none = key0 == kNoKey;  // passed over: no key counts, V rows of zeros
-                const int ks = g % kKStages, vs = g % kVStages;
-                if (g >= (uint32_t)kKStages)
-                    ok = mbar_wait_bounded(smem_u32(&ms.k_empty[ks]), (g / kKStages + 1) & 1, abort_flag, err,
-                                           kCacheWaitNs);
-                if (!ok) break;
-                if (mine && !none)
-                    convert_row<kD>(raw + slot_row * L::kRow, raw + L::kKScale + slot_row * L::kGroups, row, false,
-                                    smem + Sm::kOffK + ks * Sm::kTile);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms.k_full[ks]));
-                if (g >= (uint32_t)kVStages)
-                    ok = mbar_wait_bounded(smem_u32(&ms.v_empty[vs]), (g / kVStages + 1) & 1, abort_flag, err,
-                                           kCacheWaitNs);
-                if (!ok) break;
-                // Slots past the sequence's end hold anything: their V is zero.
-                if (mine)
-                    convert_row<kD>(raw + L::kV + slot_row * L::kRow, raw + L::kVScale + slot_row * L::kGroups, row,
-                                    none || key0 + slot_row >= sg.len.kv, smem + Sm::kOffV + vs * Sm::kTile);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&ms.v_full[vs]));
-                    if (mine) mbar_arrive(smem_u32(&ms.raw_empty[rs]));
+#pragma unroll 1
+                for (int side = 0; side < 2; ++side) {
+                    const int stages = side ? Sm::kVStages : Sm::kKStages, st = g % stages;
+                    const uint32_t full = smem_u32(side ? &ms.v_full[st] : &ms.k_full[st]);
+                    const uint32_t empty = smem_u32(side ? &ms.v_empty[st] : &ms.k_empty[st]);
+                    const uint32_t tile = sbase + (side ? Sm::kOffV : Sm::kOffK) + st * Sm::kTile;
+                    if (g >= (uint32_t)stages)
+                        ok = mbar_wait_bounded(empty, (g / stages + 1) & 1, abort_flag, err, kCacheWaitNs);
+#pragma unroll 1
+                    for (int which = 0; which < held && ok; ++which, ++j) {
+                        const int slot = j % Sm::kRaw;
+                        ok = mbar_wait_bounded(smem_u32(&ms.raw_full[slot]), (j / Sm::kRaw) & 1, abort_flag, err,
+                                               kCacheWaitNs);
+                        if (!ok) break;
+                        const int2 k0 = ms.key0[g % kMetaSteps];
+                        const int key0 = which ? k0.y : k0.x;
+                        // Slots past the sequence's end hold anything, and a page
+                        // passed over nothing: their V is zero (K is masked).
+                        const bool zero = side && (key0 == kNoKey || key0 + key >= sg.len.kv);
+                        const uint32_t raw = sbase + Sm::kOffRaw + slot * Sm::kRawBytes;
+                        convert_half_row<kD, kQ>(raw + key * (kD / 2), raw + Sm::kCodes + key * (kD / 16),
+                                                 which * kPageTokens + key, h, zero, tile);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&ms.raw_empty[slot]));
+                    }
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full);
                 }
-                j += held;
             }
         }
     } else {
@@ -443,11 +470,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t o_mine = t_lane + (G ? kTmemO1 : kTmemO0);
-        constexpr int dh = kD / 2;  // output columns of this thread: [G * dh, G * dh + dh)
+        const uint32_t s_mine = t_lane + kTmemS + G * kTmemGroup, o_mine = t_lane + kTmemO + G * kTmemGroup;
+        const int tile = kQ == 2 ? G : 0;
+        const uint32_t q_tile = sbase + Sm::kOffQ + tile * Sm::kTile;
         const float ninf = -INFINITY;
         bool ok = true;
-        uint32_t g0 = 0, ul = 0;  // steps before the unit, units
+        uint32_t g0 = 0, n = 0, units = 0;  // steps before the unit; steps and units of this group
         SoftWalk& sw = ms.soft[warp - 8];
         auto advance = [&](int to) -> bool {  // the walk's next unit into sw.unit[to]
             Walk w = sw.walk;
@@ -464,43 +492,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         if (lane == 0) sw.walk = walk;
         __syncwarp();
         bool more = advance(0);
-        if (G == 0 && more) {
-            ms.scale[0][r] = stage_query<kD>(p, sw.unit[0], r, t_lane);
-            tc_fence_before();
+        float next_c2 = 0.f;
+        auto stage = [&](int of) {  // the queries of sw.unit[of]
+            const Segment& s = sw.unit[of];
+            if (tile >= groups_of<kQ>(p, s)) return;
+            next_c2 = stage_query<kD, kQ>(p, s, s.t * (kQ * 128) + tile * 128 + r, r, q_tile);
+            if (kQ == 1) ms.scale[of][r] = next_c2;
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ms.q_full));
-        }
+            if (lane == 0) mbar_arrive(smem_u32(&ms.q_full[tile]));
+        };
+        if (more && (kQ == 2 || G == 0)) stage(0);
 #pragma unroll 1
-        for (; more; ++ul) {
+        for (uint32_t ul = 0; more; ++ul) {
             const bool next = advance((ul + 1) & 1);
             const Segment& sg = sw.unit[ul & 1];
             const int nst = steps_of(sg);
-            const int row = sg.t * 128 + r;
+            const bool mine = tile < groups_of<kQ>(p, sg);
+            const int row = sg.t * (kQ * 128) + tile * 128 + r;
             const int live_rows = sg.len.q * p.group;
             int lim = sg.len.kv;  // first key the row does not see
             if (p.causal && row < live_rows) lim = max(0, min(lim, sg.len.kv - sg.len.q + row / p.group + 1));
-            // The group that takes the next unit's first step stages its queries.
-            const bool stager = next && ((g0 + nst) & 1) == (uint32_t)G;
-            float c2 = 0.f, m = ninf, l = 0.f;
+            float c2 = next_c2, m = ninf, l = 0.f;
             bool first = true;
 #pragma unroll 1
-            for (int t = (int)((g0 + G) & 1); t < nst; t += 2) {
-                const uint32_t gs = g0 + t;
-                if (ok) ok = mbar_wait_bounded(smem_u32(&ms.s_full[G]), (gs >> 1) & 1, abort_flag, err, kCacheWaitNs);
+            for (int t = kQ == 1 ? (int)((g0 + G) & 1) : 0; t < nst && mine; t += kQ == 1 ? 2 : 1, ++n) {
+                if (ok) ok = mbar_wait_bounded(smem_u32(&ms.s_full[G]), n & 1, abort_flag, err, kCacheWaitNs);
                 tc_fence_after();
-                c2 = ms.scale[ul & 1][r];
-                const int2 k0 = ms.key0[gs % kMetaSteps];
+                if (kQ == 1) c2 = ms.scale[ul & 1][r];
+                const int2 k0 = ms.key0[(g0 + t) % kMetaSteps];
                 // Keys of the two pages that this row sees (none where no page is).
                 const int va = lim - k0.x, vb = lim - k0.y;
                 float x[128];
 #pragma unroll
-                for (int c = 0; c < 128; c += 32)
-                    tmem_ld32(t_lane + kTmemS + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
+                for (int c = 0; c < 128; c += 32) tmem_ld32(s_mine + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
                 tmem_wait_ld();
-                // S is in registers: its columns may take the next step's.
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms.s_free));
                 if (__any_sync(0xffffffffu, va < kPageTokens || vb < kPageTokens)) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) {
@@ -517,24 +542,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                     l *= alpha;
                 }
                 const float mb = m == ninf ? 0.f : m;
-                uint32_t pk[64];
-                chunk_exp64(x, c2, mb, pk, l);
-                chunk_exp64(x + 64, c2, mb, pk + 32, l);
-                // P V of the step before (the other group's) has read P.
-                if (gs > 0 && ok)
-                    ok = mbar_wait_bounded(smem_u32(&ms.pv_grp[G ^ 1]), ((gs - 1) >> 1) & 1, abort_flag, err,
-                                           kCacheWaitNs);
-                tc_fence_after();
-                if (ok) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 16)
-                        tmem_st16(t_lane + kTmemP + c, *reinterpret_cast<uint32_t(*)[16]>(&pk[c]));
-                }
-                if (ok && !first && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    // The last P V into this group's O has completed.
-                    ok = mbar_wait_bounded(smem_u32(&ms.pv_grp[G]), ((gs - 2) >> 1) & 1, abort_flag, err,
-                                           kCacheWaitNs);
-                    tc_fence_after();
+                if (!first && ok && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // (The group's last P V has completed: this S was written after it.)
 #pragma unroll 1
                     for (int c0 = 0; c0 < kD; c0 += 32) {
                         uint32_t o[32];
@@ -545,72 +554,86 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                         tmem_st32(o_mine + c0, o);
                     }
                 }
+                uint32_t pk[64];
+                chunk_exp64(x, c2, mb, pk, l);
+                chunk_exp64(x + 64, c2, mb, pk + 32, l);
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 16)
+                        tmem_st16(s_mine + c, *reinterpret_cast<uint32_t(*)[16]>(&pk[c]));
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms.p_full));
+                if (lane == 0) mbar_arrive(smem_u32(&ms.p_full[G]));
                 first = false;
             }
-            if (stager) {
-                // The unit's Q K^T have completed: Q may be overwritten.
-                if (ok) ok = mbar_wait_bounded(smem_u32(&ms.q_empty), ul & 1, abort_flag, err, kCacheWaitNs);
-                if (ok) {
-                    tc_fence_after();
-                    ms.scale[(ul + 1) & 1][r] = stage_query<kD>(p, sw.unit[(ul + 1) & 1], r, t_lane);
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms.q_full));
+            // The next unit's queries, once this one's Q K^T have completed.
+            if (mine && (kQ == 2 || ((g0 + nst) & 1) == (uint32_t)G)) {
+                if (ok && next)
+                    ok = mbar_wait_bounded(smem_u32(&ms.q_empty[tile]), units & 1, abort_flag, err, kCacheWaitNs);
             }
+            if (mine) ++units;
+            if (next && ok && (kQ == 2 || ((g0 + nst) & 1) == (uint32_t)G)) stage((ul + 1) & 1);
             // ------------------------------------------------ unit epilogue
-            //   m = max(m_0, m_1), a_k = 2^(m_k - m), l = a_0 l_0 + a_1 l_1, O = a_0 O_0 + a_1 O_1
-            ms.xm[ul & 1][G][r] = m;
-            ms.xl[ul & 1][G][r] = l;
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-            // The group of the unit's even steps comes first, whatever it is:
-            // the sums do not depend on what the CTA did before the unit.
-            const int ge = (int)(g0 & 1u);
-            const float m_e = ms.xm[ul & 1][ge][r], l_e = ms.xl[ul & 1][ge][r];
-            const float m_o = ms.xm[ul & 1][ge ^ 1][r], l_o = ms.xl[ul & 1][ge ^ 1][r];
-            const float mt = fmaxf(m_e, m_o);
-            float a_e = m_e == ninf ? 0.f : ex2_approx(m_e - mt);
-            float a_o = m_o == ninf ? 0.f : ex2_approx(m_o - mt);
-            const float lt = __fmaf_rn(a_e, l_e, __fmul_rn(a_o, l_o));
-            const uint32_t o_e = ge ? kTmemO1 : kTmemO0, o_o = ge ? kTmemO0 : kTmemO1;
-            const bool has_e = nst > 0, has_o = nst > 1;  // a group without a step holds no O of the unit
-            const bool real = ok && row < p.Sq * p.group;
+            float a_e = 1.f, a_o = 0.f, mt = m, lt = l;
+            const uint32_t ge = kQ == 1 ? (g0 & 1u) : G;  // the group of the unit's even steps comes first
+            bool has_e = nst > 0, has_o = false;          // a group without a step holds no O of the unit
+            if (kQ == 1) {
+                //   m = max(m_0, m_1), a_k = 2^(m_k - m), l = a_0 l_0 + a_1 l_1, O = a_0 O_0 + a_1 O_1
+                ms.xm[G][r] = m;
+                ms.xl[G][r] = l;
+                // This group's O is complete before the other reads its half of it.
+                if (n > 0 && ok)
+                    ok = mbar_wait_bounded(smem_u32(&ms.pv_done[G]), (n - 1) & 1, abort_flag, err, kCacheWaitNs);
+                tc_fence_before();
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                tc_fence_after();
+                const float m_e = ms.xm[ge][r], l_e = ms.xl[ge][r], m_o = ms.xm[ge ^ 1][r], l_o = ms.xl[ge ^ 1][r];
+                mt = fmaxf(m_e, m_o);
+                a_e = m_e == ninf ? 0.f : ex2_approx(m_e - mt);
+                a_o = m_o == ninf ? 0.f : ex2_approx(m_o - mt);
+                lt = __fmaf_rn(a_e, l_e, __fmul_rn(a_o, l_o));
+                has_o = nst > 1;
+            } else if (n > 0 && mine && ok) {
+                ok = mbar_wait_bounded(smem_u32(&ms.pv_done[G]), (n - 1) & 1, abort_flag, err, kCacheWaitNs);
+                tc_fence_after();
+            }
+            const bool real = ok && mine && row < p.Sq * p.group;
             const int qi = real ? row / p.group : 0;
             const int head = sg.h * p.group + (real ? row - qi * p.group : 0);
-            const bool live = row < live_rows && lt != 0.f;
-            const size_t part = (2 * (size_t)blockIdx.x + (sg.first > 0 ? 0 : 1)) * 128 + r;
-            if (sg.whole) {
+            const bool live = row < live_rows && lt != 0.f, whole = sg.whole;
+            const size_t part = (2 * (size_t)blockIdx.x + (sg.first > 0 ? 0 : 1)) * (kQ * 128) + tile * 128 + r;
+            if (whole) {
                 const float inv =
                     live ? (p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + sg.h) : 1.f) / lt : 0.f;
                 a_e *= inv;
                 a_o *= inv;
             }
-            if (ok) ok = mbar_wait_bounded(smem_u32(&ms.unit_done), ul & 1, abort_flag, err, kCacheWaitNs);
-            tc_fence_after();
-            uint4* dst = p.out + (((size_t)sg.b * p.Sq + qi) * p.heads + head) * (kD / 8) + G * (dh / 8);
-            float4* dst_part = reinterpret_cast<float4*>(p.part_o + part * kD + G * dh);
+            // kQ = 1: the groups write half of the columns each.
+            const int col0 = kQ == 1 ? G * (kD / 2) : 0, cols = kQ == 1 ? kD / 2 : kD;
+            uint4* dst = p.out + (((size_t)sg.b * p.Sq + qi) * p.heads + head) * (kD / 8) + col0 / 8;
+            float4* dst_part = reinterpret_cast<float4*>(p.part_o + part * kD + col0);
 #pragma unroll 1
-            for (int c0 = 0; c0 < dh; c0 += 32) {
+            for (int c0 = 0; c0 < (mine ? cols : 0); c0 += 32) {
                 uint32_t oa[32], ob[32];
-                tmem_ld32(t_lane + o_e + G * dh + c0, oa);
-                tmem_ld32(t_lane + o_o + G * dh + c0, ob);
+                tmem_ld32(t_lane + kTmemO + ge * kTmemGroup + col0 + c0, oa);
+                if (kQ == 1) tmem_ld32(t_lane + kTmemO + (ge ^ 1) * kTmemGroup + col0 + c0, ob);
                 tmem_wait_ld();
                 float f[32];
 #pragma unroll
-                for (int q = 0; q < 32; ++q)
-                    f[q] = __fmaf_rn(a_e, has_e ? __uint_as_float(oa[q]) : 0.f,
-                                     __fmul_rn(a_o, has_o ? __uint_as_float(ob[q]) : 0.f));
+                for (int q = 0; q < 32; ++q) {
+                    const float e = has_e ? __uint_as_float(oa[q]) : 0.f;
+                    f[q] = kQ == 1 ? __fmaf_rn(a_e, e, __fmul_rn(a_o, has_o ? __uint_as_float(ob[q]) : 0.f)) : a_e * e;
+                }
                 if (!real || !ok) continue;
-                if (sg.whole) {
+                if (whole) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) w[q] = live ? pack_bf16x2(f[8 * v + 2 * q], f[8 * v + 2 * q + 1]) : 0u;
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = live ? pack_bf16x2(f[8 * v + 2 * q], f[8 * v + 2 * q + 1]) : 0u;
                         __stcs(dst + c0 / 8 + v, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 } else {
@@ -619,12 +642,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                         dst_part[c0 / 4 + v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
                 }
             }
-            // O_0 and O_1 have been read: the next unit may start them over.
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ms.o_free));
-            if (real && ok && G == 0) {
-                if (!sg.whole)
+            if (kQ == 1) {
+                // Both groups have read O_0 and O_1 (and the exchanged statistics):
+                // the next unit's steps, which either announces after this, may start.
+                tc_fence_before();
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                tc_fence_after();
+            }
+            if (real && ok && (kQ == 2 || G == 0)) {
+                if (!whole)
                     p.part_ml[part] = make_float2(mt, lt);
                 else if (p.lse)
                     p.lse[((size_t)sg.b * p.heads + head) * p.Sq + qi] =
@@ -644,25 +670,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
 
 }  // namespace
 
-template <int kD>
-static cudaError_t launch_chunk_d(const AttnParams& p, cudaStream_t stream) {
+template <int kD, int kQ>
+static cudaError_t launch_chunk_as(const AttnParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     // The register split draws on the launch's 128 registers a thread; with
     // fewer, setmaxnreg would wait forever, so such a build is refused.
     static const int regs = [] {
         cudaFuncAttributes fa;
-        return cudaFuncGetAttributes(&fa, chunk_kernel<kD>) == cudaSuccess ? fa.numRegs : 0;
+        return cudaFuncGetAttributes(&fa, chunk_kernel<kD, kQ>) == cudaSuccess ? fa.numRegs : 0;
     }();
     if (regs != 128) return cudaErrorInvalidKernelImage;
-    const cudaError_t e = allow_smem(chunk_kernel<kD>, chunk_smem<kD>(), done);
+    const cudaError_t e = allow_smem(chunk_kernel<kD, kQ>, chunk_smem<kD, kQ>(), done);
     if (e != cudaSuccess) return e;
-    chunk_kernel<kD><<<p.grid, kChunkThreads, chunk_smem<kD>(), stream>>>(p);
+    chunk_kernel<kD, kQ><<<p.grid, kChunkThreads, chunk_smem<kD, kQ>(), stream>>>(p);
     note_launches(1);
     return cudaGetLastError();
 }
 
 cudaError_t launch_chunk(const AttnParams& p, int D, cudaStream_t stream) {
-    return D == 64 ? launch_chunk_d<64>(p, stream) : launch_chunk_d<128>(p, stream);
+    if (p.tile == 256) return D == 64 ? launch_chunk_as<64, 2>(p, stream) : launch_chunk_as<128, 2>(p, stream);
+    return D == 64 ? launch_chunk_as<64, 1>(p, stream) : launch_chunk_as<128, 1>(p, stream);
 }
 
 }  // namespace vsa
