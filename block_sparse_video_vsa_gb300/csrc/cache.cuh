@@ -113,6 +113,30 @@ __device__ __forceinline__ int q_exponent(float amax) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
 
+// Bounded wait of a whole warp for a phase of a barrier.  Between looks the warp
+// sleeps kSleep ns: waiting roles share their scheduler with working ones, and
+// looks without a pause were 45% of all instructions of the chunk kernel.
+template <int kSleep>
+__device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* err) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (kSleep > 0) __nanosleep(kSleep);
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (i % 64 != 0) continue;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, now - t0 > 2000000000ull)) {  // 2 s
+            *abort = 1;
+            if ((threadIdx.x & 31) == 0) atomicOr(err, VSA_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+constexpr int kSleepShort = 20, kSleepLong = 100;
+
 // Untiled bulk copy into shared memory (16-byte aligned, a multiple of 16 bytes), completing on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),

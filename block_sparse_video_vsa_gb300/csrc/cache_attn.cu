@@ -299,8 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
             const int slot = j % kOwn;
             const int half = pc & 1;
             if (!half || pc == piece_begin) {
-                ok = mbar_wait_bounded(smem_u32(&sm.full[warp][slot]), (j / kOwn) & 1, abort_flag, p.c.err,
-                                       kCacheWaitNs);
+                ok = cache_wait<kSleepShort>(smem_u32(&sm.full[warp][slot]), (j / kOwn) & 1, abort_flag, p.c.err);
                 if (!ok) break;
             }
             const bool page_end = half || pc + 1 == piece_end;  // done with the page after this piece
@@ -738,7 +737,7 @@ cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
 constexpr int kTokenUnitCost = 1, kChunkUnitCost = 6;
 
 // Rows of a unit: up to 16 rows a kv head go to token_kernel, more to chunk_kernel.
-int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256; }
+int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
 
 }  // namespace
 

@@ -1,26 +1,21 @@
 // Attention over the 4-bit paged cache, many query rows a kv head (chunks of
 // tokens): the same function as token_kernel (cache_attn.cu), on tcgen05.
 //
-// Tensor bound for long chunks (4 * D flops for each row and key).  A unit is
-// kQ tiles of 128 query rows, one TMEM lane each; a step is 128 keys (two
-// pages).  What stands between the cache and the tensor core is the conversion
-// of codes to fp16 operands, about 1.5 instructions an element and as many
-// bytes of shared-memory writes as the tensor core reads, so it is shared by
-// as many rows as TMEM has room for:
-//  * kQ = 2 (more than 128 rows): each softmax group has a tile of its own and
-//    takes every step; K and V are converted once for 256 rows.
-//  * kQ = 1: both groups have the same rows and take the steps in turn, each
-//    with a maximum, sum and output of its own, joined at the unit's end.
-// A producer warp copies pages (halves: K and V with their scales) into a
-// ring; a warpgroup converts them (exact, see cache.cuh) to K and V tiles in
-// the 128-byte swizzled layout the tensor core reads.  A page crosses HBM and
-// L2 in 9 bits a pair of K and V elements instead of 32.
-//  * Warp roles (512 threads): warp 0 looks pages up and copies them; warp 1
-//    owns TMEM and issues Q K^T, warp 3 P V; warps 4..7 convert; warps 8..11
-//    and 12..15 are the softmax groups.
-//  * TMEM (512 columns): S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1
-//    [384,512).  P (fp16 pairs) takes the first 64 columns of its S once the
-//    softmax has loaded that; Q is in shared memory.
+// Tensor bound for long chunks (4 * D flops for each row and key), so the
+// structure is the fine stage's: 128 query rows a unit, one TMEM lane each,
+// 128 keys (two pages) a step, Q and P as A operands in TMEM, two softmax
+// groups that take the steps in turn with a maximum, sum and output of their
+// own, joined at the unit's end.  What differs is where K and V come from: two
+// producer warps copy pages (halves: codes and scales of K or of V) into rings,
+// and two warpgroups, one for K and one for V, convert each step's two pages
+// into fp16 tiles (exact, see cache.cuh) in the 128-byte swizzled layout the
+// tensor core reads.  So a page crosses HBM and L2 in 9 bits a pair of K and V
+// elements instead of 32.
+//  * Warp roles (640 threads): warps 0 and 2 copy pages; warp 1 owns TMEM and
+//    issues Q K^T, warp 3 P V; warps 4..7 convert K, warps 8..11 V; warps
+//    12..15 and 16..19 are the softmax groups (group 0 the CTA's even steps).
+//  * TMEM (512 columns): S [0,128); P (fp16 pairs) [128,192); Q [192,256);
+//    O_0 [256,384); O_1 [384,512).
 //  * A query row is scaled by a power of two on its way to fp16 (its bf16
 //    values keep all their bits) and the inverse joins its softmax scale.
 //  * Every wait is bounded; one that runs out raises the CTA's abort flag and
@@ -31,28 +26,26 @@ namespace vsa {
 
 namespace {
 
-constexpr int kChunkThreads = 512;
+constexpr int kChunkThreads = 640;
+constexpr int kKStages = 2, kVStages = 3;
 constexpr int kMetaSteps = 16;
-// Registers: 4 warpgroups launched with 128 each; the shares add up to 512.
-constexpr int kIssueRegs = 64, kConvertRegs = 80, kSoftRegs = 184;
-static_assert(kIssueRegs + kConvertRegs + 2 * kSoftRegs <= 512, "register split exceeds the launch");
+constexpr int kRawHalves = 4;  // slots of a ring of half pages
+// Registers: 5 warpgroups launched with 96 each; the shares add up to 480.
+constexpr int kLaunchRegs = 96, kIssueRegs = 48, kConvertRegs = 56, kSoftRegs = 160;
+static_assert(kIssueRegs + 2 * kConvertRegs + 2 * kSoftRegs <= 5 * kLaunchRegs, "register split exceeds the launch");
 
-constexpr int kTmemS = 0, kTmemO = 256, kTmemGroup = 128;  // of group G: + G * kTmemGroup
+constexpr int kTmemS = 0, kTmemP = 128, kTmemQ = 192, kTmemO0 = 256, kTmemO1 = 384;
 
-template <int kD, int kQ>
+template <int kD>
 struct ChunkSmem {
-    static constexpr int kKStages = 2;
-    static constexpr int kVStages = kD == 128 && kQ == 2 ? 2 : 3;
-    static constexpr int kRaw = kD == 128 ? 6 : 12;  // half pages
-    static constexpr int kHalf = 128 * 128;          // 128 rows x 64 channels of fp16, swizzled
-    static constexpr int kTile = kHalf * (kD / 64);  // Q of a tile, K or V of a step
+    static constexpr int kHalf = 128 * 128;          // 128 keys x 64 channels of fp16, swizzled
+    static constexpr int kTile = kHalf * (kD / 64);  // K or V of a step
     static constexpr int kCodes = kPageTokens * kD / 2, kScales = kPageTokens * kD / 16;
     static constexpr int kRawBytes = kCodes + kScales;
-    static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kQ * kTile;
+    static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kKStages * kTile;
-    static constexpr int kOffRaw = kOffV + kVStages * kTile;
-    static constexpr int kOffMisc = kOffRaw + kRaw * kRawBytes;
+    static constexpr int kOffRaw = kOffV + kVStages * kTile;  // [K, V][slot]
+    static constexpr int kOffMisc = kOffRaw + 2 * kRawHalves * kRawBytes;
 };
 
 // A softmax warp's walk and its present and next unit: kept in shared memory,
@@ -63,17 +56,22 @@ struct SoftWalk {
 };
 
 struct __align__(16) ChunkMisc {
-    uint64_t raw_full[12], raw_empty[12];
-    uint64_t k_full[2], k_empty[2];
-    uint64_t v_full[3], v_empty[3];
-    // Per softmax group: S of its next step is ready; P of it (and any
-    // rescaling of O) is in TMEM; P V has completed (S may be overwritten).
-    uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t q_full[2], q_empty[2];  // per tile
+    uint64_t raw_full[2][kRawHalves], raw_empty[2][kRawHalves];  // of K, of V
+    uint64_t k_full[kKStages], k_empty[kKStages];
+    uint64_t v_full[kVStages], v_empty[kVStages];
+    uint64_t s_full[2];  // per softmax group: S of its next step is ready
+    uint64_t s_free;     // S has been loaded into registers
+    uint64_t p_full;     // P of the step (and any rescaling of O) is in TMEM
+    uint64_t pv_grp[2];  // per group: P V of its step has completed
+    uint64_t unit_done;  // every P V of the unit has completed
+    uint64_t q_full, q_empty;
+    uint64_t o_free;     // O_0 and O_1 have been read by the unit's epilogue
     uint64_t drain[2];
-    int2 key0[kMetaSteps];  // first key of a step's pages (kNoKey: none)
-    float xm[2][128], xl[2][128];  // kQ = 1: the groups' maxima and sums at the unit's end
-    float scale[2][128];           // kQ = 1: [unit parity][row]: logit -> log2 units
+    int2 key0[kMetaSteps];   // first key of a step's pages (kNoKey: none)
+    int raw_keys[2][kRawHalves];  // keys of a half page's slots that the sequence has (0: passed over)
+    float xm[2][2][128];     // [unit parity][group][row]: maximum, sum at the unit's end
+    float xl[2][2][128];
+    float scale[2][128];     // [unit parity][row]: logit -> log2 units
     SoftWalk soft[8];
     PlanScratch plan;
     uint32_t tmem_base;
@@ -81,11 +79,11 @@ struct __align__(16) ChunkMisc {
 };
 constexpr int kNoKey = 0x7FFFFFFF;  // beyond every row's limit
 
-template <int kD, int kQ>
+template <int kD>
 constexpr int chunk_smem() {
-    return ChunkSmem<kD, kQ>::kOffMisc + (int)sizeof(ChunkMisc) + 1024;  // slack for 1024-byte alignment
+    return ChunkSmem<kD>::kOffMisc + (int)sizeof(ChunkMisc) + 1024;  // slack for 1024-byte alignment
 }
-static_assert(chunk_smem<128, 1>() <= 232448 && chunk_smem<128, 2>() <= 232448, "shared memory of the chunk kernel");
+static_assert(chunk_smem<128>() <= 232448, "shared memory of the chunk kernel");
 
 // As idesc_bf16_f32, fp16 inputs.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
@@ -126,20 +124,12 @@ __device__ __forceinline__ void chunk_exp64(const float* x, float c2, float mb, 
 
 __device__ __forceinline__ int steps_of(const Segment& s) { return (s.last - s.first + 1) >> 1; }
 
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-    uint4 x;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
-    return x;
-}
-__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// Softmax thread of row r of a tile: puts query row `row` of unit s into the
-// tile's Q as fp16, scaled by a power of two, and returns the row's factor from
-// logits to log2 units.
-template <int kD, int kQ>
-__device__ __forceinline__ float stage_query(const AttnParams& p, const Segment& s, int row, int r, uint32_t tile) {
+// Softmax thread of row r: puts its query row of unit s into the TMEM Q
+// columns of its lane as fp16, scaled by a power of two, and returns the row's
+// factor from logits to log2 units.
+template <int kD>
+__device__ __forceinline__ float stage_query(const AttnParams& p, const Segment& s, int r, uint32_t t_lane) {
+    const int row = s.t * 128 + r;
     const bool real = row < p.Sq * p.group;
     const int qi = real ? row / p.group : 0;
     const int head = s.h * p.group + (real ? row - qi * p.group : 0);
@@ -156,14 +146,20 @@ __device__ __forceinline__ float stage_query(const AttnParams& p, const Segment&
     const int e = q_exponent(amax);
     const float f = pow2i(e);
 #pragma unroll
-    for (int i = 0; i < kD / 8; ++i) {
-        uint32_t y[4];
+    for (int i = 0; i < kD / 2; ++i) w[i] = pack_f16x2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = pack_f16x2(bf16_lo(w[4 * i + j]) * f, bf16_hi(w[4 * i + j]) * f);
-        sts128(tile + (i >> 3) * ChunkSmem<kD, kQ>::kHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-    }
-    fence_proxy_async_smem();
+    for (int c0 = 0; c0 < kD / 2; c0 += 32) tmem_st32(t_lane + kTmemQ + c0, *reinterpret_cast<uint32_t(*)[32]>(&w[c0]));
+    tmem_wait_st();
     return p.scale_log2 * (p.c.kv_scale ? __ldg(p.c.kv_scale + s.h) : 1.f) * pow2i(-e);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+    return x;
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // Half of one key's codes of K or V and their scales (`codes`, `scales`: the
@@ -171,7 +167,7 @@ __device__ __forceinline__ float stage_query(const AttnParams& p, const Segment&
 // (h + 1) kD / 2).  Two threads a key, neighbouring lanes, each starting at
 // another 16-byte piece (kD = 128) so that neither the loads nor the swizzled
 // stores of 8 lanes meet in a bank.
-template <int kD, int kQ>
+template <int kD>
 __device__ __forceinline__ void convert_half_row(uint32_t codes, uint32_t scales, int row, int h, bool zero,
                                                  uint32_t tile) {
     constexpr int kPieces = kD / 64;  // of 32 channels
@@ -187,7 +183,7 @@ __device__ __forceinline__ void convert_half_row(uint32_t codes, uint32_t scales
             asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc) : "r"(scales + h * 2));
     }
     // Unit u of 16 bytes (8 channels) of a 64-channel half goes to u ^ (row & 7).
-    const uint32_t base = tile + row * 128 + (kD == 128 ? h * ChunkSmem<kD, kQ>::kHalf : 0);
+    const uint32_t base = tile + row * 128 + (kD == 128 ? h * ChunkSmem<kD>::kHalf : 0);
     const uint32_t low = (row & 3) << 4, top = (row & 4) << 4;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
@@ -207,16 +203,25 @@ __device__ __forceinline__ void convert_half_row(uint32_t codes, uint32_t scales
     }
 }
 
-// Groups with rows of a unit.
-template <int kQ>
-__device__ __forceinline__ int groups_of(const AttnParams& p, const Segment& s) {
-    return kQ == 2 && s.t * 256 + 128 < p.Sq * p.group ? 2 : 1;
-}
+// A place in a ring of kN slots: the slot and how many times the ring has been gone round.
+template <int kN>
+struct Ring {
+    int slot = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void step() {
+        if (++slot == kN) {
+            slot = 0;
+            ++turn;
+        }
+    }
+    __device__ __forceinline__ uint32_t full() const { return turn & 1; }         // parity of the slot's next filling
+    __device__ __forceinline__ uint32_t empty() const { return (turn + 1) & 1; }  // and of its last emptying (turn > 0)
+};
 
-template <int kD, int kQ>
+template <int kD>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
     using L = PageLayout<kD>;
-    using Sm = ChunkSmem<kD, kQ>;
+    using Sm = ChunkSmem<kD>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     ChunkMisc& ms = *reinterpret_cast<ChunkMisc*>(smem + Sm::kOffMisc);
@@ -226,34 +231,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
     unsigned int* err = p.c.err;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Sm::kRaw; ++s) {
-            mbar_init(smem_u32(&ms.raw_full[s]), 1);
-            mbar_init(smem_u32(&ms.raw_empty[s]), 4);
+        for (int s = 0; s < 2 * kRawHalves; ++s) {
+            mbar_init(smem_u32(&ms.raw_full[0][s]), 1);
+            mbar_init(smem_u32(&ms.raw_empty[0][s]), 4);
         }
-        for (int s = 0; s < Sm::kKStages; ++s) {
+        for (int s = 0; s < kKStages; ++s) {
             mbar_init(smem_u32(&ms.k_full[s]), 4);
             mbar_init(smem_u32(&ms.k_empty[s]), 1);
         }
-        for (int s = 0; s < Sm::kVStages; ++s) {
+        for (int s = 0; s < kVStages; ++s) {
             mbar_init(smem_u32(&ms.v_full[s]), 4);
             mbar_init(smem_u32(&ms.v_empty[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&ms.s_full[s]), 1);
-            mbar_init(smem_u32(&ms.p_full[s]), 4);
-            mbar_init(smem_u32(&ms.pv_done[s]), 1);
-            mbar_init(smem_u32(&ms.q_full[s]), 4);
-            mbar_init(smem_u32(&ms.q_empty[s]), 1);
+            mbar_init(smem_u32(&ms.pv_grp[s]), 1);
             mbar_init(smem_u32(&ms.drain[s]), 1);
         }
+        mbar_init(smem_u32(&ms.s_free), 4);
+        mbar_init(smem_u32(&ms.p_full), 4);
+        mbar_init(smem_u32(&ms.unit_done), 1);
+        mbar_init(smem_u32(&ms.q_full), 4);
+        mbar_init(smem_u32(&ms.q_empty), 1);
+        mbar_init(smem_u32(&ms.o_free), 8);
         ms.abort_flag = 0;
         fence_barrier_init();
     }
     // The tiles start as zeros: the tensor core multiplies rows that no page
     // filled (an odd last page, pages passed over) by probabilities of zero.
     {
-        int4* z = reinterpret_cast<int4*>(smem + Sm::kOffK);
-        for (int e = threadIdx.x; e < (Sm::kOffRaw - Sm::kOffK) / 16; e += kChunkThreads) z[e] = make_int4(0, 0, 0, 0);
+        int4* z = reinterpret_cast<int4*>(smem);
+        for (int e = threadIdx.x; e < Sm::kOffRaw / 16; e += kChunkThreads) z[e] = make_int4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -270,58 +278,56 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 0) {
-            // ================================================= page producer
-            // Half pages in the order of their conversion: K of the step's
-            // pages, then V of them.
-            uint32_t j = 0, g = 0;  // half pages and steps so far
+        if (warp == 0 || warp == 2) {
+            // ================================ page producers: warp 0 K, warp 2 V
+            const int side = warp >> 1;
+            Ring<kRawHalves> raw;
+            uint32_t g = 0;  // steps so far
             bool ok = true;
             for (Segment sg; ok && walk.next(p, sg);) {
-                const unsigned char* pool = p.c.pool + (size_t)sg.h * L::kBytes;
+                const unsigned char* pool = p.c.pool + (size_t)sg.h * L::kBytes + (side ? L::kV : 0);
                 for (int base = sg.first; base < sg.last && ok; base += 32) {
                     int logical = 0, id = -1;
                     if (base + lane < sg.last) look_up(p, sg, base + lane, logical, id);
-                    const int n = min(32, sg.last - base);  // (32 is even: steps do not straddle)
-                    for (int i = 0; i < n && ok; i += 2, ++g) {
-                        const int held = min(2, n - i);
-                        const int page0 = __shfl_sync(0xffffffffu, id, i);
-                        const int page1 = held == 2 ? __shfl_sync(0xffffffffu, id, i + 1) : -1;
-                        const int num0 = __shfl_sync(0xffffffffu, logical, i);
-                        const int num1 = held == 2 ? __shfl_sync(0xffffffffu, logical, i + 1) : 0;
-                        if (lane == 0)
-                            ms.key0[g % kMetaSteps] = make_int2(page0 < 0 ? kNoKey : num0 * kPageTokens,
-                                                                page1 < 0 ? kNoKey : num1 * kPageTokens);
-                        for (int k = 0; k < 2 * held; ++k, ++j) {
-                            const int side = k >= held;
-                            const int page = (k - side * held) ? page1 : page0;
-                            const int slot = j % Sm::kRaw;
-                            if (j >= (uint32_t)Sm::kRaw) {
-                                ok = mbar_wait_bounded(smem_u32(&ms.raw_empty[slot]), (j / Sm::kRaw + 1) & 1,
-                                                       abort_flag, err, kCacheWaitNs);
-                                if (!ok) break;
-                            }
-                            if (lane == 0) {
-                                const uint32_t bar = smem_u32(&ms.raw_full[slot]);
-                                if (page < 0) {
-                                    mbar_arrive(bar);
-                                } else {
-                                    mbar_arrive_expect_tx(bar, Sm::kRawBytes);
-                                    const uint32_t dst = sbase + Sm::kOffRaw + slot * Sm::kRawBytes;
-                                    const unsigned char* src = pool + (size_t)page * p.c.kv_heads * L::kBytes;
-                                    bulk_load(dst, src + side * L::kV, Sm::kCodes, bar);
-                                    bulk_load(dst + Sm::kCodes, src + (side ? L::kVScale : L::kKScale), Sm::kScales,
-                                              bar);
-                                }
-                            }
-                            __syncwarp();
+                    const int n = min(32, sg.last - base);
+                    for (int i = 0; i < n; ++i, raw.step()) {
+                        const int page = __shfl_sync(0xffffffffu, id, i);
+                        const int first = __shfl_sync(0xffffffffu, logical, i) * kPageTokens;
+                        const int slot = raw.slot;
+                        if (raw.turn > 0) {
+                            ok = cache_wait<kSleepLong>(smem_u32(&ms.raw_empty[side][slot]), raw.empty(), abort_flag, err);
+                            if (!ok) break;
                         }
+                        if (lane == 0) {
+                            if (side == 0) {  // (steps start at even pages of the segment: 32 is even)
+                                int* key0 = &ms.key0[g % kMetaSteps].x;
+                                key0[i & 1] = page < 0 ? kNoKey : first;
+                                if (!(i & 1)) key0[1] = kNoKey;
+                            }
+                            ms.raw_keys[side][slot] = page < 0 ? 0 : sg.len.kv - first;
+                            const uint32_t bar = smem_u32(&ms.raw_full[side][slot]);
+                            if (page < 0) {
+                                mbar_arrive(bar);
+                            } else {
+                                mbar_arrive_expect_tx(bar, Sm::kRawBytes);
+                                const uint32_t dst = sbase + Sm::kOffRaw + (side * kRawHalves + slot) * Sm::kRawBytes;
+                                const unsigned char* src = pool + (size_t)page * p.c.kv_heads * L::kBytes;
+                                bulk_load(dst, src, Sm::kCodes, bar);
+                                bulk_load(dst + Sm::kCodes, src + (side ? L::kVScale - L::kV : L::kKScale), Sm::kScales,
+                                          bar);
+                            }
+                        }
+                        if ((i & 1) || base + i + 1 == sg.last) ++g;
+                        __syncwarp();
                     }
                 }
             }
+            // The last copy into each slot: of this turn up to raw.slot, of the last one from there on.
             if (lane == 0) {
-                for (int s = 0; s < Sm::kRaw && (uint32_t)s < j; ++s) {
-                    const uint32_t last = j - 1 - ((j - 1 - s) % Sm::kRaw);
-                    mbar_wait_drain_1(smem_u32(&ms.raw_full[s]), (last / Sm::kRaw) & 1, err, kCacheWaitNs);
+                for (int s = 0; s < kRawHalves; ++s) {
+                    const uint32_t turns = raw.turn + (s < raw.slot ? 1 : 0);
+                    if (turns > 0)
+                        mbar_wait_drain_1(smem_u32(&ms.raw_full[side][s]), (turns - 1) & 1, err, kCacheWaitNs);
                 }
             }
             __syncwarp();
@@ -329,52 +335,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             // ========================================================= Q K^T
             const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);
             const uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
-            const uint32_t lo_q = (uint32_t)smem_desc_sw128(sbase + Sm::kOffQ, 16, 1024);
             const uint32_t lo_k = (uint32_t)smem_desc_sw128(sbase + Sm::kOffK, 16, 1024);
-            uint32_t g = 0, n_s[2] = {0, 0}, n_q[2] = {0, 0};  // steps; S written, units staged, per group
+            Ring<kKStages> ring;
+            uint32_t g = 0, ul = 0;
             bool ok = true;
-            for (Segment sg; ok && walk.next(p, sg);) {
-                const int nst = steps_of(sg), groups = groups_of<kQ>(p, sg);
-                for (int t = 0; t < nst && ok; ++t, ++g) {
-                    const int slot = g % Sm::kKStages;
-                    ok = mbar_wait_bounded(smem_u32(&ms.k_full[slot]), (g / Sm::kKStages) & 1, abort_flag, err,
-                                           kCacheWaitNs);
-                    const uint32_t b0 = lo_k + ((uint32_t)(slot * Sm::kTile) >> 4);
-#pragma unroll
-                    for (int G = 0; G < 2; ++G) {
-                        if (kQ == 1 ? (g & 1) != (uint32_t)G : G >= groups) continue;
-                        const int tile = kQ == 1 ? 0 : G;
-                        if (t == 0 && ok)
-                            ok = mbar_wait_bounded(smem_u32(&ms.q_full[tile]), n_q[tile] & 1, abort_flag, err,
-                                                   kCacheWaitNs);
-                        if (n_s[G] > 0 && ok)  // P V of the group's last step has read P, which lies in S
-                            ok = mbar_wait_bounded(smem_u32(&ms.pv_done[G]), (n_s[G] - 1) & 1, abort_flag, err,
-                                                   kCacheWaitNs);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t a0 = lo_q + ((uint32_t)(tile * Sm::kTile) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < kD / 16; ++kk) {
-                            const uint32_t step = ((kk >> 2) * Sm::kHalf + (kk & 3) * 32) >> 4;
-                            mma_ss_warp(tmem + kTmemS + G * kTmemGroup, a0 + step, hi, b0 + step, hi, idesc, kk > 0);
-                        }
-                        mma_commit_warp(smem_u32(&ms.s_full[G]));
-                        ++n_s[G];
-                    }
+            for (Segment sg; ok && walk.next(p, sg); ++ul) {
+                const int nst = steps_of(sg);
+                ok = cache_wait<kSleepShort>(smem_u32(&ms.q_full), ul & 1, abort_flag, err);
+                for (int t = 0; t < nst && ok; ++t, ++g, ring.step()) {
+                    if (g >= 1)
+                        ok = cache_wait<kSleepShort>(smem_u32(&ms.s_free), (g - 1) & 1, abort_flag, err);
+                    const int slot = ring.slot;
+                    if (ok)
+                        ok = cache_wait<kSleepShort>(smem_u32(&ms.k_full[slot]), ring.full(), abort_flag, err);
                     if (!ok) break;
+                    const uint32_t b0 = lo_k + ((uint32_t)(slot * Sm::kTile) >> 4);
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kD / 16; ++kk)
+                        mma_ts_warp(tmem + kTmemS, tmem + kTmemQ + kk * 8,
+                                    b0 + (((kk >> 2) * Sm::kHalf + (kk & 3) * 32) >> 4), hi, idesc, kk > 0);
+                    mma_commit_warp(smem_u32(&ms.s_full[g & 1]));
                     mma_commit_warp(smem_u32(&ms.k_empty[slot]));
                 }
                 if (!ok) break;
-#pragma unroll
-                for (int tile = 0; tile < kQ; ++tile) {
-                    if (tile >= groups) continue;
-                    // (A unit without steps has its queries staged all the same.)
-                    if (nst == 0 && ok)
-                        ok = mbar_wait_bounded(smem_u32(&ms.q_full[tile]), n_q[tile] & 1, abort_flag, err,
-                                               kCacheWaitNs);
-                    mma_commit_warp(smem_u32(&ms.q_empty[tile]));
-                    ++n_q[tile];
-                }
+                mma_commit_warp(smem_u32(&ms.q_empty));
             }
             mma_commit_warp(smem_u32(&ms.drain[0]));
             if (lane == 0) mbar_wait_drain_1(smem_u32(&ms.drain[0]), 0, err, kCacheWaitNs);
@@ -384,99 +369,94 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);
             const uint32_t idesc = idesc_f16_f32(128, kD, 0, 1);
             const uint32_t lo_v = (uint32_t)smem_desc_sw128(sbase + Sm::kOffV, Sm::kHalf, 1024);
-            uint32_t g = 0, n_p[2] = {0, 0};
+            Ring<kVStages> ring;
+            uint32_t g = 0, ul = 0;
             bool ok = true;
-            for (Segment sg; ok && walk.next(p, sg);) {
-                const int nst = steps_of(sg), groups = groups_of<kQ>(p, sg);
-                for (int t = 0; t < nst && ok; ++t, ++g) {
-                    const int slot = g % Sm::kVStages;
-                    ok = mbar_wait_bounded(smem_u32(&ms.v_full[slot]), (g / Sm::kVStages) & 1, abort_flag, err,
-                                           kCacheWaitNs);
-                    const uint32_t b0 = lo_v + ((uint32_t)(slot * Sm::kTile) >> 4);
-#pragma unroll
-                    for (int G = 0; G < 2; ++G) {
-                        if (kQ == 1 ? (g & 1) != (uint32_t)G : G >= groups) continue;
-                        if (ok)
-                            ok = mbar_wait_bounded(smem_u32(&ms.p_full[G]), n_p[G] & 1, abort_flag, err, kCacheWaitNs);
-                        if (!ok) break;
-                        // The unit's first step of the group starts its O over.
-                        const uint32_t acc = t >= (kQ == 1 ? 2 : 1) ? 1u : 0u;
-                        const uint32_t d = tmem + kTmemO + G * kTmemGroup, a = tmem + kTmemS + G * kTmemGroup;
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ts_warp(d, a + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc, acc | (kk > 0 ? 1u : 0u));
-                        if (sg.first + 2 * t + 1 < sg.last) {
-#pragma unroll
-                            for (int kk = 4; kk < 8; ++kk)
-                                mma_ts_warp(d, a + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc, 1u);
-                        }
-                        mma_commit_warp(smem_u32(&ms.pv_done[G]));
-                        ++n_p[G];
-                    }
+            for (Segment sg; ok && walk.next(p, sg); ++ul) {
+                const int nst = steps_of(sg);
+                // O_0 and O_1 start over once the last epilogue has read them (a
+                // unit without steps waits too: unit_done stays one phase ahead).
+                if (ul >= 1) ok = cache_wait<kSleepShort>(smem_u32(&ms.o_free), (ul - 1) & 1, abort_flag, err);
+                for (int t = 0; t < nst && ok; ++t, ++g, ring.step()) {
+                    const int slot = ring.slot;
+                    ok = cache_wait<kSleepShort>(smem_u32(&ms.p_full), g & 1, abort_flag, err) &&
+                         cache_wait<kSleepShort>(smem_u32(&ms.v_full[slot]), ring.full(), abort_flag, err);
                     if (!ok) break;
+                    const uint32_t b0 = lo_v + ((uint32_t)(slot * Sm::kTile) >> 4);
+                    const uint32_t d = tmem + ((g & 1) ? kTmemO1 : kTmemO0);
+                    const uint32_t acc = t >= 2 ? 1u : 0u;  // a group's first step of the unit overwrites its O
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts_warp(d, tmem + kTmemP + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc,
+                                    acc | (kk > 0 ? 1u : 0u));
+                    if (sg.first + 2 * t + 1 < sg.last) {
+#pragma unroll
+                        for (int kk = 4; kk < 8; ++kk)
+                            mma_ts_warp(d, tmem + kTmemP + kk * 8, b0 + ((kk * 2048) >> 4), hi, idesc, 1u);
+                    }
+                    mma_commit_warp(smem_u32(&ms.pv_grp[g & 1]));
                     mma_commit_warp(smem_u32(&ms.v_empty[slot]));
                 }
+                if (!ok) break;
+                mma_commit_warp(smem_u32(&ms.unit_done));
             }
             mma_commit_warp(smem_u32(&ms.drain[1]));
             if (lane == 0) mbar_wait_drain_1(smem_u32(&ms.drain[1]), 0, err, kCacheWaitNs);
             __syncwarp();
         }
-    } else if (warp < 8) {
-        // ============================================================ convert
+    } else if (warp < 12) {
+        // ============================================ convert: warps 4..7 K, 8..11 V
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
-        const int th = threadIdx.x - 128, key = th >> 1, h = th & 1;  // two threads a key of a page
-        uint32_t j = 0, g = 0;
+        const int side = (warp - 4) >> 2;
+        const int th = threadIdx.x & 127, key = th >> 1, h = th & 1;  // two threads a key of a page
+        const uint32_t raw_at = sbase + Sm::kOffRaw + side * kRawHalves * Sm::kRawBytes;
+        const uint32_t tiles = sbase + (side ? Sm::kOffV : Sm::kOffK);
+        const uint32_t full = smem_u32(side ? ms.v_full : ms.k_full), empty = smem_u32(side ? ms.v_empty : ms.k_empty);
+        const int stages = side ? kVStages : kKStages;
+        Ring<kRawHalves> raw;
+        int st = 0;
+        uint32_t turn = 0;  // of the tile's ring
         bool ok = true;
         for (Segment sg; ok && walk.next(p, sg);) {
-            for (int i = sg.first; i < sg.last && ok; i += 2, ++g) {
+            for (int i = sg.first; i < sg.last && ok; i += 2) {
                 const int held = min(2, sg.last - i);
-#pragma unroll 1
-                for (int side = 0; side < 2; ++side) {
-                    const int stages = side ? Sm::kVStages : Sm::kKStages, st = g % stages;
-                    const uint32_t full = smem_u32(side ? &ms.v_full[st] : &ms.k_full[st]);
-                    const uint32_t empty = smem_u32(side ? &ms.v_empty[st] : &ms.k_empty[st]);
-                    const uint32_t tile = sbase + (side ? Sm::kOffV : Sm::kOffK) + st * Sm::kTile;
-                    if (g >= (uint32_t)stages)
-                        ok = mbar_wait_bounded(empty, (g / stages + 1) & 1, abort_flag, err, kCacheWaitNs);
-#pragma unroll 1
-                    for (int which = 0; which < held && ok; ++which, ++j) {
-                        const int slot = j % Sm::kRaw;
-                        ok = mbar_wait_bounded(smem_u32(&ms.raw_full[slot]), (j / Sm::kRaw) & 1, abort_flag, err,
-                                               kCacheWaitNs);
-                        if (!ok) break;
-                        const int2 k0 = ms.key0[g % kMetaSteps];
-                        const int key0 = which ? k0.y : k0.x;
-                        // Slots past the sequence's end hold anything, and a page
-                        // passed over nothing: their V is zero (K is masked).
-                        const bool zero = side && (key0 == kNoKey || key0 + key >= sg.len.kv);
-                        const uint32_t raw = sbase + Sm::kOffRaw + slot * Sm::kRawBytes;
-                        convert_half_row<kD, kQ>(raw + key * (kD / 2), raw + Sm::kCodes + key * (kD / 16),
-                                                 which * kPageTokens + key, h, zero, tile);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&ms.raw_empty[slot]));
-                    }
+                if (turn > 0) ok = cache_wait<kSleepLong>(empty + 8 * st, (turn + 1) & 1, abort_flag, err);
+                for (int which = 0; which < held && ok; ++which, raw.step()) {
+                    ok = cache_wait<kSleepLong>(smem_u32(&ms.raw_full[side][raw.slot]), raw.full(), abort_flag, err);
                     if (!ok) break;
-                    fence_proxy_async_smem();
+                    const uint32_t at = raw_at + raw.slot * Sm::kRawBytes;
+                    // Slots past the sequence's end hold anything, and a page passed
+                    // over nothing: their V is zero (their K is masked).
+                    const bool zero = key >= *reinterpret_cast<volatile int*>(&ms.raw_keys[side][raw.slot]);
+                    convert_half_row<kD>(at + key * (kD / 2), at + Sm::kCodes + key * (kD / 16),
+                                         which * kPageTokens + key, h, zero, tiles + st * Sm::kTile);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(full);
+                    if (lane == 0) mbar_arrive(smem_u32(&ms.raw_empty[side][raw.slot]));
+                }
+                if (!ok) break;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + 8 * st);
+                if (++st == stages) {
+                    st = 0;
+                    ++turn;
                 }
             }
         }
     } else {
         // ============================================================ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        const int G = (warp - 8) >> 2;
+        const int G = (warp - 12) >> 2;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t s_mine = t_lane + kTmemS + G * kTmemGroup, o_mine = t_lane + kTmemO + G * kTmemGroup;
-        const int tile = kQ == 2 ? G : 0;
-        const uint32_t q_tile = sbase + Sm::kOffQ + tile * Sm::kTile;
+        const uint32_t o_mine = t_lane + (G ? kTmemO1 : kTmemO0);
+        constexpr int dh = kD / 2;  // output columns of this thread: [G * dh, G * dh + dh)
         const float ninf = -INFINITY;
         bool ok = true;
-        uint32_t g0 = 0, n = 0, units = 0;  // steps before the unit; steps and units of this group
-        SoftWalk& sw = ms.soft[warp - 8];
+        uint32_t g0 = 0, ul = 0;  // steps before the unit, units
+        SoftWalk& sw = ms.soft[warp - 12];
         auto advance = [&](int to) -> bool {  // the walk's next unit into sw.unit[to]
             Walk w = sw.walk;
             Segment s;
@@ -492,40 +472,53 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         if (lane == 0) sw.walk = walk;
         __syncwarp();
         bool more = advance(0);
-        float next_c2 = 0.f;
-        auto stage = [&](int of) {  // the queries of sw.unit[of]
-            const Segment& s = sw.unit[of];
-            if (tile >= groups_of<kQ>(p, s)) return;
-            next_c2 = stage_query<kD, kQ>(p, s, s.t * (kQ * 128) + tile * 128 + r, r, q_tile);
-            if (kQ == 1) ms.scale[of][r] = next_c2;
+        if (G == 0 && more) {
+            ms.scale[0][r] = stage_query<kD>(p, sw.unit[0], r, t_lane);
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ms.q_full[tile]));
-        };
-        if (more && (kQ == 2 || G == 0)) stage(0);
+            if (lane == 0) mbar_arrive(smem_u32(&ms.q_full));
+        }
 #pragma unroll 1
-        for (uint32_t ul = 0; more; ++ul) {
+        for (; more; ++ul) {
             const bool next = advance((ul + 1) & 1);
             const Segment& sg = sw.unit[ul & 1];
             const int nst = steps_of(sg);
-            const bool mine = tile < groups_of<kQ>(p, sg);
-            const int row = sg.t * (kQ * 128) + tile * 128 + r;
+            const int row = sg.t * 128 + r;
             const int live_rows = sg.len.q * p.group;
             int lim = sg.len.kv;  // first key the row does not see
             if (p.causal && row < live_rows) lim = max(0, min(lim, sg.len.kv - sg.len.q + row / p.group + 1));
-            float c2 = next_c2, m = ninf, l = 0.f;
+            // The group that takes the next unit's first step stages its queries.
+            const bool stager = next && ((g0 + nst) & 1) == (uint32_t)G;
+            if (stager) {
+                const Segment& nx = sw.unit[(ul + 1) & 1];
+                const int nrow = nx.t * 128 + r, ni = nrow / p.group;
+                if (ni < p.Sq) {
+                    const uint4* src = p.q + (((size_t)nx.b * p.Sq + ni) * p.heads + nx.h * p.group + nrow -
+                                              ni * p.group) * (kD / 8);
+#pragma unroll
+                    for (int c = 0; c < kD * 2; c += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c / 16));
+                }
+            }
+            float c2 = 0.f, m = ninf, l = 0.f;
             bool first = true;
 #pragma unroll 1
-            for (int t = kQ == 1 ? (int)((g0 + G) & 1) : 0; t < nst && mine; t += kQ == 1 ? 2 : 1, ++n) {
-                if (ok) ok = mbar_wait_bounded(smem_u32(&ms.s_full[G]), n & 1, abort_flag, err, kCacheWaitNs);
+            for (int t = (int)((g0 + G) & 1); t < nst; t += 2) {
+                const uint32_t gs = g0 + t;
+                if (ok) ok = cache_wait<kSleepShort>(smem_u32(&ms.s_full[G]), (gs >> 1) & 1, abort_flag, err);
                 tc_fence_after();
-                if (kQ == 1) c2 = ms.scale[ul & 1][r];
-                const int2 k0 = ms.key0[(g0 + t) % kMetaSteps];
+                c2 = ms.scale[ul & 1][r];
+                const int2 k0 = ms.key0[gs % kMetaSteps];
                 // Keys of the two pages that this row sees (none where no page is).
                 const int va = lim - k0.x, vb = lim - k0.y;
                 float x[128];
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) tmem_ld32(s_mine + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
+                for (int c = 0; c < 128; c += 32)
+                    tmem_ld32(t_lane + kTmemS + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
                 tmem_wait_ld();
+                // S is in registers: its columns may take the next step's.
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.s_free));
                 if (__any_sync(0xffffffffu, va < kPageTokens || vb < kPageTokens)) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) {
@@ -542,8 +535,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                     l *= alpha;
                 }
                 const float mb = m == ninf ? 0.f : m;
-                if (!first && ok && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    // (The group's last P V has completed: this S was written after it.)
+                uint32_t pk[64];
+                chunk_exp64(x, c2, mb, pk, l);
+                chunk_exp64(x + 64, c2, mb, pk + 32, l);
+                // P V of the step before (the other group's) has read P.
+                if (gs > 0 && ok)
+                    ok = cache_wait<kSleepShort>(smem_u32(&ms.pv_grp[G ^ 1]), ((gs - 1) >> 1) & 1, abort_flag, err);
+                tc_fence_after();
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 16)
+                        tmem_st16(t_lane + kTmemP + c, *reinterpret_cast<uint32_t(*)[16]>(&pk[c]));
+                }
+                if (ok && !first && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // The last P V into this group's O has completed.
+                    ok = cache_wait<kSleepShort>(smem_u32(&ms.pv_grp[G]), ((gs - 2) >> 1) & 1, abort_flag, err);
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c0 = 0; c0 < kD; c0 += 32) {
                         uint32_t o[32];
@@ -554,86 +561,72 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                         tmem_st32(o_mine + c0, o);
                     }
                 }
-                uint32_t pk[64];
-                chunk_exp64(x, c2, mb, pk, l);
-                chunk_exp64(x + 64, c2, mb, pk + 32, l);
-                if (ok) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 16)
-                        tmem_st16(s_mine + c, *reinterpret_cast<uint32_t(*)[16]>(&pk[c]));
-                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms.p_full[G]));
+                if (lane == 0) mbar_arrive(smem_u32(&ms.p_full));
                 first = false;
             }
-            // The next unit's queries, once this one's Q K^T have completed.
-            if (mine && (kQ == 2 || ((g0 + nst) & 1) == (uint32_t)G)) {
-                if (ok && next)
-                    ok = mbar_wait_bounded(smem_u32(&ms.q_empty[tile]), units & 1, abort_flag, err, kCacheWaitNs);
+            if (stager) {
+                // The unit's Q K^T have completed: Q may be overwritten.
+                if (ok) ok = cache_wait<kSleepShort>(smem_u32(&ms.q_empty), ul & 1, abort_flag, err);
+                if (ok) {
+                    tc_fence_after();
+                    ms.scale[(ul + 1) & 1][r] = stage_query<kD>(p, sw.unit[(ul + 1) & 1], r, t_lane);
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.q_full));
             }
-            if (mine) ++units;
-            if (next && ok && (kQ == 2 || ((g0 + nst) & 1) == (uint32_t)G)) stage((ul + 1) & 1);
             // ------------------------------------------------ unit epilogue
-            float a_e = 1.f, a_o = 0.f, mt = m, lt = l;
-            const uint32_t ge = kQ == 1 ? (g0 & 1u) : G;  // the group of the unit's even steps comes first
-            bool has_e = nst > 0, has_o = false;          // a group without a step holds no O of the unit
-            if (kQ == 1) {
-                //   m = max(m_0, m_1), a_k = 2^(m_k - m), l = a_0 l_0 + a_1 l_1, O = a_0 O_0 + a_1 O_1
-                ms.xm[G][r] = m;
-                ms.xl[G][r] = l;
-                // This group's O is complete before the other reads its half of it.
-                if (n > 0 && ok)
-                    ok = mbar_wait_bounded(smem_u32(&ms.pv_done[G]), (n - 1) & 1, abort_flag, err, kCacheWaitNs);
-                tc_fence_before();
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                tc_fence_after();
-                const float m_e = ms.xm[ge][r], l_e = ms.xl[ge][r], m_o = ms.xm[ge ^ 1][r], l_o = ms.xl[ge ^ 1][r];
-                mt = fmaxf(m_e, m_o);
-                a_e = m_e == ninf ? 0.f : ex2_approx(m_e - mt);
-                a_o = m_o == ninf ? 0.f : ex2_approx(m_o - mt);
-                lt = __fmaf_rn(a_e, l_e, __fmul_rn(a_o, l_o));
-                has_o = nst > 1;
-            } else if (n > 0 && mine && ok) {
-                ok = mbar_wait_bounded(smem_u32(&ms.pv_done[G]), (n - 1) & 1, abort_flag, err, kCacheWaitNs);
-                tc_fence_after();
-            }
-            const bool real = ok && mine && row < p.Sq * p.group;
+            //   m = max(m_0, m_1), a_k = 2^(m_k - m), l = a_0 l_0 + a_1 l_1, O = a_0 O_0 + a_1 O_1
+            ms.xm[ul & 1][G][r] = m;
+            ms.xl[ul & 1][G][r] = l;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+            // The group of the unit's even steps comes first, whatever it is:
+            // the sums do not depend on what the CTA did before the unit.
+            const int ge = (int)(g0 & 1u);
+            const float m_e = ms.xm[ul & 1][ge][r], l_e = ms.xl[ul & 1][ge][r];
+            const float m_o = ms.xm[ul & 1][ge ^ 1][r], l_o = ms.xl[ul & 1][ge ^ 1][r];
+            const float mt = fmaxf(m_e, m_o);
+            float a_e = m_e == ninf ? 0.f : ex2_approx(m_e - mt);
+            float a_o = m_o == ninf ? 0.f : ex2_approx(m_o - mt);
+            const float lt = __fmaf_rn(a_e, l_e, __fmul_rn(a_o, l_o));
+            const uint32_t o_e = ge ? kTmemO1 : kTmemO0, o_o = ge ? kTmemO0 : kTmemO1;
+            const bool has_e = nst > 0, has_o = nst > 1;  // a group without a step holds no O of the unit
+            const bool real = ok && row < p.Sq * p.group;
             const int qi = real ? row / p.group : 0;
             const int head = sg.h * p.group + (real ? row - qi * p.group : 0);
-            const bool live = row < live_rows && lt != 0.f, whole = sg.whole;
-            const size_t part = (2 * (size_t)blockIdx.x + (sg.first > 0 ? 0 : 1)) * (kQ * 128) + tile * 128 + r;
-            if (whole) {
+            const bool live = row < live_rows && lt != 0.f;
+            const size_t part = (2 * (size_t)blockIdx.x + (sg.first > 0 ? 0 : 1)) * 128 + r;
+            if (sg.whole) {
                 const float inv =
                     live ? (p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + sg.h) : 1.f) / lt : 0.f;
                 a_e *= inv;
                 a_o *= inv;
             }
-            // kQ = 1: the groups write half of the columns each.
-            const int col0 = kQ == 1 ? G * (kD / 2) : 0, cols = kQ == 1 ? kD / 2 : kD;
-            uint4* dst = p.out + (((size_t)sg.b * p.Sq + qi) * p.heads + head) * (kD / 8) + col0 / 8;
-            float4* dst_part = reinterpret_cast<float4*>(p.part_o + part * kD + col0);
+            if (ok) ok = cache_wait<kSleepShort>(smem_u32(&ms.unit_done), ul & 1, abort_flag, err);
+            tc_fence_after();
+            uint4* dst = p.out + (((size_t)sg.b * p.Sq + qi) * p.heads + head) * (kD / 8) + G * (dh / 8);
+            float4* dst_part = reinterpret_cast<float4*>(p.part_o + part * kD + G * dh);
 #pragma unroll 1
-            for (int c0 = 0; c0 < (mine ? cols : 0); c0 += 32) {
+            for (int c0 = 0; c0 < dh; c0 += 32) {
                 uint32_t oa[32], ob[32];
-                tmem_ld32(t_lane + kTmemO + ge * kTmemGroup + col0 + c0, oa);
-                if (kQ == 1) tmem_ld32(t_lane + kTmemO + (ge ^ 1) * kTmemGroup + col0 + c0, ob);
+                tmem_ld32(t_lane + o_e + G * dh + c0, oa);
+                tmem_ld32(t_lane + o_o + G * dh + c0, ob);
                 tmem_wait_ld();
                 float f[32];
 #pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                    const float e = has_e ? __uint_as_float(oa[q]) : 0.f;
-                    f[q] = kQ == 1 ? __fmaf_rn(a_e, e, __fmul_rn(a_o, has_o ? __uint_as_float(ob[q]) : 0.f)) : a_e * e;
-                }
+                for (int q = 0; q < 32; ++q)
+                    f[q] = __fmaf_rn(a_e, has_e ? __uint_as_float(oa[q]) : 0.f,
+                                     __fmul_rn(a_o, has_o ? __uint_as_float(ob[q]) : 0.f));
                 if (!real || !ok) continue;
-                if (whole) {
+                if (sg.whole) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w[q] = live ? pack_bf16x2(f[8 * v + 2 * q], f[8 * v + 2 * q + 1]) : 0u;
+                        for (int q = 0; q < 4; ++q) w[q] = live ? pack_bf16x2(f[8 * v + 2 * q], f[8 * v + 2 * q + 1]) : 0u;
                         __stcs(dst + c0 / 8 + v, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 } else {
@@ -642,15 +635,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                         dst_part[c0 / 4 + v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
                 }
             }
-            if (kQ == 1) {
-                // Both groups have read O_0 and O_1 (and the exchanged statistics):
-                // the next unit's steps, which either announces after this, may start.
-                tc_fence_before();
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                tc_fence_after();
-            }
-            if (real && ok && (kQ == 2 || G == 0)) {
-                if (!whole)
+            // O_0 and O_1 have been read: the next unit may start them over.
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ms.o_free));
+            if (real && ok && G == 0) {
+                if (!sg.whole)
                     p.part_ml[part] = make_float2(mt, lt);
                 else if (p.lse)
                     p.lse[((size_t)sg.b * p.heads + head) * p.Sq + qi] =
@@ -670,26 +660,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
 
 }  // namespace
 
-template <int kD, int kQ>
-static cudaError_t launch_chunk_as(const AttnParams& p, cudaStream_t stream) {
+template <int kD>
+static cudaError_t launch_chunk_d(const AttnParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    // The register split draws on the launch's 128 registers a thread; with
-    // fewer, setmaxnreg would wait forever, so such a build is refused.
+    // The register split draws on the launch's registers; with fewer, setmaxnreg would wait forever, so such a build is refused.
     static const int regs = [] {
         cudaFuncAttributes fa;
-        return cudaFuncGetAttributes(&fa, chunk_kernel<kD, kQ>) == cudaSuccess ? fa.numRegs : 0;
+        return cudaFuncGetAttributes(&fa, chunk_kernel<kD>) == cudaSuccess ? fa.numRegs : 0;
     }();
-    if (regs != 128) return cudaErrorInvalidKernelImage;
-    const cudaError_t e = allow_smem(chunk_kernel<kD, kQ>, chunk_smem<kD, kQ>(), done);
+    if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    const cudaError_t e = allow_smem(chunk_kernel<kD>, chunk_smem<kD>(), done);
     if (e != cudaSuccess) return e;
-    chunk_kernel<kD, kQ><<<p.grid, kChunkThreads, chunk_smem<kD, kQ>(), stream>>>(p);
+    chunk_kernel<kD><<<p.grid, kChunkThreads, chunk_smem<kD>(), stream>>>(p);
     note_launches(1);
     return cudaGetLastError();
 }
 
 cudaError_t launch_chunk(const AttnParams& p, int D, cudaStream_t stream) {
-    if (p.tile == 256) return D == 64 ? launch_chunk_as<64, 2>(p, stream) : launch_chunk_as<128, 2>(p, stream);
-    return D == 64 ? launch_chunk_as<64, 1>(p, stream) : launch_chunk_as<128, 1>(p, stream);
+    return D == 64 ? launch_chunk_d<64>(p, stream) : launch_chunk_d<128>(p, stream);
 }
 
 }  // namespace vsa
