@@ -734,7 +734,7 @@ cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
 }
 
 // Starting and ending a unit, in pages.
-constexpr int kTokenUnitCost = 1, kChunkUnitCost = 6;
+constexpr int kTokenUnitCost = 2, kChunkUnitCost = 20;
 
 // Rows of a unit: up to 16 rows a kv head go to token_kernel, more to chunk_kernel.
 int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }

@@ -26,22 +26,44 @@ namespace {
 
 struct AppendParams {
     CacheView c;
-    const uint4* q;
-    const uint4* k;
-    const uint4* v;
-    uint4* q_out;
+    const unsigned char* q;
+    const unsigned char* k;
+    const unsigned char* v;
+    unsigned char* q_out;
     const int32_t* new_lens;   // [B], or null: S
     const int32_t* positions;  // [B][S], or null: the token's place in its sequence
     const float* rope;         // [rope_rows][R]: R / 2 cosines, R / 2 sines
     int S, heads, rope_rows, R;
+    int wide;  // q, k, v and q_out are aligned to 32 bytes
 };
 
-__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(u[i]);
-        x[2 * i + 1] = bf16_hi(u[i]);
+// 16 bf16 channels: a 32-byte sector, in one access where the tensor is aligned
+// to it (`wide`; two half sectors a lane cost L2 twice the accesses).
+struct Sector {
+    uint32_t w[8];
+};
+__device__ __forceinline__ Sector load_sector(const unsigned char* at, bool wide) {
+    Sector s;
+    if (wide) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(s.w[0]), "=r"(s.w[1]), "=r"(s.w[2]), "=r"(s.w[3]), "=r"(s.w[4]), "=r"(s.w[5]),
+                       "=r"(s.w[6]), "=r"(s.w[7])
+                     : "l"(at));
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(at)), b = __ldg(reinterpret_cast<const uint4*>(at) + 1);
+        s.w[0] = a.x; s.w[1] = a.y; s.w[2] = a.z; s.w[3] = a.w;
+        s.w[4] = b.x; s.w[5] = b.y; s.w[6] = b.z; s.w[7] = b.w;
+    }
+    return s;
+}
+__device__ __forceinline__ void store_sector(unsigned char* at, const Sector& s, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(s.w[0]), "r"(s.w[1]),
+                     "r"(s.w[2]), "r"(s.w[3]), "r"(s.w[4]), "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(at)[0] = make_uint4(s.w[0], s.w[1], s.w[2], s.w[3]);
+        reinterpret_cast<uint4*>(at)[1] = make_uint4(s.w[4], s.w[5], s.w[6], s.w[7]);
     }
 }
 
@@ -127,47 +149,66 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
     const size_t token = (size_t)b * p.S + tok;
     const int hq = p.q_out ? p.heads : 0;
     const int all = hq + 2 * p.c.kv_heads;
-    for (int h = blockIdx.y * kHeadLanes + threadIdx.x / (kSlices * kTok); h < all; h += gridDim.y * kHeadLanes) {
+    const int step = gridDim.y * kHeadLanes;
+    // Head h of all: a query head, a key head or a value head; its row of the token.
+    auto row_of = [&](int h) -> const unsigned char* {
+        const int kh = h < hq ? h : h < hq + p.c.kv_heads ? h - hq : h - hq - p.c.kv_heads;
+        return h < hq ? p.q + (token * p.heads + kh) * (kD * 2)
+                      : (h < hq + p.c.kv_heads ? p.k : p.v) + (token * p.c.kv_heads + kh) * (kD * 2);
+    };
+    int h = blockIdx.y * kHeadLanes + threadIdx.x / (kSlices * kTok);
+    if (!live) {  // a padding row: nothing to keep, its queries are zero
+        Sector zero;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) zero.w[i] = 0u;
+        for (; h < hq; h += step) {
+            unsigned char* dst = p.q_out + (token * p.heads + h) * (kD * 2);
+            store_sector(dst + g0 * 2, zero, p.wide);
+            store_sector(dst + g1 * 2, zero, p.wide);
+        }
+        return;
+    }
+    Sector a, c;
+    if (h < all) {
+        a = load_sector(row_of(h) + g0 * 2, p.wide);
+        c = load_sector(row_of(h) + g1 * 2, p.wide);
+    }
+    for (; h < all; h += step) {
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[2 * i] = bf16_lo(a.w[i]);
+            x[2 * i + 1] = bf16_hi(a.w[i]);
+            x[16 + 2 * i] = bf16_lo(c.w[i]);
+            x[16 + 2 * i + 1] = bf16_hi(c.w[i]);
+        }
+        if (h + step < all) {  // the next head's row is on its way while this one is worked on
+            a = load_sector(row_of(h + step) + g0 * 2, p.wide);
+            c = load_sector(row_of(h + step) + g1 * 2, p.wide);
+        }
         const bool is_q = h < hq, is_k = !is_q && h < hq + p.c.kv_heads;
         const int kh = is_q ? h : is_k ? h - hq : h - hq - p.c.kv_heads;
-        if (!live) {  // a padding row: nothing to keep, its query is zero
-            if (is_q) {
-                uint4* dst = p.q_out + (token * p.heads + kh) * (kD / 8);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    dst[g0 / 8 + i] = make_uint4(0, 0, 0, 0);
-                    dst[g1 / 8 + i] = make_uint4(0, 0, 0, 0);
-                }
-            }
-            continue;
-        }
-        const uint4* src = is_q ? p.q + (token * p.heads + kh) * (kD / 8)
-                                : (is_k ? p.k : p.v) + (token * p.c.kv_heads + kh) * (kD / 8);
-        float x[32];
-        unpack8(__ldg(src + g0 / 8), x);
-        unpack8(__ldg(src + g0 / 8 + 1), x + 8);
-        unpack8(__ldg(src + g1 / 8), x + 16);
-        unpack8(__ldg(src + g1 / 8 + 1), x + 24);
         if (turned && (is_q || is_k)) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 // Pair i: (2i, 2i + 1) of the 32 channels, or (i, 16 + i) of the two halves.
                 float& u = x[kPairs ? 2 * i : i];
                 float& w = x[kPairs ? 2 * i + 1 : 16 + i];
-                const float a = u, c = w;
-                u = known ? __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(c, sn[i])) : 0.f;
-                w = known ? __fadd_rn(__fmul_rn(c, cs[i]), __fmul_rn(a, sn[i])) : 0.f;
+                const float y = u, z = w;
+                u = known ? __fsub_rn(__fmul_rn(y, cs[i]), __fmul_rn(z, sn[i])) : 0.f;
+                w = known ? __fadd_rn(__fmul_rn(z, cs[i]), __fmul_rn(y, sn[i])) : 0.f;
             }
         }
         if (is_q) {
-            uint4* dst = p.q_out + (token * p.heads + kh) * (kD / 8);
+            Sector y, z;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float* y = x + 8 * i;
-                dst[(i < 2 ? g0 / 8 : g1 / 8 - 2) + i] =
-                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                               pack_bf16x2(y[6], y[7]));
+            for (int i = 0; i < 8; ++i) {
+                y.w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                z.w[i] = pack_bf16x2(x[16 + 2 * i], x[16 + 2 * i + 1]);
             }
+            unsigned char* dst = p.q_out + (token * p.heads + kh) * (kD * 2);
+            store_sector(dst + g0 * 2, y, p.wide);
+            store_sector(dst + g1 * 2, z, p.wide);
         } else if (page) {
             const float hs = p.c.kv_scale ? __ldg(p.c.kv_scale + (is_k ? 0 : p.c.kv_heads) + kh) : 1.f;
             const float inv = __frcp_rn(hs);
@@ -176,10 +217,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
             unsigned char* head = page + (size_t)kh * L::kBytes;
             unsigned char* codes = head + (is_k ? 0 : L::kV) + in_page * L::kRow;
             unsigned char* scales = head + (is_k ? L::kKScale : L::kVScale) + in_page * L::kGroups;
-            *reinterpret_cast<uint2*>(codes + g0 / 2) = make_uint2(c0[0], c0[1]);
-            *reinterpret_cast<uint2*>(codes + g1 / 2) = make_uint2(c1[0], c1[1]);
-            scales[g0 / 16] = (unsigned char)s0;
-            scales[g1 / 16] = (unsigned char)s1;
+            if (g1 == g0 + 16) {
+                *reinterpret_cast<uint4*>(codes + g0 / 2) = make_uint4(c0[0], c0[1], c1[0], c1[1]);
+                *reinterpret_cast<uint16_t*>(scales + g0 / 16) = (uint16_t)(s0 | (s1 << 8));
+            } else {
+                *reinterpret_cast<uint2*>(codes + g0 / 2) = make_uint2(c0[0], c0[1]);
+                *reinterpret_cast<uint2*>(codes + g1 / 2) = make_uint2(c1[0], c1[1]);
+                scales[g0 / 16] = (unsigned char)s0;
+                scales[g1 / 16] = (unsigned char)s1;
+            }
         }
     }
 }
@@ -248,10 +294,12 @@ cudaError_t launch_cache_append(const CacheView& c, int D, const void* q, const 
                                 cudaStream_t stream) {
     AppendParams p;
     p.c = c;
-    p.q = static_cast<const uint4*>(q);
-    p.k = static_cast<const uint4*>(k);
-    p.v = static_cast<const uint4*>(v);
-    p.q_out = static_cast<uint4*>(q_out);
+    p.q = static_cast<const unsigned char*>(q);
+    p.k = static_cast<const unsigned char*>(k);
+    p.v = static_cast<const unsigned char*>(v);
+    p.q_out = static_cast<unsigned char*>(q_out);
+    p.wide = ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+               reinterpret_cast<uintptr_t>(q_out)) & 31u) == 0;
     p.new_lens = new_lens;
     p.positions = positions;
     p.rope = rope;
