@@ -75,8 +75,15 @@ __device__ __forceinline__ uint32_t quantise16(const float* x, float inv_head, u
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         y[i] = __fmul_rn(x[i], inv_head);
-        y[i] = y[i] == y[i] ? y[i] : 0.f;
-        a = fmaxf(a, fabsf(y[i]));
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(fabsf(y[i])));
+    }
+    if (a != a) {  // (one look a group instead of one an element)
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            y[i] = y[i] == y[i] ? y[i] : 0.f;
+            a = fmaxf(a, fabsf(y[i]));
+        }
     }
     uint16_t s8;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(__fmul_rn(a, 1.f / 6.f)));
@@ -100,7 +107,7 @@ __device__ __forceinline__ uint32_t quantise16(const float* x, float inv_head, u
     return s8 & 0xFFu;
 }
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 // kTok tokens a block: 8 neighbouring tokens, or 1 for steps of few tokens
 // (then the block's threads spread over heads instead).
@@ -112,6 +119,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
     const int slice = threadIdx.x % kSlices;
     const int b = blockIdx.z;
     const int tok = blockIdx.x * kTok + (threadIdx.x / kSlices) % kTok;
+    if (tok >= p.S) return;
+    const size_t token = (size_t)b * p.S + tok;
+    const int hq = p.q_out ? p.heads : 0;
+    const int all = hq + 2 * p.c.kv_heads;
+    // The two groups of 16 channels: [g0, g0 + 16) and [g1, g1 + 16).
+    const bool turned = slice * 32 < p.R;
+    const int g0 = turned && !kPairs ? slice * 16 : slice * 32;
+    const int g1 = turned && !kPairs ? slice * 16 + p.R / 2 : slice * 32 + 16;
+    const int step = gridDim.y * kHeadLanes;
+    // Head h of all: a query head, a key head or a value head; its row of the token.
+    auto row_of = [&](int h) -> const unsigned char* {
+        const int kh = h < hq ? h : h < hq + p.c.kv_heads ? h - hq : h - hq - p.c.kv_heads;
+        return h < hq ? p.q + (token * p.heads + kh) * (kD * 2)
+                      : (h < hq + p.c.kv_heads ? p.k : p.v) + (token * p.c.kv_heads + kh) * (kD * 2);
+    };
+    int h = blockIdx.y * kHeadLanes + threadIdx.x / (kSlices * kTok);
+    // The first row is on its way while the lengths, the page and the angles are looked up.
+    Sector a, c;
+    if (h < all) {
+        a = load_sector(row_of(h) + g0 * 2, p.wide);
+        c = load_sector(row_of(h) + g1 * 2, p.wide);
+    }
     const int n = cache_len(p.c, b, threadIdx.x == 0);
     const int fresh = min(p.new_lens ? max(__ldg(p.new_lens + b), 0) : p.S, min(p.S, n));
     const bool live = tok < fresh;
@@ -126,37 +155,24 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
             atomicOr(p.c.err, VSA_DEVERR_INDEX);
     }
     const int in_page = at % kPageTokens;
-    // The two groups of 16 channels: [g0, g0 + 16) and [g1, g1 + 16).
-    const bool turned = slice * 32 < p.R;
-    const int g0 = turned && !kPairs ? slice * 16 : slice * 32;
-    const int g1 = turned && !kPairs ? slice * 16 + p.R / 2 : slice * 32 + 16;
     float cs[16], sn[16];
-    bool known = true;  // the position has a row
     if (turned && live) {
         const int pos = p.positions ? __ldg(p.positions + (size_t)b * p.S + tok) : at;
-        known = pos >= 0 && pos < p.rope_rows;
-        if (!known && slice == 0) atomicOr(p.c.err, VSA_DEVERR_INDEX);
-        const float4* row = reinterpret_cast<const float4*>(p.rope + (size_t)(known ? pos : 0) * p.R + slice * 16);
-        const float4* row_s = row + p.R / 8;
+        if (pos >= 0 && pos < p.rope_rows) {
+            const float4* row = reinterpret_cast<const float4*>(p.rope + (size_t)pos * p.R + slice * 16);
+            const float4* row_s = row + p.R / 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 a = __ldg(row + i), s = __ldg(row_s + i);
-            cs[4 * i] = a.x; cs[4 * i + 1] = a.y; cs[4 * i + 2] = a.z; cs[4 * i + 3] = a.w;
-            sn[4 * i] = s.x; sn[4 * i + 1] = s.y; sn[4 * i + 2] = s.z; sn[4 * i + 3] = s.w;
+            for (int i = 0; i < 4; ++i) {
+                const float4 u = __ldg(row + i), w = __ldg(row_s + i);
+                cs[4 * i] = u.x; cs[4 * i + 1] = u.y; cs[4 * i + 2] = u.z; cs[4 * i + 3] = u.w;
+                sn[4 * i] = w.x; sn[4 * i + 1] = w.y; sn[4 * i + 2] = w.z; sn[4 * i + 3] = w.w;
+            }
+        } else {  // no such row: a zero rotation
+            if (slice == 0) atomicOr(p.c.err, VSA_DEVERR_INDEX);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) cs[i] = sn[i] = 0.f;
         }
     }
-    if (tok >= p.S) return;
-    const size_t token = (size_t)b * p.S + tok;
-    const int hq = p.q_out ? p.heads : 0;
-    const int all = hq + 2 * p.c.kv_heads;
-    const int step = gridDim.y * kHeadLanes;
-    // Head h of all: a query head, a key head or a value head; its row of the token.
-    auto row_of = [&](int h) -> const unsigned char* {
-        const int kh = h < hq ? h : h < hq + p.c.kv_heads ? h - hq : h - hq - p.c.kv_heads;
-        return h < hq ? p.q + (token * p.heads + kh) * (kD * 2)
-                      : (h < hq + p.c.kv_heads ? p.k : p.v) + (token * p.c.kv_heads + kh) * (kD * 2);
-    };
-    int h = blockIdx.y * kHeadLanes + threadIdx.x / (kSlices * kTok);
     if (!live) {  // a padding row: nothing to keep, its queries are zero
         Sector zero;
 #pragma unroll
@@ -167,11 +183,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
             store_sector(dst + g1 * 2, zero, p.wide);
         }
         return;
-    }
-    Sector a, c;
-    if (h < all) {
-        a = load_sector(row_of(h) + g0 * 2, p.wide);
-        c = load_sector(row_of(h) + g1 * 2, p.wide);
     }
     for (; h < all; h += step) {
         float x[32];
@@ -195,8 +206,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
                 float& u = x[kPairs ? 2 * i : i];
                 float& w = x[kPairs ? 2 * i + 1 : 16 + i];
                 const float y = u, z = w;
-                u = known ? __fsub_rn(__fmul_rn(y, cs[i]), __fmul_rn(z, sn[i])) : 0.f;
-                w = known ? __fadd_rn(__fmul_rn(z, cs[i]), __fmul_rn(y, sn[i])) : 0.f;
+                u = __fsub_rn(__fmul_rn(y, cs[i]), __fmul_rn(z, sn[i]));
+                w = __fadd_rn(__fmul_rn(z, cs[i]), __fmul_rn(y, sn[i]));
             }
         }
         if (is_q) {
@@ -311,10 +322,10 @@ cudaError_t launch_cache_append(const CacheView& c, int D, const void* q, const 
     const int tok = S >= 8 ? 8 : 1;
     const int lanes = kAppendThreads / (D / 32 * tok);
     const int bx = (S + tok - 1) / tok;
-    // Heads are spread over blocks until there are some four for each SM, and not further.
+    // Heads are spread over blocks until there are some eight for each SM, and not further.
     const int most = (all + lanes - 1) / lanes;
     const long long blocks = (long long)bx * c.B;
-    int by = (int)((4LL * num_sms + blocks - 1) / blocks);
+    int by = (int)((8LL * num_sms + blocks - 1) / blocks);
     by = by < 1 ? 1 : by > most ? most : by;
     const dim3 grid((unsigned)bx, (unsigned)by, (unsigned)c.B);
     auto of_d64 = interleaved ? (tok == 8 ? append_kernel<64, 8, true> : append_kernel<64, 1, true>)

@@ -295,6 +295,80 @@ def test_long_sequence_split_over_the_grid():
     assert vsa.device_error(reset=True) == 0
 
 
+def dense_reference(q, kk, vv, n, m, causal, pages=None):
+    """float64 attention of one sequence: q [Sq, heads, D] (its first m rows live) over kk, vv [>= n, kv, D];
+    pages [kv, P] bool: the pages each kv head may see.  -> out, lse, and the error bound of out."""
+    Sq, heads, D = q.shape
+    kv, rep = kk.shape[1], heads // kk.shape[1]
+    k, v = (x[:n].double().repeat_interleave(rep, 1) for x in (kk, vv))
+    s = torch.einsum("qhd,khd->hqk", q.double(), k) / D ** 0.5
+    at, row = torch.arange(n, device="cuda"), torch.arange(Sq, device="cuda")[:, None]
+    keep = (row < m) & ((at <= n - m + row) if causal else torch.ones_like(at, dtype=torch.bool))
+    keep = keep.expand(heads, Sq, n)
+    if pages is not None:
+        keep = keep & pages.repeat_interleave(rep, 0)[:, at // 64][:, None]
+    s = s.masked_fill(~keep, -torch.inf)
+    lse = torch.logsumexp(s, -1)
+    w = (s - lse.clamp(min=-1e300)[..., None]).exp()
+    want, wabs = (torch.einsum("hqk,khd->qhd", w, x) for x in (v, v.abs()))
+    top = w.amax(-1, keepdim=True).movedim(0, 1) if n else torch.zeros((Sq, heads, 1), device="cuda")
+    big = v.abs().max() if n else 0.0
+    # P to fp16 2^-11; logits of |s| < 16 as fp32 sums of 128 terms, numerator and denominator: 2^-12;
+    # weights under fp16's smallest normal: 2^-25 of the largest, n of them; the result to bf16 2^-8
+    return want, lse, (2.0 ** -11 + 2.0 ** -12) * wabs + n * 2.0 ** -25 * top * big + 2.0 ** -8 * want.abs() + 1e-30
+
+
+@pytest.mark.parametrize("B,kv,heads,D,Sq,most,causal,sel", [
+    (33, 2, 6, 128, 1, 1500, True, 0),      # more sequences than a warp's lanes
+    (700, 1, 4, 64, 1, 300, True, 0),       # more than a block's threads
+    (3, 8, 8, 128, 3, 400, True, 0),        # short walks: units are not cut
+    (40, 1, 5, 64, 2, 2500, False, 7),      # selected pages, more than 32 sequences
+    (2, 2, 32, 128, 1, 9000, True, 0),      # 16 rows a kv head, cut over the grid
+    (5, 3, 9, 128, 60, 1200, True, 0),      # chunks of two tiles a kv head
+    (37, 1, 2, 64, 200, 700, True, 0),      # chunks, more than 32 sequences
+    (2, 1, 8, 128, 400, 6000, True, 0),     # long chunks, cut over the grid
+    (6, 2, 4, 128, 33, 4000, False, 20),    # chunks over selected pages
+    (1, 1, 1, 64, 900, 900, True, 0),       # a sequence of its queries alone
+])
+def test_ragged_batches_of_every_size(B, kv, heads, D, Sq, most, causal, sel):
+    r = np.random.default_rng(B + Sq)
+    g = torch.Generator(device="cuda").manual_seed(B + Sq)
+    lens = [0 if b % 11 == 5 else int(r.integers(1, most + 1)) for b in range(B)]
+    lens[0] = most
+    q_lens = [int(r.integers(0, Sq + 1)) for _ in range(B)]
+    q_lens[0] = Sq
+    width = -(-most // 64)
+    counts = [-(-n // 64) for n in lens]
+    pool = vsa.cache_pool(sum(counts) + 1, kv, D)
+    pool.random_(0, 255, generator=g)
+    table = dev(table_for(r, lens, width, sum(counts) + 1))
+    n = dev(np.array(lens, np.int32))
+    k, v = (torch.randn((B, most, kv, D), generator=g, device="cuda").bfloat16() for _ in "kv")
+    vsa.cache_append(pool, k, v, table, n, new_lens=n)
+    kk, vv = vsa.cache_read(pool, table, n, most)
+    q = (1.5 * torch.randn((B, Sq, heads, D), generator=g, device="cuda")).bfloat16()
+    page_sel = allowed = None
+    if sel:
+        pick = np.stack([[r.permutation(width)[:sel] for _ in range(kv)] for _ in range(B)]).astype(np.int32)
+        page_sel = dev(pick)
+        allowed = torch.zeros((B, kv, width), dtype=torch.bool, device="cuda").scatter_(2, page_sel.long(), True)
+    out, lse = vsa.cache_attn(q, pool, table, n, q_lens=dev(np.array(q_lens, np.int32)), causal=causal,
+                              page_sel=page_sel)
+    again = vsa.cache_attn(q, pool, table, n, q_lens=dev(np.array(q_lens, np.int32)), causal=causal,
+                           page_sel=page_sel)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert vsa.device_error(reset=True) == 0
+    for b in range(B):
+        want, want_lse, lim = dense_reference(q[b], kk[b], vv[b], lens[b], q_lens[b], causal,
+                                              None if allowed is None else allowed[b])
+        assert ((out[b].double() - want).abs() <= lim).all(), b
+        dead = torch.isneginf(want_lse)
+        assert torch.equal(dead, torch.isneginf(lse[b])), b
+        assert not dead.all() or not out[b].any()
+        if not dead.all():
+            assert (lse[b].double() - want_lse)[~dead].abs().max() <= 2.0 ** -12, b
+
+
 def test_pool_beyond_32_bit_offsets():
     """Pages whose byte offset passes 2^31 are written and read where they are."""
     D, kv, pages = 128, 2, 140000  # 2.6 GB
