@@ -133,6 +133,8 @@ def _declare(lib):
 def library():
     """The loaded libvsa.so (ctypes).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -610,21 +612,22 @@ def cache_pool(pages: int, kv_heads: int, D: int, device="cuda"):
 
 
 def _on(t, dtype, name, device):
-    """_need, and on `device`, with one pass over the tensor where all is well (a call takes ten of them)."""
-    if type(t) is _torch().Tensor and t.dtype is dtype and t.is_contiguous() and t.get_device() == device >= 0:
-        return t.data_ptr()
+    """_need, and on `device`, in one pass over the tensor where all is well (a call takes ten of them)."""
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _need(t, dtype, name)
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the pool's device")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be on the pool's device")
 
 
 def _cache(pool, table, kv_lens, kv_scale):
     """Checks a cache's tensors -> (VsaCache, device index, B, kv_heads, D)."""
     torch = _torch()
     i32 = torch.int32
-    if not isinstance(pool, torch.Tensor):
-        raise TypeError("pool must be a torch.Tensor")
+    if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
+        _need(pool, torch.uint8, "pool")
     dev = pool.get_device()
     ptrs = (_on(pool, torch.uint8, "pool", dev), _on(table, i32, "table", dev), _on(kv_lens, i32, "kv_lens", dev))
     shape, rows = pool.shape, table.shape

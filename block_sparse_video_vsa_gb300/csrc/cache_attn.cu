@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
                                     qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
                 }
             // Keys past a row's limit (and scores of what lies there) do not count.
-            if (key0 + kPieceTokens > min_lim) {
+            const bool masked = key0 + kPieceTokens > min_lim;
+            if (masked) {
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m)
 #pragma unroll
@@ -388,14 +389,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
                     for (int c = 0; c < 2; ++c) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], x));
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    // (No branch: the exponential of a step that needs none costs less than one.)
                     const float top = mx[c] * rs_scale[nt][c];
-                    alpha[nt][c] = 1.f;
-                    if (top > rs_m[nt][c] + kCacheRescale) {
-                        alpha[nt][c] = rs_m[nt][c] == -INFINITY ? 0.f : ex2_approx(rs_m[nt][c] - top);
-                        rs_m[nt][c] = top;
-                        rs_l[nt][c] *= alpha[nt][c];
-                        rescale = true;
-                    }
+                    const bool jump = top > rs_m[nt][c] + kCacheRescale;
+                    const float next = jump ? top : rs_m[nt][c];
+                    alpha[nt][c] = jump ? ex2_approx(rs_m[nt][c] - top) : 1.f;  // (0 from a maximum of -infinity)
+                    rs_m[nt][c] = next;
+                    rs_l[nt][c] *= alpha[nt][c];
+                    rescale |= jump;
                     const float mb = rs_m[nt][c] == -INFINITY ? 0.f : rs_m[nt][c];
                     float sum = 0.f;
 #pragma unroll
@@ -423,7 +424,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
                         for (int c = 0; c < 4; ++c) o[i][nt][c] *= alpha[nt][c & 1];
             }
             // O^T += V^T P^T
-            const bool ragged = key0 + kPieceTokens > at.len.kv;  // slots past the length hold anything
 #pragma unroll
             for (int m = 0; m < kTiles; ++m) {
                 const int tok[4] = {16 * m + v_row0, 16 * m + v_row1, 16 * m + 8 + v_row0, 16 * m + 8 + v_row1};
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
                     }
                     sc[i] = page[L::kVScale + (tok0 + tok[i]) * L::kGroups + g * kChan / 16];
                 }
-                if (ragged) {
+                if (masked) {  // slots past the length hold anything
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (key0 + tok[i] >= at.len.kv) sc[i] = 0u;
