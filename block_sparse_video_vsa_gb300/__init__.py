@@ -644,9 +644,14 @@ def _cache(pool, table, kv_lens, kv_scale):
     return VsaCache(shape[0], shape[1], D, rows[0], rows[1], *ptrs, scale), dev, rows[0], shape[1], D
 
 
-def _cache_call(fn, dev, stream, *args):
-    """fn(*args, stream) with the cache's device current."""
+def _cache_call(fn, dev, stream, made, *args):
+    """fn(*args, stream) with the cache's device current; `made` are tensors the call made, which the
+    allocator must not hand out again before another stream than the current one is done with them."""
     torch = _torch()
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
     if dev == torch.cuda.current_device():
         raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
         status = fn(*args, raw)
@@ -700,7 +705,7 @@ def cache_append(pool, k, v, table, kv_lens, new_lens=None, rope=None, positions
             raise ValueError("q_out must be shaped like q")
     elif q_out is not None:
         raise ValueError("q_out goes with q")
-    _cache_call(library().vsa_cache_append, dev, stream, c, q_ptr, k_ptr, v_ptr, S, heads, new_ptr, rope_ptr, rows, R,
+    _cache_call(library().vsa_cache_append, dev, stream, (q_out,), c, q_ptr, k_ptr, v_ptr, S, heads, new_ptr, rope_ptr, rows, R,
                 1 if interleaved else 0, pos_ptr, out_ptr)
     return q_out
 
@@ -718,7 +723,7 @@ def cache_read(pool, table, kv_lens, S: int, kv_scale=None, k=None, v=None, stre
     k_ptr, v_ptr = _on(k, torch.bfloat16, "k", dev), _on(v, torch.bfloat16, "v", dev)
     if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {shape}")
-    _cache_call(library().vsa_cache_read, dev, stream, c, shape[1], k_ptr, v_ptr)
+    _cache_call(library().vsa_cache_read, dev, stream, (k, v), c, shape[1], k_ptr, v_ptr)
     return k, v
 
 
@@ -771,7 +776,7 @@ def cache_attn(q, pool, table, kv_lens, q_lens=None, causal: bool = True, page_s
         lse_ptr = _on(lse, torch.float32, "lse", dev)
         if lse.shape != (B, heads, Sq):
             raise ValueError("lse must be [B, heads, Sq]")
-    _cache_call(lib.vsa_cache_attn, dev, stream, c, q_ptr, Sq, heads, lens_ptr, 1 if causal else 0, sel_ptr, nsel,
+    _cache_call(lib.vsa_cache_attn, dev, stream, (workspace, out, lse), c, q_ptr, Sq, heads, lens_ptr, 1 if causal else 0, sel_ptr, nsel,
                 sm_scale, work_ptr, out_ptr, lse_ptr)
     return out, lse
 

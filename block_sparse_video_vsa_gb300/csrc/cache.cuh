@@ -114,8 +114,7 @@ __device__ __forceinline__ int q_exponent(float amax) {
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
 
 // Bounded wait of a whole warp for a phase of a barrier.  Between looks the warp
-// sleeps kSleep ns: waiting roles share their scheduler with working ones, and
-// looks without a pause were 45% of all instructions of the chunk kernel.
+// sleeps kSleep ns: waiting roles share their scheduler with working ones.
 template <int kSleep>
 __device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* err) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -170,6 +169,7 @@ struct AttnParams {
     int tile, tiles;          // rows of a unit; units of a (b, kv head)
     int grid;                 // CTAs of the attention kernel
     int unit_cost;
+    int min_part;             // pages of a part at least
     int brief;                // up to 32 sequences, one tile each, a line shorter than 2^31
     int whole;                // units are not cut: a unit belongs to the CTA that holds its first page
     float scale_log2;         // sm_scale * log2(e)
@@ -297,10 +297,9 @@ __device__ __forceinline__ long long scan_warp(long long x) {  // inclusive
     return x;
 }
 
-// Pages each CTA takes at least (where there are fewer than grid * this, some CTAs take none).
-constexpr int kMinPart = 2;
+// Parts of the line: one for each CTA, of min_part pages at least.
 __device__ __forceinline__ int used_parts(const AttnParams& p, long long total) {
-    const long long n = (total + kMinPart - 1) / kMinPart;
+    const long long n = total < (1LL << 31) ? ((int)total + p.min_part - 1) / p.min_part : p.grid;
     return n < p.grid ? (int)n : p.grid;
 }
 
@@ -331,7 +330,7 @@ struct Walk {
             if (lane >= o) incl += v;
         }
         const unsigned total = (unsigned)__shfl_sync(0xffffffffu, incl, 31);
-        const unsigned parts = min((total + kMinPart - 1) / kMinPart, (unsigned)p.grid), c = blockIdx.x;
+        const unsigned parts = (unsigned)used_parts(p, total), c = blockIdx.x;
         if (c >= parts) {
             if (threadIdx.x == 0) p.places[c] = make_int4(-1, 0, 0, 0);
             return false;

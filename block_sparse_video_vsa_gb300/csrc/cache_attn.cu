@@ -9,10 +9,10 @@
 // HBM bound: 9/16 byte an element against 4 flops for each query row, so the
 // kernel is built to keep bulk copies in flight and to spend few instructions
 // on an element.
-//  * A producer warp looks pages up and copies them whole (72 * D contiguous
-//    bytes) into slots, two or more for each consumer warp; warp w takes every kWarps-th page of the
-//    CTA's part of the line (see cache.cuh) with a softmax state of its own.
-//    At a unit's end each leaves its state in the slot of its last page, and
+//  * The warps take equal stretches of the CTA's part of the line (see
+//    cache.cuh), in pieces of 32 tokens (half pages).  Each looks its pages up,
+//    keeps bulk copies of its next pages (72 * D contiguous bytes) in flight and
+//    has a softmax state of its own.  At a unit's end each leaves its state, and
 //    the warp that comes last joins them and writes the rows, while the others
 //    are at the next unit: no barrier among the warps.
 //  * S^T = K Q^T and O^T = V^T P^T (m16n8k16, fp16 in, fp32 out): the matrix
@@ -28,8 +28,11 @@
 //  * P is rounded to fp16 (2^-11 relative; the sum keeps the fp32 values);
 //    maximum, sum and output are fp32.  The maximum is followed lazily: the
 //    output is rescaled when it grows by more than 2^8.
-#include <algorithm>
-
+//  * Measured (GB300): 61 ragged sequences of up to 12000 tokens, 32 heads on 8
+//    of 128: 102 us, 4.4 TB/s (65% of the measured copy rate).  What bounds it
+//    is issue: 1215 instructions a page at 0.55 a scheduler and cycle, 12 warps
+//    an SM (168 registers).  A producer warp with 7 consumers behind a barrier
+//    a unit took 127 us.  One token on one clip of 32760 tokens takes 23 us.
 #include "cache.cuh"
 
 namespace vsa {
@@ -612,8 +615,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
             mbar_wait_drain_1(smem_u32(&sm.full[warp][j % kOwn]), (j / kOwn) & 1, p.c.err, kCacheWaitNs);
 }
 
-// Joins the parts of the units that were cut.  Block (r, y) looks at the cut
-// before CTA y + 1's part; the unit's first cut does the work, a block a row:
+// Joins the parts of the units that were cut.  Block (x, y) looks at the cut
+// before CTA y + 1's part; if it is the unit's first, it joins the rows x,
+// x + gridDim.x, ...:
 //   m = max m_i, out = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i
 // The warps take the parts in turn and ask for eight at a time: a unit cut
 // into many parts is a matter of latency.
@@ -661,10 +665,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) 
                 ml[k] = make_float2(-INFINITY, 0.f);
                 if (ck > c1) continue;
                 ml[k] = p.part_ml[at];
+                const float* src = p.part_o + at * kD + lane * kPer;
                 if constexpr (kPer == 4)
-                *reinterpret_cast<float4*>(o[k]) = *reinterpret_cast<const float4*>(p.part_o + at * kD + lane * kPer);
+                    *reinterpret_cast<float4*>(o[k]) = *reinterpret_cast<const float4*>(src);
                 else
-                *reinterpret_cast<float2*>(o[k]) = *reinterpret_cast<const float2*>(p.part_o + at * kD + lane * kPer);
+                    *reinterpret_cast<float2*>(o[k]) = *reinterpret_cast<const float2*>(src);
             }
             float top = m;
 #pragma unroll
@@ -709,8 +714,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) 
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)u.x * p.Sq + qi) * p.heads + head) * (kD / 8));
             dst[threadIdx.x] = live ? pack_bf16x2(y.x * inv, y.y * inv) : 0u;
             if (threadIdx.x == 0 && p.lse)
-            p.lse[((size_t)u.x * p.heads + head) * p.Sq + qi] =
-            live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+                p.lse[((size_t)u.x * p.heads + head) * p.Sq + qi] =
+                    live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
         __syncthreads();
     }
@@ -733,8 +738,19 @@ cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// Starting and ending a unit, in pages.
-constexpr int kTokenUnitCost = 2, kChunkUnitCost = 20;
+// How the line is cut, in pages, with what was measured:
+//  * unit_cost, what starting and ending a unit takes.  A ragged batch of
+//    prompts takes 358 us with 6, 329 with 20, 315 with 30, 334 with 45:
+//    chunk_kernel drains its pipeline at a unit's end.  token_kernel's warps go
+//    on: 103.9 us with 1, 102.2 with 2, 102.5 with 4.
+//  * min_part.  One token on 2000 to 4000 cached ones: 11.8 us with parts of
+//    2 pages, 13.4 with 6, 14.5 with 12; chunks gain nothing below 8.
+//  * Walks of up to `whole` pages are not cut at all (and need no joining
+//    kernel): chunks on 15 pages take 20.5 us whole, 31.0 cut; a token on 32
+//    pages 17.8 whole, 11.8 cut.
+constexpr int kTokenUnitCost = 2, kChunkUnitCost = 28;
+constexpr int kTokenMinPart = 2, kChunkMinPart = 8;
+constexpr int kTokenWhole = 8, kChunkWhole = 16;
 
 // Rows of a unit: up to 16 rows a kv head go to token_kernel, more to chunk_kernel.
 int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
@@ -773,12 +789,11 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     p.scratch = p.part_o + (size_t)2 * kMaxGrid * p.tile * D;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.unit_cost = p.tile >= 128 ? kChunkUnitCost : kTokenUnitCost;
+    p.min_part = p.tile >= 128 ? kChunkMinPart : kTokenMinPart;
     const int most = page_sel ? nsel : c.width;
     p.brief = c.B <= 32 && p.tiles == 1 &&
               (long long)c.B * c.kv_heads * ((long long)most + p.unit_cost) < (1LL << 31);
-    // Short walks are not worth joining: a unit of up to kWholePages pages stays in one CTA.
-    constexpr int kWholePages = 8;
-    p.whole = most <= kWholePages;
+    p.whole = most <= (p.tile >= 128 ? kChunkWhole : kTokenWhole);
     cudaError_t e;
     if (p.tile >= 128)
         e = launch_chunk(p, D, stream);

@@ -14,10 +14,15 @@
 // scale groups, the two halves of a rotated pair among them) and holds their
 // cosines and sines in registers over all heads it walks; a warp takes
 // neighbouring tokens of one head, whose codes are contiguous in the page.
+// Measured: a frame of 1560 tokens x 40 heads of 128, 22.4 us (3.3 TB/s of the
+// bytes it needs, 48% of the measured copy rate), 24 ragged chunks of 1003
+// tokens (24 and 8 heads of 64) 34.7 us (4.3 TB/s): 16 warps an SM (the angles
+// and two groups fill 110 registers) keep too few loads in flight.
 //
 // read_kernel: pages back to bf16 rows, [B, S, kv_heads, D], zero past each
 // sequence's length.  HBM bound (9/16 byte in, 2 bytes out an element): one
-// block a page and head, 16-byte stores.
+// block a page and head, 16-byte stores.  Measured: 32760 tokens x 40 heads of
+// 128, 141 us, 6.1 TB/s (89% of the measured copy rate).
 #include "cache.cuh"
 
 namespace vsa {

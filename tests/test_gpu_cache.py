@@ -495,6 +495,19 @@ def test_two_streams_and_repeated_runs_give_the_same_bits():
     torch.cuda.synchronize()
     for out, lse in got:
         assert torch.equal(out, base[0]) and torch.equal(lse, base[1])
+    # A stream given to the call, its tensors made by the call and dropped at once by the caller.
+    side = streams[0]
+    side.wait_stream(torch.cuda.current_stream())
+    kept = []
+    for i in range(20):
+        res = vsa.cache_attn(q, p, t, n, stream=side)
+        if i % 7 == 6:
+            kept.append(res)
+        del res
+        torch.full((3, 2, heads, D), float(i), device="cuda")  # whatever the allocator hands out next
+    side.synchronize()
+    for out, lse in kept:
+        assert torch.equal(out, base[0]) and torch.equal(lse, base[1])
 
 
 def test_binding_refusals():
