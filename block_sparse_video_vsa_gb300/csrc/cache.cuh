@@ -147,7 +147,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // A unit is (sequence b, kv head, tile of `tile` query rows); row r is head
 // kv_head * group + r % group of query r / group.  Units are laid end to end
 // in the order (b, kv head, tile), each as long as the pages it walks plus
-// unit_cost (what starting and ending a unit costs, in pages), and the line
+// unit_cost (what starting and ending a unit costs, in pages; idle_cost for a
+// unit that walks none and is written as zeros), and the line
 // is cut into equal parts, one for each CTA: batches of ragged lengths and
 // single long sequences fill the grid alike.  A unit that lies in one part
 // is written by its CTA; the parts of a cut unit go to the workspace (two
@@ -168,7 +169,7 @@ struct AttnParams {
     int Sq, heads, group, nsel, causal;
     int tile, tiles;          // rows of a unit; units of a (b, kv head)
     int grid;                 // CTAs of the attention kernel
-    int unit_cost;
+    int unit_cost, idle_cost;  // of a unit beside its pages, of one without pages
     int min_part;             // pages of a part at least
     int brief;                // up to 32 sequences, one tile each, a line shorter than 2^31
     int whole;                // units are not cut: a unit belongs to the CTA that holds its first page
@@ -198,7 +199,8 @@ __device__ __forceinline__ int tile_pages(const AttnParams& p, const SeqLens& s,
     return lim > 0 ? (lim + kPageTokens - 1) / kPageTokens : 0;
 }
 __device__ __forceinline__ int tile_cost(const AttnParams& p, const SeqLens& s, int t) {
-    return tile_pages(p, s, t) + p.unit_cost;
+    const int n = tile_pages(p, s, t);
+    return n > 0 ? n + p.unit_cost : p.idle_cost;
 }
 // sum of floor((a i + b) / m) for i < n (a, b >= 0, m > 0), by Euclid's steps on (a, m).
 static __device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
@@ -226,8 +228,13 @@ static __device__ __noinline__ long long floor_sum(long long n, long long m, lon
 __device__ __forceinline__ long long head_cost(const AttnParams& p, const SeqLens& s) {
     if (p.tiles == 1) return tile_cost(p, s, 0);
     const int live = min(p.tiles, (s.q * p.group + p.tile - 1) / p.tile);
-    const long long ends = (long long)p.tiles * p.unit_cost;
-    if (!p.causal || p.page_sel || live <= 1) return ends + (long long)live * tile_pages(p, s, 0);
+    const auto sum = [&](int with, long long pages) {  // tiles with pages, pages of all
+        return pages + (long long)with * p.unit_cost + (long long)(p.tiles - with) * p.idle_cost;
+    };
+    if (!p.causal || p.page_sel || live <= 1) {
+        const int n = tile_pages(p, s, 0);
+        return sum(n > 0 ? live : 0, (long long)live * n);
+    }
     // Tile t but the last sees keys up to its last row's place,
     //   pages = ceil((kv - q + 1 + floor(((t + 1) tile - 1) / group)) / 64)
     //         = floor((tile t + tile - 1 + group (kv - q + 64)) / (64 group)),
@@ -235,7 +242,8 @@ __device__ __forceinline__ long long head_cost(const AttnParams& p, const SeqLen
     const long long lead = (long long)p.group * (s.kv - s.q + kPageTokens) + p.tile - 1, per = 64LL * p.group;
     long long none = 0;
     if (lead < per) none = min((long long)live - 1, (per - lead + p.tile - 1) / p.tile);
-    return ends + tile_pages(p, s, live - 1) + floor_sum(live - 1 - none, per, p.tile, lead + none * p.tile);
+    const int end = tile_pages(p, s, live - 1);
+    return sum(live - (int)none - (end == 0), end + floor_sum(live - 1 - none, per, p.tile, lead + none * p.tile));
 }
 
 // A place on the line: page `page` of unit (b, h, t) (from the unit's number of pages on: its end).

@@ -748,7 +748,7 @@ cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
 //  * Walks of up to `whole` pages are not cut at all (and need no joining
 //    kernel): chunks on 15 pages take 20.5 us whole, 31.0 cut; a token on 32
 //    pages 17.8 whole, 11.8 cut.
-constexpr int kTokenUnitCost = 2, kChunkUnitCost = 28;
+constexpr int kTokenUnitCost = 2, kChunkUnitCost = 28, kIdleCost = 2;
 constexpr int kTokenMinPart = 2, kChunkMinPart = 8;
 constexpr int kTokenWhole = 8, kChunkWhole = 16;
 
@@ -789,6 +789,7 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     p.scratch = p.part_o + (size_t)2 * kMaxGrid * p.tile * D;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.unit_cost = p.tile >= 128 ? kChunkUnitCost : kTokenUnitCost;
+    p.idle_cost = kIdleCost;
     p.min_part = p.tile >= 128 ? kChunkMinPart : kTokenMinPart;
     const int most = page_sel ? nsel : c.width;
     p.brief = c.B <= 32 && p.tiles == 1 &&

@@ -36,9 +36,10 @@ namespace vsa {
 namespace {
 
 constexpr int kChunkThreads = 640;
-constexpr int kKStages = 2, kVStages = 3;
+constexpr int kKStages = 2;
 constexpr int kMetaSteps = 16;
 constexpr int kRawHalves = 4;  // slots of a ring of half pages
+constexpr int kRowPitch = 256 + 16;  // bytes of a row on its way in (queries) or out: rows start in other banks
 // Registers: 5 warpgroups launched with 96 each; the shares add up to 480.
 constexpr int kLaunchRegs = 96, kIssueRegs = 48, kConvertRegs = 56, kSoftRegs = 160;
 static_assert(kIssueRegs + 2 * kConvertRegs + 2 * kSoftRegs <= 5 * kLaunchRegs, "register split exceeds the launch");
@@ -51,28 +52,31 @@ struct ChunkSmem {
     static constexpr int kTile = kHalf * (kD / 64);  // K or V of a step
     static constexpr int kCodes = kPageTokens * kD / 2, kScales = kPageTokens * kD / 16;
     static constexpr int kRawBytes = kCodes + kScales;
+    static constexpr int kVStages = kD == 64 ? 3 : 2;  // (as many as fit)
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kKStages * kTile;
     static constexpr int kOffRaw = kOffV + kVStages * kTile;  // [K, V][slot]
-    static constexpr int kOffMisc = kOffRaw + 2 * kRawHalves * kRawBytes;
+    static constexpr int kOffRows = kOffRaw + 2 * kRawHalves * kRawBytes;
+    static constexpr int kOffMisc = kOffRows + 128 * kRowPitch;
 };
 
-// A softmax warp's walk and its present and next unit: kept in shared memory,
-// the steps need the registers.
+// A softmax warp's walk, its present unit and the two after that: kept in
+// shared memory, the steps need the registers.
 struct SoftWalk {
     Walk walk;
-    Segment unit[2];
+    Segment unit[3];
 };
 
 struct __align__(16) ChunkMisc {
     uint64_t raw_full[2][kRawHalves], raw_empty[2][kRawHalves];  // of K, of V
     uint64_t k_full[kKStages], k_empty[kKStages];
-    uint64_t v_full[kVStages], v_empty[kVStages];
+    uint64_t v_full[3], v_empty[3];
     uint64_t s_full[2];  // per softmax group: S of its next step is ready
     uint64_t s_free;     // S has been loaded into registers
     uint64_t p_full;     // P of the step (and any rescaling of O) is in TMEM
     uint64_t pv_grp[2];  // per group: P V of its step has completed
     uint64_t unit_done;  // every P V of the unit has completed
+    uint64_t rows_full;  // the next unit's queries are in the row buffer
     uint64_t q_full, q_empty;
     uint64_t o_free;     // O_0 and O_1 have been read by the unit's epilogue
     uint64_t drain[2];
@@ -133,35 +137,6 @@ __device__ __forceinline__ void chunk_exp64(const float* x, float c2, float mb, 
 
 __device__ __forceinline__ int steps_of(const Segment& s) { return (s.last - s.first + 1) >> 1; }
 
-// Softmax thread of row r: puts its query row of unit s into the TMEM Q
-// columns of its lane as fp16, scaled by a power of two, and returns the row's
-// factor from logits to log2 units.
-template <int kD>
-__device__ __forceinline__ float stage_query(const AttnParams& p, const Segment& s, int r, uint32_t t_lane) {
-    const int row = s.t * 128 + r;
-    const bool real = row < p.Sq * p.group;
-    const int qi = real ? row / p.group : 0;
-    const int head = s.h * p.group + (real ? row - qi * p.group : 0);
-    const uint4* src = p.q + (((size_t)s.b * p.Sq + qi) * p.heads + head) * (kD / 8);
-    uint32_t w[kD / 2];
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < kD / 8; ++i) {
-        const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
-    }
-#pragma unroll
-    for (int i = 0; i < kD / 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
-    const int e = q_exponent(amax);
-    const float f = pow2i(e);
-#pragma unroll
-    for (int i = 0; i < kD / 2; ++i) w[i] = pack_f16x2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
-#pragma unroll
-    for (int c0 = 0; c0 < kD / 2; c0 += 32) tmem_st32(t_lane + kTmemQ + c0, *reinterpret_cast<uint32_t(*)[32]>(&w[c0]));
-    tmem_wait_st();
-    return p.scale_log2 * (p.c.kv_scale ? __ldg(p.c.kv_scale + s.h) : 1.f) * pow2i(-e);
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 x;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
@@ -169,6 +144,85 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
 }
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Row r of unit s in q or out, in 16-byte pieces; real: there is such a row.
+struct RowAt {
+    int head, qi;
+    bool real;
+    size_t at;
+};
+template <int kD>
+__device__ __forceinline__ RowAt row_at(const AttnParams& p, const Segment& s, int r) {
+    RowAt x;
+    const int row = s.t * 128 + r;
+    x.real = row < p.Sq * p.group;
+    x.qi = x.real ? row / p.group : 0;
+    x.head = s.h * p.group + (x.real ? row - x.qi * p.group : 0);
+    x.at = (((size_t)s.b * p.Sq + x.qi) * p.heads + x.head) * (kD / 8);
+    return x;
+}
+
+// This thread's asynchronous 16-byte copies arrive on `bar` once they have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Rows [r0, r0 + 64) of a unit that has nothing to attend (a whole warp calls it).
+template <int kD>
+__device__ __forceinline__ void no_keys(const AttnParams& p, const Segment& s, int r0) {
+    constexpr int kLanes = kD / 8;  // of a row
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int r = r0; r < r0 + 64; r += 32) {
+        const RowAt x = row_at<kD>(p, s, r + lane);
+        if (x.real && p.lse) p.lse[((size_t)s.b * p.heads + x.head) * p.Sq + x.qi] = -INFINITY;
+        const unsigned reals = __ballot_sync(0xffffffffu, x.real);
+#pragma unroll 1
+        for (int k = lane / kLanes; k < 32; k += 32 / kLanes) {
+            const size_t at = __shfl_sync(0xffffffffu, x.at, k) + lane % kLanes;
+            if ((reals >> k) & 1u) p.out[at] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// Softmax thread of a row: puts its query (at `src` in shared memory, the second
+// half of its channels 128 bytes after the first) into the
+// TMEM Q columns of its lane as fp16, scaled by a power of two, and returns the
+// power.  The largest magnitude is found as integers: the bit patterns of bf16
+// magnitudes are in their order.  (Short loops: code that runs once a unit costs
+// more to fetch than to run.)
+template <int kD>
+__device__ __forceinline__ int stage_query(uint32_t src, uint32_t t_q) {
+    uint32_t mx = 0u;
+#pragma unroll 1
+    for (int c = 0; c < kD * 2; c += 64) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 x = lds128(src + c * (128 / kD) + 16 * i);
+            mx = __vimax3_u16x2(mx, x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu);
+            mx = __vimax3_u16x2(mx, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu);
+        }
+    }
+    const int e = q_exponent(__uint_as_float(max(mx & 0xFFFFu, mx >> 16) << 16));
+    const float f = pow2i(e);
+#pragma unroll 1
+    for (int c = 0; c < kD * 2; c += 64) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 x = lds128(src + c * (128 / kD) + 16 * i);
+            w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 x = __fmul2_rn(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), make_float2(f, f));
+            w[i] = pack_f16x2(x.x, x.y);
+        }
+        tmem_st16(t_q + c / 4, w);
+    }
+    tmem_wait_st();
+    return e;
 }
 
 // Half of one key's codes of K or V and their scales (`codes`, `scales`: the
@@ -248,7 +302,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             mbar_init(smem_u32(&ms.k_full[s]), 4);
             mbar_init(smem_u32(&ms.k_empty[s]), 1);
         }
-        for (int s = 0; s < kVStages; ++s) {
+        for (int s = 0; s < Sm::kVStages; ++s) {
             mbar_init(smem_u32(&ms.v_full[s]), 4);
             mbar_init(smem_u32(&ms.v_empty[s]), 1);
         }
@@ -260,6 +314,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         mbar_init(smem_u32(&ms.s_free), 4);
         mbar_init(smem_u32(&ms.p_full), 4);
         mbar_init(smem_u32(&ms.unit_done), 1);
+        mbar_init(smem_u32(&ms.rows_full), 256);
         mbar_init(smem_u32(&ms.q_full), 4);
         mbar_init(smem_u32(&ms.q_empty), 1);
         mbar_init(smem_u32(&ms.o_free), 8);
@@ -294,6 +349,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             uint32_t g = 0;  // steps so far
             bool ok = true;
             for (Segment sg; ok && walk.next(p, sg);) {
+                if (sg.first == sg.last) {  // a unit without pages: zeros, half of the rows by each producer
+                    no_keys<kD>(p, sg, side * 64);
+                    continue;
+                }
                 const unsigned char* pool = p.c.pool + (size_t)sg.h * L::kBytes + (side ? L::kV : 0);
                 for (int base = sg.first; base < sg.last && ok; base += 32) {
                     int logical = 0, id = -1;
@@ -346,11 +405,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             const uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
             const uint32_t lo_k = (uint32_t)smem_desc_sw128(sbase + Sm::kOffK, 16, 1024);
             Ring<kKStages> ring;
-            uint32_t g = 0, ul = 0;
+            uint32_t g = 0, ul = 0;  // so far: steps, units with steps
             bool ok = true;
-            for (Segment sg; ok && walk.next(p, sg); ++ul) {
+            for (Segment sg; ok && walk.next(p, sg);) {
                 const int nst = steps_of(sg);
-                ok = cache_wait<kSleepShort>(smem_u32(&ms.q_full), ul & 1, abort_flag, err);
+                if (nst == 0) continue;
+                ok = cache_wait<kSleepShort>(smem_u32(&ms.q_full), ul++ & 1, abort_flag, err);
                 for (int t = 0; t < nst && ok; ++t, ++g, ring.step()) {
                     if (g >= 1)
                         ok = cache_wait<kSleepShort>(smem_u32(&ms.s_free), (g - 1) & 1, abort_flag, err);
@@ -378,13 +438,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);
             const uint32_t idesc = idesc_f16_f32(128, kD, 0, 1);
             const uint32_t lo_v = (uint32_t)smem_desc_sw128(sbase + Sm::kOffV, Sm::kHalf, 1024);
-            Ring<kVStages> ring;
-            uint32_t g = 0, ul = 0;
+            Ring<Sm::kVStages> ring;
+            uint32_t g = 0, ul = 0;  // so far: steps, units with steps
             bool ok = true;
-            for (Segment sg; ok && walk.next(p, sg); ++ul) {
+            for (Segment sg; ok && walk.next(p, sg);) {
                 const int nst = steps_of(sg);
-                // O_0 and O_1 start over once the last epilogue has read them (a
-                // unit without steps waits too: unit_done stays one phase ahead).
+                if (nst == 0) continue;
+                // O_0 and O_1 start over once the last epilogue has read them.
                 if (ul >= 1) ok = cache_wait<kSleepShort>(smem_u32(&ms.o_free), (ul - 1) & 1, abort_flag, err);
                 for (int t = 0; t < nst && ok; ++t, ++g, ring.step()) {
                     const int slot = ring.slot;
@@ -408,6 +468,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                     mma_commit_warp(smem_u32(&ms.v_empty[slot]));
                 }
                 if (!ok) break;
+                ++ul;
                 mma_commit_warp(smem_u32(&ms.unit_done));
             }
             mma_commit_warp(smem_u32(&ms.drain[1]));
@@ -422,7 +483,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         const uint32_t raw_at = sbase + Sm::kOffRaw + side * kRawHalves * Sm::kRawBytes;
         const uint32_t tiles = sbase + (side ? Sm::kOffV : Sm::kOffK);
         const uint32_t full = smem_u32(side ? ms.v_full : ms.k_full), empty = smem_u32(side ? ms.v_empty : ms.k_empty);
-        const int stages = side ? kVStages : kKStages;
+        const int stages = side ? Sm::kVStages : kKStages;
         Ring<kRawHalves> raw;
         int st = 0;
         uint32_t turn = 0;  // of the tile's ring
@@ -464,12 +525,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         constexpr int dh = kD / 2;  // output columns of this thread: [G * dh, G * dh + dh)
         const float ninf = -INFINITY;
         bool ok = true;
-        uint32_t g0 = 0, ul = 0;  // steps before the unit, units
+        uint32_t g0 = 0, ul = 0;  // steps before the unit, units with steps
         SoftWalk& sw = ms.soft[warp - 12];
-        auto advance = [&](int to) -> bool {  // the walk's next unit into sw.unit[to]
+        auto advance = [&](int to) -> bool {  // the walk's next unit with steps into sw.unit[to]
             Walk w = sw.walk;
             Segment s;
-            const bool has = w.next(p, s);
+            bool has;
+            do has = w.next(p, s);
+            while (has && s.first == s.last);
             __syncwarp();
             if (lane == 0) {
                 sw.walk = w;
@@ -480,34 +543,48 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         };
         if (lane == 0) sw.walk = walk;
         __syncwarp();
-        bool more = advance(0);
-        if (G == 0 && more) {
-            ms.scale[0][r] = stage_query<kD>(p, sw.unit[0], r, t_lane);
-            tc_fence_before();
+        const uint32_t row_s = sbase + Sm::kOffRows + r * kRowPitch;  // the row's place in the row buffer
+        auto queries = [&](const Segment& s, uint32_t u) {  // of unit s, the u-th
+            if (ok) ok = cache_wait<kSleepShort>(smem_u32(&ms.rows_full), u & 1, abort_flag, err);
+            if (ok) {
+                tc_fence_after();
+                const int e = stage_query<kD>(row_s, t_lane + kTmemQ);
+                ms.scale[u & 1][r] = p.scale_log2 * (p.c.kv_scale ? __ldg(p.c.kv_scale + s.h) : 1.f) * pow2i(-e);
+                tc_fence_before();
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ms.q_full));
+        };
+        // This warp's share of the queries of unit s on their way to the row
+        // buffer: half G of the channels of its quarter's rows.
+        const uint32_t mine = row_s + G * 128;
+        auto ask_queries = [&](const Segment& s) {
+            constexpr int kLanes = kD / 16, kRows = 32 / kLanes;  // lanes of a half row, rows a turn
+            const RowAt x = row_at<kD>(p, s, r);
+            const unsigned reals = __ballot_sync(0xffffffffu, x.real);
+            const int sub = lane % kLanes;
+#pragma unroll 1
+            for (int k = lane / kLanes; k < 32; k += kRows) {
+                const size_t at = __shfl_sync(0xffffffffu, x.at, k) + G * kLanes + sub;
+                if ((reals >> k) & 1u) cp_async16(mine + (k - lane) * kRowPitch + sub * 16, p.q + at);
+            }
+            cp_async_arrive(smem_u32(&ms.rows_full));
+        };
+        auto place = [](uint32_t u) { return (int)(u % 3u); };
+        bool more = advance(0), next = more && advance(1);
+        if (more) {
+            ask_queries(sw.unit[0]);
+            if (G == 0) queries(sw.unit[0], 0);
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+            if (next) ask_queries(sw.unit[1]);
         }
 #pragma unroll 1
         for (; more; ++ul) {
-            const bool next = advance((ul + 1) & 1);
-            const Segment& sg = sw.unit[ul & 1];
+            const Segment& sg = sw.unit[place(ul)];
             const int nst = steps_of(sg);
-            const int row = sg.t * 128 + r;
-            const int live_rows = sg.len.q * p.group;
             int lim = sg.len.kv;  // first key the row does not see
-            if (p.causal && row < live_rows) lim = max(0, min(lim, sg.len.kv - sg.len.q + row / p.group + 1));
-            // The group that takes the next unit's first step stages its queries.
-            const bool stager = next && ((g0 + nst) & 1) == (uint32_t)G;
-            if (stager) {
-                const Segment& nx = sw.unit[(ul + 1) & 1];
-                const int nrow = nx.t * 128 + r, ni = nrow / p.group;
-                if (ni < p.Sq) {
-                    const uint4* src = p.q + (((size_t)nx.b * p.Sq + ni) * p.heads + nx.h * p.group + nrow -
-                                              ni * p.group) * (kD / 8);
-#pragma unroll
-                    for (int c = 0; c < kD * 2; c += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c / 16));
-                }
-            }
+            if (p.causal && sg.t * 128 + r < sg.len.q * p.group)
+                lim = max(0, min(lim, sg.len.kv - sg.len.q + (sg.t * 128 + r) / p.group + 1));
             float c2 = 0.f, m = ninf, l = 0.f;
             bool first = true;
 #pragma unroll 1
@@ -576,17 +653,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                 if (lane == 0) mbar_arrive(smem_u32(&ms.p_full));
                 first = false;
             }
-            if (stager) {
+            // The group that takes the next unit's first step stages its queries.
+            if (next && ((g0 + nst) & 1) == (uint32_t)G) {
                 // The unit's Q K^T have completed: Q may be overwritten.
                 if (ok) ok = cache_wait<kSleepShort>(smem_u32(&ms.q_empty), ul & 1, abort_flag, err);
-                if (ok) {
-                    tc_fence_after();
-                    ms.scale[(ul + 1) & 1][r] = stage_query<kD>(p, sw.unit[(ul + 1) & 1], r, t_lane);
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms.q_full));
+                queries(sw.unit[place(ul + 1)], ul + 1);
             }
+            const bool after = next && advance(place(ul + 2));
             // ------------------------------------------------ unit epilogue
             //   m = max(m_0, m_1), a_k = 2^(m_k - m), l = a_0 l_0 + a_1 l_1, O = a_0 O_0 + a_1 O_1
             ms.xm[ul & 1][G][r] = m;
@@ -602,11 +675,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             float a_o = m_o == ninf ? 0.f : ex2_approx(m_o - mt);
             const float lt = __fmaf_rn(a_e, l_e, __fmul_rn(a_o, l_o));
             const uint32_t o_e = ge ? kTmemO1 : kTmemO0, o_o = ge ? kTmemO0 : kTmemO1;
-            const bool has_e = nst > 0, has_o = nst > 1;  // a group without a step holds no O of the unit
-            const bool real = ok && row < p.Sq * p.group;
-            const int qi = real ? row / p.group : 0;
-            const int head = sg.h * p.group + (real ? row - qi * p.group : 0);
-            const bool live = row < live_rows && lt != 0.f;
+            const RowAt x = row_at<kD>(p, sg, r);
+            const bool real = ok && x.real;
+            const bool live = sg.t * 128 + r < sg.len.q * p.group && lt != 0.f;
             const size_t part = (2 * (size_t)blockIdx.x + (sg.first > 0 ? 0 : 1)) * 128 + r;
             if (sg.whole) {
                 const float inv =
@@ -616,33 +687,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             }
             if (ok) ok = cache_wait<kSleepShort>(smem_u32(&ms.unit_done), ul & 1, abort_flag, err);
             tc_fence_after();
-            uint4* dst = p.out + (((size_t)sg.b * p.Sq + qi) * p.heads + head) * (kD / 8) + G * (dh / 8);
-            float4* dst_part = reinterpret_cast<float4*>(p.part_o + part * kD + G * dh);
+            // Each thread's columns go to its place in the row buffer (the bar.sync
+            // above: the next queries have been taken from there), and from there
+            // to memory by the lanes together, 64 or 128 bytes of a row: lanes
+            // that store rows of their own take some 3 cycles a lane and piece.
+            const unsigned reals = __ballot_sync(0xffffffffu, real);
+            const bool whole = sg.whole;
+            const size_t to = whole ? x.at + G * (dh / 8) : (part * kD + G * dh) / 4;  // in 16 bytes
+            uint4* const base = whole ? p.out : reinterpret_cast<uint4*>(p.part_o);
+            const int lanes = whole ? 4 : 8, sub = lane & (lanes - 1);  // of a row
 #pragma unroll 1
             for (int c0 = 0; c0 < dh; c0 += 32) {
-                uint32_t oa[32], ob[32];
-                tmem_ld32(t_lane + o_e + G * dh + c0, oa);
-                tmem_ld32(t_lane + o_o + G * dh + c0, ob);
-                tmem_wait_ld();
-                float f[32];
+                uint32_t o[32];
+                float2 f[16];
 #pragma unroll
-                for (int q = 0; q < 32; ++q)
-                    f[q] = __fmaf_rn(a_e, has_e ? __uint_as_float(oa[q]) : 0.f,
-                                     __fmul_rn(a_o, has_o ? __uint_as_float(ob[q]) : 0.f));
-                if (!real || !ok) continue;
-                if (sg.whole) {
+                for (int q = 0; q < 16; ++q) f[q] = make_float2(0.f, 0.f);
+#pragma unroll 1
+                for (int side = 0; side < min(nst, 2); ++side) {  // (a group without a step holds no O of the unit)
+                    tmem_ld32(t_lane + (side ? o_o : o_e) + G * dh + c0, o);
+                    tmem_wait_ld();
+                    const float2 a = side ? make_float2(a_o, a_o) : make_float2(a_e, a_e);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint32_t w[4];
+                    for (int q = 0; q < 16; ++q)
+                        f[q] = __ffma2_rn(make_float2(__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1])), a, f[q]);
+                }
+                if (whole) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) w[q] = live ? pack_bf16x2(f[8 * v + 2 * q], f[8 * v + 2 * q + 1]) : 0u;
-                        __stcs(dst + c0 / 8 + v, make_uint4(w[0], w[1], w[2], w[3]));
-                    }
+                    for (int q = 0; q < 16; ++q) o[q] = live ? pack_bf16x2(f[q].x, f[q].y) : 0u;
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4) sts128(mine + q * 4, o[q], o[q + 1], o[q + 2], o[q + 3]);
                 } else {
 #pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        dst_part[c0 / 4 + v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
+                    for (int q = 0; q < 16; q += 2)
+                        sts128(mine + q * 8, __float_as_uint(f[q].x), __float_as_uint(f[q].y),
+                               __float_as_uint(f[q + 1].x), __float_as_uint(f[q + 1].y));
                 }
+                __syncwarp();
+#pragma unroll 1
+                for (int k = lane / lanes; k < 32; k += 32 / lanes) {  // row k of the warp
+                    const size_t at = __shfl_sync(0xffffffffu, to, k) + sub;
+                    const uint4 y = lds128(mine + (k - lane) * kRowPitch + sub * 16);
+                    if ((reals >> k) & 1u) base[at + c0 / (whole ? 8 : 4)] = y;
+                }
+                __syncwarp();
             }
             // O_0 and O_1 have been read: the next unit may start them over.
             tc_fence_before();
@@ -652,12 +739,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                 if (!sg.whole)
                     p.part_ml[part] = make_float2(mt, lt);
                 else if (p.lse)
-                    p.lse[((size_t)sg.b * p.heads + head) * p.Sq + qi] =
+                    p.lse[((size_t)sg.b * p.heads + x.head) * p.Sq + x.qi] =
                         live ? (mt + __log2f(lt)) * 0.69314718055994531f : ninf;
             }
+            if (after) ask_queries(sw.unit[place(ul + 2)]);
             g0 += nst;
             more = next;
+            next = after;
         }
+        cp_async_wait<0>();
     }
 
     // ------------------------------------------------------------- teardown
