@@ -14,10 +14,12 @@
 // scale groups, the two halves of a rotated pair among them) and holds their
 // cosines and sines in registers over all heads it walks; a warp takes
 // neighbouring tokens of one head, whose codes are contiguous in the page.
-// Measured: a frame of 1560 tokens x 40 heads of 128, 22.4 us (3.3 TB/s of the
-// bytes it needs, 48% of the measured copy rate), 24 ragged chunks of 1003
-// tokens (24 and 8 heads of 64) 34.7 us (4.3 TB/s): 16 warps an SM (the angles
-// and two groups fill 110 registers) keep too few loads in flight.
+// Measured: a frame of 1560 tokens x 40 heads of 128, 18.6 us (3.9 TB/s of the
+// bytes it needs, 58% of the measured copy rate), 24 ragged chunks of up to 1003
+// tokens (24 and 8 heads of 64) 34.4 us (4.3 TB/s, 64%).  16 warps an SM issue 0.47
+// instructions a scheduler and cycle and wait for loads otherwise; neither a
+// second row on its way nor 16 channels a thread (32 warps an SM, 20.1 and
+// 40.3 us) changes that for the better.
 //
 // read_kernel: pages back to bf16 rows, [B, S, kv_heads, D], zero past each
 // sequence's length.  HBM bound (9/16 byte in, 2 bytes out an element): one
@@ -128,10 +130,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
     const size_t token = (size_t)b * p.S + tok;
     const int hq = p.q_out ? p.heads : 0;
     const int all = hq + 2 * p.c.kv_heads;
-    // The two groups of 16 channels: [g0, g0 + 16) and [g1, g1 + 16).
-    const bool turned = slice * 32 < p.R;
-    const int g0 = turned && !kPairs ? slice * 16 : slice * 32;
-    const int g1 = turned && !kPairs ? slice * 16 + p.R / 2 : slice * 32 + 16;
+    // The two groups of 16 channels: [g0, g0 + 16) and [g1, g1 + 16), rotated or
+    // not.  Neighbouring lanes take neighbouring groups as far as the pairs
+    // allow: an access then covers lines rather than every other sector of them.
+    const int R0 = kPairs || slice * 32 < p.R ? 0 : p.R;  // halves: the channels that stay as they are begin at R
+    const int g0 = R0 + (slice - R0 / 32) * 16;
+    const int g1 = g0 + (kPairs ? kD : R0 == 0 && p.R > 0 ? p.R : kD - p.R) / 2;
+    const bool turn0 = g0 < p.R, turn1 = kPairs ? g1 < p.R : turn0;
     const int step = gridDim.y * kHeadLanes;
     // Head h of all: a query head, a key head or a value head; its row of the token.
     auto row_of = [&](int h) -> const unsigned char* {
@@ -161,14 +166,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
     }
     const int in_page = at % kPageTokens;
     float cs[16], sn[16];
-    if (turned && live) {
+    if (turn0 && live) {
         const int pos = p.positions ? __ldg(p.positions + (size_t)b * p.S + tok) : at;
         if (pos >= 0 && pos < p.rope_rows) {
-            const float4* row = reinterpret_cast<const float4*>(p.rope + (size_t)pos * p.R + slice * 16);
-            const float4* row_s = row + p.R / 8;
+            // Angle i is that of channels (g0 + 2i, + 1) and, from 8 on, (g1 + 2i - 16, + 1), or of (g0 + i, g1 + i).
+            const float4* row = reinterpret_cast<const float4*>(p.rope + (size_t)pos * p.R + (kPairs ? g0 / 2 : g0));
+            const int skip = kPairs ? (turn1 ? (g1 - g0) / 8 - 2 : -2) : 0;  // of 16 bytes, to the second group's
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float4 u = __ldg(row + i), w = __ldg(row_s + i);
+                const float4* at4 = row + i + (i < 2 ? 0 : skip);
+                const float4 u = __ldg(at4), w = __ldg(at4 + p.R / 8);
                 cs[4 * i] = u.x; cs[4 * i + 1] = u.y; cs[4 * i + 2] = u.z; cs[4 * i + 3] = u.w;
                 sn[4 * i] = w.x; sn[4 * i + 1] = w.y; sn[4 * i + 2] = w.z; sn[4 * i + 3] = w.w;
             }
@@ -204,10 +211,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
         }
         const bool is_q = h < hq, is_k = !is_q && h < hq + p.c.kv_heads;
         const int kh = is_q ? h : is_k ? h - hq : h - hq - p.c.kv_heads;
-        if (turned && (is_q || is_k)) {
+        if (turn0 && (is_q || is_k)) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                // Pair i: (2i, 2i + 1) of the 32 channels, or (i, 16 + i) of the two halves.
+                if (kPairs && i >= 8 && !turn1) break;
+                // Pair i: (2i, 2i + 1) of the 32 channels, or (i, 16 + i) of the two groups.
                 float& u = x[kPairs ? 2 * i : i];
                 float& w = x[kPairs ? 2 * i + 1 : 16 + i];
                 const float y = u, z = w;
@@ -327,10 +335,11 @@ cudaError_t launch_cache_append(const CacheView& c, int D, const void* q, const 
     const int tok = S >= 8 ? 8 : 1;
     const int lanes = kAppendThreads / (D / 32 * tok);
     const int bx = (S + tok - 1) / tok;
-    // Heads are spread over blocks until there are some eight for each SM, and not further.
+    // Heads are spread over blocks as long as all blocks are resident at once (four
+    // an SM): a frame's 585 blocks take 18.6 us, 1560 in 2.6 turns 22.5.
     const int most = (all + lanes - 1) / lanes;
     const long long blocks = (long long)bx * c.B;
-    int by = (int)((8LL * num_sms + blocks - 1) / blocks);
+    int by = (int)(4LL * num_sms / blocks);
     by = by < 1 ? 1 : by > most ? most : by;
     const dim3 grid((unsigned)bx, (unsigned)by, (unsigned)c.B);
     auto of_d64 = interleaved ? (tok == 8 ? append_kernel<64, 8, true> : append_kernel<64, 1, true>)
