@@ -644,14 +644,21 @@ def _cache(pool, table, kv_lens, kv_scale):
     return VsaCache(shape[0], shape[1], D, rows[0], rows[1], *ptrs, scale), dev, rows[0], shape[1], D
 
 
-def _cache_call(fn, dev, stream, made, *args):
-    """fn(*args, stream) with the cache's device current; `made` are tensors the call made, which the
-    allocator must not hand out again before another stream than the current one is done with them."""
+def _make(stream, make, *args, **kw):
+    """A tensor that a call makes for `stream`, kept from that stream's later work until the current
+    stream, where the caller goes on, is done with it as well."""
+    if stream is None:
+        return make(*args, **kw)
     torch = _torch()
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _cache_call(fn, dev, stream, *args):
+    """fn(*args, stream) with the cache's device current."""
+    torch = _torch()
     if dev == torch.cuda.current_device():
         raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
         status = fn(*args, raw)
@@ -699,13 +706,13 @@ def cache_append(pool, k, v, table, kv_lens, new_lens=None, rope=None, positions
             raise ValueError("q must be [B, S, heads, D] with k's tokens")
         heads = q.shape[2]
         if q_out is None:
-            q_out = torch.empty_like(q)
+            q_out = _make(stream, torch.empty_like, q)
         out_ptr = _on(q_out, bf16, "q_out", dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must be shaped like q")
     elif q_out is not None:
         raise ValueError("q_out goes with q")
-    _cache_call(library().vsa_cache_append, dev, stream, (q_out,), c, q_ptr, k_ptr, v_ptr, S, heads, new_ptr, rope_ptr, rows, R,
+    _cache_call(library().vsa_cache_append, dev, stream, c, q_ptr, k_ptr, v_ptr, S, heads, new_ptr, rope_ptr, rows, R,
                 1 if interleaved else 0, pos_ptr, out_ptr)
     return q_out
 
@@ -717,13 +724,13 @@ def cache_read(pool, table, kv_lens, S: int, kv_scale=None, k=None, v=None, stre
     c, dev, B, kv, D = _cache(pool, table, kv_lens, kv_scale)
     shape = (B, int(S), kv, D)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
+        k = _make(stream, torch.empty, shape, dtype=torch.bfloat16, device=pool.device)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
+        v = _make(stream, torch.empty, shape, dtype=torch.bfloat16, device=pool.device)
     k_ptr, v_ptr = _on(k, torch.bfloat16, "k", dev), _on(v, torch.bfloat16, "v", dev)
     if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {shape}")
-    _cache_call(library().vsa_cache_read, dev, stream, (k, v), c, shape[1], k_ptr, v_ptr)
+    _cache_call(library().vsa_cache_read, dev, stream, c, shape[1], k_ptr, v_ptr)
     return k, v
 
 
@@ -761,22 +768,22 @@ def cache_attn(q, pool, table, kv_lens, q_lens=None, causal: bool = True, page_s
         nsel = page_sel.shape[2]
     nbytes = lib.vsa_cache_attn_workspace_bytes(kv, D, Sq, heads)
     if workspace is None:
-        workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=q.device)
+        workspace = _make(stream, torch.empty, (max(nbytes, 16),), dtype=torch.uint8, device=q.device)
     work_ptr = _on(workspace, torch.uint8, "workspace", dev)
     if workspace.numel() < nbytes:
         raise ValueError(f"workspace needs {nbytes} bytes")
     if out is None:
-        out = torch.empty_like(q)
+        out = _make(stream, torch.empty_like, q)
     out_ptr = _on(out, torch.bfloat16, "out", dev)
     if out.shape != shape:
         raise ValueError("out must be shaped like q")
     if want_lse and lse is None:
-        lse = torch.empty((B, heads, Sq), dtype=torch.float32, device=q.device)
+        lse = _make(stream, torch.empty, (B, heads, Sq), dtype=torch.float32, device=q.device)
     if lse is not None:
         lse_ptr = _on(lse, torch.float32, "lse", dev)
         if lse.shape != (B, heads, Sq):
             raise ValueError("lse must be [B, heads, Sq]")
-    _cache_call(lib.vsa_cache_attn, dev, stream, (workspace, out, lse), c, q_ptr, Sq, heads, lens_ptr, 1 if causal else 0, sel_ptr, nsel,
+    _cache_call(lib.vsa_cache_attn, dev, stream, c, q_ptr, Sq, heads, lens_ptr, 1 if causal else 0, sel_ptr, nsel,
                 sm_scale, work_ptr, out_ptr, lse_ptr)
     return out, lse
 

@@ -1,8 +1,9 @@
 // C ABI of the VSA library: argument validation on the host, then dispatch
 // to the kernels of tile.cu, coarse.cu, pair.cu, fine.cu, coarse_attn.cu,
-// block_select.cu, cache_store.cu and cache_attn.cu
+// block_select.cu, cache_store.cu and cache_attn.cu (which passes on to cache_chunk.cu)
 // (coarse_noalloc.cu holds the allocation-free coarse entry point).  See
 // include/vsa.h for the contract of each entry point.
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
@@ -408,8 +409,8 @@ vsa_status vsa_cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t
     vsa_status st = cache_args(c, Sq);
     if (st != VSA_OK) return st;
     if (!q || !workspace || !out || heads <= 0 || heads % c->kv_heads) return VSA_ERR_INVALID_ARG;
-    if (nsel < 0 || (nsel > 0) != (page_sel != nullptr) || !(sm_scale == sm_scale)) return VSA_ERR_INVALID_ARG;
-    if (heads > 65535 || (int64_t)Sq * (heads / c->kv_heads) >= (1 << 24)) return VSA_ERR_UNSUPPORTED;
+    if (nsel < 0 || (nsel > 0) != (page_sel != nullptr) || !(sm_scale <= FLT_MAX)) return VSA_ERR_INVALID_ARG;
+    if (heads > 65535 || (int64_t)Sq * (heads / c->kv_heads) >= (1 << 24) || nsel >= (1 << 25)) return VSA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(workspace) || !aligned16(out) || !aligned4(q_lens) || !aligned4(page_sel) ||
         !aligned4(lse))
         return VSA_ERR_ALIGNMENT;

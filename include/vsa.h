@@ -521,14 +521,15 @@ vsa_status vsa_cache_read(const vsa_cache* c, int32_t S, void* k, void* v, vsa_s
  *               (columns of the table), distinct within a row, in any order;
  *               numbers outside the sequence's pages (-1) are passed over.
  *               Or NULL with nsel = 0: every page
- *   sm_scale  : <= 0 selects 1 / sqrt(D)
+ *   sm_scale  : finite; <= 0 selects 1 / sqrt(D)
  *   workspace : vsa_cache_attn_workspace_bytes(...) bytes, 16-byte aligned,
  *               overwritten; calls that may overlap (other streams, graphs
  *               replayed at once) need workspaces of their own
  *   out       : bf16 [B, Sq, heads, D] (written in full)
  *   lse       : fp32 [B, heads, Sq] (written), or NULL
  * Softmax statistics and sums are fp32, P is rounded to fp16.
- * Limits: Sq * heads / kv_heads < 2^24, heads <= 65535, B * Sq < 2^31.
+ * Limits: Sq * heads / kv_heads < 2^24, heads <= 65535, B * Sq < 2^31, nsel <
+ * 2^25.
  */
 size_t vsa_cache_attn_workspace_bytes(int32_t kv_heads, int32_t D, int32_t Sq, int32_t heads);
 vsa_status vsa_cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t heads, const int32_t* q_lens,

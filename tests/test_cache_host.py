@@ -124,3 +124,10 @@ def test_binding_refuses_cpu_tensors_and_bad_sizes():
         vsa.cache_pool(2, 2, 96, device="cpu")
     with pytest.raises(ValueError):
         vsa.cache_pool(0, 2, 64, device="cpu")
+
+
+def test_attn_refuses_an_infinite_scale_and_a_selection_beyond_any_table(lib):
+    def call(sel=None, nsel=0, scale=0.0):
+        return lib.vsa_cache_attn(cache(), A, 1, 4, None, 1, sel, nsel, scale, A, A, None, None)
+    assert call(scale=float("inf")) == INVALID
+    assert call(sel=A, nsel=1 << 25) == UNSUPPORTED

@@ -369,9 +369,10 @@ def test_ragged_batches_of_every_size(B, kv, heads, D, Sq, most, causal, sel):
             assert (lse[b].double() - want_lse)[~dead].abs().max() <= 2.0 ** -12, b
 
 
-def test_pool_beyond_32_bit_offsets():
-    """Pages whose byte offset passes 2^31 are written and read where they are."""
-    D, kv, pages = 128, 2, 140000  # 2.6 GB
+@pytest.mark.parametrize("pages", [140000, 280000])  # 2.6 and 5.2 GB
+def test_pool_beyond_32_bit_offsets(pages):
+    """Pages whose byte offset passes 2^31 and 2^32 are written and read where they are."""
+    D, kv = 128, 2
     pool = vsa.cache_pool(pages, kv, D)
     table = torch.tensor([[pages - 1, 3, pages - 2]], dtype=torch.int32, device="cuda")
     lens = torch.tensor([150], dtype=torch.int32, device="cuda")
@@ -383,9 +384,10 @@ def test_pool_beyond_32_bit_offsets():
     vsa.cache_append(small, k, v, t2, lens)
     assert torch.equal(pool[table[0].long()], small[t2[0].long()])
     assert int((pool.view(torch.int64) != 0).any(-1).any(-1).sum()) == 3
-    q = torch.randn((1, 1, 4, D), generator=g, device="cuda").bfloat16()
-    for a, b in zip(vsa.cache_attn(q, pool, table, lens), vsa.cache_attn(q, small, t2, lens)):
-        assert torch.equal(a, b)
+    for Sq in (1, 40):
+        q = torch.randn((1, Sq, 4, D), generator=g, device="cuda").bfloat16()
+        for a, b in zip(vsa.cache_attn(q, pool, table, lens), vsa.cache_attn(q, small, t2, lens)):
+            assert torch.equal(a, b)
     assert torch.equal(vsa.cache_read(pool, table, lens, 150)[0], vsa.cache_read(small, t2, lens, 150)[0])
 
 
