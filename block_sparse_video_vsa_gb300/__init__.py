@@ -3,7 +3,8 @@
 Python binding of ``libvsa.so`` (C ABI declared in ``include/vsa.h``).  Every
 function here only marshals arguments: it checks tensor placement, dtype and
 shape, allocates outputs with PyTorch, and calls the C entry point of the same
-name on the current CUDA stream.  All computation runs in the library's
+name on the current CUDA stream (the cache calls through a native module that
+does the same, csrc/front.cpp).  All computation runs in the library's
 sm_103a kernels; there is no CPU fallback, and a missing library raises.
 
     xt, vbs  = tile(x, grid)                       # raster -> cube-major
@@ -14,6 +15,8 @@ sm_103a kernels; there is no CPU fallback, and a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 import threading
@@ -656,6 +659,28 @@ def _make(stream, make, *args, **kw):
     return t
 
 
+_front_module = None  # False: not built for this PyTorch
+
+
+def _front():
+    """The native front of the cache calls (csrc/front.cpp), or False where it has not been built."""
+    global _front_module
+    if _front_module is None:
+        from .build import front_path
+        _torch()
+        lib, path = library(), front_path()
+        if os.path.exists(path):
+            loader = importlib.machinery.ExtensionFileLoader("_front", path)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_front", loader))
+            loader.exec_module(m)
+            m.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+                lib.vsa_cache_append, lib.vsa_cache_read, lib.vsa_cache_attn, lib.vsa_cache_attn_workspace_bytes)))
+            _front_module = m
+        else:
+            _front_module = False
+    return _front_module
+
+
 def _cache_call(fn, dev, stream, *args):
     """fn(*args, stream) with the cache's device current."""
     torch = _torch()
@@ -677,6 +702,13 @@ def cache_append(pool, k, v, table, kv_lens, new_lens=None, rope=None, positions
 
     kv_lens (int32 [B]) counts the step's tokens already; new_lens says how many each sequence
     has (None: S).  positions int32 [B, S] are rows of rope (None: places in the sequence)."""
+    if stream is None and (_front_module or _front()):
+        got = _front_module.append(pool, k, v, table, kv_lens, new_lens, rope, positions, interleaved, q, q_out,
+                                   kv_scale)
+        if got.__class__ is int:
+            raise VsaError(got, "vsa_cache_append")
+        if got is not False:
+            return got
     torch = _torch()
     bf16, i32 = torch.bfloat16, torch.int32
     c, dev, B, kv, D = _cache(pool, table, kv_lens, kv_scale)
@@ -720,6 +752,12 @@ def cache_append(pool, k, v, table, kv_lens, new_lens=None, rope=None, positions
 def cache_read(pool, table, kv_lens, S: int, kv_scale=None, k=None, v=None, stream=None):
     """The first S cached tokens of every sequence -> (k, v) bf16 [B, S, kv_heads, D], zero past each
     length; with S a multiple of 64 they are tiled tensors for sparse_attn_fwd (vsa_cache_read)."""
+    if stream is None and (_front_module or _front()):
+        got = _front_module.read(pool, table, kv_lens, S, kv_scale, k, v)
+        if got.__class__ is int:
+            raise VsaError(got, "vsa_cache_read")
+        if got is not False:
+            return got
     torch = _torch()
     c, dev, B, kv, D = _cache(pool, table, kv_lens, kv_scale)
     shape = (B, int(S), kv, D)
@@ -745,6 +783,13 @@ def cache_attn(q, pool, table, kv_lens, q_lens=None, causal: bool = True, page_s
 
     q_lens (int32 [B]) are each sequence's query rows (None: Sq), its last tokens when causal;
     page_sel (int32 [B, kv_heads, n]) limits each kv head to n pages of its sequence (-1: none)."""
+    if stream is None and (_front_module or _front()):
+        got = _front_module.attn(q, pool, table, kv_lens, q_lens, causal, page_sel, kv_scale, sm_scale, workspace, out,
+                                 lse, want_lse)
+        if got.__class__ is int:
+            raise VsaError(got, "vsa_cache_attn")
+        if got is not False:
+            return got
     torch = _torch()
     lib = library()
     c, dev, B, kv, D = _cache(pool, table, kv_lens, kv_scale)

@@ -2,14 +2,19 @@
 
 Each CUDA translation unit compiles in its own nvcc process (in parallel),
 then nvcc links them into ``block_sparse_video_vsa_gb300/_build/libvsa.so``.
-Rebuilds only when a source or header is newer than the library.
+Beside them g++ compiles the Python module ``_front`` (csrc/front.cpp) against
+the installed PyTorch, under a name with its version.  Rebuilds only when a
+source or header is newer than what was built.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +25,29 @@ LIB_PATH = os.path.join(BUILD_DIR, "libvsa.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                      f"-I{os.path.join(REPO_DIR, 'include')}"]
+
+
+FRONT_SRC = os.path.join(CSRC, "front.cpp")
+
+
+def front_path() -> str:
+    """Where the module for the installed PyTorch and this Python is built."""
+    tag = f"{importlib.metadata.version('torch')}-{sysconfig.get_config_var('SOABI')}"
+    return os.path.join(BUILD_DIR, f"_front-{tag}.so")
+
+
+def _build_front(path: str) -> None:
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    lib = os.path.join(torch_dir, "lib")
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{os.path.join(torch_dir, 'include')}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{os.environ.get('CUDA_HOME', '/usr/local/cuda')}/include",
+           f"-I{os.path.join(REPO_DIR, 'include')}", FRONT_SRC, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {FRONT_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
 
 
 def _nvcc() -> str:
@@ -37,16 +65,30 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    return _newer(LIB_PATH, _deps())
+
+
+def _newer(path, deps) -> bool:
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(p) <= t for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
+    front = front_path()
+    stale_front = force or not _newer(front, [FRONT_SRC, os.path.join(REPO_DIR, "include", "vsa.h"), os.path.abspath(__file__)])
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        made = ex.submit(_build_front, front) if stale_front else None
+        if force or not up_to_date():
+            _build_library(verbose)
+        if made:
+            made.result()
+    return LIB_PATH
+
+
+def _build_library(verbose: bool) -> None:
     nvcc = _nvcc()
 
     def compile_one(src):
@@ -66,7 +108,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

@@ -131,3 +131,18 @@ def test_attn_refuses_an_infinite_scale_and_a_selection_beyond_any_table(lib):
         return lib.vsa_cache_attn(cache(), A, 1, 4, None, 1, sel, nsel, scale, A, A, None, None)
     assert call(scale=float("inf")) == INVALID
     assert call(sel=A, nsel=1 << 25) == UNSUPPORTED
+
+
+def test_native_front_leaves_what_it_does_not_take():
+    """Built beside the library; CPU tensors, wrong counts of arguments and anything else go to the Python path."""
+    front = vsa._front()
+    assert front
+    pool = vsa.cache_pool(2, 2, 64, device="cpu")
+    table, lens = torch.zeros((1, 2), dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    k = torch.zeros((1, 1, 2, 64), dtype=torch.bfloat16)
+    assert front.append(pool, k, k, table, lens, None, None, None, False, None, None, None) is False
+    assert front.read(pool, table, lens, 64, None, None, None) is False
+    assert front.attn(k, pool, table, lens, None, True, None, None, 0.0, None, None, None, True) is False
+    assert front.attn() is False and front.read(1, 2, 3, 4, 5, 6, 7) is False
+    with pytest.raises(TypeError):
+        front.bind(1)

@@ -512,6 +512,59 @@ def test_two_streams_and_repeated_runs_give_the_same_bits():
         assert torch.equal(out, base[0]) and torch.equal(lse, base[1])
 
 
+def test_native_front_and_python_path_agree(monkeypatch):
+    """The same bits, tensors of the same kind, and the same refusals by either path."""
+    r = np.random.default_rng(3)
+    lens, kv, D, heads = [90, 200], 2, 64, 6
+    one = np.ones((2, kv), np.float32)
+    pool, table = filled(r, lens, 8, kv, D, one)
+    t, n = dev(table), dev(np.array(lens, np.int32))
+    q, k, v = (bf16(r, 2, 3, h, D)[0] for h in (heads, kv, kv))
+    rope = dev(rope_table(256, 32))
+    new = dev(np.array([3, 2], np.int32))
+    scale = torch.ones(2, kv, device="cuda")
+    sel = dev(np.array([[[0, 1], [1, -1]], [[3, 0], [2, 1]]], np.int32))
+
+    def calls():
+        p = dev(pool)
+        qr = vsa.cache_append(p, k, v, t, n, new_lens=new, rope=rope, q=q, kv_scale=scale, interleaved=True)
+        assert vsa.cache_append(p, k, v, t, n, positions=torch.zeros(2, 3, dtype=torch.int32, device="cuda")) is None
+        out, lse = torch.empty_like(q), torch.empty((2, heads, 3), device="cuda")
+        ws = torch.empty(vsa.cache_attn_workspace_bytes(kv, D, 3, heads), dtype=torch.uint8, device="cuda")
+        res = [p, qr, *vsa.cache_attn(qr, p, t, n, q_lens=new, kv_scale=scale, sm_scale=0.25),
+               *vsa.cache_attn(qr, p, t, n, causal=False, page_sel=sel, workspace=ws, out=out, lse=lse),
+               vsa.cache_attn(qr, p, t, n, want_lse=False)[0], *vsa.cache_read(p, t, n, 130, kv_scale=scale)]
+        assert vsa.cache_attn(qr, p, t, n, want_lse=False)[1] is None
+        a, b = vsa.cache_attn(qr, p, t, n, out=out, lse=lse)
+        assert a is out and b is lse
+        mine = torch.empty_like(q)
+        assert vsa.cache_append(p, k, v, t, n, q=q, q_out=mine) is mine
+        said = []
+        for call in (lambda: vsa.cache_attn(q[:, :, :5], p, t, n), lambda: vsa.cache_attn(q, p, t, n, q_lens=new[:1]),
+                     lambda: vsa.cache_attn(q, p, t, n, workspace=ws[:16]), lambda: vsa.cache_attn(q, p, t.long(), n),
+                     lambda: vsa.cache_attn(q, p, t, n, page_sel=sel[0]), lambda: vsa.cache_attn(q.float(), p, t, n),
+                     lambda: vsa.cache_append(p, k, v[:, :2], t, n), lambda: vsa.cache_append(p, k, v, t, n, q_out=mine),
+                     lambda: vsa.cache_append(p, k, v, t, n, rope=rope[0]), lambda: vsa.cache_read(p, t, n, 64, k=k)):
+            with pytest.raises((TypeError, ValueError)) as e:
+                call()
+            said.append(str(e.value))
+        for call in (lambda: vsa.cache_append(p, k, v, t, n, rope=rope[:, :16].contiguous()),
+                     lambda: vsa.cache_attn(q, p, t, n, sm_scale=float("nan")), lambda: vsa.cache_read(p, t, n, 0)):
+            with pytest.raises(vsa.VsaError) as e:
+                call()
+            said.append(str(e.value))
+        return res, said
+
+    assert vsa._front()
+    native, said_native = calls()
+    monkeypatch.setattr(vsa, "_front_module", False)
+    assert not vsa._front()
+    python, said_python = calls()
+    assert said_native == said_python
+    for a, b in zip(native, python):
+        assert a.dtype == b.dtype and a.shape == b.shape and a.is_contiguous() and torch.equal(a, b)
+
+
 def test_binding_refusals():
     D, kv = 64, 2
     pool = vsa.cache_pool(3, kv, D)
