@@ -182,8 +182,9 @@ struct SeqLens {
 
 __device__ __forceinline__ SeqLens seq_lens(const AttnParams& p, int b, bool note = false) {
     SeqLens s;
+    const int q = p.q_lens ? __ldg(p.q_lens + b) : p.Sq;  // (asked for first: both loads are on their way at once)
     s.kv = cache_len(p.c, b, note);
-    s.q = p.q_lens ? min(max(__ldg(p.q_lens + b), 0), p.Sq) : p.Sq;
+    s.q = min(max(q, 0), p.Sq);
     return s;
 }
 

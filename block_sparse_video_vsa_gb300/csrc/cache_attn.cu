@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
         Tasks<kWarps> tk;
         tk.begin_part(p, w);
         if (lane == 0) {
-            sm.ask_walk[warp] = sm.walk[warp] = w;
-            sm.ask_tasks[warp] = sm.tasks[warp] = tk;
+            sm.walk[warp] = w;
+            sm.tasks[warp] = tk;
         }
         __syncwarp();
     }
@@ -221,9 +221,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
         ++asked;
         ++ask;
     };
-#pragma unroll 1
-    for (int i = 0; i < kOwn; ++i) ask_next();
-
     // Row r of a token tile sits at token f(r) = r ^ ((r >> 1) & 1) of its 8: of
     // the four tokens that a V load's lanes t = 0..3 read, two are even and two
     // odd (64-byte rows: 2-way bank conflicts instead of 4-way).
@@ -232,10 +229,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
     const int R = p.Sq * p.group;
     uint32_t j = 0;            // this warp's pages so far
     unsigned int unit = 0;     // units so far
-    bool ok = true;
-    int piece_begin, piece_end;
+    int piece_begin = 0, piece_end = 0;
     const Segment& at = sm.unit[warp];
-    while (ok && next_task(sm.walk[warp], sm.tasks[warp], sm.unit[warp], piece_begin, piece_end, unit)) {
+    bool ok = next_task(sm.walk[warp], sm.tasks[warp], sm.unit[warp], piece_begin, piece_end, unit);
+    if (ok) {  // the first unit is also the first to ask for
+        if (lane == 0) {
+            sm.ask_walk[warp] = sm.walk[warp];
+            sm.ask_tasks[warp] = sm.tasks[warp];
+            sm.ask_unit[warp] = at;
+        }
+        __syncwarp();
+        ask = piece_begin >> 1;
+        ask_end = (piece_end + 1) >> 1;
+        if (ask < ask_end) look_up_32(ask);
+#pragma unroll 1
+        for (int i = 0; i < kOwn; ++i) ask_next();
+    }
+    for (; ok; ok = ok && next_task(sm.walk[warp], sm.tasks[warp], sm.unit[warp], piece_begin, piece_end, unit)) {
         const int present = sm.tasks[warp].count, first_warp = sm.tasks[warp].first_warp;  // the unit's warps
         const bool none = at.first == at.last;  // no pages: this warp writes the rows alone
         // ------------------------------------------------ the unit's queries

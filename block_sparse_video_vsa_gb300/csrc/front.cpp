@@ -19,6 +19,12 @@
 
 namespace {
 
+// Other Python threads go on while tensors are made and kernels launched.
+struct NoGil {
+    PyThreadState* state = PyEval_SaveThread();
+    ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 decltype(&vsa_cache_append) append_fn;
 decltype(&vsa_cache_read) read_fn;
 decltype(&vsa_cache_attn) attn_fn;
@@ -126,11 +132,15 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int interleaved = PyObject_IsTrue(a[8]);
     if (interleaved < 0) return nullptr;
     at::Tensor made;
-    if (q) q_out = given_or_new(q_out, q->sizes(), at::kBFloat16, x, &made);
-    const vsa_status st = append_fn(&x.c, data<void>(q), data<void>(k), data<void>(v), (int32_t)S,
-                                    q ? (int32_t)q->size(2) : 0, data<int32_t>(fresh), data<float>(rope),
-                                    rope ? (int32_t)rope->size(0) : 0, rope ? (int32_t)rope->size(1) : 0, interleaved,
-                                    data<int32_t>(positions), data<void>(q_out), x.stream);
+    vsa_status st;
+    {
+        NoGil no_gil;
+        if (q) q_out = given_or_new(q_out, q->sizes(), at::kBFloat16, x, &made);
+        st = append_fn(&x.c, data<void>(q), data<void>(k), data<void>(v), (int32_t)S, q ? (int32_t)q->size(2) : 0,
+                       data<int32_t>(fresh), data<float>(rope), rope ? (int32_t)rope->size(0) : 0,
+                       rope ? (int32_t)rope->size(1) : 0, interleaved, data<int32_t>(positions), data<void>(q_out),
+                       x.stream);
+    }
     if (st != VSA_OK) return PyLong_FromLong(st);
     if (!q) Py_RETURN_NONE;
     return result(a[10], made);
@@ -151,9 +161,13 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::IntArrayRef sizes(shape, 4);
     if ((k && k->sizes() != sizes) || (v && v->sizes() != sizes)) Py_RETURN_FALSE;
     at::Tensor made_k, made_v;
-    k = given_or_new(k, sizes, at::kBFloat16, x, &made_k);
-    v = given_or_new(v, sizes, at::kBFloat16, x, &made_v);
-    const vsa_status st = read_fn(&x.c, (int32_t)S, data<void>(k), data<void>(v), x.stream);
+    vsa_status st;
+    {
+        NoGil no_gil;
+        k = given_or_new(k, sizes, at::kBFloat16, x, &made_k);
+        v = given_or_new(v, sizes, at::kBFloat16, x, &made_v);
+        st = read_fn(&x.c, (int32_t)S, data<void>(k), data<void>(v), x.stream);
+    }
     if (st != VSA_OK) return PyLong_FromLong(st);
     PyObject* first = result(a[5], made_k);
     return pair(first, result(a[6], made_v));
@@ -185,12 +199,16 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t bytes = (int64_t)workspace_fn(x.c.kv_heads, x.c.D, (int32_t)Sq, (int32_t)heads);
     if (bytes == 0 || (work && work->numel() < bytes)) Py_RETURN_FALSE;
     at::Tensor made_work, made_out, made_lse;
-    work = given_or_new(work, {bytes}, at::kByte, x, &made_work);
-    out = given_or_new(out, q->sizes(), at::kBFloat16, x, &made_out);
-    if (want_lse) lse = given_or_new(lse, at::IntArrayRef(shape, 3), at::kFloat, x, &made_lse);
-    const vsa_status st = attn_fn(&x.c, data<void>(q), (int32_t)Sq, (int32_t)heads, data<int32_t>(q_lens), causal,
-                                  data<int32_t>(sel), sel ? (int32_t)sel->size(2) : 0, (float)scale, data<void>(work),
-                                  data<void>(out), data<float>(lse), x.stream);
+    vsa_status st;
+    {
+        NoGil no_gil;
+        work = given_or_new(work, {bytes}, at::kByte, x, &made_work);
+        out = given_or_new(out, q->sizes(), at::kBFloat16, x, &made_out);
+        if (want_lse) lse = given_or_new(lse, at::IntArrayRef(shape, 3), at::kFloat, x, &made_lse);
+        st = attn_fn(&x.c, data<void>(q), (int32_t)Sq, (int32_t)heads, data<int32_t>(q_lens), causal, data<int32_t>(sel),
+                     sel ? (int32_t)sel->size(2) : 0, (float)scale, data<void>(work), data<void>(out), data<float>(lse),
+                     x.stream);
+    }
     if (st != VSA_OK) return PyLong_FromLong(st);
     PyObject* first = result(a[10], made_out);
     return pair(first, lse ? result(a[11], made_lse) : Py_NewRef(Py_None));
