@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
             sm.walk[warp] = w;
             sm.tasks[warp] = tk;
         }
-        __syncwarp();
+        __syncthreads();  // the barriers and flags above are every warp's
     }
     volatile int* abort_flag = &sm.abort_flag;
 
