@@ -1,6 +1,8 @@
 """GPU: the 4-bit paged cache (append, attention, read back) against the plain
 statement in cache_ref: stored bytes exactly, attention within bounds derived
 from its roundings (cache_ref.attention_bounds)."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -510,6 +512,44 @@ def test_two_streams_and_repeated_runs_give_the_same_bits():
     side.synchronize()
     for out, lse in kept:
         assert torch.equal(out, base[0]) and torch.equal(lse, base[1])
+
+
+def test_threads_call_at_once():
+    """Four host threads, each on a stream of its own, append to sequences of their own and attend over them."""
+    r = np.random.default_rng(21)
+    lens, kv, D, heads = [130, 700, 64, 5], 2, 128, 6
+    one = np.ones((2, kv), np.float32)
+    pool, table = filled(r, lens, 24, kv, D, one)
+    p = dev(pool)
+    t = [dev(table[i:i + 1]) for i in range(4)]
+    n = [dev(np.array([x], np.int32)) for x in lens]
+    q, k, v = (bf16(r, 4, 5, h, D)[0] for h in (heads, kv, kv))
+
+    def work(i, pool):
+        vsa.cache_append(pool, k[i:i + 1], v[i:i + 1], t[i], n[i])
+        return (*vsa.cache_attn(q[i:i + 1], pool, t[i], n[i]), *vsa.cache_read(pool, t[i], n[i], 700))
+
+    alone = p.clone()
+    want = [work(i, alone) for i in range(4)]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def thread(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(30):
+                got[i] = work(i, p)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join(60)
+    torch.cuda.synchronize()
+    assert torch.equal(p, alone)
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
 
 
 def test_native_front_and_python_path_agree(monkeypatch):
