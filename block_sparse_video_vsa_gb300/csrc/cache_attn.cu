@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
         if (threadIdx.x == 0) sm.abort_flag = 0;
         fence_barrier_init();
     }
-    // The joining kernel may be set up meanwhile (its blocks wait for this grid's end).
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    early();
+    begin_work();
     {
         Walk w;
         if (!w.begin(p, sm.plan)) return;
@@ -637,7 +637,8 @@ template <int kD>
 __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) {
     __shared__ float s_o[kJoinWarps][kD];
     __shared__ float2 s_ml[kJoinWarps];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    early();
+    begin_work();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = blockIdx.y;  // the CTA that begins the unit, if this is its first cut
     // Lane i: where CTA c0 + i's part begins (b < 0: not inside a unit).
@@ -743,9 +744,7 @@ cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
     const cudaError_t e = allow_smem(kernel, smem, done);
     if (e != cudaSuccess) return e;
     static_assert(kWarps <= kTokenWarps && kWarps <= 16, "states in the workspace");
-    kernel<<<p.grid, kWarps * 32, smem, stream>>>(p);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3((unsigned)p.grid), kWarps * 32, smem, stream, p);
 }
 
 // How the line is cut, in pages, with what was measured:
@@ -813,20 +812,9 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     else
         e = p.tile == 8 ? launch_token<128, 1, 12, 2>(p, stream) : launch_token<128, 2, 8, 3>(p, stream);
     if (e != cudaSuccess || p.whole) return e;
-    // Launched early (it waits for the attention kernel's end by itself).
     if (p.grid < 2) return cudaSuccess;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min(p.tiles == 1 ? rows : p.tile, 16), (unsigned)(p.grid - 1));
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = D == 64 ? cudaLaunchKernelEx(&cfg, combine_kernel<64>, p) : cudaLaunchKernelEx(&cfg, combine_kernel<128>, p);
-    note_launches(1);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const dim3 grid((unsigned)std::min(p.tiles == 1 ? rows : p.tile, 16), (unsigned)(p.grid - 1));
+    return launch_early(D == 64 ? combine_kernel<64> : combine_kernel<128>, grid, kJoinWarps * 32, 0, stream, p);
 }
 
 }  // namespace vsa

@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
         for (int e = threadIdx.x; e < Sm::kOffRaw / 16; e += kChunkThreads) z[e] = make_int4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    early();
     Walk walk;
     if (!walk.begin(p, ms.plan)) return;  // the whole CTA: TMEM is not allocated yet
     if (warp == 1) {
@@ -770,6 +770,8 @@ static cudaError_t launch_chunk_d(const AttnParams& p, cudaStream_t stream) {
     if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
     const cudaError_t e = allow_smem(chunk_kernel<kD>, chunk_smem<kD>(), done);
     if (e != cudaSuccess) return e;
+    // Not launched early itself: over 32760 keys, 64 rows of 40 heads take 95.4 us
+    // so and 102.2 launched early (a ragged batch of prompts 289.6 and 281.1).
     chunk_kernel<kD><<<p.grid, kChunkThreads, chunk_smem<kD>(), stream>>>(p);
     note_launches(1);
     return cudaGetLastError();

@@ -123,6 +123,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
     using L = PageLayout<kD>;
     constexpr int kSlices = kD / 32;                              // threads of a head row
     constexpr int kHeadLanes = kAppendThreads / (kSlices * kTok);  // heads in flight
+    early();
+    begin_work();
     const int slice = threadIdx.x % kSlices;
     const int b = blockIdx.z;
     const int tok = blockIdx.x * kTok + (threadIdx.x / kSlices) % kTok;
@@ -268,6 +270,8 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(ReadParams p) {
     using L = PageLayout<kD>;
     constexpr int kLanes = kD / 8;                  // threads of a token row (8 channels each)
     constexpr int kStep = kReadThreads / kLanes;    // tokens a pass
+    early();
+    begin_work();
     const int h = blockIdx.y, b = blockIdx.z;
     const int first = blockIdx.x * kPageTokens;
     const int lane = threadIdx.x % kLanes;
@@ -346,9 +350,7 @@ cudaError_t launch_cache_append(const CacheView& c, int D, const void* q, const 
                               : (tok == 8 ? append_kernel<64, 8, false> : append_kernel<64, 1, false>);
     auto of_d128 = interleaved ? (tok == 8 ? append_kernel<128, 8, true> : append_kernel<128, 1, true>)
                                : (tok == 8 ? append_kernel<128, 8, false> : append_kernel<128, 1, false>);
-    (D == 64 ? of_d64 : of_d128)<<<grid, kAppendThreads, 0, stream>>>(p);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_early(D == 64 ? of_d64 : of_d128, grid, kAppendThreads, 0, stream, p);
 }
 
 cudaError_t launch_cache_read(const CacheView& c, int D, int S, void* k, void* v, cudaStream_t stream) {
@@ -358,9 +360,7 @@ cudaError_t launch_cache_read(const CacheView& c, int D, int S, void* k, void* v
     p.v = static_cast<uint4*>(v);
     p.S = S;
     const dim3 grid((unsigned)((S + kPageTokens - 1) / kPageTokens), (unsigned)c.kv_heads, (unsigned)c.B);
-    (D == 64 ? read_kernel<64> : read_kernel<128>)<<<grid, kReadThreads, 0, stream>>>(p);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_early(D == 64 ? read_kernel<64> : read_kernel<128>, grid, kReadThreads, 0, stream, p);
 }
 
 }  // namespace vsa

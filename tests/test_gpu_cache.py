@@ -514,6 +514,70 @@ def test_two_streams_and_repeated_runs_give_the_same_bits():
         assert torch.equal(out, base[0]) and torch.equal(lse, base[1])
 
 
+def test_calls_between_copies_other_kernels_and_streams_captured_and_not():
+    """A call starts its blocks while the kernel before it runs: what copies, other kernels, a join of two
+    streams or the call before wrote is seen all the same, in a graph too."""
+    r = np.random.default_rng(33)
+    lens, kv, D, heads, S = [700, 1500], 2, 128, 4, 70
+    one = np.ones((2, kv), np.float32)
+    pool, table = filled(r, lens, 24, kv, D, one)
+    t, n = dev(table), dev(np.array(lens, np.int32))
+    sets = [[bf16(r, 2, S, h, D)[0] for h in (heads, kv, kv)] for _ in range(4)]
+    p, q, k, v = dev(pool), *(torch.zeros_like(x) for x in sets[0])
+    side = torch.cuda.Stream()
+
+    def step(src):
+        q.copy_(src[0])  # a copy before
+        k.copy_(src[1])
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            v.copy_(src[2])
+            v.mul_(2.0)
+        here.wait_stream(side)  # a join before
+        vsa.cache_append(p, k, v, t, n)
+        a = vsa.cache_attn(q, p, t, n)  # straight after a call that wrote what it reads
+        b = vsa.cache_attn(q[:, -1:].contiguous(), p, t, n)
+        kb, vb = vsa.cache_read(p, t, n, 1536)
+        return [*a, *b, kb, vb, kb + vb]  # another kernel straight after
+
+    slow = []
+    for src in sets:
+        p.copy_(dev(pool))
+        out = []
+        for x in (q.copy_, k.copy_, v.copy_):
+            x(src[len(out)]), out.append(0)
+        v.mul_(2.0)
+        torch.cuda.synchronize()
+        vsa.cache_append(p, k, v, t, n)
+        torch.cuda.synchronize()
+        a = vsa.cache_attn(q, p, t, n)
+        torch.cuda.synchronize()
+        b = vsa.cache_attn(q[:, -1:].contiguous(), p, t, n)
+        torch.cuda.synchronize()
+        kb, vb = vsa.cache_read(p, t, n, 1536)
+        torch.cuda.synchronize()
+        slow.append([*a, *b, kb, vb, kb + vb])
+    for _ in range(10):
+        fast = [step(src) for src in sets]
+        for x, y in zip(slow, fast):
+            for c, d in zip(x, y):
+                assert torch.equal(c, d)
+    now = [x.clone() for x in sets[0]]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        res = step(now)
+    for _ in range(5):
+        for src, want in zip(sets, slow):
+            for x, y in zip(now, src):
+                x.copy_(y)
+            g.replay()
+            for c, d in zip(want, res):
+                assert torch.equal(c, d)
+
+
 def test_threads_call_at_once():
     """Four host threads, each on a stream of its own, append to sequences of their own and attend over them."""
     r = np.random.default_rng(21)
