@@ -29,10 +29,10 @@
 //    maximum, sum and output are fp32.  The maximum is followed lazily: the
 //    output is rescaled when it grows by more than 2^8.
 //  * Measured (GB300): 61 ragged sequences of up to 12000 tokens, 32 heads on 8
-//    of 128: 102 us, 4.4 TB/s (65% of the measured copy rate).  What bounds it
+//    of 128: 100.5 us, 4.5 TB/s (66% of the measured copy rate).  What bounds it
 //    is issue: 1215 instructions a page at 0.55 a scheduler and cycle, 12 warps
 //    an SM (168 registers).  A producer warp with 7 consumers behind a barrier
-//    a unit took 127 us.  One token on one clip of 32760 tokens takes 23 us.
+//    a unit took 127 us.  One token on one clip of 32760 tokens takes 22 us.
 #include "cache.cuh"
 
 namespace vsa {
