@@ -78,7 +78,8 @@ def _newer(path, deps) -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     front = front_path()
-    stale_front = force or not _newer(front, [FRONT_SRC, os.path.join(REPO_DIR, "include", "vsa.h"), os.path.abspath(__file__)])
+    header = os.path.join(REPO_DIR, "include", "vsa.h")
+    stale_front = force or not _newer(front, [FRONT_SRC, header, os.path.abspath(__file__)])
     with ThreadPoolExecutor(max_workers=1) as ex:
         made = ex.submit(_build_front, front) if stale_front else None
         if force or not up_to_date():

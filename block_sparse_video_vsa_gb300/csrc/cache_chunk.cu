@@ -762,7 +762,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
 template <int kD>
 static cudaError_t launch_chunk_d(const AttnParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    // The register split draws on the launch's registers; with fewer, setmaxnreg would wait forever, so such a build is refused.
+    // The register split draws on the launch's registers; with fewer, setmaxnreg
+    // would wait forever, so such a build is refused.
     static const int regs = [] {
         cudaFuncAttributes fa;
         return cudaFuncGetAttributes(&fa, chunk_kernel<kD>) == cudaSuccess ? fa.numRegs : 0;

@@ -2,10 +2,10 @@
 // tensors that it makes and the call itself, for calls on the current device
 // and stream.  A cache call's kernels take from 3 us; through ctypes, with its
 // arguments looked at one attribute at a time, a call took 18 to 24 us of the
-// host, here 2.4 with its tensors given and 5 to 7 with those it makes.  What this front does not take as it is (other types, another
-// device, a shape that does not fit) it leaves, by returning False, to the
-// Python function, which says what is wrong; a status of the library comes back
-// as a number.
+// host, here 2.4 with its tensors given and 5 to 7 with those it makes.  What
+// this front does not take as it is (other types, another device, a shape that
+// does not fit) it leaves, by returning False, to the Python function, which
+// says what is wrong; a status of the library comes back as a number.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

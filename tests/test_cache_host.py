@@ -133,7 +133,7 @@ def test_attn_refuses_an_infinite_scale_and_a_selection_beyond_any_table(lib):
     assert call(sel=A, nsel=1 << 25) == UNSUPPORTED
 
 
-def test_native_front_leaves_what_it_does_not_take():
+def test_native_front_leaves_what_it_does_not_take(lib):
     """Built beside the library; CPU tensors, wrong counts of arguments and anything else go to the Python path."""
     front = vsa._front()
     assert front
