@@ -52,9 +52,12 @@ inline cudaError_t allow_smem(K kernel, int smem, std::atomic<uint64_t>& done) {
 // early(), as they all do):
 // blocks are set up as soon as an SM has room, and wait in begin_work() until
 // the kernel before has ended and its writes can be seen.  Nothing is read
-// from or written to global memory before that.  A step is a chain of kernels
-// of 3 to 20 us; one token on 300 takes 8.2 us a call so, 9.2 without, a
-// frame's append and a read 29.0 and 32.6.
+// from or written to global memory before that, and nothing is read as
+// read-only data (the non-coherent loads): a kernel's life begins before its
+// predecessor's last write, so what anything before it on the stream may have
+// written is loaded as ordinary memory, which the wait orders.  A step is a
+// chain of kernels of 3 to 20 us; one token on 300 takes 8.2 us a call so, 9.2
+// without, a frame's append and a read 29.0 and 32.6.
 template <class... P>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, P... args) {
     cudaLaunchConfig_t cfg = {};
@@ -88,7 +91,7 @@ static_assert(PageLayout<128>::kBytes == 72 * 128 && PageLayout<64>::kBytes == 7
 // Tokens of sequence b in the cache; a length the page table cannot hold is
 // cut to what it holds (and noted in the error word by the caller's choice).
 __device__ __forceinline__ int cache_len(const CacheView& c, int b, bool note) {
-    const int n = __ldg(c.kv_lens + b);
+    const int n = c.kv_lens[b];
     const long long cap = (long long)c.width * kPageTokens;
     if (n < 0 || n > cap) {
         if (note) atomicOr(c.err, VSA_DEVERR_INDEX);
@@ -209,7 +212,7 @@ struct SeqLens {
 
 __device__ __forceinline__ SeqLens seq_lens(const AttnParams& p, int b, bool note = false) {
     SeqLens s;
-    const int q = p.q_lens ? __ldg(p.q_lens + b) : p.Sq;  // (asked for first: both loads are on their way at once)
+    const int q = p.q_lens ? p.q_lens[b] : p.Sq;  // (asked for first: both loads are on their way at once)
     s.kv = cache_len(p.c, b, note);
     s.q = min(max(q, 0), p.Sq);
     return s;
@@ -493,10 +496,10 @@ struct Walk {
 // Looks up page `i` of a segment's walk: its page number within the sequence,
 // and its place in the pool (-1: passed over).
 __device__ __forceinline__ void look_up(const AttnParams& p, const Segment& s, int i, int& logical, int& id) {
-    logical = p.page_sel ? __ldg(p.page_sel + ((size_t)s.b * p.c.kv_heads + s.h) * p.nsel + i) : i;
+    logical = p.page_sel ? p.page_sel[((size_t)s.b * p.c.kv_heads + s.h) * p.nsel + i] : i;
     id = -1;
     if (logical < 0 || logical >= (s.len.kv + kPageTokens - 1) / kPageTokens) return;
-    id = __ldg(p.c.table + (size_t)s.b * p.c.width + logical);
+    id = p.c.table[(size_t)s.b * p.c.width + logical];
     if (id < 0 || id >= p.c.pages) {
         atomicOr(p.c.err, VSA_DEVERR_INDEX);
         id = -1;

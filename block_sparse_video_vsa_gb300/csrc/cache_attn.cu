@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
         const int row0 = at.t * p.tile;
         const int live_rows = min(at.len.q * p.group, row0 + 8 * kNT);
         int min_lim = at.len.kv;
-        const float c_head = p.scale_log2 * (p.c.kv_scale ? __ldg(p.c.kv_scale + at.h) : 1.f);
+        const float c_head = p.scale_log2 * (p.c.kv_scale ? p.c.kv_scale[at.h] : 1.f);
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             const int row = row0 + nt * 8 + g;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
             float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
-                const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                const uint4 x = real ? src[i] : make_uint4(0, 0, 0, 0);
                 w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
             }
 #pragma unroll
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
         // ------------------------- the last warp: join the states, write the rows
         // (in the order of their pieces: the sums do not depend on which came last).
         constexpr int kPer = kD / 32;  // channels of a lane
-        const float v_head = p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + at.h) : 1.f;
+        const float v_head = p.c.kv_scale ? p.c.kv_scale[p.c.kv_heads + at.h] : 1.f;
         const int n = none ? 0 : present;
         // (Short loops: code that runs once a unit costs more to fetch than to run.)
         constexpr int kRows = State::kRows, kLanes = 32 / kRows;  // lanes of a row
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) 
             }
             const int qi = row / p.group, head = u.y * p.group + row - qi * p.group;
             const bool live = row < seq_lens(p, u.x).q * p.group && l != 0.f;
-            const float inv = live ? (p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + u.y) : 1.f) / l : 0.f;
+            const float inv = live ? (p.c.kv_scale ? p.c.kv_scale[p.c.kv_heads + u.y] : 1.f) / l : 0.f;
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)u.x * p.Sq + qi) * p.heads + head) * (kD / 8));
             dst[threadIdx.x] = live ? pack_bf16x2(y.x * inv, y.y * inv) : 0u;
             if (threadIdx.x == 0 && p.lse)

@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             if (ok) {
                 tc_fence_after();
                 const int e = stage_query<kD>(row_s, t_lane + kTmemQ);
-                ms.scale[u & 1][r] = p.scale_log2 * (p.c.kv_scale ? __ldg(p.c.kv_scale + s.h) : 1.f) * pow2i(-e);
+                ms.scale[u & 1][r] = p.scale_log2 * (p.c.kv_scale ? p.c.kv_scale[s.h] : 1.f) * pow2i(-e);
                 tc_fence_before();
             }
             __syncwarp();
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             const size_t part = (2 * (size_t)blockIdx.x + (sg.first > 0 ? 0 : 1)) * 128 + r;
             if (sg.whole) {
                 const float inv =
-                    live ? (p.c.kv_scale ? __ldg(p.c.kv_scale + p.c.kv_heads + sg.h) : 1.f) / lt : 0.f;
+                    live ? (p.c.kv_scale ? p.c.kv_scale[p.c.kv_heads + sg.h] : 1.f) / lt : 0.f;
                 a_e *= inv;
                 a_o *= inv;
             }

@@ -52,12 +52,13 @@ struct Sector {
 __device__ __forceinline__ Sector load_sector(const unsigned char* at, bool wide) {
     Sector s;
     if (wide) {
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(s.w[0]), "=r"(s.w[1]), "=r"(s.w[2]), "=r"(s.w[3]), "=r"(s.w[4]), "=r"(s.w[5]),
                        "=r"(s.w[6]), "=r"(s.w[7])
-                     : "l"(at));
+                     : "l"(at)
+                     : "memory");
     } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(at)), b = __ldg(reinterpret_cast<const uint4*>(at) + 1);
+        const uint4 a = reinterpret_cast<const uint4*>(at)[0], b = reinterpret_cast<const uint4*>(at)[1];
         s.w[0] = a.x; s.w[1] = a.y; s.w[2] = a.z; s.w[3] = a.w;
         s.w[4] = b.x; s.w[5] = b.y; s.w[6] = b.z; s.w[7] = b.w;
     }
@@ -154,13 +155,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
         c = load_sector(row_of(h) + g1 * 2, p.wide);
     }
     const int n = cache_len(p.c, b, threadIdx.x == 0);
-    const int fresh = min(p.new_lens ? max(__ldg(p.new_lens + b), 0) : p.S, min(p.S, n));
+    const int fresh = min(p.new_lens ? max(p.new_lens[b], 0) : p.S, min(p.S, n));
     const bool live = tok < fresh;
     const int at = n - fresh + tok;  // place in the sequence
     // Where the token goes.
     unsigned char* page = nullptr;
     if (live) {
-        const int id = __ldg(p.c.table + (size_t)b * p.c.width + at / kPageTokens);
+        const int id = p.c.table[(size_t)b * p.c.width + at / kPageTokens];
         if (id >= 0 && id < p.c.pages)
             page = p.c.pool + (size_t)id * p.c.kv_heads * L::kBytes;
         else if (slice == 0)
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
     const int in_page = at % kPageTokens;
     float cs[16], sn[16];
     if (turn0 && live) {
-        const int pos = p.positions ? __ldg(p.positions + (size_t)b * p.S + tok) : at;
+        const int pos = p.positions ? p.positions[(size_t)b * p.S + tok] : at;
         if (pos >= 0 && pos < p.rope_rows) {
             // Angle i is that of channels (g0 + 2i, + 1) and, from 8 on, (g1 + 2i - 16, + 1), or of (g0 + i, g1 + i).
             const float4* row = reinterpret_cast<const float4*>(p.rope + (size_t)pos * p.R + (kPairs ? g0 / 2 : g0));
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4* at4 = row + i + (i < 2 ? 0 : skip);
-                const float4 u = __ldg(at4), w = __ldg(at4 + p.R / 8);
+                const float4 u = at4[0], w = at4[p.R / 8];
                 cs[4 * i] = u.x; cs[4 * i + 1] = u.y; cs[4 * i + 2] = u.z; cs[4 * i + 3] = u.w;
                 sn[4 * i] = w.x; sn[4 * i + 1] = w.y; sn[4 * i + 2] = w.z; sn[4 * i + 3] = w.w;
             }
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
             store_sector(dst + g0 * 2, y, p.wide);
             store_sector(dst + g1 * 2, z, p.wide);
         } else if (page) {
-            const float hs = p.c.kv_scale ? __ldg(p.c.kv_scale + (is_k ? 0 : p.c.kv_heads) + kh) : 1.f;
+            const float hs = p.c.kv_scale ? p.c.kv_scale[(is_k ? 0 : p.c.kv_heads) + kh] : 1.f;
             const float inv = __frcp_rn(hs);
             uint32_t c0[2], c1[2];
             const uint32_t s0 = quantise16(x, inv, c0), s1 = quantise16(x + 16, inv, c1);
@@ -278,35 +279,41 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(ReadParams p) {
     const int n = cache_len(p.c, b, threadIdx.x == 0);
     const unsigned char* page = nullptr;
     if (first < n) {
-        const int id = __ldg(p.c.table + (size_t)b * p.c.width + blockIdx.x);
+        const int id = p.c.table[(size_t)b * p.c.width + blockIdx.x];
         if (id >= 0 && id < p.c.pages)
             page = p.c.pool + ((size_t)id * p.c.kv_heads + h) * L::kBytes;
         else if (threadIdx.x == 0)
             atomicOr(p.c.err, VSA_DEVERR_INDEX);
     }
+    // Both sides' loads come before the first store, which may be to anywhere.
+    constexpr int kTurns = kPageTokens / kStep;
+    float hs[2];
+    uint32_t code[2][kTurns], scale[2][kTurns];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-        const float hs = p.c.kv_scale ? __ldg(p.c.kv_scale + side * p.c.kv_heads + h) : 1.f;
-        uint32_t code[kPageTokens / kStep], scale[kPageTokens / kStep];
+        hs[side] = p.c.kv_scale ? p.c.kv_scale[side * p.c.kv_heads + h] : 1.f;
 #pragma unroll
-        for (int i = 0; i < kPageTokens / kStep; ++i) {
+        for (int i = 0; i < kTurns; ++i) {
             const int t = threadIdx.x / kLanes + i * kStep;
             const bool held = page && first + t < n;
-            code[i] = held ? __ldg(reinterpret_cast<const uint32_t*>(page + side * L::kV + t * L::kRow) + lane) : 0u;
-            scale[i] = held ? (uint32_t)__ldg(page + (side ? L::kVScale : L::kKScale) + t * L::kGroups + lane / 2) : 0u;
+            code[side][i] = held ? reinterpret_cast<const uint32_t*>(page + side * L::kV + t * L::kRow)[lane] : 0u;
+            scale[side][i] = held ? (uint32_t)page[(side ? L::kVScale : L::kKScale) + t * L::kGroups + lane / 2] : 0u;
         }
+    }
 #pragma unroll
-        for (int i = 0; i < kPageTokens / kStep; ++i) {
+    for (int side = 0; side < 2; ++side) {
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
             const int t = first + threadIdx.x / kLanes + i * kStep;
             if (t >= p.S) continue;
             uint32_t e[4], w[4];
-            e2m1_to_f16(code[i], e);
-            const uint32_t s = e4m3_to_f16(scale[i] * 0x101u);
+            e2m1_to_f16(code[side][i], e);
+            const uint32_t s = e4m3_to_f16(scale[side][i] * 0x101u);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t y = mul_f16x2(e[j], s);
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y));
-                w[j] = pack_bf16x2(f.x * hs, f.y * hs);
+                w[j] = pack_bf16x2(f.x * hs[side], f.y * hs[side]);
             }
             uint4* dst = (side ? p.v : p.k) + (((size_t)b * p.S + t) * p.c.kv_heads + h) * kLanes + lane;
             __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));

@@ -2,6 +2,7 @@
 against hand values, and the refusals of the C ABI and the Python binding
 (nothing here launches a kernel)."""
 import ctypes
+import os
 
 import numpy as np
 import pytest
@@ -146,3 +147,17 @@ def test_native_front_leaves_what_it_does_not_take(lib):
     assert front.attn() is False and front.read(1, 2, 3, 4, 5, 6, 7) is False
     with pytest.raises(TypeError):
         front.bind(1)
+
+
+def test_cache_kernels_read_nothing_as_read_only_data():
+    """They are launched before the kernel ahead of them has ended, which may write what they read: a
+    non-coherent load asks for memory that nobody writes during the reading kernel's life, and the
+    compiler may move it before the wait for that end."""
+    csrc = os.path.dirname(vbuild.FRONT_SRC)
+    names = [n for n in sorted(os.listdir(csrc)) if n.startswith("cache") and n.endswith((".cu", ".cuh"))]
+    assert names == ["cache.cuh", "cache_attn.cu", "cache_chunk.cu", "cache_store.cu"]
+    for name in names:
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        for word in ("__ldg", ".nc.", "ld.global.nc", "__restrict__", "__ldca", "tex1D"):
+            assert word not in text, (name, word)
