@@ -685,16 +685,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) 
             float top = m;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) top = fmaxf(top, ml[k].x);
-            if (top == -INFINITY) continue;
-            const float keep = ex2_approx(m - top);
+            // (Parts without a key leave the maximum at -infinity, and so does a row of NaN,
+            // whose sum is NaN: only an empty part is passed over.)
+            const float keep = m == top ? 1.f : ex2_approx(m - top);
             m = top;
             l *= keep;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) sum[i] *= keep;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                if (ml[k].x == -INFINITY) continue;
-                const float a = ex2_approx(ml[k].x - m);
+                if (ml[k].x == -INFINITY && ml[k].y == 0.f) continue;
+                const float a = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - m);
                 l = fmaf(a, ml[k].y, l);
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) sum[i] = fmaf(a, o[k][i], sum[i]);

@@ -1,0 +1,65 @@
+"""GPU: values at the edges of what the 4-bit cache's attention takes: NaN in
+queries, scales so small that they leave fp32, weights far below the largest,
+queries whose channels are far apart."""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_video_vsa_gb300 as vsa
+import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def random_cache(seed, lens, kv, D):
+    """(pool, table, lens on the GPU, k and v as read back) of sequences of `lens` random tokens."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    counts = [-(-n // 64) for n in lens]
+    width, most = max(counts), max(lens)
+    pool = vsa.cache_pool(sum(counts), kv, D)
+    table = torch.full((len(lens), width), -1, dtype=torch.int32, device="cuda")
+    order = torch.randperm(sum(counts), generator=g, device="cuda").int()
+    at = 0
+    for b, c in enumerate(counts):
+        table[b, :c] = order[at:at + c]
+        at += c
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((len(lens), most, kv, D), generator=g, device="cuda").bfloat16() for _ in "kv")
+    vsa.cache_append(pool, k, v, table, n, new_lens=n)
+    return pool, table, n, *vsa.cache_read(pool, table, n, most), g
+
+
+@pytest.mark.parametrize("D,kv,heads,Sq,lens", [
+    (128, 1, 1, 1, [300]),         # a unit that is not cut
+    (128, 1, 8, 1, [20000]),       # one row a head, cut over the grid
+    (64, 2, 32, 1, [20000, 70]),   # 16 rows a kv head, cut
+    (128, 1, 4, 40, [20000]),      # chunks, cut
+    (64, 2, 6, 50, [513, 64]),     # chunks, whole
+])
+def test_a_nan_query_gives_nan_however_the_work_is_cut(D, kv, heads, Sq, lens):
+    """By the definition a NaN in a query makes every logit of its row NaN; the other rows keep their bits."""
+    pool, table, n, _, _, g = random_cache(Sq + D, lens, kv, D)
+    q = torch.randn((len(lens), Sq, heads, D), generator=g, device="cuda").bfloat16()
+    base = vsa.cache_attn(q, pool, table, n, causal=False)
+    sick = q.clone()
+    rows = {(0, 0, heads - 1), (len(lens) - 1, Sq - 1, 0), (0, Sq // 2, heads // 2)}
+    for j, (b, i, h) in enumerate(sorted(rows)):  # (an infinity's products with keys of both signs and 0 too)
+        sick[b, i, h, (7 * i + h) % D] = float("inf" if j == 1 else "nan")
+    out, lse = vsa.cache_attn(sick, pool, table, n, causal=False)
+    for b in range(len(lens)):
+        for i in range(Sq):
+            for h in range(heads):
+                if (b, i, h) in rows:
+                    assert out[b, i, h].isnan().all() and lse[b, h, i].isnan(), (b, i, h)
+                else:
+                    assert torch.equal(out[b, i, h], base[0][b, i, h]), (b, i, h)
+                    assert torch.equal(lse[b, h, i], base[1][b, h, i]), (b, i, h)
+    # Rows from a sequence's query count on have no key, whatever they hold.
+    out, lse = vsa.cache_attn(torch.full_like(q, float("nan")), pool, table, n,
+                              q_lens=torch.zeros_like(n), causal=False)
+    assert not out.any() and torch.isneginf(lse).all()
+    assert vsa.device_error(reset=True) == 0
