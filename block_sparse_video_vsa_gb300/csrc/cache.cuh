@@ -143,6 +143,14 @@ __device__ __forceinline__ int q_exponent(float amax) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
 
+// What a row's logits are multiplied with (log2 units): a normal number whatever
+// its factors are, for keys that a row does not see have a logit of -infinity,
+// and -infinity * 0 is NaN.  (A logit is below 2^34 before: one that small a
+// factor brings below 2^-92, where it is 0 to the exponential as it should be.)
+__device__ __forceinline__ float logit_scale(float scale_log2, float k_head, int e) {
+    return fmaxf(scale_log2 * k_head * pow2i(-e), 1.17549435e-38f);
+}
+
 // Bounded wait of a whole warp for a phase of a barrier.  Between looks the warp
 // sleeps kSleep ns: waiting roles share their scheduler with working ones.
 template <int kSleep>

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
         const int row0 = at.t * p.tile;
         const int live_rows = min(at.len.q * p.group, row0 + 8 * kNT);
         int min_lim = at.len.kv;
-        const float c_head = p.scale_log2 * (p.c.kv_scale ? p.c.kv_scale[at.h] : 1.f);
+        const float k_head = p.c.kv_scale ? p.c.kv_scale[at.h] : 1.f;
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             const int row = row0 + nt * 8 + g;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
             for (int c = 0; c < 2; ++c) {
                 const int er = __shfl_sync(0xffffffffu, e, (2 * t + c) * 4);
                 const int r = row0 + nt * 8 + 2 * t + c;
-                rs_scale[nt][c] = c_head * pow2i(-er);
+                rs_scale[nt][c] = logit_scale(p.scale_log2, k_head, er);
                 rs_m[nt][c] = -INFINITY;
                 rs_l[nt][c] = 0.f;
                 int lim = at.len.kv;

@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             if (ok) {
                 tc_fence_after();
                 const int e = stage_query<kD>(row_s, t_lane + kTmemQ);
-                ms.scale[u & 1][r] = p.scale_log2 * (p.c.kv_scale ? p.c.kv_scale[s.h] : 1.f) * pow2i(-e);
+                ms.scale[u & 1][r] = logit_scale(p.scale_log2, p.c.kv_scale ? p.c.kv_scale[s.h] : 1.f, e);
                 tc_fence_before();
             }
             __syncwarp();

@@ -63,3 +63,23 @@ def test_a_nan_query_gives_nan_however_the_work_is_cut(D, kv, heads, Sq, lens):
                               q_lens=torch.zeros_like(n), causal=False)
     assert not out.any() and torch.isneginf(lse).all()
     assert vsa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("Sq", [1, 40])
+def test_a_scale_below_fp32_leaves_masked_keys_out(Sq):
+    """Queries of 1e-34 on a head scale of 1e-10: every logit is 0 to fp32, and the slots past the length
+    stay out of the sum."""
+    D, kv, heads, n = 128, 2, 4, 100
+    pool, table, lens, _, vv, g = random_cache(5, [n], kv, D)
+    scale = torch.tensor([[1e-10] * kv, [1.0] * kv], device="cuda")
+    q = (1e-34 * torch.randn((1, Sq, heads, D), generator=g, device="cuda")).bfloat16()
+    for causal in (False, True):
+        out, lse = vsa.cache_attn(q, pool, table, lens, causal=causal, kv_scale=scale)
+        for i in range(Sq):
+            seen = n - Sq + i + 1 if causal else n
+            want = vv[0, :seen].double().mean(0).repeat_interleave(heads // kv, 0)
+            mag = vv[0, :seen].double().abs().mean(0).repeat_interleave(heads // kv, 0)
+            # equal weights: P and the sum are exact up to 2^-21; the result to bf16 2^-8
+            assert ((out[0, i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * mag).all()
+            assert (lse[0, :, i].double() - np.log(seen)).abs().max() <= 2.0 ** -20 * (1 + np.log(seen))
+    assert vsa.device_error(reset=True) == 0
