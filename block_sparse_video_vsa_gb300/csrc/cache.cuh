@@ -201,7 +201,7 @@ struct AttnParams {
     uint4* out;
     float* lse;               // [B][heads][Sq], or null
     float* part_o;            // [2 * grid][tile][D]
-    float2* part_ml;          // [2 * grid][tile]: maximum (log2 units), sum
+    float2* part_ml;          // [2 * grid][tile]: reference (log2 units), sum
     void* scratch;            // token_kernel: [grid][warps][2] states
     int4* places;             // [grid]: where each CTA's part begins (b, h, t, page); b = -1: between units
     int Sq, heads, group, nsel, causal;
@@ -516,7 +516,13 @@ __device__ __forceinline__ void look_up(const AttnParams& p, const Segment& s, i
 
 constexpr int kMaxGrid = 160;                     // CTAs of an attention launch: one for each SM (152 on GB300)
 constexpr uint64_t kCacheWaitNs = 2000000000ull;  // 2 s
-constexpr float kCacheRescale = 8.0f;             // growth of the maximum (log2 units) that rescales the output
+// The reference that a row's weights are taken against, 2^(logit - reference),
+// starts kCacheHeadroom (log2 units) below the row's maximum, and moves when the
+// maximum has grown by more than kCacheRescale.  Weights then reach 2^15, inside
+// fp16, and what fp16 cannot hold at the other end (below 2^-25) is under 2^-32
+// of the row's largest; against the maximum itself it would be 2^-25, and many
+// such weights on a long cache would be missing from the output, not from the sum.
+constexpr float kCacheHeadroom = 7.0f, kCacheRescale = 8.0f;
 
 // cache_chunk.cu
 cudaError_t launch_chunk(const AttnParams& p, int D, cudaStream_t stream);

@@ -25,9 +25,10 @@
 //    of four tokens and the conversion's byte holds two tokens' codes of a
 //    channel.  Conversion and scale are two instructions for two elements
 //    (a conversion and a product), exact in fp16.
-//  * P is rounded to fp16 (2^-11 relative; the sum keeps the fp32 values);
-//    maximum, sum and output are fp32.  The maximum is followed lazily: the
-//    output is rescaled when it grows by more than 2^8.
+//  * P is rounded to fp16 (2^-11 relative, down to 2^-32 of the row's largest;
+//    the sum keeps the fp32 values); reference, sum and output are fp32.  The
+//    reference (7 below the maximum, see kCacheHeadroom) follows lazily: the
+//    output is rescaled when the maximum grows by more than 2^8.
 //  * Measured (GB300): 61 ragged sequences of up to 12000 tokens, 32 heads on 8
 //    of 128: 100.5 us, 4.5 TB/s (66% of the measured copy rate).  What bounds it
 //    is issue: 1215 instructions a page at 0.55 a scheduler and cycle, 12 warps
@@ -90,7 +91,7 @@ struct Tasks {
     }
 };
 
-// A warp's state at a unit's end: O [kRows][kRowPad], then (maximum in log2
+// A warp's state at a unit's end: O [kRows][kRowPad], then (reference in log2
 // units, sum) [kRows].
 template <int kD, int kNT>
 struct TokenState {
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
         const bool none = at.first == at.last;  // no pages: this warp writes the rows alone
         // ------------------------------------------------ the unit's queries
         uint32_t qf[kNT][2 * kWords][2];
-        float rs_m[kNT][2], rs_l[kNT][2];  // rows nt * 8 + 2 t + c: maximum (log2 units), this lane's share of the sum
+        float rs_m[kNT][2], rs_l[kNT][2];  // rows nt * 8 + 2 t + c: reference (log2 units), this lane's share of the sum
         float rs_scale[kNT][2];            // logit -> log2 units
         int rs_lim[kNT][2];                // first key the row does not see
         const int row0 = at.t * p.tile;
@@ -404,9 +405,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
                 for (int c = 0; c < 2; ++c) {
                     // (No branch: the exponential of a step that needs none costs less than one.)
                     const float top = mx[c] * rs_scale[nt][c];
-                    const bool jump = top > rs_m[nt][c] + kCacheRescale;
-                    const float next = jump ? top : rs_m[nt][c];
-                    alpha[nt][c] = jump ? ex2_approx(rs_m[nt][c] - top) : 1.f;  // (0 from a maximum of -infinity)
+                    const bool jump = top > rs_m[nt][c] + (kCacheHeadroom + kCacheRescale);
+                    const float next = jump ? top - kCacheHeadroom : rs_m[nt][c];
+                    alpha[nt][c] = jump ? ex2_approx(rs_m[nt][c] - next) : 1.f;  // (0 from a reference of -infinity)
                     rs_m[nt][c] = next;
                     rs_l[nt][c] *= alpha[nt][c];
                     rescale |= jump;
@@ -685,7 +686,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) 
             float top = m;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) top = fmaxf(top, ml[k].x);
-            // (Parts without a key leave the maximum at -infinity, and so does a row of NaN,
+            // (Parts without a key leave the reference at -infinity, and so does a row of NaN,
             // whose sum is NaN: only an empty part is passed over.)
             const float keep = m == top ? 1.f : ex2_approx(m - top);
             m = top;

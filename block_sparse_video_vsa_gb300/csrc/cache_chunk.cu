@@ -4,7 +4,7 @@
 // Tensor bound for long chunks (4 * D flops for each row and key), so the
 // structure is the fine stage's: 128 query rows a unit, one TMEM lane each,
 // 128 keys (two pages) a step, Q and P as A operands in TMEM, two softmax
-// groups that take the steps in turn with a maximum, sum and output of their
+// groups that take the steps in turn with a reference, sum and output of their
 // own, joined at the unit's end.  What differs is where K and V come from: two
 // producer warps copy pages (halves: codes and scales of K or of V) into rings,
 // and two warpgroups, one for K and one for V, convert each step's two pages
@@ -82,7 +82,7 @@ struct __align__(16) ChunkMisc {
     uint64_t drain[2];
     int2 key0[kMetaSteps];   // first key of a step's pages (kNoKey: none)
     int raw_keys[2][kRawHalves];  // keys of a half page's slots that the sequence has (0: passed over)
-    float xm[2][2][128];     // [unit parity][group][row]: maximum, sum at the unit's end
+    float xm[2][2][128];     // [unit parity][group][row]: reference, sum at the unit's end
     float xl[2][2][128];
     float scale[2][128];     // [unit parity][row]: logit -> log2 units
     SoftWalk soft[8];
@@ -613,11 +613,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                     }
                 }
                 const float mx = fmaxf(chunk_max64(x), chunk_max64(x + 64)) * c2;
-                // Lazy maximum: O and l are rescaled on a jump only.
+                // The reference m follows the maximum lazily: O and l are rescaled on a jump only.
                 float alpha = 1.f;
-                if (mx > m + kCacheRescale) {
-                    alpha = m == ninf ? 0.f : ex2_approx(m - mx);
-                    m = mx;
+                if (mx > m + (kCacheHeadroom + kCacheRescale)) {
+                    const float next = mx - kCacheHeadroom;
+                    alpha = m == ninf ? 0.f : ex2_approx(m - next);
+                    m = next;
                     l *= alpha;
                 }
                 const float mb = m == ninf ? 0.f : m;

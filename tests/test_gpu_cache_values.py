@@ -83,3 +83,37 @@ def test_a_scale_below_fp32_leaves_masked_keys_out(Sq):
             assert ((out[0, i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * mag).all()
             assert (lse[0, :, i].double() - np.log(seen)).abs().max() <= 2.0 ** -20 * (1 + np.log(seen))
     assert vsa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("D,Sq", [(64, 1), (128, 1), (64, 17), (128, 17)])
+def test_many_small_weights_count_beside_a_large_one(D, Sq):
+    """One key of weight 1 and n - 1 of weight 2^-26: together they are 2^-8 of the sum, and with v = 0 at
+    the first and 1 at the others all of the output.  The pages of the small keys are one page, shared."""
+    B, kv, pages = 8, 40, 4096
+    n = 64 * pages
+    pool = np.zeros((2, kv, 72 * D), np.uint8)
+    one, zero = np.full(D, 2, np.uint8), np.zeros(D, np.uint8)  # codes of 1 and 0
+    unit = np.full(D // 16, 0x38, np.uint8)                      # scales of 1
+    six = zero.copy()
+    six[0] = 7                                                   # a 6 in channel 0
+    for h in range(kv):
+        for page in (0, 1):
+            for t in range(64):
+                first = page == 0 and t == 0
+                ref.put(pool, page, t, h, D, 0, six if first else zero, unit)
+                ref.put(pool, page, t, h, D, 1, zero if first else one, unit)
+    table = np.ones((B, pages), np.int32)
+    table[:, 0] = 0
+    lens = np.full(B, n, np.int32)
+    q = torch.zeros((B, Sq, kv, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    sm = 26 * np.log(2.0) / 6
+    out, lse = vsa.cache_attn(q, dev(pool), dev(table), dev(lens), causal=False, sm_scale=float(sm))
+    small = (n - 1) * 2.0 ** -26
+    want = small / (1 + small)
+    # A weight of 2^-26 is a whole number of fp16's smallest steps once the largest is 2^7, so what is left
+    # is exp2 and the fp32 sums (the logit is off by 26 * 2^-23, exp2 by 2^-21, sums of 2^12 terms a lane
+    # by 2^-12 at most) and the result's rounding to bf16, 2^-8 of it.
+    assert ((out.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * want).all(), out.double().mean().item() / want
+    assert ((lse.double() - (26 * np.log(2.0) + np.log1p(small))).abs() <= 2.0 ** -11).all()
+    assert vsa.device_error(reset=True) == 0
