@@ -133,9 +133,11 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // Power-of-two factor that brings a query row of largest magnitude `amax`
-// near 2^14, so that its bf16 values (8 significant bits) convert to fp16 (11)
-// without rounding down to 2^-38 of the row's largest; 1 for a row of zeros,
-// infinities or NaN alone.  The inverse goes into the row's softmax scale.
+// into [2^14, 2^15), so that its bf16 values (8 significant bits) convert to
+// fp16 (11, steps of 2^-24 at least) without rounding down to 2^-31 of the row's
+// largest; what is smaller is off by 2^-25 at most, 2^-39 of the largest (rows
+// below 2^-106 are scaled by 2^120 only: off by 2^-145).  1 for a row of zeros
+// or with an infinity.  The inverse goes into the row's softmax scale.
 __device__ __forceinline__ int q_exponent(float amax) {
     if (!(amax > 0.f) || amax > 3.4e38f) return 0;
     const int e = (int)((__float_as_uint(amax) >> 23) & 0xFFu) - 127;  // below the normals: -127

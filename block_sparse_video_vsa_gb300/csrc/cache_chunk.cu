@@ -17,7 +17,8 @@
 //  * TMEM (512 columns): S [0,128); P (fp16 pairs) [128,192); Q [192,256);
 //    O_0 [256,384); O_1 [384,512).
 //  * A query row is scaled by a power of two on its way to fp16 (its bf16
-//    values keep all their bits) and the inverse joins its softmax scale.
+//    values keep all their bits down to 2^-31 of its largest, see q_exponent)
+//    and the inverse joins its softmax scale.
 //  * Every wait is bounded; one that runs out raises the CTA's abort flag and
 //    the device error word, and each role winds down.
 //  * Measured (GB300): 1560 queries x 40 heads of 128 over 32760 keys, 957 us =

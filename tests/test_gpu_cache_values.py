@@ -117,3 +117,33 @@ def test_many_small_weights_count_beside_a_large_one(D, Sq):
     assert ((out.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * want).all(), out.double().mean().item() / want
     assert ((lse.double() - (26 * np.log(2.0) + np.log1p(small))).abs() <= 2.0 ** -11).all()
     assert vsa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("D,heads,Sq", [(128, 2, 1), (64, 16, 1), (128, 2, 40), (64, 3, 20)])
+def test_queries_with_channels_far_apart(D, heads, Sq):
+    """A channel of 2^20 whose keys are 0 beside channels of 2^-12 to 1 (2^-32 to 2^-20 of the largest): the
+    small ones make the logits, and lose at most 2^-39 of the row's largest each on their way to fp16."""
+    n, kv = 700, 1
+    r = np.random.default_rng(D)
+    k = r.standard_normal((1, n, kv, D)).astype(np.float32) * 2.0
+    k[..., 0] = 0
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pool, table, lens, _, _, _ = random_cache(2, [n], kv, D)
+    v = torch.randn((1, n, kv, D), generator=g, device="cuda").bfloat16()
+    vsa.cache_append(pool, dev(k).bfloat16(), v, table, lens)
+    kk, vv = (x[0, :, 0].double() for x in vsa.cache_read(pool, table, lens, n))
+    q = torch.randn((1, Sq, heads, D), generator=g, device="cuda") * torch.exp2(
+        torch.randint(-12, 1, (1, Sq, heads, D), generator=g, device="cuda").float())
+    q[..., 0] = 2.0 ** 20
+    q = q.bfloat16()
+    out, lse = vsa.cache_attn(q, pool, table, lens, causal=False, sm_scale=0.5)
+    s = 0.5 * torch.einsum("qhd,kd->qhk", q[0].double(), kk)
+    w = s.softmax(-1)
+    want, wabs = w @ vv, w @ vv.abs()
+    # logits: 2^-39 * 2^20 a channel from fp16, fp32 sums of D products (D + 4 roundings of 2^-24)
+    absk = 0.5 * kk.abs().sum(-1).max()
+    d = 2.0 ** -19 * absk + (D + 4) * 2.0 ** -24 * 0.5 * torch.einsum("qhd,kd->qhk", q[0].double().abs(), kk.abs()).amax()
+    lim = (2.0 ** -11 + 2.0 ** -21 + 2 * d) * wabs + n * 2.0 ** -25 * vv.abs().max() * w.amax(-1, keepdim=True)
+    assert ((out[0].double() - want).abs() <= lim + 2.0 ** -8 * (want.abs() + lim)).all()
+    assert (lse[0].T.double() - torch.logsumexp(s, -1)).abs().max() <= d + 2.0 ** -19
+    assert vsa.device_error(reset=True) == 0
