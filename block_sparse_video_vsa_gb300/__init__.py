@@ -751,7 +751,8 @@ def cache_append(pool, k, v, table, kv_lens, new_lens=None, rope=None, positions
 
 def cache_read(pool, table, kv_lens, S: int, kv_scale=None, k=None, v=None, stream=None):
     """The first S cached tokens of every sequence -> (k, v) bf16 [B, S, kv_heads, D], zero past each
-    length; with S a multiple of 64 they are tiled tensors for sparse_attn_fwd (vsa_cache_read)."""
+    length; if tiled rows were appended, with their padding slots, S = 64 * num_cubes(grid) gives the
+    tiled tensors that sparse_attn_fwd takes with the grid's vbs (vsa_cache_read)."""
     if stream is None and (_front_module or _front()):
         got = _front_module.read(pool, table, kv_lens, S, kv_scale, k, v)
         if got.__class__ is int:
@@ -782,7 +783,9 @@ def cache_attn(q, pool, table, kv_lens, q_lens=None, causal: bool = True, page_s
     (out bf16 like q, lse fp32 [B, heads, Sq] or None) (vsa_cache_attn).
 
     q_lens (int32 [B]) are each sequence's query rows (None: Sq), its last tokens when causal;
-    page_sel (int32 [B, kv_heads, n]) limits each kv head to n pages of its sequence (-1: none)."""
+    page_sel (int32 [B, kv_heads, n]) limits each kv head to n pages of its sequence (-1: none).
+    Every place below kv_lens is a key: append raster tokens, or tiled ones of a grid whose sides are
+    multiples of 4 (other grids' tiled rows hold padding slots, which would be attended)."""
     if stream is None and (_front_module or _front()):
         got = _front_module.attn(q, pool, table, kv_lens, q_lens, causal, page_sel, kv_scale, sm_scale, workspace, out,
                                  lse, want_lse)

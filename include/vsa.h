@@ -20,7 +20,7 @@
  * (vsa_sparse_attn_fwd_gated), and a mean-pool block selector with a
  * cumulative threshold for sequences in 128-token blocks
  * (vsa_block_select).  For video generated chunk by chunk, a paged cache of
- * earlier keys and values in 4 bits, one cube (64 tokens) a page:
+ * earlier keys and values in 4 bits, 64 tokens a page:
  * vsa_cache_append, vsa_cache_attn and vsa_cache_read.
  *
  * Sources (page title, section):
@@ -427,7 +427,16 @@ vsa_status vsa_block_select(const void* q, const void* k, int32_t B, int32_t S, 
 
 /*
  * A paged cache of keys and values in 4 bits (no counterpart in the pages: it
- * keeps a clip's earlier cubes for queries that come later).
+ * keeps a clip's earlier tokens for queries that come later).
+ * Order of tokens: a page is 64 tokens of a sequence in the order that they
+ * were appended in, and every place below kv_lens is a token: these calls know
+ * no vbs.  If T, H and W are multiples of 4, every cube is full, a tiled clip can
+ * be appended as it is, and pages (and the pages of a selection) are cubes.  On
+ * any other grid a tiled clip has padding slots between its tokens;
+ * vsa_cache_attn would attend them as keys (of zeros, or what they hold).  There
+ * append raster tokens for vsa_cache_attn: pages are then runs of 64 raster
+ * tokens.  A tiled clip's pages may still be kept for vsa_cache_read and the
+ * sparse attention, which takes vbs.
  *   pool     : uint8 [pages, kv_heads, 72 * D], 16-byte aligned; page p of kv
  *              head h holds 64 tokens:
  *                K codes [64][D / 2] | V codes [64][D / 2] |
@@ -501,7 +510,8 @@ vsa_status vsa_cache_append(const vsa_cache* c, const void* q, const void* k, co
  *   k, v : bf16 [B, S, kv_heads, D] (written in full; rows from kv_lens[b] on
  *          are zero).  code * scale * head scale, rounded to bf16 once (exact
  *          for head scales that are powers of two).
- * With S = 64 * ncubes these are tiled tensors for vsa_sparse_attn_fwd.
+ * Where tiled rows were appended (padding slots included), S = 64 * ncubes gives
+ * the tiled tensors that vsa_sparse_attn_fwd takes with the grid's vbs.
  * B * S < 2^31, S <= 64 * 2^24.
  */
 vsa_status vsa_cache_read(const vsa_cache* c, int32_t S, void* k, void* v, vsa_stream_t stream);
@@ -517,8 +527,9 @@ vsa_status vsa_cache_read(const vsa_cache* c, int32_t S, void* k, void* v, vsa_s
  *   q         : bf16 [B, Sq, heads, D], rotated as the keys were
  *               (vsa_cache_append's q_out); heads a multiple of kv_heads
  *   q_lens    : int32 [B], cut to [0, Sq], or NULL: Sq
- *   page_sel  : int32 [B, kv_heads, nsel]: page numbers within the sequence
- *               (columns of the table), distinct within a row, in any order;
+ *   page_sel  : int32 [B, kv_heads, nsel], one list for all rows of a call:
+ *               page numbers within the sequence (columns of the table; cubes
+ *               only on grids of full cubes, see above), distinct within a row, in any order;
  *               numbers outside the sequence's pages (-1) are passed over.
  *               Or NULL with nsel = 0: every page
  *   sm_scale  : finite; <= 0 selects 1 / sqrt(D)
