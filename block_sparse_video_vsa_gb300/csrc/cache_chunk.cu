@@ -678,7 +678,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             const float lt = __fmaf_rn(a_e, l_e, __fmul_rn(a_o, l_o));
             const uint32_t o_e = ge ? kTmemO1 : kTmemO0, o_o = ge ? kTmemO0 : kTmemO1;
             const RowAt x = row_at<kD>(p, sg, r);
-            const bool real = ok && x.real;
             const bool live = sg.t * 128 + r < sg.len.q * p.group && lt != 0.f;
             const size_t part = (2 * (size_t)blockIdx.x + (sg.first > 0 ? 0 : 1)) * 128 + r;
             if (sg.whole) {
@@ -689,6 +688,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
             }
             if (ok) ok = cache_wait<kSleepShort>(smem_u32(&ms.unit_done), ul & 1, abort_flag, err);
             tc_fence_after();
+            const bool real = ok && x.real;  // (a wait that ran out leaves no whole O to store)
             // Each thread's columns go to its place in the row buffer (the bar.sync
             // above: the next queries have been taken from there), and from there
             // to memory by the lanes together, 64 or 128 bytes of a row: lanes

@@ -161,3 +161,12 @@ def test_cache_kernels_read_nothing_as_read_only_data():
             text = f.read()
         for word in ("__ldg", ".nc.", "ld.global.nc", "__restrict__", "__ldca", "tex1D"):
             assert word not in text, (name, word)
+
+
+def test_chunk_rows_are_stored_only_after_the_wait_for_their_last_product():
+    """The rows that the epilogue stores are chosen after that wait: one that runs out stores none."""
+    with open(os.path.join(os.path.dirname(vbuild.FRONT_SRC), "cache_chunk.cu")) as f:
+        text = f.read()
+    wait, stored = "cache_wait<kSleepShort>(smem_u32(&ms.unit_done)", "const bool real = ok && x.real;"
+    assert text.count(wait) == 1 and text.count(stored) == 1
+    assert text.index(wait) < text.index(stored) < text.index("__ballot_sync(0xffffffffu, real)")
