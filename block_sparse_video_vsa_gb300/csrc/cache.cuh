@@ -153,10 +153,15 @@ __device__ __forceinline__ float logit_scale(float scale_log2, float k_head, int
     return fmaxf(scale_log2 * k_head * pow2i(-e), 1.17549435e-38f);
 }
 
-// Bounded wait of a whole warp for a phase of a barrier.  Between looks the warp
-// sleeps kSleep ns: waiting roles share their scheduler with working ones.
+constexpr uint64_t kCacheWaitNs = 2000000000ull;  // limit of the kernels' waits: 2 s
+
+// Bounded wait of a whole warp for a phase of a barrier: false if *abort was
+// raised, or if limit_ns have passed since the 64th look (then it raises *abort
+// and sets the timeout bit).  Between looks the warp sleeps kSleep ns: waiting
+// roles share their scheduler with working ones.
 template <int kSleep>
-__device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* err) {
+__device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* err,
+                                           uint64_t limit_ns = kCacheWaitNs) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     uint64_t t0 = 0;
 #pragma unroll 1
@@ -167,7 +172,7 @@ __device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, volati
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
         if (__any_sync(0xffffffffu, *abort != 0)) return false;
-        if (__any_sync(0xffffffffu, now - t0 > 2000000000ull)) {  // 2 s
+        if (__any_sync(0xffffffffu, now - t0 > limit_ns)) {
             *abort = 1;
             if ((threadIdx.x & 31) == 0) atomicOr(err, VSA_DEVERR_TIMEOUT);
             return false;
@@ -517,7 +522,6 @@ __device__ __forceinline__ void look_up(const AttnParams& p, const Segment& s, i
 }
 
 constexpr int kMaxGrid = 160;                     // CTAs of an attention launch: one for each SM (152 on GB300)
-constexpr uint64_t kCacheWaitNs = 2000000000ull;  // 2 s
 // The reference that a row's weights are taken against, 2^(logit - reference),
 // starts kCacheHeadroom (log2 units) below the row's maximum, and moves when the
 // maximum has grown by more than kCacheRescale.  Weights then reach 2^15, inside
