@@ -45,6 +45,20 @@ inline cudaError_t allow_smem(K kernel, int smem, std::atomic<uint64_t>& done) {
     return e;
 }
 
+// Registers a thread of `kernel` is launched with; `known` (one for each kernel)
+// keeps the answer once there is one (0: none yet), and no failure.
+template <class K>
+inline cudaError_t launch_registers(K kernel, std::atomic<int>& known, int* regs) {
+    *regs = known.load(std::memory_order_relaxed);
+    if (*regs != 0) return cudaSuccess;
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    *regs = fa.numRegs;
+    known.store(fa.numRegs, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
 #if defined(__CUDACC__)
 
 // The kernels of the cache calls, chunk_kernel apart, are launched while the

@@ -764,14 +764,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
 template <int kD>
 static cudaError_t launch_chunk_d(const AttnParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
+    static std::atomic<int> known{0};
     // The register split draws on the launch's registers; with fewer, setmaxnreg
     // would wait forever, so such a build is refused.
-    static const int regs = [] {
-        cudaFuncAttributes fa;
-        return cudaFuncGetAttributes(&fa, chunk_kernel<kD>) == cudaSuccess ? fa.numRegs : 0;
-    }();
+    int regs = 0;
+    cudaError_t e = launch_registers(chunk_kernel<kD>, known, &regs);
+    if (e != cudaSuccess) return e;
     if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-    const cudaError_t e = allow_smem(chunk_kernel<kD>, chunk_smem<kD>(), done);
+    e = allow_smem(chunk_kernel<kD>, chunk_smem<kD>(), done);
     if (e != cudaSuccess) return e;
     // Not launched early itself: over 32760 keys, 64 rows of 40 heads take 95.4 us
     // so and 102.2 launched early (a ragged batch of prompts 289.6 and 281.1).
