@@ -669,7 +669,7 @@ def _front():
         from .build import front_path
         _torch()
         lib, path = library(), front_path()
-        if os.path.exists(path):
+        if path is not None and os.path.exists(path):
             loader = importlib.machinery.ExtensionFileLoader("_front", path)
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_front", loader))
             loader.exec_module(m)
