@@ -262,27 +262,27 @@ __device__ __forceinline__ int tile_cost(const AttnParams& p, const SeqLens& s, 
     const int n = tile_pages(p, s, t);
     return n > 0 ? n + p.unit_cost : p.idle_cost;
 }
-// sum of floor((a i + b) / m) for i < n (a, b >= 0, m > 0), by Euclid's steps on (a, m).
-static __device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
-    long long sum = 0;
-    while (n > 0) {
-        if (a >= m) {
-            sum += n * (n - 1) / 2 * (a / m);
-            a %= m;
+// sum of floor((k t + c) / g) for t < n (c >= 0, g > 0), in k terms without steps:
+// floor(k z) is the sum of floor(z + j / k) over j < k (Hermite's identity), so
+// with z = (t + c / k) / g every term is the sum of floor((t + c_j) / g) over j,
+// c_j = floor((c + j g) / k), and x / g sums in closed form over whole runs of g.
+// (Loops that stay loops: unrolled, the same sums make a ragged batch of prompts
+// take 312 us instead of 291, for code that a CTA runs once or twice.)
+static __host__ __device__ __noinline__ long long steps_sum(int n, int k, long long c, int g) {
+    unsigned long long sum = 0;  // (terms may pass 2^64 for the longest caches, their differences do not)
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {
+        const long long c_j = (c + j * g) / k;
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {  // the terms below n + c_j, then less those below c_j
+            const long long x = e ? c_j : n + c_j;
+            const long long runs = x < (1LL << 31) ? (long long)((unsigned)x / (unsigned)g) : x / g;
+            const unsigned long long below =
+                (unsigned long long)g * (runs * (runs - 1) / 2) + (unsigned long long)(runs * (x - runs * g));
+            sum += e ? 0ull - below : below;
         }
-        if (b >= m) {
-            sum += n * (b / m);
-            b %= m;
-        }
-        const long long y = a * n + b;
-        if (y < m) break;
-        n = y / m;
-        b = y % m;
-        const long long t = m;
-        m = a;
-        a = t;
     }
-    return sum;
+    return (long long)sum;
 }
 // Cost of one kv head of a sequence: the sum of its tiles.
 __device__ __forceinline__ long long head_cost(const AttnParams& p, const SeqLens& s) {
@@ -299,11 +299,14 @@ __device__ __forceinline__ long long head_cost(const AttnParams& p, const SeqLen
     //   pages = ceil((kv - q + 1 + floor(((t + 1) tile - 1) / group)) / 64)
     //         = floor((tile t + tile - 1 + group (kv - q + 64)) / (64 group)),
     // from the first tile with a key on (a sequence may be shorter than its queries).
+    // A tile of several is 128 rows, a whole number of 64 (see tile_rows).
     const long long lead = (long long)p.group * (s.kv - s.q + kPageTokens) + p.tile - 1, per = 64LL * p.group;
     long long none = 0;
     if (lead < per) none = min((long long)live - 1, (per - lead + p.tile - 1) / p.tile);
     const int end = tile_pages(p, s, live - 1);
-    return sum(live - (int)none - (end == 0), end + floor_sum(live - 1 - none, per, p.tile, lead + none * p.tile));
+    const long long pages =
+        end + steps_sum(live - 1 - (int)none, p.tile / kPageTokens, (lead + none * p.tile) / kPageTokens, p.group);
+    return sum(live - (int)none - (end == 0), pages);
 }
 
 // A place on the line: page `page` of unit (b, h, t) (from the unit's number of pages on: its end).
