@@ -538,8 +538,8 @@ vsa_status vsa_cache_read(const vsa_cache* c, int32_t S, void* k, void* v, vsa_s
  *               replayed at once) need workspaces of their own
  *   out       : bf16 [B, Sq, heads, D] (written in full)
  *   lse       : fp32 [B, heads, Sq] (written), or NULL
- * Logits, softmax statistics and sums are fp32 (|logit| < 2^23: beyond, fp32 has
- * no fractions left, and what comes out is undefined).  P is rounded to fp16:
+ * Logits, softmax statistics and sums are fp32 (|logit| < 2^22: beyond, fp32 has
+ * hardly a fraction left, and what comes out is undefined).  P is rounded to fp16:
  * 2^-11 of each weight; weights below 2^-32 of a row's largest are left out of
  * out, not of lse.  Channels of q below 2^-31 of their row's largest are rounded
  * too, by 2^-39 of that largest at most.

@@ -147,3 +147,29 @@ def test_queries_with_channels_far_apart(D, heads, Sq):
     assert ((out[0].double() - want).abs() <= lim + 2.0 ** -8 * (want.abs() + lim)).all()
     assert (lse[0].T.double() - torch.logsumexp(s, -1)).abs().max() <= d + 2.0 ** -19
     assert vsa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("D,heads,Sq", [(128, 2, 1), (64, 12, 1), (128, 2, 40)])
+def test_logits_near_their_limit_stay_finite(D, heads, Sq):
+    """Logits of up to 2^22: weights may pass 2^15 by what fp32 rounds off a logit, and still fit fp16."""
+    n, kv = 2000, 2 if heads == 2 else 1
+    pool, table, lens, kk, vv, g = random_cache(9, [n], kv, D)
+    rep = heads // kv
+    k, v = (x[0].double().repeat_interleave(rep, 1) for x in (kk, vv))
+    q = torch.randn((1, Sq, heads, D), generator=g, device="cuda")
+    s = torch.einsum("qhd,khd->qhk", q[0].double(), k) / D ** 0.5
+    q = (q * (4.0e6 / s.abs().amax(-1)[None, ..., None])).bfloat16()  # (bf16 moves a logit by 2^-9 of 2^22 or so)
+    s = torch.einsum("qhd,khd->qhk", q[0].double(), k) / D ** 0.5
+    assert 2.0 ** 21 < s.abs().max() < 2.0 ** 22
+    out, lse = vsa.cache_attn(q, pool, table, lens, causal=False)
+    assert out.isfinite().all() and lse.isfinite().all()
+    # Each logit is off by at most (D + 4) roundings of 2^-24 of sum |q k|, and so is the log of their sum.
+    d = (D + 4) * 2.0 ** -24 * torch.einsum("qhd,khd->qhk", q[0].double().abs(), k.abs()).amax(-1) / D ** 0.5
+    assert ((lse[0].T.double() - torch.logsumexp(s, -1)).abs() <= d + 2.0 ** -22 * lse[0].T.abs()).all()
+    # Where the largest logit leads by more than both can be off, the row is its value (bf16: exact for a head scale of 1).
+    top2 = s.topk(2, -1)
+    sure = top2.values[..., 0] - top2.values[..., 1] > 2 * d + 20
+    assert sure.any()
+    pick = v[top2.indices[..., 0], torch.arange(heads, device="cuda")[None, :]]
+    assert ((out[0].double() - pick).abs() <= 2.0 ** -8 * pick.abs() + 1e-6)[sure].all()
+    assert vsa.device_error(reset=True) == 0
