@@ -30,9 +30,9 @@
 //    reference (7 below the maximum, see kCacheHeadroom) follows lazily: the
 //    output is rescaled when the maximum grows by more than 2^8.
 //  * Measured (GB300): 61 ragged sequences of up to 12000 tokens, 32 heads on 8
-//    of 128: 100.5 us, 4.5 TB/s (66% of the measured copy rate).  What bounds it
-//    is issue: 1215 instructions a page at 0.55 a scheduler and cycle, 12 warps
-//    an SM (168 registers).  A producer warp with 7 consumers behind a barrier
+//    of 128: 101 us, 4.45 TB/s (65% of the measured copy rate).  What bounds it
+//    is issue: 1200 instructions a page at 0.55 a scheduler and cycle, 12 warps
+//    an SM (163 registers).  A producer warp with 7 consumers behind a barrier
 //    a unit took 127 us.  One token on one clip of 32760 tokens takes 22 us.
 #include "cache.cuh"
 
@@ -757,13 +757,31 @@ cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
 //  * min_part.  One token on 2000 to 4000 cached ones: 11.8 us with parts of
 //    2 pages, 13.4 with 6, 14.5 with 12; chunks gain nothing below 8.
 //  * Walks of up to `whole` pages are not cut at all (and need no joining
-//    kernel): chunks on 15 pages take 20.5 us whole, 31.0 cut; a token on 32
-//    pages 17.8 whole, 11.8 cut.
+//    kernel).  Times in us, cut and whole, keys of 8 kv heads of 128:
+//      pages                    8            16           32           48
+//      8 rows                   10.2  9.5    10.5 11.9    11.0 15.8    11.3 20.3
+//      8 rows, 8 sequences      11.7 10.1    12.5 12.6    15.6 16.5    17.4 20.9
+//      64 rows                  18.6 13.4    19.3 17.1    22.0 25.3    22.4 33.3
+//      64 rows, 8 sequences     22.5 14.7    28.0 19.3    33.7 26.6    37.2 35.3
+//      500 rows, 8 sequences    42.1 28.9    55.3 38.3    77.6 54.6    91.1 70.6
+//    Whole wins up to 8 pages (token_kernel) and 16 (chunk_kernel) in all cases
+//    measured, D = 64 and 40 kv heads too; beyond, it depends on how many units
+//    there are.
 constexpr int kTokenUnitCost = 2, kChunkUnitCost = 28, kIdleCost = 2;
 constexpr int kTokenMinPart = 2, kChunkMinPart = 8;
 constexpr int kTokenWhole = 8, kChunkWhole = 16;
 
 // Rows of a unit: up to 16 rows a kv head go to token_kernel, more to chunk_kernel.
+// Times in us for 8 kv heads, token_kernel in tiles of 8 | of 16 | chunk_kernel:
+//   rows of a kv head                  8                  9..16        17..24       32..48
+//   D = 128, 4 sequences of 300        9.4 | 10.9 | 12.2  11.5 | 12.2  13.7 | 12.3  13.7 | 12.6
+//            1 of 32760               20.5 | 25.0 | 28.5  26.3 | 28.8  37.7 | 30.7  48.7 | 33.1
+//            16 of 8000               41.2 | 56.1 | 85.7  59.3 | 87.6  98.8 | 89.5   139 | 92.9
+//   D = 64,  4 of 300                  8.4 |  9.7 |  9.9  10.3 | 10.0  12.6 | 10.0  12.6 | 10.0
+//            1 of 32760               15.2 | 18.4 | 24.4  19.4 | 25.0  27.7 | 26.4  33.9 | 29.4
+//            16 of 8000               33.0 | 39.4 | 67.8  41.5 | 69.3  64.6 | 71.0  89.6 | 74.4
+// (the larger number of rows of each column; D = 64 with 17 to 32 rows on long
+// caches could go either way).
 int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
 
 }  // namespace

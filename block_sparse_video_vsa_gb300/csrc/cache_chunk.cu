@@ -21,14 +21,17 @@
 //    and the inverse joins its softmax scale.
 //  * Every wait is bounded; one that runs out raises the CTA's abort flag and
 //    the device error word, and each role winds down.
-//  * Measured (GB300): 1560 queries x 40 heads of 128 over 32760 keys, 957 us =
-//    1.09 PFLOP/s (58% of the measured bf16 burst).  A step takes some 2080
-//    cycles of an SM, of which the tensor pipe is busy 48%; the converting and
-//    softmax warps and the waiting roles issue 5600 instructions for it, 0.67 a
-//    scheduler and cycle.  With one converting warpgroup it took 1200 us, with
+//  * Measured (GB300): 1560 queries x 40 heads of 128 over 32760 keys, 960 us =
+//    1.09 PFLOP/s (57% of the measured bf16 burst).  A step takes some 2010
+//    cycles of an SM, of which the tensor pipe is busy 51%; the converting and
+//    softmax warps and the waiting roles issue 5540 instructions for it, 0.69 a
+//    scheduler and cycle.  1% of them are spills (144 bytes stored and 248 loaded
+//    by ptxas at D = 128, 112 and 216 at D = 64; 45 loads and 9 stores a step).
+//    With one converting warpgroup it took 1200 us, with
 //    256 rows a unit, a tile a softmax group (a conversion then serves twice the
 //    rows, but TMEM has no room for Q, so Q K^T reads both operands from shared
-//    memory, nor for a second S to work ahead in) 1160 to 1215.  How long the
+//    memory, nor for a second S to work ahead in) 1160 to 1215: at D = 128, where
+//    all was measured; at D = 64 two tiles would leave room for Q.  How long the
 //    waits sleep (20 to 250 ns) changes nothing.
 #include "cache.cuh"
 

@@ -14,17 +14,17 @@
 // scale groups, the two halves of a rotated pair among them) and holds their
 // cosines and sines in registers over all heads it walks; a warp takes
 // neighbouring tokens of one head, whose codes are contiguous in the page.
-// Measured: a frame of 1560 tokens x 40 heads of 128, 18.6 us (3.9 TB/s of the
-// bytes it needs, 58% of the measured copy rate), 24 ragged chunks of up to 1003
-// tokens (24 and 8 heads of 64) 34.4 us (4.3 TB/s, 64%).  16 warps an SM issue 0.47
+// Measured: a frame of 1560 tokens x 40 heads of 128, 19.2 us (3.8 TB/s of the
+// bytes it needs, 56% of the measured copy rate), 24 ragged chunks of up to 1003
+// tokens (24 and 8 heads of 64) 33.9 us (4.4 TB/s, 65%).  16 warps an SM issue 0.47
 // instructions a scheduler and cycle and wait for loads otherwise; neither a
 // second row on its way nor 16 channels a thread (32 warps an SM, 20.1 and
-// 40.3 us) changes that for the better.
+// 40.3 us beside 18.6 and 34.4 on the same day) made it better.
 //
 // read_kernel: pages back to bf16 rows, [B, S, kv_heads, D], zero past each
 // sequence's length.  HBM bound (9/16 byte in, 2 bytes out an element): one
 // block a page and head, 16-byte stores.  Measured: 32760 tokens x 40 heads of
-// 128, 141 us, 6.1 TB/s (89% of the measured copy rate).
+// 128, 139 us, 6.2 TB/s (91% of the measured copy rate).
 #include "cache.cuh"
 
 namespace vsa {
