@@ -164,7 +164,8 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 // and -infinity * 0 is NaN.  (A logit is below 2^34 before: one that small a
 // factor brings below 2^-92, where it is 0 to the exponential as it should be.)
 __device__ __forceinline__ float logit_scale(float scale_log2, float k_head, int e) {
-    return fmaxf(scale_log2 * k_head * pow2i(-e), 1.17549435e-38f);
+    const float f = scale_log2 * k_head * pow2i(-e);
+    return f < 1.17549435e-38f ? 1.17549435e-38f : f;  // (NaN stays NaN)
 }
 
 constexpr uint64_t kCacheWaitNs = 2000000000ull;  // limit of the kernels' waits: 2 s

@@ -173,3 +173,20 @@ def test_logits_near_their_limit_stay_finite(D, heads, Sq):
     pick = v[top2.indices[..., 0], torch.arange(heads, device="cuda")[None, :]]
     assert ((out[0].double() - pick).abs() <= 2.0 ** -8 * pick.abs() + 1e-6)[sure].all()
     assert vsa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("Sq", [1, 40])
+def test_a_nan_head_scale_is_not_hidden(Sq):
+    """Head scales are finite by contract; a NaN one gives NaN in its head's rows and leaves the others alone."""
+    kv, D = 2, 64
+    pool, table, lens, _, _, g = random_cache(3, [700], kv, D)
+    q = torch.randn((1, Sq, 4, D), generator=g, device="cuda").bfloat16()
+    scale = torch.ones(2, kv, device="cuda")
+    base = vsa.cache_attn(q, pool, table, lens, kv_scale=scale)
+    for side in (0, 1):
+        bad = scale.clone()
+        bad[side, 1] = float("nan")
+        out, lse = vsa.cache_attn(q, pool, table, lens, kv_scale=bad)
+        assert out[:, :, 2:].isnan().all() and (side == 1 or lse[:, 2:].isnan().all())
+        assert torch.equal(out[:, :, :2], base[0][:, :, :2]) and torch.equal(lse[:, :2], base[1][:, :2])
+    assert vsa.device_error(reset=True) == 0
