@@ -409,7 +409,7 @@ vsa_status vsa_cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t
     vsa_status st = cache_args(c, Sq);
     if (st != VSA_OK) return st;
     if (!q || !workspace || !out || heads <= 0 || heads % c->kv_heads) return VSA_ERR_INVALID_ARG;
-    if (nsel < 0 || (nsel > 0) != (page_sel != nullptr) || !(sm_scale <= FLT_MAX)) return VSA_ERR_INVALID_ARG;
+    if (nsel < 0 || (nsel > 0) != (page_sel != nullptr) || !(fabsf(sm_scale) <= FLT_MAX)) return VSA_ERR_INVALID_ARG;
     if (heads > 65535 || (int64_t)Sq * (heads / c->kv_heads) >= (1 << 24) || nsel >= (1 << 25)) return VSA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(workspace) || !aligned16(out) || !aligned4(q_lens) || !aligned4(page_sel) ||
         !aligned4(lse))

@@ -170,3 +170,8 @@ def test_chunk_rows_are_stored_only_after_the_wait_for_their_last_product():
     wait, stored = "cache_wait<kSleepShort>(smem_u32(&ms.unit_done)", "const bool real = ok && x.real;"
     assert text.count(wait) == 1 and text.count(stored) == 1
     assert text.index(wait) < text.index(stored) < text.index("__ballot_sync(0xffffffffu, real)")
+
+
+def test_attn_refuses_a_scale_of_minus_infinity(lib):
+    """The scale is finite; below zero it selects the default, at minus infinity it is an error."""
+    assert lib.vsa_cache_attn(cache(), A, 1, 4, None, 1, None, 0, float("-inf"), A, A, None, None) == INVALID
