@@ -30,6 +30,7 @@ __all__ = [
     "coarse_attn", "coarse_attn_workspace_bytes", "pair_cubes", "pair_workspace_bytes", "kernel_launches",
     "table_from_csr", "block_select", "block_select_workspace_bytes", "sparse_attn_fwd_peak", "all_cubes",
     "PipelineGraph", "cache_pool", "cache_append", "cache_attn", "cache_attn_workspace_bytes", "cache_read",
+    "cache_tree", "cache_accept", "cache_weigh", "cache_evict",
 ]
 
 _STATUS = {0: "VSA_OK", 1: "VSA_ERR_INVALID_ARG", 2: "VSA_ERR_UNSUPPORTED", 3: "VSA_ERR_ALIGNMENT",
@@ -128,6 +129,17 @@ def _declare(lib):
     lib.vsa_cache_attn.restype = ctypes.c_int
     lib.vsa_cache_attn.argtypes = [ctypes.POINTER(VsaCache), _p, _i32, _i32, _p, _i32, _p, _i32, ctypes.c_float, _p,
                                    _p, _p, _p]
+    lib.vsa_cache_attn_tree.restype = ctypes.c_int
+    lib.vsa_cache_attn_tree.argtypes = [ctypes.POINTER(VsaCache), _p, _i32, _i32, _p, _p, _p, _i32, ctypes.c_float, _p,
+                                        _p, _p, _p]
+    lib.vsa_cache_tree.restype = ctypes.c_int
+    lib.vsa_cache_tree.argtypes = [_p, _i32, _i32, _p, _p, _p, _p, _p, _p]
+    lib.vsa_cache_accept.restype = ctypes.c_int
+    lib.vsa_cache_accept.argtypes = [ctypes.POINTER(VsaCache), _p, _p, _p, _i32, _p, _p]
+    lib.vsa_cache_weigh.restype = ctypes.c_int
+    lib.vsa_cache_weigh.argtypes = [ctypes.POINTER(VsaCache), _p, _p, _i32, _i32, _p, _i32, ctypes.c_float, _p, _p, _p]
+    lib.vsa_cache_evict.restype = ctypes.c_int
+    lib.vsa_cache_evict.argtypes = [ctypes.POINTER(VsaCache), _p, _i32, _i32, _i32, _p, _i32, _p, _p, _p, _p]
     lib.vsa_kernel_launches.restype = ctypes.c_uint64
     lib.vsa_kernel_launches.argtypes = []
     return lib
@@ -674,7 +686,9 @@ def _front():
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_front", loader))
             loader.exec_module(m)
             m.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
-                lib.vsa_cache_append, lib.vsa_cache_read, lib.vsa_cache_attn, lib.vsa_cache_attn_workspace_bytes)))
+                lib.vsa_cache_append, lib.vsa_cache_read, lib.vsa_cache_attn, lib.vsa_cache_attn_workspace_bytes,
+                lib.vsa_cache_attn_tree, lib.vsa_cache_tree, lib.vsa_cache_accept, lib.vsa_cache_weigh,
+                lib.vsa_cache_evict)))
             _front_module = m
         else:
             _front_module = False
@@ -778,19 +792,23 @@ def cache_attn_workspace_bytes(kv_heads: int, D: int, Sq: int, heads: int) -> in
 
 
 def cache_attn(q, pool, table, kv_lens, q_lens=None, causal: bool = True, page_sel=None, kv_scale=None,
-               sm_scale: float = 0.0, workspace=None, out=None, lse=None, want_lse: bool = True, stream=None):
+               sm_scale: float = 0.0, workspace=None, out=None, lse=None, want_lse: bool = True, stream=None,
+               tree=None):
     """Attention of q (bf16 [B, Sq, heads, D], rotated as the keys were) over the 4-bit cache ->
     (out bf16 like q, lse fp32 [B, heads, Sq] or None) (vsa_cache_attn).
 
     q_lens (int32 [B]) are each sequence's query rows (None: Sq), its last tokens when causal;
     page_sel (int32 [B, kv_heads, n]) limits each kv head to n pages of its sequence (-1: none).
     Every place below kv_lens is a key: append raster tokens, or tiled ones of a grid whose sides are
-    multiples of 4 (other grids' tiled rows hold padding slots, which would be attended)."""
+    multiples of 4 (other grids' tiled rows hold padding slots, which would be attended).
+    With tree (int64 [B, Sq, ceil(Sq / 64)], bit j of row i: query i sees the step's token j; see
+    cache_tree) the step's tokens are those of a drafted tree and causal is not looked at
+    (vsa_cache_attn_tree)."""
     if stream is None and (_front_module or _front()):
         got = _front_module.attn(q, pool, table, kv_lens, q_lens, causal, page_sel, kv_scale, sm_scale, workspace, out,
-                                 lse, want_lse)
+                                 lse, want_lse, tree)
         if got.__class__ is int:
-            raise VsaError(got, "vsa_cache_attn")
+            raise VsaError(got, "vsa_cache_attn" if tree is None else "vsa_cache_attn_tree")
         if got is not False:
             return got
     torch = _torch()
@@ -814,6 +832,10 @@ def cache_attn(q, pool, table, kv_lens, q_lens=None, causal: bool = True, page_s
         if page_sel.dim() != 3 or page_sel.shape[:2] != (B, kv) or not page_sel.shape[2]:
             raise ValueError("page_sel must be [B, kv_heads, n] with n > 0")
         nsel = page_sel.shape[2]
+    if tree is not None:
+        tree_ptr = _on(tree, torch.int64, "tree", dev)
+        if tree.shape != (B, Sq, (Sq + 63) // 64):
+            raise ValueError("tree must be [B, Sq, ceil(Sq / 64)]")
     nbytes = lib.vsa_cache_attn_workspace_bytes(kv, D, Sq, heads)
     if workspace is None:
         workspace = _make(stream, torch.empty, (max(nbytes, 16),), dtype=torch.uint8, device=q.device)
@@ -831,9 +853,175 @@ def cache_attn(q, pool, table, kv_lens, q_lens=None, causal: bool = True, page_s
         lse_ptr = _on(lse, torch.float32, "lse", dev)
         if lse.shape != (B, heads, Sq):
             raise ValueError("lse must be [B, heads, Sq]")
-    _cache_call(lib.vsa_cache_attn, dev, stream, c, q_ptr, Sq, heads, lens_ptr, 1 if causal else 0, sel_ptr, nsel,
-                sm_scale, work_ptr, out_ptr, lse_ptr)
+    if tree is not None:
+        _cache_call(lib.vsa_cache_attn_tree, dev, stream, c, q_ptr, Sq, heads, lens_ptr, tree_ptr, sel_ptr, nsel,
+                    sm_scale, work_ptr, out_ptr, lse_ptr)
+    else:
+        _cache_call(lib.vsa_cache_attn, dev, stream, c, q_ptr, Sq, heads, lens_ptr, 1 if causal else 0, sel_ptr, nsel,
+                    sm_scale, work_ptr, out_ptr, lse_ptr)
     return out, lse
+
+
+def _vector(t, name, B, device):
+    """Pointer of an int32 [B], or None."""
+    if t is None:
+        return None
+    ptr = _on(t, _torch().int32, name, device)
+    if t.shape != (B,):
+        raise ValueError(f"{name} must be [B]")
+    return ptr
+
+
+def cache_tree(parents, kv_lens=None, new_lens=None, starts=None, mask=None, positions=None, stream=None):
+    """A step's drafted trees (parents int32 [B, S]: a node before, or -1 after the cached tokens) ->
+    (mask int64 [B, S, ceil(S / 64)] for cache_attn's tree, positions int32 [B, S] for cache_append)
+    (vsa_cache_tree).
+
+    new_lens says how many nodes each sequence has (None: S); kv_lens counts them already.  Positions
+    start at starts (int32 [B]), else at kv_lens - new_lens, else at 0."""
+    if stream is None and (_front_module or _front()):
+        got = _front_module.tree(parents, kv_lens, new_lens, starts, mask, positions)
+        if got.__class__ is int:
+            raise VsaError(got, "vsa_cache_tree")
+        if got is not False:
+            return got
+    torch = _torch()
+    _need(parents, torch.int32, "parents")
+    dev = parents.get_device()
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, S]")
+    B, S = parents.shape
+    ptrs = [_vector(t, name, B, dev) for t, name in ((kv_lens, "kv_lens"), (new_lens, "new_lens"), (starts, "starts"))]
+    shape = (B, S, (S + 63) // 64)
+    if mask is None:
+        mask = _make(stream, torch.empty, shape, dtype=torch.int64, device=parents.device)
+    if positions is None:
+        positions = _make(stream, torch.empty, (B, S), dtype=torch.int32, device=parents.device)
+    mask_ptr, pos_ptr = _on(mask, torch.int64, "mask", dev), _on(positions, torch.int32, "positions", dev)
+    if mask.shape != shape or positions.shape != parents.shape:
+        raise ValueError("mask must be [B, S, ceil(S / 64)] and positions [B, S]")
+    _cache_call(library().vsa_cache_tree, dev, stream, parents.data_ptr(), B, S, *ptrs, mask_ptr, pos_ptr)
+    return mask, positions
+
+
+def cache_accept(pool, table, kv_lens, new_lens, path, path_lens, lens=None, stream=None):
+    """Of a step's drafted nodes (the last new_lens tokens of each sequence) keeps those of the accepted
+    path (int32 [B, n], ascending; path_lens int32 [B] of them): their keys and values move to the first
+    places of the step -> the new lengths, int32 [B] (vsa_cache_accept)."""
+    if stream is None and (_front_module or _front()):
+        got = _front_module.accept(pool, table, kv_lens, new_lens, path, path_lens, lens)
+        if got.__class__ is int:
+            raise VsaError(got, "vsa_cache_accept")
+        if got is not False:
+            return got
+    torch = _torch()
+    c, dev, B, _, _ = _cache(pool, table, kv_lens, None)
+    if new_lens is None or path_lens is None:
+        raise ValueError("new_lens and path_lens are needed")
+    new_ptr, len_ptr = _vector(new_lens, "new_lens", B, dev), _vector(path_lens, "path_lens", B, dev)
+    path_ptr = _on(path, torch.int32, "path", dev)
+    if path.dim() != 2 or path.shape[0] != B:
+        raise ValueError("path must be [B, n]")
+    if lens is None:
+        lens = _make(stream, torch.empty_like, kv_lens)
+    out_ptr = _vector(lens, "lens", B, dev)
+    _cache_call(library().vsa_cache_accept, dev, stream, c, new_ptr, path_ptr, len_ptr, path.shape[1], out_ptr)
+    return lens
+
+
+def cache_weigh(q, lse, pool, table, kv_lens, q_lens=None, causal: bool = True, weights=None, out=None, kv_scale=None,
+                sm_scale: float = 0.0, stream=None):
+    """Attention weight that each cached key gets from q (bf16 [B, Sq, heads, D]), summed over its rows and
+    the heads of a kv head, with cache_attn's lse (fp32 [B, heads, Sq]) -> fp32 [B, kv_heads, 64 * width]
+    (vsa_cache_weigh).
+
+    Added to weights (likewise shaped; None: zeros) in place, or to out where that is given; a new tensor
+    with neither.  Rows whose lse is not finite add nothing."""
+    if out is None:
+        out = weights
+    if stream is None and (_front_module or _front()):
+        got = _front_module.weigh(q, lse, pool, table, kv_lens, q_lens, causal, weights, out, kv_scale, sm_scale)
+        if got.__class__ is int:
+            raise VsaError(got, "vsa_cache_weigh")
+        if got is not False:
+            return got
+    torch = _torch()
+    c, dev, B, kv, D = _cache(pool, table, kv_lens, kv_scale)
+    q_ptr, lse_ptr = _on(q, torch.bfloat16, "q", dev), _on(lse, torch.float32, "lse", dev)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != D:
+        raise ValueError("q must be [B, Sq, heads, D]")
+    Sq, heads = shape[1], shape[2]
+    if heads == 0 or heads % kv:
+        raise ValueError("heads must be a multiple of kv_heads")
+    if lse.shape != (B, heads, Sq):
+        raise ValueError("lse must be [B, heads, Sq]")
+    lens_ptr = _vector(q_lens, "q_lens", B, dev)
+    places = (B, kv, 64 * table.shape[1])
+    before_ptr = None
+    if weights is not None:
+        before_ptr = _on(weights, torch.float32, "weights", dev)
+        if weights.shape != places:
+            raise ValueError("weights must be [B, kv_heads, 64 * width]")
+    if out is None:
+        out = _make(stream, torch.empty, places, dtype=torch.float32, device=q.device)
+    out_ptr = _on(out, torch.float32, "out", dev)
+    if out.shape != places:
+        raise ValueError("out must be [B, kv_heads, 64 * width]")
+    _cache_call(library().vsa_cache_weigh, dev, stream, c, q_ptr, lse_ptr, Sq, heads, lens_ptr, 1 if causal else 0,
+                sm_scale, before_ptr, out_ptr)
+    return out
+
+
+def cache_evict(pool, table, kv_lens, weights, budget: int, first: int = 0, recent: int = 0, to_table=None, kept=None,
+                lens=None, moved=None, stream=None):
+    """Cuts every sequence to at most `budget` tokens: for each kv head the first `first`, the last `recent`
+    and of the others those with the largest weights (fp32 [B, kv_heads, 64 * width], as cache_weigh sums
+    them) -> (lens int32 [B], kept int32 [B, kv_heads, budget]: their old places, then -1, and the weights
+    of the places they have now) (vsa_cache_evict).
+
+    The kept tokens move together within the sequence's pages, and weights with them in place; with to_table
+    (int32 [B, to_width]) they are copied to its pages instead, their weights to `moved` (fp32 [B, kv_heads,
+    64 * to_width]).  Later tokens are appended with positions of their own: places are no positions now."""
+    if stream is None and (_front_module or _front()):
+        got = _front_module.evict(pool, table, kv_lens, weights, budget, first, recent, to_table, kept, lens, moved)
+        if got.__class__ is int:
+            raise VsaError(got, "vsa_cache_evict")
+        if got is not False:
+            return got
+    torch = _torch()
+    c, dev, B, kv, _ = _cache(pool, table, kv_lens, None)
+    budget, first, recent = int(budget), int(first), int(recent)
+    if not 0 < budget < 2 ** 31 or first < 0 or recent < 0 or first + recent > budget:
+        raise ValueError("budget must be positive and hold first + recent")
+    w_ptr = _on(weights, torch.float32, "weights", dev)
+    if weights.shape != (B, kv, 64 * table.shape[1]):
+        raise ValueError("weights must be [B, kv_heads, 64 * width]")
+    to_ptr = moved_ptr = None
+    width = 0
+    if to_table is not None:
+        to_ptr = _on(to_table, torch.int32, "to_table", dev)
+        if to_table.dim() != 2 or to_table.shape[0] != B or not to_table.shape[1]:
+            raise ValueError("to_table must be [B, to_width]")
+        width = to_table.shape[1]
+        if moved is None:
+            moved = _make(stream, torch.empty, (B, kv, 64 * width), dtype=torch.float32, device=pool.device)
+        moved_ptr = _on(moved, torch.float32, "moved", dev)
+        if moved.shape != (B, kv, 64 * width):
+            raise ValueError("moved must be [B, kv_heads, 64 * to_width]")
+    elif moved is not None:
+        raise ValueError("moved goes with to_table")
+    if kept is None:
+        kept = _make(stream, torch.empty, (B, kv, budget), dtype=torch.int32, device=pool.device)
+    kept_ptr = _on(kept, torch.int32, "kept", dev)
+    if kept.shape != (B, kv, budget):
+        raise ValueError("kept must be [B, kv_heads, budget]")
+    if lens is None:
+        lens = _make(stream, torch.empty_like, kv_lens)
+    lens_ptr = _vector(lens, "lens", B, dev)
+    _cache_call(library().vsa_cache_evict, dev, stream, c, w_ptr, budget, first, recent, to_ptr, width, kept_ptr,
+                lens_ptr, moved_ptr)
+    return lens, kept, weights if to_table is None else moved
 
 
 def kernel_launches() -> int:

@@ -1,12 +1,14 @@
 // C ABI of the VSA library: argument validation on the host, then dispatch
 // to the kernels of tile.cu, coarse.cu, pair.cu, fine.cu, coarse_attn.cu,
-// block_select.cu, cache_store.cu and cache_attn.cu (which passes on to cache_chunk.cu)
+// block_select.cu, cache_store.cu, cache_attn.cu (which passes on to cache_chunk.cu),
+// tree.cu, weigh.cu (which passes on to weigh_chunk.cu) and evict.cu
 // (coarse_noalloc.cu holds the allocation-free coarse entry point).  See
 // include/vsa.h for the contract of each entry point.
 #include <float.h>
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -401,9 +403,14 @@ size_t vsa_cache_attn_workspace_bytes(int32_t kv_heads, int32_t D, int32_t Sq, i
     return cache_attn_workspace_bytes(D, Sq, heads / kv_heads);
 }
 
-vsa_status vsa_cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t heads, const int32_t* q_lens,
-                          int32_t causal, const int32_t* page_sel, int32_t nsel, float sm_scale, void* workspace,
-                          void* out, float* lse, vsa_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// vsa_cache_attn, and with a tree vsa_cache_attn_tree.
+vsa_status cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t heads, const int32_t* q_lens,
+                      int32_t causal, const uint64_t* tree, const int32_t* page_sel, int32_t nsel, float sm_scale,
+                      void* workspace, void* out, float* lse, vsa_stream_t stream) {
     CacheView cv;
     DevCtx ctx;
     vsa_status st = cache_args(c, Sq);
@@ -417,8 +424,100 @@ vsa_status vsa_cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t
     st = cache_view(c, &cv, &ctx);
     if (st != VSA_OK) return st;
     if (sm_scale <= 0.f) sm_scale = 1.0f / sqrtf((float)c->D);
-    return from_cuda(launch_cache_attn(cv, c->D, q, Sq, heads, q_lens, causal, page_sel, nsel, sm_scale, workspace,
-                                       out, lse, ctx.num_sms, static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_cache_attn(cv, c->D, q, Sq, heads, q_lens, causal, tree, page_sel, nsel, sm_scale,
+                                       workspace, out, lse, ctx.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+vsa_status vsa_cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t heads, const int32_t* q_lens,
+                          int32_t causal, const int32_t* page_sel, int32_t nsel, float sm_scale, void* workspace,
+                          void* out, float* lse, vsa_stream_t stream) {
+    return cache_attn(c, q, Sq, heads, q_lens, causal, nullptr, page_sel, nsel, sm_scale, workspace, out, lse, stream);
+}
+
+vsa_status vsa_cache_attn_tree(const vsa_cache* c, const void* q, int32_t Sq, int32_t heads, const int32_t* q_lens,
+                               const uint64_t* tree, const int32_t* page_sel, int32_t nsel, float sm_scale,
+                               void* workspace, void* out, float* lse, vsa_stream_t stream) {
+    const vsa_status st = cache_args(c, Sq);
+    if (st != VSA_OK) return st;
+    if (!tree) return VSA_ERR_INVALID_ARG;
+    if (Sq > tree_max_nodes()) return VSA_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(tree) & 7u) return VSA_ERR_ALIGNMENT;
+    return cache_attn(c, q, Sq, heads, q_lens, 0, tree, page_sel, nsel, sm_scale, workspace, out, lse, stream);
+}
+
+vsa_status vsa_cache_tree(const int32_t* parents, int32_t B, int32_t S, const int32_t* kv_lens,
+                          const int32_t* new_lens, const int32_t* starts, uint64_t* mask, int32_t* positions,
+                          vsa_stream_t stream) {
+    if (!parents || !mask || B <= 0 || S <= 0) return VSA_ERR_INVALID_ARG;
+    if (B > 65535 || S > tree_max_nodes()) return VSA_ERR_UNSUPPORTED;
+    if (!aligned4(parents) || !aligned4(kv_lens) || !aligned4(new_lens) || !aligned4(starts) || !aligned4(positions) ||
+        (reinterpret_cast<uintptr_t>(mask) & 7u))
+        return VSA_ERR_ALIGNMENT;
+    DevCtx ctx;
+    if (get_dev_ctx(&ctx) != cudaSuccess) return VSA_ERR_CUDA;
+    return from_cuda(launch_cache_tree(parents, B, S, kv_lens, new_lens, starts, mask, positions, ctx.err,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+vsa_status vsa_cache_accept(const vsa_cache* c, const int32_t* new_lens, const int32_t* path, const int32_t* path_lens,
+                            int32_t n, int32_t* lens, vsa_stream_t stream) {
+    CacheView cv;
+    DevCtx ctx;
+    vsa_status st = cache_args(c, n);
+    if (st != VSA_OK) return st;
+    if (!new_lens || !path || !path_lens || !lens || lens == c->kv_lens || lens == new_lens || lens == path_lens)
+        return VSA_ERR_INVALID_ARG;
+    if (n > tree_max_nodes()) return VSA_ERR_UNSUPPORTED;
+    if (!aligned4(new_lens) || !aligned4(path) || !aligned4(path_lens) || !aligned4(lens)) return VSA_ERR_ALIGNMENT;
+    st = cache_view(c, &cv, &ctx);
+    if (st != VSA_OK) return st;
+    return from_cuda(launch_cache_accept(cv, c->D, new_lens, path, path_lens, n, lens,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+vsa_status vsa_cache_weigh(const vsa_cache* c, const void* q, const float* lse, int32_t Sq, int32_t heads,
+                           const int32_t* q_lens, int32_t causal, float sm_scale, const float* weights, float* out,
+                           vsa_stream_t stream) {
+    CacheView cv;
+    DevCtx ctx;
+    vsa_status st = cache_args(c, Sq);
+    if (st != VSA_OK) return st;
+    if (!q || !lse || !out || heads <= 0 || heads % c->kv_heads || !(fabsf(sm_scale) <= FLT_MAX))
+        return VSA_ERR_INVALID_ARG;
+    if (heads > 65535 || (int64_t)Sq * (heads / c->kv_heads) >= (1 << 24)) return VSA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(weights) || !aligned16(out) || !aligned4(lse) || !aligned4(q_lens))
+        return VSA_ERR_ALIGNMENT;
+    st = cache_view(c, &cv, &ctx);
+    if (st != VSA_OK) return st;
+    if (sm_scale <= 0.f) sm_scale = 1.0f / sqrtf((float)c->D);
+    return from_cuda(launch_cache_weigh(cv, c->D, q, lse, Sq, heads, q_lens, causal, sm_scale, weights, out,
+                                        ctx.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+vsa_status vsa_cache_evict(const vsa_cache* c, float* weights, int32_t budget, int32_t first, int32_t recent,
+                           const int32_t* to_table, int32_t to_width, int32_t* kept, int32_t* lens, float* moved,
+                           vsa_stream_t stream) {
+    CacheView cv;
+    DevCtx ctx;
+    vsa_status st = cache_args(c, 1);
+    if (st != VSA_OK) return st;
+    if (!weights || !kept || !lens || lens == c->kv_lens) return VSA_ERR_INVALID_ARG;
+    if (budget <= 0 || first < 0 || recent < 0 || (int64_t)first + recent > budget) return VSA_ERR_INVALID_ARG;
+    if (to_table ? to_width <= 0 || !moved || moved == weights : to_width != 0 || moved) return VSA_ERR_INVALID_ARG;
+    const int64_t most = std::min<int64_t>(budget, (int64_t)c->width * kPageTokens);
+    if (to_table && (int64_t)to_width * kPageTokens < most) return VSA_ERR_INVALID_ARG;
+    if ((int64_t)c->B * c->kv_heads >= (1 << 27) || (int64_t)to_width * kPageTokens >= ((int64_t)1 << 31))
+        return VSA_ERR_UNSUPPORTED;
+    if (!aligned4(weights) || !aligned4(moved) || !aligned4(kept) || !aligned4(lens) || !aligned4(to_table))
+        return VSA_ERR_ALIGNMENT;
+    st = cache_view(c, &cv, &ctx);
+    if (st != VSA_OK) return st;
+    return from_cuda(launch_cache_evict(cv, c->D, weights, budget, first, recent, to_table, to_width, kept, lens,
+                                        to_table ? moved : weights, static_cast<cudaStream_t>(stream)));
 }
 
 size_t vsa_pair_workspace_bytes(int32_t B, int32_t heads, int32_t ncubes, int32_t topk) {

@@ -219,6 +219,7 @@ struct AttnParams {
     CacheView c;
     const int32_t* q_lens;    // [B], or null: Sq
     const int32_t* page_sel;  // [B][kv_heads][nsel], or null
+    const uint64_t* tree;     // [B][Sq][tree_words]: the step's tokens that a query sees (kernels of trees only)
     const uint4* q;           // bf16 [B][Sq][heads][D]
     uint4* out;
     float* lse;               // [B][heads][Sq], or null
@@ -226,7 +227,7 @@ struct AttnParams {
     float2* part_ml;          // [2 * grid][tile]: reference (log2 units), sum
     void* scratch;            // token_kernel: [grid][warps][2] states
     int4* places;             // [grid]: where each CTA's part begins (b, h, t, page); b = -1: between units
-    int Sq, heads, group, nsel, causal;
+    int Sq, heads, group, nsel, causal, tree_words;
     int tile, tiles;          // rows of a unit; units of a (b, kv head)
     int grid;                 // CTAs of the attention kernel
     int unit_cost, idle_cost;  // of a unit beside its pages, of one without pages
@@ -525,6 +526,19 @@ struct Walk {
         return true;
     }
 };
+
+// Bits j0 .. j0 + 63 of a query's row of the tree (bit i: key j0 + i from the step's
+// first token on): the keys before the step's tokens, which every query sees, are
+// ones, those past the row's words zeros.
+__device__ __forceinline__ uint64_t tree_window(const uint64_t* row, int words, int j0) {
+    if (j0 <= -64) return ~0ull;
+    if (j0 < 0) return (row[0] << -j0) | ((1ull << -j0) - 1);
+    const int w = j0 >> 6, s = j0 & 63;
+    if (w >= words) return 0;
+    uint64_t x = row[w] >> s;
+    if (s && w + 1 < words) x |= row[w + 1] << (64 - s);
+    return x;
+}
 
 // Looks up page `i` of a segment's walk: its page number within the sequence,
 // and its place in the pool (-1: passed over).

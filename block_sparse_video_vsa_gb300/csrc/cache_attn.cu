@@ -127,7 +127,9 @@ struct TokenSmem {
     static_assert(sizeof(TokenState<kD, kNT>) <= kOwn * PageLayout<kD>::kBytes, "a state fits a warp's slots");
 };
 
-template <int kD, int kNT, int kWarps, int kOwn>
+// kTree: which of the step's tokens a query sees is in p.tree, a bit for each (the
+// keys before them it sees all); else a range, up to its own place when causal.
+template <int kD, int kNT, int kWarps, int kOwn, bool kTree>
 __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
     using L = PageLayout<kD>;
     using Smem = TokenSmem<kD, kNT, kWarps, kOwn>;
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
                 int lim = at.len.kv;
                 if (p.causal && r < live_rows) lim = min(lim, at.len.kv - at.len.q + r / p.group + 1);
                 rs_lim[nt][c] = lim;
-                min_lim = min(min_lim, lim);
+                min_lim = min(min_lim, kTree ? at.len.kv - at.len.q : lim);
             }
         }
         min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 1));
@@ -373,7 +375,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
                 }
             // Keys past a row's limit (and scores of what lies there) do not count.
             const bool masked = key0 + kPieceTokens > min_lim;
-            if (masked) {
+            if (masked && kTree) {
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int r = row0 + nt * 8 + 2 * t + c;
+                        uint32_t seen = 0u;  // of the piece's 32 keys
+                        if (r < live_rows)
+                            seen = (uint32_t)tree_window(
+                                p.tree + ((size_t)at.b * p.Sq + r / p.group) * p.tree_words, p.tree_words,
+                                key0 - (at.len.kv - at.len.q));
+#pragma unroll
+                        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int i = 16 * m + 8 * half + k_row;
+                                if (key0 + i >= at.len.kv || !((seen >> i) & 1u)) s[m][nt][2 * half + c] = -INFINITY;
+                            }
+                    }
+            } else if (masked) {
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m)
 #pragma unroll
@@ -736,17 +757,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) 
 
 constexpr int kTokenWarps = 12;  // at most: states in the workspace
 
-template <int kD, int kNT, int kWarps, int kOwn>
-cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
+template <int kD, int kNT, int kWarps, int kOwn, bool kTree>
+cudaError_t launch_token_as(const AttnParams& p, cudaStream_t stream) {
     constexpr int smem = (int)sizeof(TokenSmem<kD, kNT, kWarps, kOwn>);
     static_assert(smem <= 232448, "shared memory of the token kernel");
     static_assert(kOwn >= 2 && kOwn <= 32, "a piece to come beside the present one");
-    auto kernel = token_kernel<kD, kNT, kWarps, kOwn>;
+    auto kernel = token_kernel<kD, kNT, kWarps, kOwn, kTree>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(kernel, smem, done);
     if (e != cudaSuccess) return e;
     static_assert(kWarps <= kTokenWarps && kWarps <= 16, "states in the workspace");
     return launch_early(kernel, dim3((unsigned)p.grid), kWarps * 32, smem, stream, p);
+}
+template <int kD, int kNT, int kWarps, int kOwn>
+cudaError_t launch_token(const AttnParams& p, cudaStream_t stream) {
+    return p.tree ? launch_token_as<kD, kNT, kWarps, kOwn, true>(p, stream)
+                  : launch_token_as<kD, kNT, kWarps, kOwn, false>(p, stream);
 }
 
 // How the line is cut, in pages, with what was measured:
@@ -794,12 +820,14 @@ size_t cache_attn_workspace_bytes(int D, int Sq, int group) {
 }
 
 cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, int heads, const int32_t* q_lens,
-                              int causal, const int32_t* page_sel, int nsel, float sm_scale, void* workspace,
-                              void* out, float* lse, int num_sms, cudaStream_t stream) {
+                              int causal, const uint64_t* tree, const int32_t* page_sel, int nsel, float sm_scale,
+                              void* workspace, void* out, float* lse, int num_sms, cudaStream_t stream) {
     AttnParams p;
     p.c = c;
     p.q_lens = q_lens;
     p.page_sel = page_sel;
+    p.tree = tree;
+    p.tree_words = (Sq + 63) / 64;
     p.q = static_cast<const uint4*>(q);
     p.out = static_cast<uint4*>(out);
     p.lse = lse;
@@ -807,7 +835,7 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     p.heads = heads;
     p.group = heads / c.kv_heads;
     p.nsel = nsel;
-    p.causal = causal;
+    p.causal = causal && !tree;
     const int rows = Sq * p.group;
     p.tile = tile_rows(rows);
     p.tiles = (rows + p.tile - 1) / p.tile;

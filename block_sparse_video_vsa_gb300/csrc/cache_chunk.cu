@@ -285,7 +285,7 @@ struct Ring {
     __device__ __forceinline__ uint32_t empty() const { return (turn + 1) & 1; }  // and of its last emptying (turn > 0)
 };
 
-template <int kD>
+template <int kD, bool kTree>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
     using L = PageLayout<kD>;
     using Sm = ChunkSmem<kD>;
@@ -609,7 +609,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms.s_free));
-                if (__any_sync(0xffffffffu, va < kPageTokens || vb < kPageTokens)) {
+                if (kTree) {
+                    // Pages with the step's tokens, or with keys past the last: which of
+                    // them the row sees, a bit for each.
+                    const int context = max(sg.len.kv - sg.len.q, 0);
+                    if (context - k0.x < kPageTokens || context - k0.y < kPageTokens) {
+                        const int row = sg.t * 128 + r;
+                        const uint64_t* bits =
+                            p.tree + ((size_t)sg.b * p.Sq + (row < sg.len.q * p.group ? row / p.group : 0)) * p.tree_words;
+                        uint64_t seen[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int first = i ? k0.y : k0.x, held = i ? vb : va;  // keys of the page
+                            seen[i] = held <= 0 ? 0ull : tree_window(bits, p.tree_words, first - (sg.len.kv - sg.len.q));
+                            if (held > 0 && held < kPageTokens) seen[i] &= (1ull << held) - 1;
+                        }
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) {
+                            x[c] = (seen[0] >> c) & 1 ? x[c] : ninf;
+                            x[64 + c] = (seen[1] >> c) & 1 ? x[64 + c] : ninf;
+                        }
+                    }
+                } else if (__any_sync(0xffffffffu, va < kPageTokens || vb < kPageTokens)) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) {
                         x[c] = c < va ? x[c] : ninf;
@@ -764,27 +785,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnParams p) {
 
 }  // namespace
 
-template <int kD>
-static cudaError_t launch_chunk_d(const AttnParams& p, cudaStream_t stream) {
+template <int kD, bool kTree>
+static cudaError_t launch_chunk_as(const AttnParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> known{0};
     // The register split draws on the launch's registers; with fewer, setmaxnreg
     // would wait forever, so such a build is refused.
     int regs = 0;
-    cudaError_t e = launch_registers(chunk_kernel<kD>, known, &regs);
+    cudaError_t e = launch_registers(chunk_kernel<kD, kTree>, known, &regs);
     if (e != cudaSuccess) return e;
     if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-    e = allow_smem(chunk_kernel<kD>, chunk_smem<kD>(), done);
+    e = allow_smem(chunk_kernel<kD, kTree>, chunk_smem<kD>(), done);
     if (e != cudaSuccess) return e;
     // Not launched early itself: over 32760 keys, 64 rows of 40 heads take 95.4 us
     // so and 102.2 launched early (a ragged batch of prompts 289.6 and 281.1).
-    chunk_kernel<kD><<<p.grid, kChunkThreads, chunk_smem<kD>(), stream>>>(p);
+    chunk_kernel<kD, kTree><<<p.grid, kChunkThreads, chunk_smem<kD>(), stream>>>(p);
     note_launches(1);
     return cudaGetLastError();
 }
 
 cudaError_t launch_chunk(const AttnParams& p, int D, cudaStream_t stream) {
-    return D == 64 ? launch_chunk_d<64>(p, stream) : launch_chunk_d<128>(p, stream);
+    if (p.tree) return D == 64 ? launch_chunk_as<64, true>(p, stream) : launch_chunk_as<128, true>(p, stream);
+    return D == 64 ? launch_chunk_as<64, false>(p, stream) : launch_chunk_as<128, false>(p, stream);
 }
 
 }  // namespace vsa

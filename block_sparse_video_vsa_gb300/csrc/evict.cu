@@ -1,0 +1,331 @@
+// Eviction from the 4-bit paged cache: of a sequence's n tokens each kv head keeps
+// the first few, the most recent, and of those between the ones with the largest
+// weights (those that cache_weigh sums, or any others).
+//
+// choose_kernel writes the places kept, ascending: the k-th largest weight T of
+// the middle is found digit by digit from the top (11, 11 and 10 bits of the
+// weights' bit patterns, put in their order), every place above T is kept and
+// of those at T the lowest.  A cluster of up to 8 blocks takes a (sequence, kv
+// head), each a stretch of its places: keys go to shared memory once,
+// histograms are summed over the cluster by distributed shared memory (all
+// blocks form the same sums, one barrier a digit).  Counting is in integers:
+// the same places in every run.
+//
+// move_kernel and move_within_kernel bring the kept tokens' codes, scales and
+// weights to the places 0, 1, ...: 9/8 D + 4 bytes a token and head each way,
+// HBM bound.  To other pages a block takes a page of 64 places.  Within the
+// sequence's own pages a cluster takes a (sequence, kv head) and goes along the
+// places in order: kept[j] >= j and ascends, so once all its blocks have read the
+// places of a turn, no place that the turn writes is read again.
+#include <algorithm>
+
+#include "move.cuh"
+
+namespace vsa {
+
+namespace {
+
+constexpr int kChooseThreads = 512, kMaxCluster = 8;
+constexpr int kDigits = 3;
+constexpr int kBins = 2048;
+constexpr int kHeldKeys = 40 * 1024;  // keys of a block's stretch that go to shared memory
+
+struct EvictParams {
+    CacheView c;
+    const int32_t* to_table;  // [B][to_width], or null: the tokens stay in their pages
+    const float* weights;     // [B][kv_heads][64 * width]
+    float* moved;             // [B][kv_heads][64 * to_width] (in place: weights)
+    int32_t* kept;            // [B][kv_heads][budget]
+    int32_t* lens;            // [B]
+    int budget, first, recent, to_width;
+    int keys;                 // of shared memory, a block
+};
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// The word at `p`, a shared address of this block, in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t load_from_rank(const void* p, uint32_t rank) {
+    uint32_t at, x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+
+// Bit patterns in the order of the numbers: NaN below all, -0 with 0.
+__device__ __forceinline__ uint32_t order_key(float w) {
+    if (w != w) return 0u;
+    const uint32_t u = __float_as_uint(w + 0.f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+struct ChooseSmem {
+    unsigned int hist[kDigits][kBins];
+    unsigned int warp_sum[kChooseThreads / 32];
+    unsigned int counts[2][kChooseThreads / 32];  // above T, at T: of a warp's stretch
+    unsigned int totals[2];                       // of the block
+    unsigned int found, before;
+};
+
+__global__ void __launch_bounds__(kChooseThreads) choose_kernel(EvictParams p) {
+    __shared__ ChooseSmem sm;
+    extern __shared__ uint32_t keys[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kDigits * kBins; i += kChooseThreads) (&sm.hist[0][0])[i] = 0u;
+    early();
+    begin_work();
+    const int blocks = (int)cluster_size(), rank = (int)cluster_rank();
+    const int row = blockIdx.x / blocks;  // of B * kv_heads
+    const int b = row / p.c.kv_heads, h = row - b * p.c.kv_heads;
+    const int n = cache_len(p.c, b, h == 0 && rank == 0 && threadIdx.x == 0);
+    int32_t* kept = p.kept + (size_t)row * p.budget;
+    const int me = rank * kChooseThreads + threadIdx.x, all = blocks * kChooseThreads;
+    if (h == 0 && me == 0) p.lens[b] = min(n, p.budget);
+    if (n <= p.budget) {  // nothing to choose
+        for (int j = me; j < p.budget; j += all) kept[j] = j < n ? j : -1;
+        return;
+    }
+    for (int j = me; j < p.first; j += all) kept[j] = j;
+    for (int j = me; j < p.recent; j += all) kept[p.budget - p.recent + j] = n - p.recent + j;
+    const int want = p.budget - p.first - p.recent;
+    if (want == 0) return;
+    // This block's stretch of the middle, in whole warps' worth.
+    const int middle = n - p.recent - p.first;
+    const long long per = (long long)((middle - 1) / blocks / 32 + 1) * 32;
+    const int begin = (int)min((long long)middle, rank * per), size = (int)min((long long)middle, begin + per) - begin;
+    const float* w = p.weights + (size_t)row * p.c.width * kPageTokens + p.first + begin;
+    const bool held = size <= p.keys;
+    auto key = [&](int i) { return held ? keys[i] : order_key(w[i]); };
+    if (held)
+        for (int i = threadIdx.x; i < size; i += kChooseThreads) keys[i] = order_key(w[i]);
+    __syncthreads();
+    // The digits of T; `left` of the places with T's digits so far are still to be found.
+    uint32_t top = 0u, mask = 0u;
+    unsigned left = (unsigned)want;
+#pragma unroll 1
+    for (int d = 0; d < kDigits; ++d) {
+        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? 1024 : 2048;
+        for (int i = threadIdx.x; i < size; i += kChooseThreads) {
+            const uint32_t k = key(i);
+            if ((k & mask) == top) atomicAdd(&sm.hist[d][(k >> shift) & (bins - 1)], 1u);
+        }
+        cluster_arrive();
+        cluster_wait();
+        // Thread t: bins 4 t .. 4 t + 3 from the top down, summed over the cluster.
+        unsigned bin[kBins / kChooseThreads], sum = 0u;
+#pragma unroll
+        for (int j = 0; j < kBins / kChooseThreads; ++j) {
+            const int x = bins - 1 - (threadIdx.x * (kBins / kChooseThreads) + j);
+            bin[j] = 0u;
+            if (x >= 0)
+                for (int r = 0; r < blocks; ++r) bin[j] += load_from_rank(&sm.hist[d][x], (uint32_t)r);
+            sum += bin[j];
+        }
+        unsigned incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sm.warp_sum[warp] = incl;
+        __syncthreads();
+        unsigned base = 0u;
+        for (int i = 0; i < warp; ++i) base += sm.warp_sum[i];
+        unsigned before = base + incl - sum;
+        if (before < left && before + sum >= left) {
+#pragma unroll
+            for (int j = 0; j < kBins / kChooseThreads; ++j) {
+                if (before < left && before + bin[j] >= left) {
+                    sm.found = (unsigned)(bins - 1 - (threadIdx.x * (kBins / kChooseThreads) + j));
+                    sm.before = before;
+                }
+                before += bin[j];
+            }
+        }
+        __syncthreads();
+        top |= sm.found << shift;
+        mask |= (unsigned)(bins - 1) << shift;
+        left -= sm.before;
+        __syncthreads();
+    }
+    // `left` of the places at T are kept, the lowest.  Where each warp's kept places go:
+    const int part = ((size - 1) / (kChooseThreads / 32) / 32 + 1) * 32;  // of a warp (size > 0 or nothing to do)
+    const int from = min(size, warp * part), to = min(size, from + part);
+    unsigned above = 0u, same = 0u;
+    for (int i = from + lane; i < to; i += 32) {
+        const uint32_t k = key(i);
+        above += k > top;
+        same += k == top;
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    same = __reduce_add_sync(0xffffffffu, same);
+    if (lane == 0) {
+        sm.counts[0][warp] = above;
+        sm.counts[1][warp] = same;
+    }
+    __syncthreads();
+    unsigned above_before = 0u, same_before = 0u;
+    for (int i = 0; i < kChooseThreads / 32; ++i) {
+        if (i == warp) {
+            above = above_before;
+            same = same_before;
+        }
+        above_before += sm.counts[0][i];
+        same_before += sm.counts[1][i];
+    }
+    if (threadIdx.x == 0) {
+        sm.totals[0] = above_before;
+        sm.totals[1] = same_before;
+    }
+    cluster_arrive();
+    cluster_wait();
+    for (int r = 0; r < rank; ++r) {
+        above += load_from_rank(&sm.totals[0], (uint32_t)r);
+        same += load_from_rank(&sm.totals[1], (uint32_t)r);
+    }
+    cluster_arrive();  // no block leaves while another reads from it
+    const unsigned below_me = (1u << lane) - 1;
+    for (int i0 = from; i0 < to; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < to ? key(i) : 0u;
+        const unsigned is_above = __ballot_sync(0xffffffffu, i < to && k > top);
+        const unsigned is_same = __ballot_sync(0xffffffffu, i < to && k == top);
+        const unsigned same_here = same + __popc(is_same & below_me);
+        const bool keep = (is_above >> lane & 1u) || ((is_same >> lane & 1u) && same_here < left);
+        if (keep) {
+            const unsigned j = above + __popc(is_above & below_me) + min(same_here, left);
+            kept[p.first + j] = p.first + begin + i;
+        }
+        above += __popc(is_above);
+        same += __popc(is_same);
+    }
+    cluster_wait();
+}
+
+// To other pages: block (x, h, b) fills places 64 x .. 64 x + 63.
+template <int kD>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictParams p) {
+    __shared__ int source[kPageTokens];
+    early();
+    begin_work();
+    const int h = blockIdx.y, b = blockIdx.z, first = blockIdx.x * kPageTokens;
+    const size_t row = (size_t)b * p.c.kv_heads + h;
+    const int n = min(cache_len(p.c, b, false), p.budget), size = min(kPageTokens, n - first);
+    if (threadIdx.x < kPageTokens) {
+        const int t = threadIdx.x;
+        const int s = t < size ? p.kept[row * p.budget + first + t] : -1;
+        source[t] = s;
+        p.moved[row * p.to_width * kPageTokens + first + t] =
+            s >= 0 ? p.weights[row * p.c.width * kPageTokens + s] : 0.f;
+    }
+    if (size <= 0) return;
+    __syncthreads();
+    MovedToken<kD> x[MovedToken<kD>::kTurns];
+    take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source, size, x);
+    put_tokens<kD>(p.c, p.to_table, p.to_width, b, h, first, size, x);
+}
+
+// Within the sequence's pages: a cluster goes along the row, 64 places a block and turn.
+template <int kD>
+__global__ void __launch_bounds__(kMoveThreads) move_within_kernel(EvictParams p) {
+    __shared__ int source[2][kPageTokens];
+    early();
+    begin_work();
+    const int blocks = (int)cluster_size(), rank = (int)cluster_rank();
+    const size_t row = blockIdx.x / blocks;
+    const int b = (int)(row / p.c.kv_heads), h = (int)(row - (size_t)b * p.c.kv_heads);
+    const int n = cache_len(p.c, b, false);
+    if (n <= p.budget) return;  // (the whole cluster)
+    const int32_t* kept = p.kept + row * p.budget;
+    float* w = p.moved + row * p.c.width * kPageTokens;
+    MovedToken<kD> x[MovedToken<kD>::kTurns];
+    float weight = 0.f;
+    const int step = blocks * kPageTokens;
+    int turn = 0;
+    for (int first = rank * kPageTokens; first - rank * kPageTokens < p.budget; first += step, turn ^= 1) {
+        const int size = min(kPageTokens, p.budget - first);
+        if ((int)threadIdx.x < size) {
+            source[turn][threadIdx.x] = kept[first + threadIdx.x];
+            weight = w[source[turn][threadIdx.x]];
+        }
+        __syncthreads();
+        if (size > 0) take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source[turn], size, x);
+        cluster_arrive();
+        cluster_wait();
+        if (size > 0) put_tokens<kD>(p.c, p.c.table, p.c.width, b, h, first, size, x);
+        if ((int)threadIdx.x < size) w[first + threadIdx.x] = weight;
+    }
+    for (int i = p.budget + rank * kMoveThreads + threadIdx.x; i < n; i += blocks * kMoveThreads) w[i] = 0.f;
+}
+
+// As launch_early, in clusters of `cluster` blocks along x.
+template <class... P>
+cudaError_t launch_clusters(void (*kernel)(P...), dim3 grid, int cluster, int threads, int smem, cudaStream_t stream,
+                            P... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    note_launches(1);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, int budget, int first, int recent,
+                               const int32_t* to_table, int to_width, int32_t* kept, int32_t* lens, float* moved,
+                               cudaStream_t stream) {
+    EvictParams p;
+    p.c = c;
+    p.to_table = to_table;
+    p.weights = weights;
+    p.moved = moved;
+    p.kept = kept;
+    p.lens = lens;
+    p.budget = budget;
+    p.first = first;
+    p.recent = recent;
+    p.to_width = to_width;
+    // Blocks of a row: 2048 places each, up to 8.
+    const long long places = (long long)c.width * kPageTokens;
+    int cluster = 1;
+    while (cluster < kMaxCluster && places > 2048LL * cluster) cluster *= 2;
+    const long long stretch = (places + cluster - 1) / cluster + 32;
+    p.keys = (int)std::min<long long>(stretch, kHeldKeys);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(choose_kernel, kHeldKeys * 4, done);
+    if (e != cudaSuccess) return e;
+    const unsigned rows = (unsigned)c.B * (unsigned)c.kv_heads;
+    e = launch_clusters(choose_kernel, dim3(rows * cluster), cluster, kChooseThreads, p.keys * 4, stream, p);
+    if (e != cudaSuccess) return e;
+    if (to_table) {
+        const dim3 grid((unsigned)to_width, (unsigned)c.kv_heads, (unsigned)c.B);
+        return launch_early(D == 64 ? move_kernel<64> : move_kernel<128>, grid, kMoveThreads, 0, stream, p);
+    }
+    const int turns = (budget + kPageTokens - 1) / kPageTokens;
+    cluster = 1;
+    while (cluster < kMaxCluster && cluster < turns) cluster *= 2;
+    return launch_clusters(D == 64 ? move_within_kernel<64> : move_within_kernel<128>, dim3(rows * cluster), cluster,
+                           kMoveThreads, 0, stream, p);
+}
+
+}  // namespace vsa

@@ -29,6 +29,11 @@ decltype(&vsa_cache_append) append_fn;
 decltype(&vsa_cache_read) read_fn;
 decltype(&vsa_cache_attn) attn_fn;
 decltype(&vsa_cache_attn_workspace_bytes) workspace_fn;
+decltype(&vsa_cache_attn_tree) attn_tree_fn;
+decltype(&vsa_cache_tree) tree_fn;
+decltype(&vsa_cache_accept) accept_fn;
+decltype(&vsa_cache_weigh) weigh_fn;
+decltype(&vsa_cache_evict) evict_fn;
 
 // A contiguous tensor of `type` on CUDA device `dev`, or null.
 const at::Tensor* tensor(PyObject* o, at::ScalarType type, int dev) {
@@ -174,21 +179,23 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// attn(q, pool, table, kv_lens, q_lens, causal, page_sel, kv_scale, sm_scale, workspace, out, lse, want_lse)
+// attn(q, pool, table, kv_lens, q_lens, causal, page_sel, kv_scale, sm_scale, workspace, out, lse, want_lse, tree)
 PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     Cache x;
-    if (n != 13 || !cache(a[1], a[2], a[3], a[7], x)) Py_RETURN_FALSE;
-    const at::Tensor *q = tensor(a[0], at::kBFloat16, x.dev), *q_lens, *sel, *work, *out, *lse;
+    if (n != 14 || !cache(a[1], a[2], a[3], a[7], x)) Py_RETURN_FALSE;
+    const at::Tensor *q = tensor(a[0], at::kBFloat16, x.dev), *q_lens, *sel, *work, *out, *lse, *tree;
     if (!q || !optional(a[4], at::kInt, x.dev, q_lens) || !optional(a[6], at::kInt, x.dev, sel) ||
         !optional(a[9], at::kByte, x.dev, work) || !optional(a[10], at::kBFloat16, x.dev, out) ||
-        !optional(a[11], at::kFloat, x.dev, lse))
+        !optional(a[11], at::kFloat, x.dev, lse) || !optional(a[13], at::kLong, x.dev, tree))
         Py_RETURN_FALSE;
     if (!rows(q, x.c.B, x.c.D)) Py_RETURN_FALSE;
     const int64_t Sq = q->size(1), heads = q->size(2);
     if (heads == 0 || x.c.kv_heads == 0 || heads % x.c.kv_heads) Py_RETURN_FALSE;
     if (q_lens && !vector(q_lens, x.c.B)) Py_RETURN_FALSE;
     if (sel && (sel->dim() != 3 || sel->size(0) != x.c.B || sel->size(1) != x.c.kv_heads || sel->size(2) == 0))
+        Py_RETURN_FALSE;
+    if (tree && (tree->dim() != 3 || tree->size(0) != x.c.B || tree->size(1) != Sq || tree->size(2) != (Sq + 63) / 64))
         Py_RETURN_FALSE;
     if (out && out->sizes() != q->sizes()) Py_RETURN_FALSE;
     const int64_t shape[3] = {x.c.B, heads, Sq};
@@ -205,9 +212,15 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         work = given_or_new(work, {bytes}, at::kByte, x, &made_work);
         out = given_or_new(out, q->sizes(), at::kBFloat16, x, &made_out);
         if (want_lse) lse = given_or_new(lse, at::IntArrayRef(shape, 3), at::kFloat, x, &made_lse);
-        st = attn_fn(&x.c, data<void>(q), (int32_t)Sq, (int32_t)heads, data<int32_t>(q_lens), causal, data<int32_t>(sel),
-                     sel ? (int32_t)sel->size(2) : 0, (float)scale, data<void>(work), data<void>(out), data<float>(lse),
-                     x.stream);
+        const int32_t nsel = sel ? (int32_t)sel->size(2) : 0;
+        if (tree)
+            st = attn_tree_fn(&x.c, data<void>(q), (int32_t)Sq, (int32_t)heads, data<int32_t>(q_lens),
+                              data<uint64_t>(tree), data<int32_t>(sel), nsel, (float)scale, data<void>(work),
+                              data<void>(out), data<float>(lse), x.stream);
+        else
+            st = attn_fn(&x.c, data<void>(q), (int32_t)Sq, (int32_t)heads, data<int32_t>(q_lens), causal,
+                         data<int32_t>(sel), nsel, (float)scale, data<void>(work), data<void>(out), data<float>(lse),
+                         x.stream);
     }
     if (st != VSA_OK) return PyLong_FromLong(st);
     PyObject* first = result(a[10], made_out);
@@ -215,14 +228,156 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// bind(append, read, attn, workspace_bytes): addresses of the library's functions
+// tree(parents, kv_lens, new_lens, starts, mask, positions)
+PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 6 || !THPVariable_Check(a[0])) Py_RETURN_FALSE;
+    const at::Tensor& p = THPVariable_Unpack(a[0]);
+    if (!p.defined() || !p.is_cuda()) Py_RETURN_FALSE;
+    Cache x;
+    x.dev = (int)p.get_device();
+    if (x.dev != (int)c10::cuda::current_device()) Py_RETURN_FALSE;
+    const at::Tensor *parents = tensor(a[0], at::kInt, x.dev), *lens, *fresh, *starts, *mask, *positions;
+    if (!parents || parents->dim() != 2 || !optional(a[1], at::kInt, x.dev, lens) ||
+        !optional(a[2], at::kInt, x.dev, fresh) || !optional(a[3], at::kInt, x.dev, starts) ||
+        !optional(a[4], at::kLong, x.dev, mask) || !optional(a[5], at::kInt, x.dev, positions))
+        Py_RETURN_FALSE;
+    const int64_t B = parents->size(0), S = parents->size(1);
+    if ((lens && !vector(lens, B)) || (fresh && !vector(fresh, B)) || (starts && !vector(starts, B))) Py_RETURN_FALSE;
+    const int64_t shape[3] = {B, S, (S + 63) / 64};
+    if ((mask && mask->sizes() != at::IntArrayRef(shape, 3)) || (positions && positions->sizes() != parents->sizes()))
+        Py_RETURN_FALSE;
+    at::Tensor made_mask, made_positions;
+    vsa_status st;
+    {
+        NoGil no_gil;
+        const cudaStream_t stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)x.dev).stream();
+        mask = given_or_new(mask, at::IntArrayRef(shape, 3), at::kLong, x, &made_mask);
+        positions = given_or_new(positions, parents->sizes(), at::kInt, x, &made_positions);
+        st = tree_fn(data<int32_t>(parents), (int32_t)B, (int32_t)S, data<int32_t>(lens), data<int32_t>(fresh),
+                     data<int32_t>(starts), data<uint64_t>(mask), data<int32_t>(positions), stream);
+    }
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    PyObject* first = result(a[4], made_mask);
+    return pair(first, result(a[5], made_positions));
+    END_HANDLE_TH_ERRORS
+}
+
+// accept(pool, table, kv_lens, new_lens, path, path_lens, lens)
+PyObject* accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Cache x;
+    if (n != 7 || !cache(a[0], a[1], a[2], Py_None, x)) Py_RETURN_FALSE;
+    const at::Tensor *fresh = tensor(a[3], at::kInt, x.dev), *path = tensor(a[4], at::kInt, x.dev),
+                     *path_lens = tensor(a[5], at::kInt, x.dev), *lens;
+    if (!fresh || !path || !path_lens || !optional(a[6], at::kInt, x.dev, lens)) Py_RETURN_FALSE;
+    if (!vector(fresh, x.c.B) || !vector(path_lens, x.c.B) || path->dim() != 2 || path->size(0) != x.c.B ||
+        (lens && !vector(lens, x.c.B)))
+        Py_RETURN_FALSE;
+    at::Tensor made;
+    vsa_status st;
+    {
+        NoGil no_gil;
+        lens = given_or_new(lens, {x.c.B}, at::kInt, x, &made);
+        st = accept_fn(&x.c, data<int32_t>(fresh), data<int32_t>(path), data<int32_t>(path_lens),
+                       (int32_t)path->size(1), data<int32_t>(lens), x.stream);
+    }
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    return result(a[6], made);
+    END_HANDLE_TH_ERRORS
+}
+
+// weigh(q, lse, pool, table, kv_lens, q_lens, causal, weights, out, kv_scale, sm_scale); out: None is a new tensor
+PyObject* weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Cache x;
+    if (n != 11 || !cache(a[2], a[3], a[4], a[9], x)) Py_RETURN_FALSE;
+    const at::Tensor *q = tensor(a[0], at::kBFloat16, x.dev), *lse = tensor(a[1], at::kFloat, x.dev), *q_lens, *before,
+                     *out;
+    if (!q || !lse || !optional(a[5], at::kInt, x.dev, q_lens) || !optional(a[7], at::kFloat, x.dev, before) ||
+        !optional(a[8], at::kFloat, x.dev, out))
+        Py_RETURN_FALSE;
+    if (!rows(q, x.c.B, x.c.D)) Py_RETURN_FALSE;
+    const int64_t Sq = q->size(1), heads = q->size(2);
+    if (heads == 0 || x.c.kv_heads == 0 || heads % x.c.kv_heads) Py_RETURN_FALSE;
+    const int64_t sums[3] = {x.c.B, heads, Sq}, places[3] = {x.c.B, x.c.kv_heads, (int64_t)x.c.width * 64};
+    if (lse->sizes() != at::IntArrayRef(sums, 3) || (q_lens && !vector(q_lens, x.c.B))) Py_RETURN_FALSE;
+    if ((before && before->sizes() != at::IntArrayRef(places, 3)) || (out && out->sizes() != at::IntArrayRef(places, 3)))
+        Py_RETURN_FALSE;
+    const int causal = PyObject_IsTrue(a[6]);
+    const double scale = PyFloat_AsDouble(a[10]);
+    if (causal < 0 || (scale == -1.0 && PyErr_Occurred())) return nullptr;
+    at::Tensor made;
+    vsa_status st;
+    {
+        NoGil no_gil;
+        out = given_or_new(out, at::IntArrayRef(places, 3), at::kFloat, x, &made);
+        st = weigh_fn(&x.c, data<void>(q), data<float>(lse), (int32_t)Sq, (int32_t)heads, data<int32_t>(q_lens), causal,
+                      (float)scale, data<float>(before), data<float>(out), x.stream);
+    }
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    return result(a[8], made);
+    END_HANDLE_TH_ERRORS
+}
+
+// evict(pool, table, kv_lens, weights, budget, first, recent, to_table, kept, lens, moved)
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Cache x;
+    if (n != 11 || !cache(a[0], a[1], a[2], Py_None, x)) Py_RETURN_FALSE;
+    const at::Tensor *weights = tensor(a[3], at::kFloat, x.dev), *to, *kept, *lens, *moved;
+    if (!weights || !optional(a[7], at::kInt, x.dev, to) || !optional(a[8], at::kInt, x.dev, kept) ||
+        !optional(a[9], at::kInt, x.dev, lens) || !optional(a[10], at::kFloat, x.dev, moved))
+        Py_RETURN_FALSE;
+    int64_t sizes[3];
+    for (int i = 0; i < 3; ++i) {
+        if (!PyLong_Check(a[4 + i])) Py_RETURN_FALSE;
+        sizes[i] = PyLong_AsLongLong(a[4 + i]);
+        if (sizes[i] == -1 && PyErr_Occurred()) PyErr_Clear();
+        if (sizes[i] < 0 || sizes[i] > INT32_MAX) Py_RETURN_FALSE;
+    }
+    const int64_t places[3] = {x.c.B, x.c.kv_heads, (int64_t)x.c.width * 64}, chosen[3] = {x.c.B, x.c.kv_heads, sizes[0]};
+    if (sizes[0] == 0 || weights->sizes() != at::IntArrayRef(places, 3)) Py_RETURN_FALSE;
+    if (to ? to->dim() != 2 || to->size(0) != x.c.B || to->size(1) == 0 : moved != nullptr) Py_RETURN_FALSE;
+    const int64_t width = to ? to->size(1) : 0, after[3] = {x.c.B, x.c.kv_heads, width * 64};
+    if ((kept && kept->sizes() != at::IntArrayRef(chosen, 3)) || (lens && !vector(lens, x.c.B)) ||
+        (moved && moved->sizes() != at::IntArrayRef(after, 3)))
+        Py_RETURN_FALSE;
+    at::Tensor made_kept, made_lens, made_moved;
+    vsa_status st;
+    {
+        NoGil no_gil;
+        kept = given_or_new(kept, at::IntArrayRef(chosen, 3), at::kInt, x, &made_kept);
+        lens = given_or_new(lens, {x.c.B}, at::kInt, x, &made_lens);
+        if (to) moved = given_or_new(moved, at::IntArrayRef(after, 3), at::kFloat, x, &made_moved);
+        st = evict_fn(&x.c, data<float>(weights), (int32_t)sizes[0], (int32_t)sizes[1], (int32_t)sizes[2],
+                      data<int32_t>(to), (int32_t)width, data<int32_t>(kept), data<int32_t>(lens), data<float>(moved),
+                      x.stream);
+    }
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    PyObject* t = PyTuple_New(3);
+    if (!t) return nullptr;
+    PyTuple_SET_ITEM(t, 0, result(a[9], made_lens));
+    PyTuple_SET_ITEM(t, 1, result(a[8], made_kept));
+    PyTuple_SET_ITEM(t, 2, to ? result(a[10], made_moved) : Py_NewRef(a[3]));
+    for (int i = 0; i < 3; ++i)
+        if (!PyTuple_GET_ITEM(t, i)) {
+            Py_DECREF(t);
+            return nullptr;
+        }
+    return t;
+    END_HANDLE_TH_ERRORS
+}
+
+// bind(append, read, attn, workspace_bytes, attn_tree, tree, accept, weigh, evict): addresses of the library's functions
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 4) {
-        PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+    constexpr int kAddresses = 9;
+    if (n != kAddresses) {
+        PyErr_SetString(PyExc_TypeError, "bind takes nine addresses");
         return nullptr;
     }
-    void* p[4];
-    for (int i = 0; i < 4; ++i) {
+    void* p[kAddresses];
+    for (int i = 0; i < kAddresses; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i] && PyErr_Occurred()) return nullptr;
     }
@@ -230,6 +385,11 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     read_fn = reinterpret_cast<decltype(read_fn)>(p[1]);
     attn_fn = reinterpret_cast<decltype(attn_fn)>(p[2]);
     workspace_fn = reinterpret_cast<decltype(workspace_fn)>(p[3]);
+    attn_tree_fn = reinterpret_cast<decltype(attn_tree_fn)>(p[4]);
+    tree_fn = reinterpret_cast<decltype(tree_fn)>(p[5]);
+    accept_fn = reinterpret_cast<decltype(accept_fn)>(p[6]);
+    weigh_fn = reinterpret_cast<decltype(weigh_fn)>(p[7]);
+    evict_fn = reinterpret_cast<decltype(evict_fn)>(p[8]);
     Py_RETURN_NONE;
 }
 
@@ -238,6 +398,10 @@ PyMethodDef methods[] = {
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
     {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(read)), METH_FASTCALL, nullptr},
     {"attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn)), METH_FASTCALL, nullptr},
+    {"tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree)), METH_FASTCALL, nullptr},
+    {"accept", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(accept)), METH_FASTCALL, nullptr},
+    {"weigh", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(weigh)), METH_FASTCALL, nullptr},
+    {"evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(evict)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_front", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

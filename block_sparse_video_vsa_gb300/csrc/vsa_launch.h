@@ -69,8 +69,26 @@ cudaError_t launch_cache_read(const CacheView& c, int D, int S, void* k, void* v
 // cache_attn.cu
 size_t cache_attn_workspace_bytes(int D, int Sq, int group);
 cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, int heads, const int32_t* q_lens,
-                              int causal, const int32_t* page_sel, int nsel, float sm_scale, void* workspace,
-                              void* out, float* lse, int num_sms, cudaStream_t stream);
+                              int causal, const uint64_t* tree, const int32_t* page_sel, int nsel, float sm_scale,
+                              void* workspace, void* out, float* lse, int num_sms, cudaStream_t stream);
+
+// tree.cu
+int tree_max_nodes();
+cudaError_t launch_cache_tree(const int32_t* parents, int B, int S, const int32_t* kv_lens, const int32_t* new_lens,
+                              const int32_t* starts, uint64_t* mask, int32_t* positions, unsigned int* err,
+                              cudaStream_t stream);
+cudaError_t launch_cache_accept(const CacheView& c, int D, const int32_t* new_lens, const int32_t* path,
+                                const int32_t* path_lens, int n, int32_t* lens, cudaStream_t stream);
+
+// weigh.cu (which passes on to weigh_chunk.cu)
+cudaError_t launch_cache_weigh(const CacheView& c, int D, const void* q, const float* lse, int Sq, int heads,
+                               const int32_t* q_lens, int causal, float sm_scale, const float* weights, float* out,
+                               int num_sms, cudaStream_t stream);
+
+// evict.cu
+cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, int budget, int first, int recent,
+                               const int32_t* to_table, int to_width, int32_t* kept, int32_t* lens, float* moved,
+                               cudaStream_t stream);
 
 // pair.cu
 int pair_words(int ncubes);

@@ -1,0 +1,45 @@
+// What the two kernels of cache_weigh share.
+#pragma once
+
+#include "cache.cuh"
+
+namespace vsa {
+
+struct WeighParams {
+    CacheView c;
+    const uint4* q;         // bf16 [B][Sq][heads][D]
+    const float* lse;       // [B][heads][Sq]
+    const int32_t* q_lens;  // [B], or null: Sq
+    const float* weights;   // [B][kv_heads][64 * width], or null: zeros
+    float* out;             // likewise; may be `weights`
+    int Sq, heads, group, causal;
+    float scale_log2;       // sm_scale * log2(e)
+};
+
+#if defined(__CUDACC__)
+
+// Places from a sequence's length on: what `weights` has there, or zero
+// (nothing is to be done in place).  The blocks share the rows.
+__device__ __forceinline__ void fill_rest(const WeighParams& p) {
+    if (p.out == p.weights) return;
+    const long long rows = (long long)p.c.B * p.c.kv_heads;
+    const long long share = max(1LL, (long long)gridDim.x / rows), step = gridDim.x / share;  // blocks of a row; rows at once
+    const long long places = (long long)p.c.width * kPageTokens;
+    for (long long row = blockIdx.x / share; row < rows; row += step) {
+        const int kv = cache_len(p.c, (int)(row / p.c.kv_heads), false);
+        const float* in = p.weights ? p.weights + row * places : nullptr;
+        float* out = p.out + row * places;
+        const long long whole = ((long long)kv + 3) / 4 * 4;  // from here on in 16 bytes
+        const long long i0 = (blockIdx.x % share) * blockDim.x + threadIdx.x;
+        if (kv + i0 < whole) out[kv + i0] = in ? in[kv + i0] : 0.f;
+        for (long long i = whole / 4 + i0; i < places / 4; i += share * blockDim.x)
+            reinterpret_cast<float4*>(out)[i] = in ? reinterpret_cast<const float4*>(in)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+
+// weigh_chunk.cu
+cudaError_t launch_weigh_chunk(const WeighParams& p, int D, int num_sms, cudaStream_t stream);
+
+#endif  // __CUDACC__
+
+}  // namespace vsa

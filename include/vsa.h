@@ -21,7 +21,9 @@
  * cumulative threshold for sequences in 128-token blocks
  * (vsa_block_select).  For video generated chunk by chunk, a paged cache of
  * earlier keys and values in 4 bits, 64 tokens a page:
- * vsa_cache_append, vsa_cache_attn and vsa_cache_read.
+ * vsa_cache_append, vsa_cache_attn and vsa_cache_read; drafted trees over it
+ * (vsa_cache_tree, vsa_cache_attn_tree, vsa_cache_accept) and eviction from it by
+ * attention weight (vsa_cache_weigh, vsa_cache_evict).
  *
  * Sources (page title, section):
  *   [VSA-AMD] "VSA: Accelerating Video Diffusion Inference with Sparse
@@ -61,7 +63,8 @@
  *     Faults of a launched kernel surface at the caller's next
  *     synchronisation.  Kernels never trap: a bounded wait that runs out sets
  *     a device error word (see vsa_device_error) and the kernel returns.
- *   - In-place operation is not supported (outputs must not alias inputs).
+ *   - In-place operation is not supported (outputs must not alias inputs) unless an
+ *     entry point says so.
  *   - Results are bit-reproducible from run to run on the same device.
  */
 #ifndef VSA_H_
@@ -550,6 +553,109 @@ size_t vsa_cache_attn_workspace_bytes(int32_t kv_heads, int32_t D, int32_t Sq, i
 vsa_status vsa_cache_attn(const vsa_cache* c, const void* q, int32_t Sq, int32_t heads, const int32_t* q_lens,
                           int32_t causal, const int32_t* page_sel, int32_t nsel, float sm_scale, void* workspace,
                           void* out, float* lse, vsa_stream_t stream);
+
+/*
+ * Attention of a drafted tree over the cache: vsa_cache_attn with, of the step's
+ * q_lens[b] tokens (the sequence's last), only those that a mask names for a query.
+ * Query i attends the keys
+ *   x < kv_lens[b] - q_lens[b]  and  x = kv_lens[b] - q_lens[b] + j < kv_lens[b]
+ *   for the bits j of its row of the mask.
+ *   tree : uint64 [B, Sq, (Sq + 63) / 64], 8-byte aligned: bit j % 64 of word
+ *          j / 64 of row i is set where query i sees the step's token j (its own
+ *          bit included, or it does not see itself).  Any mask; those of trees
+ *          come from vsa_cache_tree.  Bits from q_lens[b] on are not read as keys.
+ * Other arguments, results, workspace and errors as vsa_cache_attn; Sq <= 1024.
+ */
+vsa_status vsa_cache_attn_tree(const vsa_cache* c, const void* q, int32_t Sq, int32_t heads, const int32_t* q_lens,
+                               const uint64_t* tree, const int32_t* page_sel, int32_t nsel, float sm_scale,
+                               void* workspace, void* out, float* lse, vsa_stream_t stream);
+
+/*
+ * Masks and positions of drafted trees.  Node i < new_lens[b] of sequence b has
+ * the parent parents[b, i], a node before it, or -1: it follows the cached tokens.
+ *   mask[b, i]      : node i and all its ancestors, as vsa_cache_attn_tree takes them
+ *   positions[b, i] : start + the number of its ancestors, where start is starts[b],
+ *                     else kv_lens[b] - new_lens[b], else (both NULL) 0; as
+ *                     vsa_cache_append takes them
+ *   parents   : int32 [B, S];  a parent that is no node before i (nor -1) counts as
+ *               -1 (VSA_DEVERR_INDEX)
+ *   kv_lens   : int32 [B], the step's tokens included, or NULL
+ *   new_lens  : int32 [B], cut to [0, S], or NULL: S
+ *   starts    : int32 [B] or NULL: positions of the first drafted token where they
+ *               are not the places in the cache (after evictions)
+ *   mask      : uint64 [B, S, (S + 63) / 64] (written in full: rows from new_lens[b]
+ *               on are 0), 8-byte aligned
+ *   positions : int32 [B, S] (written in full, 0 from new_lens[b] on), or NULL
+ * S <= 1024, B <= 65535.
+ */
+vsa_status vsa_cache_tree(const int32_t* parents, int32_t B, int32_t S, const int32_t* kv_lens,
+                          const int32_t* new_lens, const int32_t* starts, uint64_t* mask, int32_t* positions,
+                          vsa_stream_t stream);
+
+/*
+ * Keeps the accepted path of a drafted tree: of the sequence's last new_lens[b]
+ * tokens, at places base = kv_lens[b] - new_lens[b] on, those of the path move to
+ * base, base + 1, ... (K and V of all kv heads), and the sequence ends there:
+ *   lens[b] = base + path_lens[b]
+ *   new_lens  : int32 [B], cut to [0, kv_lens[b]]
+ *   path      : int32 [B, n], the nodes of the path from its root on: each in [0,
+ *               new_lens[b]) and larger than the one before.  For one that is not,
+ *               nothing is moved to its place (VSA_DEVERR_INDEX)
+ *   path_lens : int32 [B], cut to [0, min(n, new_lens[b])] (VSA_DEVERR_INDEX)
+ *   lens      : int32 [B] (written); not kv_lens
+ * Places from lens[b] on hold what was there, or tokens moved from.  n <= 1024.
+ */
+vsa_status vsa_cache_accept(const vsa_cache* c, const int32_t* new_lens, const int32_t* path, const int32_t* path_lens,
+                            int32_t n, int32_t* lens, vsa_stream_t stream);
+
+/*
+ * Attention weight that the cached keys get: for every kv head h and place x <
+ * kv_lens[b]
+ *   out[b, h, x] = weights[b, h, x] + sum of exp(sm_scale * (q . k_x) - lse)
+ * over the queries i < q_lens[b] that see x (all; with causal != 0 those with x <=
+ * kv_lens[b] - q_lens[b] + i) and the heads that share h.  With the lse of
+ * vsa_cache_attn on the same keys these are its softmax weights.  Rows whose lse is
+ * not finite (no key, NaN) add nothing, whatever their q holds.
+ *   q        : bf16 [B, Sq, heads, D], as vsa_cache_attn; rows from q_lens[b] on are
+ *              not read
+ *   lse      : fp32 [B, heads, Sq]
+ *   q_lens   : int32 [B], cut to [0, Sq], or NULL: Sq
+ *   sm_scale : finite; <= 0 selects 1 / sqrt(D)
+ *   weights  : fp32 [B, kv_heads, 64 * width], 16-byte aligned, or NULL: zeros
+ *   out      : likewise (written); may be `weights`, added to in place.  Places from
+ *              kv_lens[b] on: as in weights (zero without)
+ * Products and sums are fp32, in an order that the call's sizes fix.  q . k must stay
+ * finite in fp32 before the scale.  Limits as vsa_cache_attn.
+ */
+vsa_status vsa_cache_weigh(const vsa_cache* c, const void* q, const float* lse, int32_t Sq, int32_t heads,
+                           const int32_t* q_lens, int32_t causal, float sm_scale, const float* weights, float* out,
+                           vsa_stream_t stream);
+
+/*
+ * Evicts tokens by weight.  A sequence of n = kv_lens[b] > budget tokens keeps, for
+ * each kv head by itself, `budget` of them: the first `first`, the last `recent`, and
+ * of those between the budget - first - recent with the largest weights (equal
+ * weights: the lowest places; NaN below all others).  They move to places 0, 1, ...
+ * in their order, codes and scales of K and V and their weights.  Sequences of at
+ * most `budget` tokens keep all.
+ *   weights  : fp32 [B, kv_heads, 64 * width]
+ *   budget   : > 0; first, recent >= 0, first + recent <= budget
+ *   to_table : NULL: the tokens stay in the sequence's pages, which no other sequence
+ *              may share; weights moves along in place (zero from budget to n, as it
+ *              is from n on).  Or int32 [B, to_width], 64 * to_width >= min(budget,
+ *              64 * width): the kept tokens are copied to these pages of the pool,
+ *              which no sequence of the call reads; the old pages stay as they are
+ *   kept     : int32 [B, kv_heads, budget] (written in full): the places kept,
+ *              ascending, then -1
+ *   lens     : int32 [B] (written): min(n, budget); not kv_lens
+ *   moved    : with to_table fp32 [B, kv_heads, 64 * to_width] (written in full, zero
+ *              from lens[b] on), else NULL
+ * Keys keep the rotation they were stored with: append later tokens with their own
+ * positions, which are no longer their places.  B * kv_heads < 2^27.
+ */
+vsa_status vsa_cache_evict(const vsa_cache* c, float* weights, int32_t budget, int32_t first, int32_t recent,
+                           const int32_t* to_table, int32_t to_width, int32_t* kept, int32_t* lens, float* moved,
+                           vsa_stream_t stream);
 
 /*
  * Debug aid for the block-sparse encoding ([VSA-AMD] Block-Sparse Encoding):
