@@ -517,7 +517,7 @@ vsa_status vsa_cache_evict(const vsa_cache* c, float* weights, int32_t budget, i
     st = cache_view(c, &cv, &ctx);
     if (st != VSA_OK) return st;
     return from_cuda(launch_cache_evict(cv, c->D, weights, budget, first, recent, to_table, to_width, kept, lens,
-                                        to_table ? moved : weights, static_cast<cudaStream_t>(stream)));
+                                        to_table ? moved : weights, ctx.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t vsa_pair_workspace_bytes(int32_t B, int32_t heads, int32_t ncubes, int32_t topk) {

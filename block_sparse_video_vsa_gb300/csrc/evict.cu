@@ -5,11 +5,10 @@
 // choose_kernel writes the places kept, ascending: the k-th largest weight T of
 // the middle is found digit by digit from the top (11, 11 and 10 bits of the
 // weights' bit patterns, put in their order), every place above T is kept and
-// of those at T the lowest.  A cluster of up to 8 blocks takes a (sequence, kv
-// head), each a stretch of its places: keys go to shared memory once,
-// histograms are summed over the cluster by distributed shared memory (all
-// blocks form the same sums, one barrier a digit).  Counting is in integers:
-// the same places in every run.
+// of those at T the lowest.  A block takes a (sequence, kv head), or a cluster of up
+// to 8, each a stretch of its places: keys go to shared memory once, histograms are
+// summed over the cluster by distributed shared memory (all blocks form the same
+// sums, one barrier a digit).  Counting is in integers: the same places in every run.
 //
 // move_kernel and move_within_kernel bring the kept tokens' codes, scales and
 // weights to the places 0, 1, ...: 9/8 D + 4 bytes a token and head each way,
@@ -25,9 +24,10 @@ namespace vsa {
 
 namespace {
 
-constexpr int kChooseThreads = 512, kMaxCluster = 8;
+constexpr int kChooseThreads = 1024, kChooseWarps = kChooseThreads / 32, kMaxCluster = 8;
 constexpr int kDigits = 3;
 constexpr int kBins = 2048;
+constexpr int kCopies = 4;            // of a histogram: neighbouring lanes add to different ones
 constexpr int kHeldKeys = 40 * 1024;  // keys of a block's stretch that go to shared memory
 
 struct EvictParams {
@@ -53,11 +53,20 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-// The word at `p`, a shared address of this block, in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t load_from_rank(const void* p, uint32_t rank) {
-    uint32_t at, x;
+// The words at `p`, a shared address of this block, in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
+    uint32_t at;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return at;
+}
+__device__ __forceinline__ uint32_t load_from_rank(const void* p, uint32_t rank) {
+    uint32_t x;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at_rank(p, rank)) : "memory");
+    return x;
+}
+__device__ __forceinline__ uint2 load2_from_rank(const void* p, uint32_t rank) {
+    uint2 x;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at_rank(p, rank)) : "memory");
     return x;
 }
 
@@ -69,18 +78,19 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 }
 
 struct ChooseSmem {
-    unsigned int hist[kDigits][kBins];
-    unsigned int warp_sum[kChooseThreads / 32];
-    unsigned int counts[2][kChooseThreads / 32];  // above T, at T: of a warp's stretch
-    unsigned int totals[2];                       // of the block
-    unsigned int found, before;
+    unsigned int hist[kCopies][kBins];
+    alignas(8) unsigned int total[kDigits][kBins];  // of this block, for the others of the cluster
+    unsigned int warp_sum[kChooseWarps];
+    unsigned int counts[2][kChooseWarps];  // above T, at T: of a warp's stretch
+    unsigned int totals[2];                // of the block
+    unsigned int found, before, there, unused[3];
 };
 
-__global__ void __launch_bounds__(kChooseThreads) choose_kernel(EvictParams p) {
-    __shared__ ChooseSmem sm;
-    extern __shared__ uint32_t keys[];
+__global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p) {
+    extern __shared__ __align__(16) unsigned char choose_smem[];
+    ChooseSmem& sm = *reinterpret_cast<ChooseSmem*>(choose_smem);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(choose_smem + sizeof(ChooseSmem));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < kDigits * kBins; i += kChooseThreads) (&sm.hist[0][0])[i] = 0u;
     early();
     begin_work();
     const int blocks = (int)cluster_size(), rank = (int)cluster_rank();
@@ -105,31 +115,59 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(EvictParams p) {
     const float* w = p.weights + (size_t)row * p.c.width * kPageTokens + p.first + begin;
     const bool held = size <= p.keys;
     auto key = [&](int i) { return held ? keys[i] : order_key(w[i]); };
-    if (held)
-        for (int i = threadIdx.x; i < size; i += kChooseThreads) keys[i] = order_key(w[i]);
-    __syncthreads();
+    if (held) {
+        constexpr int kAhead = 8;
+        for (int i0 = threadIdx.x; i0 < size; i0 += kAhead * kChooseThreads) {
+            float x[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) x[k] = i0 + k * kChooseThreads < size ? w[i0 + k * kChooseThreads] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k * kChooseThreads < size) keys[i0 + k * kChooseThreads] = order_key(x[k]);
+        }
+    }
     // The digits of T; `left` of the places with T's digits so far are still to be found.
     uint32_t top = 0u, mask = 0u;
     unsigned left = (unsigned)want;
 #pragma unroll 1
     for (int d = 0; d < kDigits; ++d) {
         const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? 1024 : 2048;
+        for (int i = threadIdx.x; i < kCopies * kBins / 4; i += kChooseThreads)
+            reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+#pragma unroll 4
         for (int i = threadIdx.x; i < size; i += kChooseThreads) {
             const uint32_t k = key(i);
-            if ((k & mask) == top) atomicAdd(&sm.hist[d][(k >> shift) & (bins - 1)], 1u);
+            if ((k & mask) == top) atomicAdd(&sm.hist[lane % kCopies][(k >> shift) & (bins - 1)], 1u);
         }
-        cluster_arrive();
-        cluster_wait();
-        // Thread t: bins 4 t .. 4 t + 3 from the top down, summed over the cluster.
-        unsigned bin[kBins / kChooseThreads], sum = 0u;
+        __syncthreads();
+        // Thread t: bins 2 x + 1 and 2 x, x = bins / 2 - 1 - t: from the top down.
+        const int x = bins / 2 - 1 - (int)threadIdx.x;
+        uint2 bin = make_uint2(0u, 0u);
+        if (x >= 0) {
 #pragma unroll
-        for (int j = 0; j < kBins / kChooseThreads; ++j) {
-            const int x = bins - 1 - (threadIdx.x * (kBins / kChooseThreads) + j);
-            bin[j] = 0u;
-            if (x >= 0)
-                for (int r = 0; r < blocks; ++r) bin[j] += load_from_rank(&sm.hist[d][x], (uint32_t)r);
-            sum += bin[j];
+            for (int k = 0; k < kCopies; ++k) {
+                const uint2 y = *reinterpret_cast<const uint2*>(&sm.hist[k][2 * x]);
+                bin.x += y.x;
+                bin.y += y.y;
+            }
         }
+        if (blocks > 1) {  // sums over the cluster
+            if (x >= 0) *reinterpret_cast<uint2*>(&sm.total[d][2 * x]) = bin;
+            cluster_arrive();
+            cluster_wait();
+            if (x >= 0) {
+                bin = make_uint2(0u, 0u);
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) {
+                    if (r >= blocks) break;
+                    const uint2 y = load2_from_rank(&sm.total[d][2 * x], (uint32_t)r);
+                    bin.x += y.x;
+                    bin.y += y.y;
+                }
+            }
+        }
+        const unsigned sum = bin.x + bin.y;
         unsigned incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -138,31 +176,33 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(EvictParams p) {
         }
         if (lane == 31) sm.warp_sum[warp] = incl;
         __syncthreads();
-        unsigned base = 0u;
-        for (int i = 0; i < warp; ++i) base += sm.warp_sum[i];
-        unsigned before = base + incl - sum;
-        if (before < left && before + sum >= left) {
+        const unsigned mine = sm.warp_sum[lane];
+        unsigned base = mine;
 #pragma unroll
-            for (int j = 0; j < kBins / kChooseThreads; ++j) {
-                if (before < left && before + bin[j] >= left) {
-                    sm.found = (unsigned)(bins - 1 - (threadIdx.x * (kBins / kChooseThreads) + j));
-                    sm.before = before;
-                }
-                before += bin[j];
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, base, o);
+            if (lane >= o) base += v;
+        }
+        const unsigned before = __shfl_sync(0xffffffffu, base - mine, warp) + incl - sum;
+        if (before < left && before + sum >= left) {
+            const bool high = before + bin.y >= left;
+            sm.found = (unsigned)(2 * x + (high ? 1 : 0));
+            sm.before = before + (high ? 0u : bin.y);
+            sm.there = high ? bin.y : bin.x;
         }
         __syncthreads();
         top |= sm.found << shift;
         mask |= (unsigned)(bins - 1) << shift;
         left -= sm.before;
-        __syncthreads();
+        if (sm.there == left) break;  // all of them are kept: their other digits do not matter
+        __syncthreads();              // (the next digit writes what was read here)
     }
     // `left` of the places at T are kept, the lowest.  Where each warp's kept places go:
-    const int part = ((size - 1) / (kChooseThreads / 32) / 32 + 1) * 32;  // of a warp (size > 0 or nothing to do)
+    const int part = ((size - 1) / kChooseWarps / 32 + 1) * 32;  // of a warp (size > 0 or nothing to do)
     const int from = min(size, warp * part), to = min(size, from + part);
     unsigned above = 0u, same = 0u;
     for (int i = from + lane; i < to; i += 32) {
-        const uint32_t k = key(i);
+        const uint32_t k = key(i) & mask;
         above += k > top;
         same += k == top;
     }
@@ -174,7 +214,7 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(EvictParams p) {
     }
     __syncthreads();
     unsigned above_before = 0u, same_before = 0u;
-    for (int i = 0; i < kChooseThreads / 32; ++i) {
+    for (int i = 0; i < kChooseWarps; ++i) {
         if (i == warp) {
             above = above_before;
             same = same_before;
@@ -182,21 +222,23 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(EvictParams p) {
         above_before += sm.counts[0][i];
         same_before += sm.counts[1][i];
     }
-    if (threadIdx.x == 0) {
-        sm.totals[0] = above_before;
-        sm.totals[1] = same_before;
+    if (blocks > 1) {
+        if (threadIdx.x == 0) {
+            sm.totals[0] = above_before;
+            sm.totals[1] = same_before;
+        }
+        cluster_arrive();
+        cluster_wait();
+        for (int r = 0; r < rank; ++r) {
+            above += load_from_rank(&sm.totals[0], (uint32_t)r);
+            same += load_from_rank(&sm.totals[1], (uint32_t)r);
+        }
+        cluster_arrive();  // no block leaves while another reads from it
     }
-    cluster_arrive();
-    cluster_wait();
-    for (int r = 0; r < rank; ++r) {
-        above += load_from_rank(&sm.totals[0], (uint32_t)r);
-        same += load_from_rank(&sm.totals[1], (uint32_t)r);
-    }
-    cluster_arrive();  // no block leaves while another reads from it
     const unsigned below_me = (1u << lane) - 1;
     for (int i0 = from; i0 < to; i0 += 32) {
         const int i = i0 + lane;
-        const uint32_t k = i < to ? key(i) : 0u;
+        const uint32_t k = i < to ? key(i) & mask : 0u;
         const unsigned is_above = __ballot_sync(0xffffffffu, i < to && k > top);
         const unsigned is_same = __ballot_sync(0xffffffffu, i < to && k == top);
         const unsigned same_here = same + __popc(is_same & below_me);
@@ -208,7 +250,7 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(EvictParams p) {
         above += __popc(is_above);
         same += __popc(is_same);
     }
-    cluster_wait();
+    if (blocks > 1) cluster_wait();
 }
 
 // To other pages: block (x, h, b) fills places 64 x .. 64 x + 63.
@@ -293,7 +335,7 @@ cudaError_t launch_clusters(void (*kernel)(P...), dim3 grid, int cluster, int th
 
 cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, int budget, int first, int recent,
                                const int32_t* to_table, int to_width, int32_t* kept, int32_t* lens, float* moved,
-                               cudaStream_t stream) {
+                               int num_sms, cudaStream_t stream) {
     EvictParams p;
     p.c = c;
     p.to_table = to_table;
@@ -305,17 +347,23 @@ cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, 
     p.first = first;
     p.recent = recent;
     p.to_width = to_width;
-    // Blocks of a row: 2048 places each, up to 8.
+    // Blocks of a row: as many as its keys need shared memory of, and more while the
+    // rows leave SMs idle.
     const long long places = (long long)c.width * kPageTokens;
+    const long long rows = (long long)c.B * c.kv_heads;
     int cluster = 1;
-    while (cluster < kMaxCluster && places > 2048LL * cluster) cluster *= 2;
+    while (cluster < kMaxCluster &&
+           (places > (long long)kHeldKeys * cluster || (2 * rows * cluster <= num_sms && places > 4096LL * cluster)))
+        cluster *= 2;
     const long long stretch = (places + cluster - 1) / cluster + 32;
     p.keys = (int)std::min<long long>(stretch, kHeldKeys);
+    constexpr int kFixed = (int)sizeof(ChooseSmem);
+    static_assert(kFixed % 16 == 0 && kFixed + kHeldKeys * 4 <= 232448, "shared memory of the choosing kernel");
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(choose_kernel, kHeldKeys * 4, done);
+    cudaError_t e = allow_smem(choose_kernel, kFixed + kHeldKeys * 4, done);
     if (e != cudaSuccess) return e;
-    const unsigned rows = (unsigned)c.B * (unsigned)c.kv_heads;
-    e = launch_clusters(choose_kernel, dim3(rows * cluster), cluster, kChooseThreads, p.keys * 4, stream, p);
+    e = launch_clusters(choose_kernel, dim3((unsigned)(rows * cluster)), cluster, kChooseThreads, kFixed + p.keys * 4,
+                        stream, p);
     if (e != cudaSuccess) return e;
     if (to_table) {
         const dim3 grid((unsigned)to_width, (unsigned)c.kv_heads, (unsigned)c.B);
@@ -324,7 +372,7 @@ cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, 
     const int turns = (budget + kPageTokens - 1) / kPageTokens;
     cluster = 1;
     while (cluster < kMaxCluster && cluster < turns) cluster *= 2;
-    return launch_clusters(D == 64 ? move_within_kernel<64> : move_within_kernel<128>, dim3(rows * cluster), cluster,
+    return launch_clusters(D == 64 ? move_within_kernel<64> : move_within_kernel<128>, dim3((unsigned)(rows * cluster)), cluster,
                            kMoveThreads, 0, stream, p);
 }
 

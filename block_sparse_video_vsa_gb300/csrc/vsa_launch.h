@@ -88,7 +88,7 @@ cudaError_t launch_cache_weigh(const CacheView& c, int D, const void* q, const f
 // evict.cu
 cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, int budget, int first, int recent,
                                const int32_t* to_table, int to_width, int32_t* kept, int32_t* lens, float* moved,
-                               cudaStream_t stream);
+                               int num_sms, cudaStream_t stream);
 
 // pair.cu
 int pair_words(int ncubes);

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) weigh_kernel(WeighParams p) 
             left -= n;
         }
     }
-    fill_rest(p);
+    fill_rest(p, false);
 }
 
 }  // namespace

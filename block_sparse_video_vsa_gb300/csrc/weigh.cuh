@@ -20,13 +20,15 @@ struct WeighParams {
 
 // Places from a sequence's length on: what `weights` has there, or zero
 // (nothing is to be done in place).  The blocks share the rows.
-__device__ __forceinline__ void fill_rest(const WeighParams& p) {
+__device__ __forceinline__ void fill_rest(const WeighParams& p, bool idle) {
     if (p.out == p.weights) return;
     const long long rows = (long long)p.c.B * p.c.kv_heads;
     const long long share = max(1LL, (long long)gridDim.x / rows), step = gridDim.x / share;  // blocks of a row; rows at once
     const long long places = (long long)p.c.width * kPageTokens;
     for (long long row = blockIdx.x / share; row < rows; row += step) {
-        const int kv = cache_len(p.c, (int)(row / p.c.kv_heads), false);
+        const int b = (int)(row / p.c.kv_heads);
+        // (All of a sequence without queries, which nobody else writes, where `idle` says so.)
+        const int kv = idle && p.q_lens && p.q_lens[b] <= 0 ? 0 : cache_len(p.c, b, false);
         const float* in = p.weights ? p.weights + row * places : nullptr;
         float* out = p.out + row * places;
         const long long whole = ((long long)kv + 3) / 4 * 4;  // from here on in 16 bytes

@@ -14,12 +14,19 @@
 //    tensor memory as the A operand, while the queries stream through shared
 //    memory as they are (bf16, TMA, 128-byte swizzle) as the B operand: each tile
 //    of rows serves two tiles of keys, so that L2 gives 32 KB for some 1000 cycles.
-//  * Warp roles (640 threads): warp 0 loads queries, warp 1 owns TMEM and issues the
-//    products, warp 2 copies pages, warp 3 loads log-sums; warps 4..7 and 8..11
-//    convert the two key tiles, warps 12..15 and 16..19 sum them up.
-//  * TMEM (512 columns): K of two units, S^T of the two key tiles.
-//  * Units are dealt to the CTAs in turn.  Where there are few, the row tiles of a
-//    unit are dealt to the CTAs of a cluster and their sums added in rank order.
+//  * Rows that fit one tile (a window of recent queries) stay in shared memory for
+//    all units of their head: the CTAs take runs of neighbouring units then, and
+//    pages are all that moves.  Else units are dealt to the CTAs in turn, which
+//    balances causal calls.  Where there are few units, the row tiles of one are
+//    dealt to the CTAs of a cluster and their sums added in rank order.
+//  * S^T is issued and summed in halves of a tile's columns, with a buffer and a
+//    warpgroup for each half and key tile: a half's products run while the others'
+//    exponentials do, and four warps a scheduler cover one another's loads.
+//  * Warp roles (896 threads): warp 0 loads queries and log-sums, warps 1 (which owns
+//    TMEM) and 3 issue the products of a key tile each, warp 2 walks the units,
+//    describes them to the others and copies their pages; warps 4..7 and 8..11
+//    convert the two key tiles; warps 12..27 sum up.
+//  * TMEM (512 columns): K of two units, two halves of S^T of the two key tiles.
 //  * Every wait is bounded; one that runs out raises the CTA's abort flag and the
 //    device error word, and each role winds down.
 #include <stddef.h>
@@ -32,36 +39,51 @@ namespace vsa {
 
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr int kKeys = 256, kPages = kKeys / kPageTokens;
-constexpr int kNlStages = 8, kHeldUnits = 8;
-constexpr int kRawUnits = 2;  // units whose pages are on their way or being converted
-constexpr uint32_t kSlots = kRawUnits * kPages;
+// Log-sums of the last tiles.  A place is written again 8 tiles later, when the products
+// of the tile three before that have been issued and completed: those waited for the
+// sums of the tiles before, so the place's readers are done.
+constexpr int kNlStages = 8;
+constexpr int kUnits = 16;                       // described at a time
+constexpr int kReaders = kThreads / 32 - 1;      // warps that read the descriptions
+constexpr uint32_t kSlots = 24;  // pages on their way or being converted: six units
 constexpr int kTmemS = 256;
 
 template <int kD>
 struct Sm {
     static constexpr int kHalf = 128 * 128;               // 128 rows x 64 channels of bf16, swizzled
     static constexpr int kTile = kHalf * (kD / 64);
-    static constexpr int kStages = 5;                     // of queries
+    static constexpr int kStages = 3;                     // of queries
     static constexpr int kCodes = kPageTokens * kD / 2, kScales = kPageTokens * kD / 16;
     static constexpr int kRaw = kCodes + kScales;
-    static constexpr int kOffRaw = kStages * kTile;       // [unit parity][page]
-    static constexpr int kOffMisc = kOffRaw + kRawUnits * kPages * kRaw;
+    static constexpr int kOffRaw = kStages * kTile;       // [slot]
+    static constexpr int kOffMisc = kOffRaw + (int)kSlots * kRaw;
     static constexpr int kKCols = kD / 2;                 // TMEM columns of a key tile
 };
 
+// A unit: keys [first, first + 256) of (b, h), its row tiles [t0, tiles) in steps of
+// p.cluster; fresh_rows: other rows than the unit before had.  b < 0: no more units.
+struct alignas(16) Unit {
+    int b, h, first, kv;
+    int fresh, t0, tiles, fresh_rows;
+    float c2;  // logit (log2 units) of a product
+    int held;  // bit i: page i is there
+};
+
 struct __align__(16) Misc {
-    uint64_t q_full[5], q_empty[5];
-    uint64_t raw_full[kRawUnits][kPages], raw_empty[kRawUnits][kPages];
-    uint64_t k_full[2][2], k_empty[2];  // [key tile][unit parity], [unit parity]
-    uint64_t s_full[2], s_free[2];      // per key tile
-    uint64_t nl_full[kNlStages], nl_empty[kNlStages];
-    uint64_t drain;
+    uint64_t q_full[3], q_empty[3];
+    uint64_t raw_full[kSlots], raw_empty[kSlots];
+    uint64_t k_full[2][2], k_empty[2][2];  // [key tile][unit parity]
+    uint64_t s_full[2][2], s_free[2][2];  // [key tile][buffer]
+    uint64_t unit_full[kUnits], unit_empty[kUnits];
+    uint64_t part_full[2][2], part_empty[2][2];  // [key tile][unit parity]
+    uint64_t drain[2];
     alignas(16) float nl[kNlStages][128];  // minus the log-sums (log2 units), read in 16 bytes
-    int odd[kNlStages];                 // a row of the tile weighs nothing: its logits may be anything
-    int held[kHeldUnits][kPages];       // the page is there
-    float sums[kKeys];                  // of a cluster's CTA
+    int odd[kNlStages];                    // a row of the tile weighs nothing: its logits may be anything
+    float part[2][kKeys];                  // [unit parity]: the odd buffers' share of the sums
+    float sums[kKeys];                     // of a cluster's CTA
+    Unit unit[kUnits];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -75,17 +97,13 @@ static_assert(smem_bytes<128>() <= 232448, "shared memory of the chunk kernel");
 
 struct ChunkParams {
     WeighParams w;
-    int per;      // queries of a tile (one, with 128 heads of it, for groups of more than 128)
-    int splits;   // tiles of a query for such groups, else 1
-    int cluster;  // CTAs that share a unit
+    int per;       // queries of a tile (one, with 128 heads of it, for groups of more than 128)
+    int splits;    // tiles of a query for such groups, else 1
+    int cluster;   // CTAs that share a unit
+    int resident;  // one tile of rows: CTAs take runs of units and keep it for all of a head
+    int half;      // columns of a tile that are issued and summed at once
 };
 
-// A unit of the walk: keys [first, first + 256) of (b, h), its row tiles [t0, tiles)
-// in steps of p.cluster.
-struct Unit {
-    int b, h, first, kv, fresh, t0, tiles;
-    __device__ int count(const ChunkParams& p) const { return t0 < tiles ? (tiles - t0 - 1) / p.cluster + 1 : 0; }
-};
 struct TileRows {
     int query, head, columns;  // first query and head (of the kv head's); rows
 };
@@ -97,53 +115,104 @@ __device__ __forceinline__ TileRows tile_rows_of(const ChunkParams& p, const Uni
 
 __device__ __forceinline__ int blocks_of(int kv) { return kv > 0 ? (kv - 1) / kKeys + 1 : 0; }
 
-// Units of all sequences and heads, those of cluster i of n: i, i + n, ... (a whole warp walks).
+// The units of all sequences and heads in their order; CTA (or cluster) i of n takes
+// i, i + n, ..., or the i-th of n equal runs (a whole warp walks).
 struct UnitWalk {
-    long long at;  // the next unit, from sequence b0's first on
-    int b0;
-    long long step;
+    int b, h, block;  // the next unit
+    int kv, blocks;   // of its sequence
+    int step;
     int rank;
-    __device__ void begin(const ChunkParams& p) {
-        at = blockIdx.x / p.cluster;
-        step = gridDim.x / p.cluster;
-        rank = blockIdx.x % p.cluster;
-        b0 = 0;
-    }
-    __device__ bool next(const ChunkParams& p, Unit& u) {
+    long long left;  // units of a run
+    bool any, moved;
+    int known, fresh, tiles;  // the sequence whose queries are known, and they
+
+    // The unit `at` places behind sequence b0's first; false: there is none.
+    __device__ bool find(const ChunkParams& p, int b0, long long at) {
         const CacheView& c = p.w.c;
         const int lane = threadIdx.x & 31;
-        for (;;) {
-            const int b = b0 + lane;
-            const int kv = b < c.B ? cache_len(c, b, false) : 0;
-            const long long mine = (long long)c.kv_heads * blocks_of(kv);
+        for (; b0 < c.B; b0 += 32) {
+            const int n = b0 + lane < c.B ? cache_len(c, b0 + lane, false) : 0;
+            const long long mine = (long long)c.kv_heads * blocks_of(n);
             const long long incl = scan_warp(mine);
             const unsigned past = __ballot_sync(0xffffffffu, at < incl);
             if (!past) {
                 at -= __shfl_sync(0xffffffffu, incl, 31);
-                b0 += 32;
-                if (b0 >= c.B) return false;
                 continue;
             }
             const int l = __ffs(past) - 1;
-            const long long within = at - __shfl_sync(0xffffffffu, incl - mine, l);
-            u.b = b0 + l;
-            u.kv = __shfl_sync(0xffffffffu, kv, l);
-            const int blocks = blocks_of(u.kv);
-            u.h = (int)(within / blocks);
-            u.first = (int)(within - (long long)u.h * blocks) * kKeys;
-            break;
+            at -= __shfl_sync(0xffffffffu, incl - mine, l);
+            b = b0 + l;
+            kv = __shfl_sync(0xffffffffu, n, l);
+            blocks = blocks_of(kv);
+            h = (int)(at / blocks);
+            block = (int)(at - (long long)h * blocks);
+            return true;
         }
-        u.fresh = p.w.q_lens ? min(max(p.w.q_lens[u.b], 0), p.w.Sq) : p.w.Sq;
-        u.tiles = p.splits == 1 ? (u.fresh + p.per - 1) / p.per : u.fresh * p.splits;
-        // Tiles whose queries all come before the unit's keys see none of them.
-        int t0 = 0;
-        if (p.w.causal) {
-            const int q0 = min(max(u.first - (u.kv - u.fresh), 0), u.fresh);
-            t0 = p.splits == 1 ? q0 / p.per : q0 * p.splits;
+        return false;
+    }
+    __device__ void begin(const ChunkParams& p) {
+        const CacheView& c = p.w.c;
+        rank = blockIdx.x % p.cluster;
+        const int i = blockIdx.x / p.cluster, n = gridDim.x / p.cluster;
+        moved = true;
+        known = -1;
+        step = n;
+        left = 1LL << 62;
+        long long from = i;
+        if (p.resident) {
+            long long total = 0;
+            for (int b0 = threadIdx.x & 31; b0 < c.B; b0 += 32)
+                total += (long long)c.kv_heads * blocks_of(cache_len(c, b0, false));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            from = total / n * i + min((long long)i, total % n);
+            left = total / n + (i < total % n ? 1 : 0);
+            step = 1;
         }
-        u.t0 = t0 + rank;
-        at += step;
-        return true;
+        any = left > 0 && find(p, 0, from);
+    }
+    // The next unit with tiles, and the page numbers of its pages (lane i: page i).
+    __device__ bool next(const ChunkParams& p, Unit& u, int& id) {
+        const CacheView& c = p.w.c;
+        while (any) {
+            if (b != known) {
+                known = b;
+                fresh = p.w.q_lens ? min(max(p.w.q_lens[b], 0), p.w.Sq) : p.w.Sq;
+                tiles = p.splits == 1 ? (fresh + p.per - 1) / p.per : fresh * p.splits;
+            }
+            u.b = b;
+            u.h = h;
+            u.first = block * kKeys;
+            u.kv = kv;
+            u.fresh = fresh;
+            u.tiles = tiles;
+            // Tiles whose queries all come before the unit's keys see none of them.
+            int t0 = 0;
+            if (p.w.causal && tiles > 1) {
+                const int q0 = min(max(u.first - (kv - fresh), 0), fresh);
+                t0 = p.splits == 1 ? q0 / p.per : q0 * p.splits;
+            }
+            u.t0 = t0 + rank;
+            u.fresh_rows = moved || !p.resident;
+            // On to the next.
+            moved = false;
+            any = --left > 0;
+            block += step;
+            if (any && block >= blocks) {
+                h += block / blocks;
+                block %= blocks;
+                moved = true;
+                if (h >= c.kv_heads) any = find(p, b + 1, (long long)(h - c.kv_heads) * blocks + block);
+            }
+            if (u.t0 >= u.tiles) continue;
+            const int lane = threadIdx.x & 31;
+            const int page = u.first / kPageTokens + lane;
+            id = -1;
+            if (lane < kPages && (long long)page * kPageTokens < u.kv) id = c.table[(size_t)u.b * c.width + page];
+            u.c2 = p.w.scale_log2 * (c.kv_scale ? c.kv_scale[u.h] : 1.f);
+            return true;
+        }
+        return false;
     }
 };
 
@@ -161,6 +230,60 @@ __device__ __forceinline__ uint32_t f16_to_bf16x2(uint32_t h) {
     return pack_bf16x2(f.x, f.y);
 }
 
+// 4-byte asynchronous global -> shared copy, tracked by commit groups.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The kD / 16 products of a half: d = a (kD / 2 columns of tensor memory) * b (shared
+// memory, 16 channels 32 bytes apart, 64 channels kHalf), and an arrival on `done` once
+// they and those before have completed.  All lanes call it; one issues, in one branch.
+#define VSA_MMA "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, "
+#define VSA_NEXT "add.u32 ta, ta, 8;\n\tadd.u64 db, db, 2;\n\t"
+template <int kD>
+__device__ __forceinline__ void issue_half(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                           uint32_t done) {
+    if constexpr (kD == 128)
+        asm volatile(
+            "{\n\t.reg .pred one, p;\n\t.reg .b32 ta;\n\t.reg .b64 db;\n\t"
+            "elect.sync _|one, 0xffffffff;\n\t"
+            "mov.b64 db, {%2, %3};\n\tmov.b32 ta, %1;\n\tsetp.ne.b32 p, 0, 0;\n\t"
+            "@!one bra skip%=;\n\t" VSA_MMA "p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+            VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t"
+            "add.u64 db, db, 1016;\n\t"  // (the next 64 channels: 1024 from the first of these)
+            VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t"
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+            "skip%=:\n\t}" ::"r"(d),
+            "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(done)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred one, p;\n\t.reg .b32 ta;\n\t.reg .b64 db;\n\t"
+            "elect.sync _|one, 0xffffffff;\n\t"
+            "mov.b64 db, {%2, %3};\n\tmov.b32 ta, %1;\n\tsetp.ne.b32 p, 0, 0;\n\t"
+            "@!one bra skip%=;\n\t" VSA_MMA "p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+            VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t"
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+            "skip%=:\n\t}" ::"r"(d),
+            "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(done)
+            : "memory");
+    __syncwarp();
+}
+#undef VSA_MMA
+#undef VSA_NEXT
+// An arrival once everything issued so far has completed, by the lane that issues.
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
+        "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
+// The same number for the compiler, too, all over the warp (which holds it in a
+// uniform register then, as the products' operands have to be).
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 x;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
@@ -169,7 +292,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
 
 template <int kD>
 __global__ void __launch_bounds__(kThreads, 1)
-    weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const ChunkParams p) {
+    weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ ChunkParams p) {
     using L = PageLayout<kD>;
     using S = Sm<kD>;
     extern __shared__ unsigned char smem_raw[];
@@ -184,28 +307,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tm_q);
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(smem_u32(&ms.q_full[s]), 1);
-            mbar_init(smem_u32(&ms.q_empty[s]), 1);
+            mbar_init(smem_u32(&ms.q_full[s]), 2);  // queries, log-sums
+            mbar_init(smem_u32(&ms.q_empty[s]), 2);
         }
-        for (int s = 0; s < kRawUnits * kPages; ++s) {
-            mbar_init(smem_u32(&ms.raw_full[0][s]), 1);
-            mbar_init(smem_u32(&ms.raw_empty[0][s]), 2);
+        for (int s = 0; s < (int)kSlots; ++s) {
+            mbar_init(smem_u32(&ms.raw_full[s]), 1);
+            mbar_init(smem_u32(&ms.raw_empty[s]), 2);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&ms.k_full[s][0]), 4);
-            mbar_init(smem_u32(&ms.k_full[s][1]), 4);
-            mbar_init(smem_u32(&ms.k_empty[s]), 1);
-            mbar_init(smem_u32(&ms.s_full[s]), 1);
-            mbar_init(smem_u32(&ms.s_free[s]), 4);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&ms.k_full[s][i]), 4);
+                mbar_init(smem_u32(&ms.k_empty[s][i]), 1);
+                mbar_init(smem_u32(&ms.s_full[s][i]), 1);
+                mbar_init(smem_u32(&ms.s_free[s][i]), 4);
+                mbar_init(smem_u32(&ms.part_full[s][i]), 4);
+                mbar_init(smem_u32(&ms.part_empty[s][i]), 4);
+            }
+            mbar_init(smem_u32(&ms.drain[s]), 1);
         }
-        for (int s = 0; s < kNlStages; ++s) {
-            mbar_init(smem_u32(&ms.nl_full[s]), 1);
-            mbar_init(smem_u32(&ms.nl_empty[s]), 8);
+        for (int s = 0; s < kUnits; ++s) {
+            mbar_init(smem_u32(&ms.unit_full[s]), 1);
+            mbar_init(smem_u32(&ms.unit_empty[s]), kReaders);
         }
-        mbar_init(smem_u32(&ms.drain), 1);
         ms.abort_flag = 0;
         fence_barrier_init();
     }
+    if (threadIdx.x < kKeys) ms.sums[threadIdx.x] = 0.f;
     if (warp == 1) {
         tmem_alloc(smem_u32(&ms.tmem_base), 512);
         tmem_relinquish();
@@ -216,22 +343,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     early();
     begin_work();
     const uint32_t tmem = ms.tmem_base;
-    UnitWalk walk;
-    walk.begin(p);
-    Unit u;
+
+    // The n-th unit, once it is described; false: there are no more (or the kernel was called off).
+    auto take = [&](uint32_t n, bool& ok, Unit& u) {
+        ok = ok && cache_wait<kSleepShort>(smem_u32(&ms.unit_full[n % kUnits]), (n / kUnits) & 1, abort_flag, err);
+        if (!ok) return false;
+        u = ms.unit[n % kUnits];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms.unit_empty[n % kUnits]));
+        return __any_sync(0xffffffffu, u.b >= 0) != 0;
+    };
 
     if (warp == 0) {
-        // ====================================================== queries by TMA
+        // =================================== queries (by TMA) and their log-sums
+        // The log-sums are copied to their place asynchronously, and when the next tile
+        // of the unit has been asked for turned into what the sums take there.  A
+        // column without a row is marked.
+        constexpr uint32_t kNoRow = 0x7FFFDEADu;
         const int box_rows = p.splits == 1 ? p.per * p.w.group : 128;
         uint32_t i = 0;  // tiles so far
         bool ok = true;
-        while (ok && walk.next(p, u)) {
+        auto finish = [&](uint32_t tile) {  // whose log-sums have landed
+            float* nl = ms.nl[tile % kNlStages];
+            bool odd = false;
+#pragma unroll
+            for (int k = 0; k < 128; k += 32) {
+                const float l = nl[k + lane];
+                const bool finite = fabsf(l) < INFINITY;
+                odd |= !finite && __float_as_uint(l) != kNoRow;
+                nl[k + lane] = finite ? l * -1.4426950408889634f : -INFINITY;
+            }
+            odd = __any_sync(0xffffffffu, odd);
+            if (lane == 0) ms.odd[tile % kNlStages] = odd;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ms.q_full[tile % S::kStages]));
+        };
+        Unit u;
+        for (uint32_t n = 0; take(n, ok, u); ++n) {
+            if (!u.fresh_rows) continue;
+            bool pending = false;
+#pragma unroll 1
             for (int t = u.t0; t < u.tiles; t += p.cluster, ++i) {
-                const int st = i % S::kStages;
-                if (i >= S::kStages) ok = cache_wait<kSleepLong>(smem_u32(&ms.q_empty[st]), (i / S::kStages + 1) & 1, abort_flag, err);
+                const uint32_t st = i % S::kStages;
+                if (i >= S::kStages)
+                    ok = cache_wait<kSleepShort>(smem_u32(&ms.q_empty[st]), (i / S::kStages + 1) & 1, abort_flag, err);
                 if (!ok) break;
+                const TileRows x = tile_rows_of(p, u, t);
                 if (lane == 0) {
-                    const TileRows x = tile_rows_of(p, u, t);
                     const uint32_t bar = smem_u32(&ms.q_full[st]);
                     mbar_arrive_expect_tx(bar, box_rows * kD * 2);
 #pragma unroll
@@ -240,81 +398,115 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     u.h * p.w.group + x.head, x.query, u.b);
                 }
                 __syncwarp();
+                const float* lse = p.w.lse + ((size_t)u.b * p.w.heads + u.h * p.w.group + x.head) * p.w.Sq + x.query;
+                float* nl = ms.nl[i % kNlStages];
+#pragma unroll 1
+                for (int r = lane; r < 128; r += 32) {
+                    const int q = p.splits == 1 ? r / p.w.group : 0, head = r - q * p.w.group;
+                    if (r < x.columns)
+                        cp_async4(smem_u32(&nl[r]), lse + (size_t)head * p.w.Sq + q);
+                    else
+                        nl[r] = __uint_as_float(kNoRow);
+                }
+                cp_async_commit();
+                if (pending) {
+                    cp_async_wait<1>();
+                    finish(i - 1);
+                }
+                pending = true;
             }
+            cp_async_wait<0>();
+            if (pending) finish(i - 1);  // (the last one asked for, also where a wait ran out)
         }
         // The last load into each stage has landed before the CTA's shared memory is released.
         if (lane == 0)
             for (uint32_t s = 0; s < (uint32_t)S::kStages && s < i; ++s)
                 mbar_wait_drain_1(smem_u32(&ms.q_full[s]), ((i - 1 - s) / S::kStages) & 1, err, kCacheWaitNs);
-    } else if (warp == 1) {
-        // ============================================================ K Q^T
+    } else if (warp == 1 || warp == 3) {
+        // ================================ K Q^T: warp 1 of the first key tile, warp 3 of the other
+        const int s = warp >> 1;
         const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);
-        const uint32_t lo_q = (uint32_t)smem_desc_sw128(sbase, 16, 1024);
-        uint32_t i = 0, n = 0;  // tiles, units with tiles so far
+        const uint32_t lo_q = uniform((uint32_t)smem_desc_sw128(sbase, 16, 1024));
+        const uint32_t t_k = uniform(tmem) + s * S::kKCols, t_s = uniform(tmem) + kTmemS + s * 128;
+        uint32_t i = 0, used[2] = {0, 0};  // tiles so far, halves so far
         bool ok = true;
-        while (ok && walk.next(p, u)) {
-            if (u.count(p) == 0) continue;
-            for (int t = u.t0; t < u.tiles && ok; t += p.cluster, ++i) {
-                const int st = i % S::kStages;
+        Unit u;
+        for (uint32_t n = 0; take(n, ok, u); ++n) {
+            u.t0 = uniform(u.t0);
+            u.tiles = uniform(u.tiles);
+            u.fresh = uniform(u.fresh);
+            u.fresh_rows = uniform(u.fresh_rows);
+            // (A resident tile is the one that was loaded last: it is let go when the next is taken up.)
+            if (p.resident && u.fresh_rows && i++ > 0) commit_one(smem_u32(&ms.q_empty[(i - 2) % S::kStages]));
+            ok = cache_wait<kSleepShort>(smem_u32(&ms.k_full[s][n & 1]), (n >> 1) & 1, abort_flag, err);
+            const uint32_t a0 = t_k + (n & 1) * 2 * S::kKCols;
+#pragma unroll 1
+            for (int t = u.t0; t < u.tiles && ok; t += p.cluster) {
+                const uint32_t tile = p.resident ? i - 1 : i++;
+                const uint32_t st = tile % S::kStages;
                 const int columns = tile_rows_of(p, u, t).columns;
-                const uint32_t idesc = idesc_bf16_f32(128, (columns + 15) & ~15, 0, 0);
-                ok = cache_wait<kSleepShort>(smem_u32(&ms.q_full[st]), (i / S::kStages) & 1, abort_flag, err);
-                const uint32_t b0 = lo_q + ((uint32_t)(st * S::kTile) >> 4);
+                if (u.fresh_rows)
+                    ok = cache_wait<kSleepShort>(smem_u32(&ms.q_full[st]), (tile / S::kStages) & 1, abort_flag, err);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (ok && t == u.t0)
-                        ok = cache_wait<kSleepShort>(smem_u32(&ms.k_full[s][n & 1]), (n >> 1) & 1, abort_flag, err);
-                    if (ok && i > 0) ok = cache_wait<kSleepShort>(smem_u32(&ms.s_free[s]), (i - 1) & 1, abort_flag, err);
+                for (int e = 0; e < 2; ++e) {
+                    const int c0 = e * p.half;
+                    if (c0 >= columns) break;
+                    if (used[e] > 0)
+                        ok = ok && cache_wait<kSleepShort>(smem_u32(&ms.s_free[s][e]), (used[e] + 1) & 1, abort_flag, err);
                     if (!ok) break;
+                    ++used[e];
                     tc_fence_after();
-                    const uint32_t a0 = tmem + ((n & 1) * 2 + s) * S::kKCols;
-#pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk)
-                        mma_ts_warp(tmem + kTmemS + s * 128, a0 + kk * 8,
-                                    b0 + (((kk >> 2) * S::kHalf + (kk & 3) * 32) >> 4), hi, idesc, kk > 0);
-                    mma_commit_warp(smem_u32(&ms.s_full[s]));
+                    issue_half<kD>(t_s + e * 64, a0, lo_q + ((st * S::kTile + c0 * 128) >> 4), hi,
+                                   idesc_bf16_f32(128, (min(columns - c0, p.half) + 15) & ~15, 0, 0),
+                                   smem_u32(&ms.s_full[s][e]));
                 }
-                if (!ok) break;
-                mma_commit_warp(smem_u32(&ms.q_empty[st]));
+                if (ok && !p.resident) commit_one(smem_u32(&ms.q_empty[st]));
             }
             if (!ok) break;
-            mma_commit_warp(smem_u32(&ms.k_empty[n & 1]));
-            ++n;
+            commit_one(smem_u32(&ms.k_empty[s][n & 1]));
         }
-        mma_commit_warp(smem_u32(&ms.drain));
-        if (lane == 0) mbar_wait_drain_1(smem_u32(&ms.drain), 0, err, kCacheWaitNs);
+        commit_one(smem_u32(&ms.drain[s]));
+        if (lane == 0) mbar_wait_drain_1(smem_u32(&ms.drain[s]), 0, err, kCacheWaitNs);
     } else if (warp == 2) {
-        // ============================================================= pages
+        // ===================================================== units and pages
         if (blockIdx.x == 0)  // lengths out of range are noted once
             for (int b = lane; b < c.B; b += 32) cache_len(c, b, true);
-        uint32_t g = 0;  // pages so far
+        UnitWalk walk;
+        walk.begin(p);
+        uint32_t g = 0, n = 0;  // pages, units so far
         bool ok = true;
-        while (ok && walk.next(p, u)) {
-            if (u.count(p) == 0) continue;
-            int id = -1;
-            const int page0 = u.first / kPageTokens;
-            if (lane < kPages && (page0 + lane) * kPageTokens < u.kv) {
-                id = c.table[(size_t)u.b * c.width + page0 + lane];
-                if (id < 0 || id >= c.pages) {
-                    atomicOr(err, VSA_DEVERR_INDEX);
-                    id = -1;
-                }
+        Unit u;
+        int id = -1;
+        bool more = walk.next(p, u, id);
+        for (; ok && more; ++n) {
+            if (id != -1 && (id < 0 || id >= c.pages)) id = -2;
+            const bool there = lane < kPages && (long long)(u.first + lane * kPageTokens) < u.kv;
+            if (there && id < 0) atomicOr(err, VSA_DEVERR_INDEX);
+            const int page_id = there && id >= 0 ? id : -1;
+            u.held = (int)__ballot_sync(0xffffffffu, page_id >= 0);
+            const int h = u.h;
+            if (n >= kUnits)
+                ok = cache_wait<kSleepShort>(smem_u32(&ms.unit_empty[n % kUnits]), (n / kUnits + 1) & 1, abort_flag, err);
+            if (!ok) break;
+            if (lane == 0) {
+                ms.unit[n % kUnits] = u;
+                mbar_arrive(smem_u32(&ms.unit_full[n % kUnits]));
             }
+            more = walk.next(p, u, id);  // (its page numbers are asked for before this unit's pages)
             for (int i = 0; i < kPages; ++i, ++g) {
-                const int page = __shfl_sync(0xffffffffu, id, i);
-                const int slot = g % kSlots;
+                const int page = __shfl_sync(0xffffffffu, page_id, i);
+                const uint32_t slot = g % kSlots;
                 if (g >= kSlots)
-                    ok = cache_wait<kSleepLong>(smem_u32(&ms.raw_empty[0][slot]), (g / kSlots + 1) & 1, abort_flag, err);
+                    ok = cache_wait<kSleepShort>(smem_u32(&ms.raw_empty[slot]), (g / kSlots + 1) & 1, abort_flag, err);
                 if (!ok) break;
                 if (lane == 0) {
-                    ms.held[(g / kPages) % kHeldUnits][i] = page >= 0;
-                    const uint32_t bar = smem_u32(&ms.raw_full[0][slot]);
+                    const uint32_t bar = smem_u32(&ms.raw_full[slot]);
                     if (page < 0) {
                         mbar_arrive(bar);
                     } else {
                         mbar_arrive_expect_tx(bar, S::kRaw);
                         const uint32_t dst = sbase + S::kOffRaw + slot * S::kRaw;
-                        const unsigned char* src = c.pool + ((size_t)page * c.kv_heads + u.h) * L::kBytes;
+                        const unsigned char* src = c.pool + ((size_t)page * c.kv_heads + h) * L::kBytes;
                         bulk_load(dst, src, S::kCodes, bar);
                         bulk_load(dst + S::kCodes, src + L::kKScale, S::kScales, bar);
                     }
@@ -322,69 +514,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
         }
+        if (ok && n >= kUnits)
+            ok = cache_wait<kSleepShort>(smem_u32(&ms.unit_empty[n % kUnits]), (n / kUnits + 1) & 1, abort_flag, err);
+        if (lane == 0 && ok) {
+            ms.unit[n % kUnits].b = -1;
+            mbar_arrive(smem_u32(&ms.unit_full[n % kUnits]));
+        }
         if (lane == 0)
             for (uint32_t s = 0; s < kSlots && s < g; ++s)
-                mbar_wait_drain_1(smem_u32(&ms.raw_full[0][s]), ((g - 1 - s) / kSlots) & 1, err, kCacheWaitNs);
-    } else if (warp == 3) {
-        // ========================================================= log-sums
-        uint32_t i = 0;
-        bool ok = true;
-        while (ok && walk.next(p, u)) {
-            for (int t = u.t0; t < u.tiles; t += p.cluster, ++i) {
-                const TileRows x = tile_rows_of(p, u, t);
-                float y[4];
-                bool odd = false;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = 32 * k + lane;
-                    y[k] = -INFINITY;
-                    if (r < x.columns) {
-                        const int q = p.splits == 1 ? r / p.w.group : 0;
-                        const int head = u.h * p.w.group + x.head + r - q * p.w.group;
-                        const float l = p.w.lse[((size_t)u.b * p.w.heads + head) * p.w.Sq + x.query + q];
-                        if (fabsf(l) < INFINITY)
-                            y[k] = l * -1.4426950408889634f;
-                        else
-                            odd = true;
-                    }
-                }
-                const int st = i % kNlStages;
-                if (i >= kNlStages) ok = cache_wait<kSleepLong>(smem_u32(&ms.nl_empty[st]), (i / kNlStages + 1) & 1, abort_flag, err);
-                if (!ok) break;
-                odd = __any_sync(0xffffffffu, odd);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) ms.nl[st][32 * k + lane] = y[k];
-                if (lane == 0) ms.odd[st] = odd;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms.nl_full[st]));
-            }
-        }
+                mbar_wait_drain_1(smem_u32(&ms.raw_full[s]), ((g - 1 - s) / kSlots) & 1, err, kCacheWaitNs);
     } else if (warp < 12) {
         // ============================ convert: warps 4..7 the first 128 keys, 8..11 the others
         const int s = (warp - 4) >> 2, quarter = warp & 3;
-        const int key = quarter * 32 + lane;          // of the tile
-        const int page = 2 * s + (key >> 6), slot = key & 63;
+        const int key = quarter * 32 + lane;  // of the tile
+        const int page = 2 * s + (key >> 6), place = key & 63;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-        uint32_t n = 0;
+        uint32_t slot = page, turn = 0;
         bool ok = true;
-        while (ok && walk.next(p, u)) {
-            if (u.count(p) == 0) continue;
+        Unit u;
+        for (uint32_t n = 0; take(n, ok, u); ++n) {
             const int par = n & 1;
-            ok = cache_wait<kSleepShort>(smem_u32(&ms.raw_full[par][page]), (n >> 1) & 1, abort_flag, err);
-            if (ok && n >= 2) ok = cache_wait<kSleepShort>(smem_u32(&ms.k_empty[par]), ((n >> 1) + 1) & 1, abort_flag, err);
+            ok = cache_wait<kSleepShort>(smem_u32(&ms.raw_full[slot]), turn & 1, abort_flag, err);
+            if (ok && n >= 2) ok = cache_wait<kSleepShort>(smem_u32(&ms.k_empty[s][par]), ((n >> 1) + 1) & 1, abort_flag, err);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t raw = sbase + S::kOffRaw + (par * kPages + page) * S::kRaw;
-            const uint32_t codes = raw + slot * L::kRow, scales = raw + S::kCodes + slot * L::kGroups;
+            const uint32_t raw = sbase + S::kOffRaw + slot * S::kRaw;
+            const uint32_t codes = raw + place * L::kRow, scales = raw + S::kCodes + place * L::kGroups;
             const uint32_t to = t_lane + (par * 2 + s) * S::kKCols;
-            uint32_t sc[kD / 64];
-#pragma unroll
-            for (int k = 0; k < kD / 64; ++k) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc[k]) : "r"(scales + 4 * k));
-#pragma unroll
+            // (A short loop: code that runs once a unit costs more to fetch than to run.)
+#pragma unroll 1
             for (int piece = 0; piece < kD / 32; ++piece) {
                 const uint4 x = lds128(codes + piece * 16);
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                const uint32_t two = e4m3_to_f16(sc[piece / 2] >> (16 * (piece & 1)));
+                uint16_t sc;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sc) : "r"(scales + piece * 2));
+                const uint32_t two = e4m3_to_f16(sc);
                 const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
                 uint32_t out[16];
 #pragma unroll
@@ -397,60 +561,71 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st16(to + piece * 16, out);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ms.raw_empty[par][page]));
+            if (lane == 0) mbar_arrive(smem_u32(&ms.raw_empty[slot]));
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ms.k_full[s][par]));
-            ++n;
+            slot += kPages;
+            if (slot >= kSlots) {
+                slot -= kSlots;
+                ++turn;
+            }
         }
-    } else {
-        // ============================ sums: warps 12..15 the first 128 keys, 16..19 the others
-        const int s = (warp - 12) >> 2, quarter = warp & 3;
+    } else if (warp < 28) {
+        // ============================ sums: a warpgroup for each key tile s and buffer e
+        const int s = (warp - 12) >> 3, e = ((warp - 12) >> 2) & 1, quarter = warp & 3;
         const int key = quarter * 32 + lane;
-        const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemS + s * 128;
-        uint32_t i = 0, n = 0;
+        const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemS + s * 128 + e * 64;
+        uint32_t i = 0, used = 0;  // tiles, halves of this group so far
         bool ok = true;
-        while (ok && walk.next(p, u)) {
+        Unit u;
+        for (uint32_t n = 0; take(n, ok, u); ++n) {
             const int x = u.first + s * 128 + key;  // the thread's key
-            const float c2 = p.w.scale_log2 * (c.kv_scale ? c.kv_scale[u.h] : 1.f);
-            const float2 c2v = make_float2(c2, c2);
+            const bool there = (u.held >> (2 * s + (key >> 6))) & 1;
+            const size_t at = ((size_t)u.b * c.kv_heads + u.h) * ((size_t)c.width * kPageTokens) + x;
+            float before = 0.f;
+            if (e == 0 && p.cluster == 1 && p.w.weights && x < u.kv) before = p.w.weights[at];
+            const float2 c2v = make_float2(u.c2, u.c2);
             float total = 0.f;
-            for (int t = u.t0; t < u.tiles; t += p.cluster, ++i) {
-                const TileRows rows = tile_rows_of(p, u, t);
-                const int st = i % kNlStages;
-                // Columns [low, columns) are rows that see the key.
-                int low = 0;
-                if (p.w.causal) {
-                    const int ahead = x - (u.kv - u.fresh) - rows.query;  // queries of the tile before the key
-                    low = ahead <= 0 ? 0 : p.splits > 1 ? 128 : min(ahead, 128) * p.w.group;
+            if (p.resident && u.fresh_rows) ++i;
+            // Columns from `low` on are rows that see the key; of the tile at hand.
+            const int step = p.per * p.w.group * p.cluster;
+            int low = -0x40000000;
+            if (p.w.causal) low = (max(x - (u.kv - u.fresh), 0) - u.t0 * p.per) * p.w.group;
+#pragma unroll 1
+            for (int t = u.t0; t < u.tiles; t += p.cluster, low -= step) {
+                const uint32_t tile = p.resident ? i - 1 : i++;
+                int columns;
+                if (p.splits == 1) {
+                    columns = min(p.per, u.fresh - t * p.per) * p.w.group;
+                } else {
+                    const TileRows rows = tile_rows_of(p, u, t);
+                    columns = rows.columns;
+                    if (p.w.causal) low = x - (u.kv - u.fresh) > rows.query ? 128 : 0;
                 }
-                ok = cache_wait<kSleepShort>(smem_u32(&ms.nl_full[st]), (i / kNlStages) & 1, abort_flag, err) &&
-                     cache_wait<kSleepShort>(smem_u32(&ms.s_full[s]), i & 1, abort_flag, err);
+                const int c0 = e * p.half, end = min(c0 + p.half, columns);
+                if (c0 >= end) continue;
+                ok = cache_wait<kSleepShort>(smem_u32(&ms.s_full[s][e]), used++ & 1, abort_flag, err);
                 if (!ok) break;
                 tc_fence_after();
-                const bool odd = *reinterpret_cast<volatile int*>(&ms.odd[st]);
+                const float* nls = ms.nl[tile % kNlStages];
+                const bool odd = *reinterpret_cast<volatile int*>(&ms.odd[tile % kNlStages]);
+                const bool plain = !odd && end == c0 + p.half && !__any_sync(0xffffffffu, low > c0);
                 float2 a = make_float2(0.f, 0.f), b = make_float2(0.f, 0.f);
 #pragma unroll 1
-                for (int c0 = 0; c0 < rows.columns; c0 += 32) {
+                for (int c1 = c0; c1 < end; c1 += 32) {
                     uint32_t v[32];
-                    tmem_ld32(t_s + c0, v);
-                    const float4* nl = reinterpret_cast<const float4*>(&ms.nl[st][c0]);
+                    tmem_ld32(t_s + c1 - c0, v);
+                    const float4* nl = reinterpret_cast<const float4*>(&nls[c1]);
                     tmem_wait_ld();
-                    if (__any_sync(0xffffffffu, low > c0) || odd || c0 + 32 > rows.columns) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 l = nl[k / 4];
-                            const float ls[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int col = c0 + k + j;
-                                const bool sees = col >= low && col < rows.columns && ls[j] > -INFINITY;
-                                const float y = ex2_approx(fmaf(__uint_as_float(v[k + j]), c2, ls[j]));
-                                a.x += sees ? y : 0.f;
-                            }
-                        }
-                    } else {
+                    if (c1 + 32 >= end) {
+                        // All of S is in registers: its columns may take the next tile's.
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&ms.s_free[s][e]));
+                    }
+                    if (plain) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
                             const float4 l = nl[k / 4];
@@ -461,27 +636,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                             a = __fadd2_rn(a, make_float2(ex2_approx(e0.x), ex2_approx(e0.y)));
                             b = __fadd2_rn(b, make_float2(ex2_approx(e1.x), ex2_approx(e1.y)));
                         }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 l = nl[k / 4];
+                            const float ls[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int col = c1 + k + q;
+                                const bool sees = col >= low && col < columns && ls[q] > -INFINITY;
+                                const float y = ex2_approx(fmaf(__uint_as_float(v[k + q]), u.c2, ls[q]));
+                                a.x += sees ? y : 0.f;
+                            }
+                        }
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&ms.s_free[s]));
-                    mbar_arrive(smem_u32(&ms.nl_empty[st]));
                 }
                 total += (a.x + a.y) + (b.x + b.y);
             }
             if (!ok) break;
-            if (u.count(p) > 0) {  // (a page that is not there has no weight)
-                if (!*reinterpret_cast<volatile int*>(&ms.held[n % kHeldUnits][2 * s + (key >> 6)])) total = 0.f;
-                ++n;
+            // The two halves' shares.
+            float* part = &ms.part[n & 1][s * 128 + key];
+            const uint32_t part_full = smem_u32(&ms.part_full[s][n & 1]), part_empty = smem_u32(&ms.part_empty[s][n & 1]);
+            if (e == 1) {
+                if (n >= 2) ok = cache_wait<kSleepShort>(part_empty, ((n >> 1) + 1) & 1, abort_flag, err);
+                if (!ok) break;
+                *part = total;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(part_full);
+                continue;
             }
-            if (p.cluster > 1) {
+            ok = cache_wait<kSleepShort>(part_full, (n >> 1) & 1, abort_flag, err);
+            if (!ok) break;
+            total += *part;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(part_empty);
+            if (!there) total = 0.f;  // (a page that is not there has no weight)
+            if (p.cluster > 1)
                 ms.sums[s * 128 + key] = total;
-            } else if (x < u.kv) {
-                const size_t at = ((size_t)u.b * c.kv_heads + u.h) * ((size_t)c.width * kPageTokens) + x;
-                p.w.out[at] = (p.w.weights ? p.w.weights[at] : 0.f) + total;
-            }
+            else if (x < u.kv)
+                p.w.out[at] = before + total;
         }
     }
 
@@ -492,10 +685,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
     if (p.cluster > 1) {
         // The cluster's one unit: its CTAs' sums in the order of their ranks, a share of the keys each.
+        UnitWalk walk;
         walk.begin(p);
-        const bool has = walk.next(p, u);
+        walk.rank = 0;
+        Unit u;
+        int id;
+        const bool has = walk.next(p, u, id);
+        const int rank = blockIdx.x % p.cluster;
         asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-        const int each = kKeys / p.cluster, key = walk.rank * each + (int)threadIdx.x;
+        const int each = kKeys / p.cluster, key = rank * each + (int)threadIdx.x;
         if (has && (int)threadIdx.x < each && u.first + key < u.kv && !*abort_flag) {
             float total = 0.f;
             for (int r = 0; r < p.cluster; ++r) {
@@ -510,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     }
-    fill_rest(p.w);
+    fill_rest(p.w, true);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -582,6 +780,9 @@ cudaError_t launch_weigh_chunk(const WeighParams& w, int D, int num_sms, cudaStr
     const long long tiles = p.splits == 1 ? (w.Sq + p.per - 1) / p.per : (long long)w.Sq * p.splits;
     p.cluster = 1;
     while (p.cluster < 8 && 2 * p.cluster * most <= num_sms && 2 * p.cluster <= tiles) p.cluster *= 2;
+    p.resident = tiles == 1;
+    const int columns = std::min<long long>(tiles == 1 ? (long long)w.Sq * w.group : 128, 128);
+    p.half = columns > 64 ? 64 : 32;
     const int grid = p.cluster > 1 ? (int)most * p.cluster : (int)std::min<long long>(num_sms, most);
     return D == 64 ? launch<64>(p, grid, stream) : launch<128>(p, grid, stream);
 }
