@@ -47,7 +47,7 @@ constexpr int kKeys = 256, kPages = kKeys / kPageTokens;
 constexpr int kNlStages = 8;
 constexpr int kUnits = 16;                       // described at a time
 constexpr int kReaders = kThreads / 32 - 1;      // warps that read the descriptions
-constexpr uint32_t kSlots = 24;  // pages on their way or being converted: six units
+constexpr uint32_t kRaw = 6;     // units whose pages are on their way or being converted
 constexpr int kTmemS = 256;
 
 template <int kD>
@@ -56,9 +56,9 @@ struct Sm {
     static constexpr int kTile = kHalf * (kD / 64);
     static constexpr int kStages = 3;                     // of queries
     static constexpr int kCodes = kPageTokens * kD / 2, kScales = kPageTokens * kD / 16;
-    static constexpr int kRaw = kCodes + kScales;
-    static constexpr int kOffRaw = kStages * kTile;       // [slot]
-    static constexpr int kOffMisc = kOffRaw + (int)kSlots * kRaw;
+    static constexpr int kPage = kCodes + kScales;        // K of a page
+    static constexpr int kOffRaw = kStages * kTile;       // [unit][page]
+    static constexpr int kOffMisc = kOffRaw + (int)kRaw * kPages * kPage;
     static constexpr int kKCols = kD / 2;                 // TMEM columns of a key tile
 };
 
@@ -73,7 +73,7 @@ struct alignas(16) Unit {
 
 struct __align__(16) Misc {
     uint64_t q_full[3], q_empty[3];
-    uint64_t raw_full[kSlots], raw_empty[kSlots];
+    uint64_t raw_full[kRaw][2], raw_empty[kRaw];  // [unit][key tile]
     uint64_t k_full[2][2], k_empty[2][2];  // [key tile][unit parity]
     uint64_t s_full[2][2], s_free[2][2];  // [key tile][buffer]
     uint64_t unit_full[kUnits], unit_empty[kUnits];
@@ -310,9 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ms.q_full[s]), 2);  // queries, log-sums
             mbar_init(smem_u32(&ms.q_empty[s]), 2);
         }
-        for (int s = 0; s < (int)kSlots; ++s) {
-            mbar_init(smem_u32(&ms.raw_full[s]), 1);
-            mbar_init(smem_u32(&ms.raw_empty[s]), 2);
+        for (int s = 0; s < (int)kRaw; ++s) {
+            mbar_init(smem_u32(&ms.raw_full[s][0]), 1);
+            mbar_init(smem_u32(&ms.raw_full[s][1]), 1);
+            mbar_init(smem_u32(&ms.raw_empty[s]), 8);
         }
         for (int s = 0; s < 2; ++s) {
             for (int i = 0; i < 2; ++i) {
@@ -361,6 +362,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // column without a row is marked.
         constexpr uint32_t kNoRow = 0x7FFFDEADu;
         const int box_rows = p.splits == 1 ? p.per * p.w.group : 128;
+        int off[4];  // of the lane's columns from the tile's first log-sum on
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = 32 * k + lane, q = p.splits == 1 ? r / p.w.group : 0;
+            off[k] = min(r - q * p.w.group, p.w.group) * p.w.Sq + q;  // (below 2^25: the rows of a kv head are below 2^24)
+        }
         uint32_t i = 0;  // tiles so far
         bool ok = true;
         auto finish = [&](uint32_t tile) {  // whose log-sums have landed
@@ -400,11 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 const float* lse = p.w.lse + ((size_t)u.b * p.w.heads + u.h * p.w.group + x.head) * p.w.Sq + x.query;
                 float* nl = ms.nl[i % kNlStages];
-#pragma unroll 1
-                for (int r = lane; r < 128; r += 32) {
-                    const int q = p.splits == 1 ? r / p.w.group : 0, head = r - q * p.w.group;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 32 * k + lane;
                     if (r < x.columns)
-                        cp_async4(smem_u32(&nl[r]), lse + (size_t)head * p.w.Sq + q);
+                        cp_async4(smem_u32(&nl[r]), lse + off[k]);
                     else
                         nl[r] = __uint_as_float(kNoRow);
                 }
@@ -473,18 +480,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = lane; b < c.B; b += 32) cache_len(c, b, true);
         UnitWalk walk;
         walk.begin(p);
-        uint32_t g = 0, n = 0;  // pages, units so far
+        uint32_t n = 0;  // units so far
         bool ok = true;
         Unit u;
         int id = -1;
         bool more = walk.next(p, u, id);
         for (; ok && more; ++n) {
-            if (id != -1 && (id < 0 || id >= c.pages)) id = -2;
             const bool there = lane < kPages && (long long)(u.first + lane * kPageTokens) < u.kv;
-            if (there && id < 0) atomicOr(err, VSA_DEVERR_INDEX);
-            const int page_id = there && id >= 0 ? id : -1;
-            u.held = (int)__ballot_sync(0xffffffffu, page_id >= 0);
-            const int h = u.h;
+            if (there && (id < 0 || id >= c.pages)) {
+                atomicOr(err, VSA_DEVERR_INDEX);
+                id = -1;
+            }
+            u.held = (int)__ballot_sync(0xffffffffu, there && id >= 0);
+            const int h = u.h, held = u.held, ids = id;
+            const uint32_t raw = n % kRaw;
             if (n >= kUnits)
                 ok = cache_wait<kSleepShort>(smem_u32(&ms.unit_empty[n % kUnits]), (n / kUnits + 1) & 1, abort_flag, err);
             if (!ok) break;
@@ -493,52 +502,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(&ms.unit_full[n % kUnits]));
             }
             more = walk.next(p, u, id);  // (its page numbers are asked for before this unit's pages)
-            for (int i = 0; i < kPages; ++i, ++g) {
-                const int page = __shfl_sync(0xffffffffu, page_id, i);
-                const uint32_t slot = g % kSlots;
-                if (g >= kSlots)
-                    ok = cache_wait<kSleepShort>(smem_u32(&ms.raw_empty[slot]), (g / kSlots + 1) & 1, abort_flag, err);
-                if (!ok) break;
-                if (lane == 0) {
-                    const uint32_t bar = smem_u32(&ms.raw_full[slot]);
-                    if (page < 0) {
-                        mbar_arrive(bar);
-                    } else {
-                        mbar_arrive_expect_tx(bar, S::kRaw);
-                        const uint32_t dst = sbase + S::kOffRaw + slot * S::kRaw;
-                        const unsigned char* src = c.pool + ((size_t)page * c.kv_heads + h) * L::kBytes;
-                        bulk_load(dst, src, S::kCodes, bar);
-                        bulk_load(dst + S::kCodes, src + L::kKScale, S::kScales, bar);
-                    }
-                }
-                __syncwarp();
+            if (n >= kRaw)
+                ok = cache_wait<kSleepShort>(smem_u32(&ms.raw_empty[raw]), (n / kRaw + 1) & 1, abort_flag, err);
+            if (!ok) break;
+            // Lanes 0 and 1 announce the bytes of a key tile's two pages; lane 2 i copies
+            // page i's codes, lane 2 i + 1 its scales.
+            if (lane < 2) mbar_arrive_expect_tx(smem_u32(&ms.raw_full[raw][lane]), S::kPage * __popc((held >> (2 * lane)) & 3));
+            __syncwarp();
+            const int page = __shfl_sync(0xffffffffu, ids, (lane >> 1) % kPages);
+            if (lane < 2 * kPages && ((held >> (lane >> 1)) & 1)) {
+                const uint32_t dst = sbase + S::kOffRaw + (raw * kPages + (lane >> 1)) * S::kPage;
+                const unsigned char* src = c.pool + ((size_t)page * c.kv_heads + h) * L::kBytes;
+                const uint32_t bar = smem_u32(&ms.raw_full[raw][lane >> 2]);
+                if (lane & 1)
+                    bulk_load(dst + S::kCodes, src + L::kKScale, S::kScales, bar);
+                else
+                    bulk_load(dst, src, S::kCodes, bar);
             }
+            __syncwarp();
         }
+        const uint32_t asked = n;  // (a unit that a wait cut short has none asked for)
         if (ok && n >= kUnits)
             ok = cache_wait<kSleepShort>(smem_u32(&ms.unit_empty[n % kUnits]), (n / kUnits + 1) & 1, abort_flag, err);
         if (lane == 0 && ok) {
             ms.unit[n % kUnits].b = -1;
             mbar_arrive(smem_u32(&ms.unit_full[n % kUnits]));
         }
-        if (lane == 0)
-            for (uint32_t s = 0; s < kSlots && s < g; ++s)
-                mbar_wait_drain_1(smem_u32(&ms.raw_full[s]), ((g - 1 - s) / kSlots) & 1, err, kCacheWaitNs);
+        if (lane < 2)
+            for (uint32_t s = 0; s < kRaw && s < asked; ++s)
+                mbar_wait_drain_1(smem_u32(&ms.raw_full[s][lane]), ((asked - 1 - s) / kRaw) & 1, err, kCacheWaitNs);
     } else if (warp < 12) {
         // ============================ convert: warps 4..7 the first 128 keys, 8..11 the others
         const int s = (warp - 4) >> 2, quarter = warp & 3;
         const int key = quarter * 32 + lane;  // of the tile
         const int page = 2 * s + (key >> 6), place = key & 63;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-        uint32_t slot = page, turn = 0;
+        uint32_t slot = 0, turn = 0;
         bool ok = true;
         Unit u;
         for (uint32_t n = 0; take(n, ok, u); ++n) {
             const int par = n & 1;
-            ok = cache_wait<kSleepShort>(smem_u32(&ms.raw_full[slot]), turn & 1, abort_flag, err);
+            ok = cache_wait<kSleepShort>(smem_u32(&ms.raw_full[slot][s]), turn & 1, abort_flag, err);
             if (ok && n >= 2) ok = cache_wait<kSleepShort>(smem_u32(&ms.k_empty[s][par]), ((n >> 1) + 1) & 1, abort_flag, err);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t raw = sbase + S::kOffRaw + slot * S::kRaw;
+            const uint32_t raw = sbase + S::kOffRaw + (slot * kPages + page) * S::kPage;
             const uint32_t codes = raw + place * L::kRow, scales = raw + S::kCodes + place * L::kGroups;
             const uint32_t to = t_lane + (par * 2 + s) * S::kKCols;
             // (A short loop: code that runs once a unit costs more to fetch than to run.)
@@ -566,9 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ms.k_full[s][par]));
-            slot += kPages;
-            if (slot >= kSlots) {
-                slot -= kSlots;
+            if (++slot == kRaw) {
+                slot = 0;
                 ++turn;
             }
         }
