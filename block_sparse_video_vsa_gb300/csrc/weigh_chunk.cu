@@ -102,6 +102,7 @@ struct ChunkParams {
     int cluster;   // CTAs that share a unit
     int resident;  // one tile of rows: CTAs take runs of units and keep it for all of a head
     int half;      // columns of a tile that are issued and summed at once
+    int one_half;  // resident rows that fit half a tile: units alternate between the buffers
 };
 
 struct TileRows {
@@ -236,13 +237,13 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 }
 
 // The kD / 16 products of a half: d = a (kD / 2 columns of tensor memory) * b (shared
-// memory, 16 channels 32 bytes apart, 64 channels kHalf), and an arrival on `done` once
-// they and those before have completed.  All lanes call it; one issues, in one branch.
+// memory, 16 channels 32 bytes apart, 64 channels kHalf), and an arrival on `done` (and
+// on `also`, where that is not 0) once they and those before have completed.  All lanes call it; one issues, in one branch.
 #define VSA_MMA "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, "
 #define VSA_NEXT "add.u32 ta, ta, 8;\n\tadd.u64 db, db, 2;\n\t"
 template <int kD>
 __device__ __forceinline__ void issue_half(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
-                                           uint32_t done) {
+                                           uint32_t done, uint32_t also) {
     if constexpr (kD == 128)
         asm volatile(
             "{\n\t.reg .pred one, p;\n\t.reg .b32 ta;\n\t.reg .b64 db;\n\t"
@@ -253,8 +254,10 @@ __device__ __forceinline__ void issue_half(uint32_t d, uint32_t a, uint32_t b_lo
             "add.u64 db, db, 1016;\n\t"  // (the next 64 channels: 1024 from the first of these)
             VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t"
             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t"
             "skip%=:\n\t}" ::"r"(d),
-            "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(done)
+            "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(done), "r"(also)
             : "memory");
     else
         asm volatile(
@@ -264,8 +267,10 @@ __device__ __forceinline__ void issue_half(uint32_t d, uint32_t a, uint32_t b_lo
             "@!one bra skip%=;\n\t" VSA_MMA "p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
             VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t" VSA_NEXT VSA_MMA "p;\n\t"
             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t"
             "skip%=:\n\t}" ::"r"(d),
-            "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(done)
+            "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(done), "r"(also)
             : "memory");
     __syncwarp();
 }
@@ -279,11 +284,40 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
         : "memory");
 }
 
+// cache_wait for a barrier and a phase of each lane's own, where it is `needed`.
+__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, bool needed, volatile int* abort,
+                                           unsigned int* err) {
+    bool there = !needed;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (!there) there = mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, there)) {
+            __syncwarp();  // (what one lane has seen the others may rely on)
+            return true;
+        }
+        __nanosleep(kSleepShort);
+        if (i % 64 != 0) continue;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, now - t0 > kCacheWaitNs)) {
+            *abort = 1;
+            if ((threadIdx.x & 31) == 0) atomicOr(err, VSA_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 // The same number for the compiler, too, all over the warp (which holds it in a
 // uniform register then, as the products' operands have to be).
-__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 
+__device__ __forceinline__ float4 lds_f4(uint32_t at) {
+    float4 x;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
+    return x;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 x;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
@@ -435,42 +469,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t hi = (uint32_t)(smem_desc_sw128(0, 16, 1024) >> 32);
         const uint32_t lo_q = uniform((uint32_t)smem_desc_sw128(sbase, 16, 1024));
         const uint32_t t_k = uniform(tmem) + s * S::kKCols, t_s = uniform(tmem) + kTmemS + s * 128;
-        uint32_t i = 0, used[2] = {0, 0};  // tiles so far, halves so far
+        uint32_t i = 0, used[2] = {0, 0};  // tiles so far, products so far in each buffer
         bool ok = true;
         Unit u;
         for (uint32_t n = 0; take(n, ok, u); ++n) {
-            u.t0 = uniform(u.t0);
-            u.tiles = uniform(u.tiles);
-            u.fresh = uniform(u.fresh);
-            u.fresh_rows = uniform(u.fresh_rows);
             // (A resident tile is the one that was loaded last: it is let go when the next is taken up.)
             if (p.resident && u.fresh_rows && i++ > 0) commit_one(smem_u32(&ms.q_empty[(i - 2) % S::kStages]));
-            ok = cache_wait<kSleepShort>(smem_u32(&ms.k_full[s][n & 1]), (n >> 1) & 1, abort_flag, err);
-            const uint32_t a0 = t_k + (n & 1) * 2 * S::kKCols;
+            const uint32_t a0 = t_k + (n & 1) * 2 * S::kKCols, k_empty = smem_u32(&ms.k_empty[s][n & 1]);
 #pragma unroll 1
-            for (int t = u.t0; t < u.tiles && ok; t += p.cluster) {
+            for (int t = u.t0; t < u.tiles; t += p.cluster) {
                 const uint32_t tile = p.resident ? i - 1 : i++;
                 const uint32_t st = tile % S::kStages;
-                const int columns = tile_rows_of(p, u, t).columns;
-                if (u.fresh_rows)
-                    ok = cache_wait<kSleepShort>(smem_u32(&ms.q_full[st]), (tile / S::kStages) & 1, abort_flag, err);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c0 = e * p.half;
-                    if (c0 >= columns) break;
-                    if (used[e] > 0)
-                        ok = ok && cache_wait<kSleepShort>(smem_u32(&ms.s_free[s][e]), (used[e] + 1) & 1, abort_flag, err);
-                    if (!ok) break;
-                    ++used[e];
-                    tc_fence_after();
-                    issue_half<kD>(t_s + e * 64, a0, lo_q + ((st * S::kTile + c0 * 128) >> 4), hi,
-                                   idesc_bf16_f32(128, (min(columns - c0, p.half) + 15) & ~15, 0, 0),
-                                   smem_u32(&ms.s_full[s][e]));
+                const int columns = p.splits == 1 ? min(p.per, u.fresh - t * p.per) * p.w.group : tile_rows_of(p, u, t).columns;
+                // The halves in both buffers, or (one_half) the tile in the buffer of the unit's parity.
+                const int e0 = p.one_half ? (int)(n & 1) : 0, halves = !p.one_half && columns > p.half ? 2 : 1;
+                const uint32_t q_empty = p.resident ? 0u : smem_u32(&ms.q_empty[st]);
+                const bool last = t + p.cluster >= u.tiles;
+                // Lane by lane, what the first half waits for: the buffer, the unit's K, the tile's rows.
+                {
+                    const uint32_t use = e0 ? used[1] : used[0];
+                    uint32_t bar = smem_u32(&ms.s_free[s][e0]), parity = (use + 1) & 1;
+                    bool needed = use > 0;
+                    if (lane & 1) {
+                        bar = smem_u32(&ms.k_full[s][n & 1]);
+                        parity = (n >> 1) & 1;
+                        needed = t == u.t0;
+                    } else if (lane & 2) {
+                        bar = smem_u32(&ms.q_full[st]);
+                        parity = (tile / S::kStages) & 1;
+                        needed = u.fresh_rows;
+                    }
+                    ok = wait_lanes(bar, parity, needed, abort_flag, err);
                 }
-                if (ok && !p.resident) commit_one(smem_u32(&ms.q_empty[st]));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t b0 = lo_q + ((st * S::kTile) >> 4);
+                issue_half<kD>(t_s + e0 * 64, a0, b0, hi, idesc_bf16_f32(128, (min(columns, p.half) + 15) & ~15, 0, 0),
+                               smem_u32(&ms.s_full[s][e0]), halves == 1 ? q_empty : 0u);
+                if (e0)
+                    ++used[1];
+                else
+                    ++used[0];
+                if (halves == 2) {
+                    if (used[1] > 0)
+                        ok = cache_wait<kSleepShort>(smem_u32(&ms.s_free[s][1]), (used[1] + 1) & 1, abort_flag, err);
+                    if (!ok) break;
+                    ++used[1];
+                    tc_fence_after();
+                    issue_half<kD>(t_s + 64, a0, b0 + (p.half * 128 >> 4), hi,
+                                   idesc_bf16_f32(128, (columns - p.half + 15) & ~15, 0, 0), smem_u32(&ms.s_full[s][1]), q_empty);
+                }
+                if (last) commit_one(k_empty);
             }
             if (!ok) break;
-            commit_one(smem_u32(&ms.k_empty[s][n & 1]));
         }
         commit_one(smem_u32(&ms.drain[s]));
         if (lane == 0) mbar_wait_drain_1(smem_u32(&ms.drain[s]), 0, err, kCacheWaitNs);
@@ -592,17 +643,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool there = (u.held >> (2 * s + (key >> 6))) & 1;
             const size_t at = ((size_t)u.b * c.kv_heads + u.h) * ((size_t)c.width * kPageTokens) + x;
             float before = 0.f;
-            if (e == 0 && p.cluster == 1 && p.w.weights && x < u.kv) before = p.w.weights[at];
+            if ((e == 0 || p.one_half) && p.cluster == 1 && p.w.weights && x < u.kv) before = p.w.weights[at];
+            if (p.one_half && (int)(n & 1) != e) {
+                if (p.resident && u.fresh_rows) ++i;
+                continue;
+            }
             const float2 c2v = make_float2(u.c2, u.c2);
             float total = 0.f;
             if (p.resident && u.fresh_rows) ++i;
+            const int c0 = p.one_half ? 0 : e * p.half;
             // Columns from `low` on are rows that see the key; of the tile at hand.
             const int step = p.per * p.w.group * p.cluster;
             int low = -0x40000000;
             if (p.w.causal) low = (max(x - (u.kv - u.fresh), 0) - u.t0 * p.per) * p.w.group;
 #pragma unroll 1
             for (int t = u.t0; t < u.tiles; t += p.cluster, low -= step) {
-                const uint32_t tile = p.resident ? i - 1 : i++;
+                const uint32_t place = (p.resident ? i - 1 : i++) % kNlStages;
                 int columns;
                 if (p.splits == 1) {
                     columns = min(p.per, u.fresh - t * p.per) * p.w.group;
@@ -611,20 +667,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     columns = rows.columns;
                     if (p.w.causal) low = x - (u.kv - u.fresh) > rows.query ? 128 : 0;
                 }
-                const int c0 = e * p.half, end = min(c0 + p.half, columns);
+                const int end = min(c0 + p.half, columns);
                 if (c0 >= end) continue;
                 ok = cache_wait<kSleepShort>(smem_u32(&ms.s_full[s][e]), used++ & 1, abort_flag, err);
                 if (!ok) break;
                 tc_fence_after();
-                const float* nls = ms.nl[tile % kNlStages];
-                const bool odd = *reinterpret_cast<volatile int*>(&ms.odd[tile % kNlStages]);
+                const bool odd = *reinterpret_cast<volatile int*>(&ms.odd[place]);
                 const bool plain = !odd && end == c0 + p.half && !__any_sync(0xffffffffu, low > c0);
                 float2 a = make_float2(0.f, 0.f), b = make_float2(0.f, 0.f);
 #pragma unroll 1
                 for (int c1 = c0; c1 < end; c1 += 32) {
                     uint32_t v[32];
                     tmem_ld32(t_s + c1 - c0, v);
-                    const float4* nl = reinterpret_cast<const float4*>(&nls[c1]);
+                    const float4* nl = reinterpret_cast<const float4*>(&ms.nl[place][c1]);
                     tmem_wait_ld();
                     if (c1 + 32 >= end) {
                         // All of S is in registers: its columns may take the next tile's.
@@ -662,21 +717,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             // The two halves' shares.
-            float* part = &ms.part[n & 1][s * 128 + key];
-            const uint32_t part_full = smem_u32(&ms.part_full[s][n & 1]), part_empty = smem_u32(&ms.part_empty[s][n & 1]);
-            if (e == 1) {
-                if (n >= 2) ok = cache_wait<kSleepShort>(part_empty, ((n >> 1) + 1) & 1, abort_flag, err);
+            if (!p.one_half) {
+                float* part = &ms.part[n & 1][s * 128 + key];
+                const uint32_t part_full = smem_u32(&ms.part_full[s][n & 1]), part_empty = smem_u32(&ms.part_empty[s][n & 1]);
+                if (e == 1) {
+                    if (n >= 2) ok = cache_wait<kSleepShort>(part_empty, ((n >> 1) + 1) & 1, abort_flag, err);
+                    if (!ok) break;
+                    *part = total;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(part_full);
+                    continue;
+                }
+                ok = cache_wait<kSleepShort>(part_full, (n >> 1) & 1, abort_flag, err);
                 if (!ok) break;
-                *part = total;
+                total += *part;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(part_full);
-                continue;
+                if (lane == 0) mbar_arrive(part_empty);
             }
-            ok = cache_wait<kSleepShort>(part_full, (n >> 1) & 1, abort_flag, err);
-            if (!ok) break;
-            total += *part;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(part_empty);
             if (!there) total = 0.f;  // (a page that is not there has no weight)
             if (p.cluster > 1)
                 ms.sums[s * 128 + key] = total;
@@ -788,8 +845,8 @@ cudaError_t launch_weigh_chunk(const WeighParams& w, int D, int num_sms, cudaStr
     p.cluster = 1;
     while (p.cluster < 8 && 2 * p.cluster * most <= num_sms && 2 * p.cluster <= tiles) p.cluster *= 2;
     p.resident = tiles == 1;
-    const int columns = std::min<long long>(tiles == 1 ? (long long)w.Sq * w.group : 128, 128);
-    p.half = columns > 64 ? 64 : 32;
+    p.half = 64;
+    p.one_half = p.resident && w.Sq * w.group <= p.half;
     const int grid = p.cluster > 1 ? (int)most * p.cluster : (int)std::min<long long>(num_sms, most);
     return D == 64 ? launch<64>(p, grid, stream) : launch<128>(p, grid, stream);
 }
