@@ -313,11 +313,6 @@ __device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, bool n
 // uniform register then, as the products' operands have to be).
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 
-__device__ __forceinline__ float4 lds_f4(uint32_t at) {
-    float4 x;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
-    return x;
-}
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 x;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
