@@ -861,7 +861,7 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
         e = p.tile == 8 ? launch_token<128, 1, 12, 2>(p, stream) : launch_token<128, 2, 8, 3>(p, stream);
     if (e != cudaSuccess || p.whole) return e;
     if (p.grid < 2) return cudaSuccess;
-    const dim3 grid((unsigned)std::min(p.tiles == 1 ? rows : p.tile, 16), (unsigned)(p.grid - 1));
+    const dim3 grid((unsigned)std::min(p.tiles == 1 ? rows : p.tile, 32), (unsigned)(p.grid - 1));
     return launch_early(D == 64 ? combine_kernel<64> : combine_kernel<128>, grid, kJoinWarps * 32, 0, stream, p);
 }
 

@@ -110,11 +110,20 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
     if (want == 0) return;
     // This block's stretch of the middle, in whole warps' worth.
     const int middle = n - p.recent - p.first;
-    const long long per = (long long)((middle - 1) / blocks / 32 + 1) * 32;
+    const long long per = (long long)((middle - 1) / blocks / 128 + 1) * 128;
     const int begin = (int)min((long long)middle, rank * per), size = (int)min((long long)middle, begin + per) - begin;
     const float* w = p.weights + (size_t)row * p.c.width * kPageTokens + p.first + begin;
     const bool held = size <= p.keys;
-    auto key = [&](int i) { return held ? keys[i] : order_key(w[i]); };
+    // Keys i .. i + 3 (i a multiple of 4; those from `size` on are anything).
+    auto keys_at = [&](int i) {
+        if (held) return *reinterpret_cast<const uint4*>(&keys[i]);
+        uint4 k;
+        k.x = order_key(w[i]);
+        k.y = i + 1 < size ? order_key(w[i + 1]) : 0u;
+        k.z = i + 2 < size ? order_key(w[i + 2]) : 0u;
+        k.w = i + 3 < size ? order_key(w[i + 3]) : 0u;
+        return k;
+    };
     if (held) {
         constexpr int kAhead = 8;
         for (int i0 = threadIdx.x; i0 < size; i0 += kAhead * kChooseThreads) {
@@ -135,10 +144,13 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
         for (int i = threadIdx.x; i < kCopies * kBins / 4; i += kChooseThreads)
             reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-#pragma unroll 4
-        for (int i = threadIdx.x; i < size; i += kChooseThreads) {
-            const uint32_t k = key(i);
-            if ((k & mask) == top) atomicAdd(&sm.hist[lane % kCopies][(k >> shift) & (bins - 1)], 1u);
+        unsigned* hist = sm.hist[lane % kCopies];
+        for (int i = 4 * threadIdx.x; i < size; i += 4 * kChooseThreads) {
+            const uint4 k4 = keys_at(i);
+            const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j < size && (k[j] & mask) == top) atomicAdd(&hist[(k[j] >> shift) & (bins - 1)], 1u);
         }
         __syncthreads();
         // Thread t: bins 2 x + 1 and 2 x, x = bins / 2 - 1 - t: from the top down.
@@ -198,13 +210,17 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
         __syncthreads();              // (the next digit writes what was read here)
     }
     // `left` of the places at T are kept, the lowest.  Where each warp's kept places go:
-    const int part = ((size - 1) / kChooseWarps / 32 + 1) * 32;  // of a warp (size > 0 or nothing to do)
+    const int part = ((size - 1) / kChooseWarps / 128 + 1) * 128;  // of a warp (size > 0 or nothing to do)
     const int from = min(size, warp * part), to = min(size, from + part);
     unsigned above = 0u, same = 0u;
-    for (int i = from + lane; i < to; i += 32) {
-        const uint32_t k = key(i) & mask;
-        above += k > top;
-        same += k == top;
+    for (int i = from + 4 * lane; i < to; i += 128) {
+        const uint4 k4 = keys_at(i);
+        const uint32_t k[4] = {k4.x & mask, k4.y & mask, k4.z & mask, k4.w & mask};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            above += i + j < to && k[j] > top;
+            same += i + j < to && k[j] == top;
+        }
     }
     above = __reduce_add_sync(0xffffffffu, above);
     same = __reduce_add_sync(0xffffffffu, same);
@@ -235,20 +251,40 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
         }
         cluster_arrive();  // no block leaves while another reads from it
     }
-    const unsigned below_me = (1u << lane) - 1;
-    for (int i0 = from; i0 < to; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < to ? key(i) & mask : 0u;
-        const unsigned is_above = __ballot_sync(0xffffffffu, i < to && k > top);
-        const unsigned is_same = __ballot_sync(0xffffffffu, i < to && k == top);
-        const unsigned same_here = same + __popc(is_same & below_me);
-        const bool keep = (is_above >> lane & 1u) || ((is_same >> lane & 1u) && same_here < left);
-        if (keep) {
-            const unsigned j = above + __popc(is_above & below_me) + min(same_here, left);
-            kept[p.first + j] = p.first + begin + i;
+    for (int i0 = from; i0 < to; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        uint32_t k[4] = {0u, 0u, 0u, 0u};
+        unsigned live = 0u;  // of this lane's four
+        if (i < to) {
+            const uint4 k4 = keys_at(i);
+            k[0] = k4.x & mask, k[1] = k4.y & mask, k[2] = k4.z & mask, k[3] = k4.w & mask;
+            live = (unsigned)min(4, to - i);
         }
-        above += __popc(is_above);
-        same += __popc(is_same);
+        unsigned mine = 0u;  // above T in the low half, at T in the high one
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if ((unsigned)j < live) mine += k[j] > top ? 1u : k[j] == top ? 0x10000u : 0u;
+        unsigned incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        unsigned a = above + ((incl - mine) & 0xFFFFu), t = same + ((incl - mine) >> 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if ((unsigned)j < live && (k[j] > top || (k[j] == top && t < left))) {
+                kept[p.first + a + min(t, left)] = p.first + begin + i + j;
+                if (k[j] > top)
+                    ++a;
+                else
+                    ++t;
+            } else if ((unsigned)j < live && k[j] == top) {
+                ++t;
+            }
+        const unsigned all_of_them = __shfl_sync(0xffffffffu, incl, 31);
+        above += all_of_them & 0xFFFFu;
+        same += all_of_them >> 16;
     }
     if (blocks > 1) cluster_wait();
 }
@@ -348,14 +384,15 @@ cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, 
     p.recent = recent;
     p.to_width = to_width;
     // Blocks of a row: as many as its keys need shared memory of, and more while the
-    // rows leave SMs idle.
+    // rows leave SMs idle (32760 keys of 40 heads: 23 us with one, 17 with two, 34 with
+    // four, which share SMs).
     const long long places = (long long)c.width * kPageTokens;
     const long long rows = (long long)c.B * c.kv_heads;
     int cluster = 1;
     while (cluster < kMaxCluster &&
            (places > (long long)kHeldKeys * cluster || (2 * rows * cluster <= num_sms && places > 4096LL * cluster)))
         cluster *= 2;
-    const long long stretch = (places + cluster - 1) / cluster + 32;
+    const long long stretch = ((places + cluster - 1) / cluster + 127) / 128 * 128 + 128;
     p.keys = (int)std::min<long long>(stretch, kHeldKeys);
     constexpr int kFixed = (int)sizeof(ChooseSmem);
     static_assert(kFixed % 16 == 0 && kFixed + kHeldKeys * 4 <= 232448, "shared memory of the choosing kernel");

@@ -9,8 +9,8 @@
 // weight is the sum over a token's row of the accumulator, so nothing is joined
 // across warps and each weight has one owner: same bits in every run.
 //  * All warps take equal stretches of the line of half pages (32 tokens) of all
-//    sequences and heads; codes and scales come straight to registers, the next
-//    half page's while this one is worked on.
+//    sequences and heads; codes and scales come straight to registers, the next two
+//    half pages' while this one is worked on.
 //  * A key's 64 (or 32) code bytes are four lanes' loads; the order of channels
 //    within K Q^T is free, so a lane's 32 (16) channels need no shuffle.
 #include "weigh.cuh"
@@ -103,6 +103,57 @@ __global__ void __launch_bounds__(kWeighThreads, 1) weigh_kernel(WeighParams p) 
             const float k_head = c.kv_scale ? c.kv_scale[h] : 1.f;
             const float* in = p.weights ? p.weights + ((size_t)b * c.kv_heads + h) * row_places : nullptr;
             float* out = p.out + ((size_t)b * c.kv_heads + h) * row_places;
+            // Places in the pool of the 32 pages from page0 on.
+            int page0 = u >> 1, id = -1;
+            auto look_up = [&]() {
+                id = -1;
+                if (page0 + lane < (end + 1) >> 1) {
+                    id = c.table[(size_t)b * c.width + page0 + lane];
+                    if (id < 0 || id >= c.pages) {
+                        atomicOr(c.err, VSA_DEVERR_INDEX);
+                        id = -1;
+                    }
+                }
+            };
+            look_up();
+            auto load = [&](int unit, KUnit<kD>& k) {
+                if ((unit >> 1) - page0 == 32) {
+                    page0 += 32;
+                    look_up();
+                }
+                const int page = __shfl_sync(0xffffffffu, id, (unit >> 1) - page0);
+                const unsigned char* base = c.pool + ((size_t)max(page, 0) * c.kv_heads + h) * L::kBytes;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int tok = (unit & 1) * kUnit + 16 * m + 8 * half + g;
+                        const unsigned char* src = base + tok * L::kRow + t * (kWords * 4);
+                        const unsigned char* sc = base + L::kKScale + tok * L::kGroups + t * (kWords / 2);
+                        if constexpr (kWords == 4) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(src);
+                            k.codes[m][half][0] = x.x; k.codes[m][half][1] = x.y;
+                            k.codes[m][half][2] = x.z; k.codes[m][half][3] = x.w;
+                            k.scales[m][half] = *reinterpret_cast<const uint16_t*>(sc);
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2*>(src);
+                            k.codes[m][half][0] = x.x; k.codes[m][half][1] = x.y;
+                            k.scales[m][half] = (uint32_t)*sc * 0x101u;
+                        }
+                    }
+                const int x = unit * kUnit + 16 * (t >> 1) + 8 * (t & 1) + g;
+                k.before = in ? in[x] : 0.f;
+                return page >= 0;
+            };
+            // The first keys are on their way before the rows are looked at.
+            constexpr int kAhead = kNT == 1 ? 2 : 1;  // half pages on their way (two rows' registers leave room for one)
+            KUnit<kD> next[kAhead];
+            bool there_next[kAhead];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                there_next[a] = false;
+                if (u + a < end) there_next[a] = load(u + a, next[a]);
+            }
             // The rows as the matrix instruction's columns.
             uint32_t qf[kNT][2 * kWords][2];
             float scale[kNT][2], off[kNT][2];  // logit = s scale - off (log2 units) of rows nt * 8 + 2 t + i
@@ -148,55 +199,16 @@ __global__ void __launch_bounds__(kWeighThreads, 1) weigh_kernel(WeighParams p) 
             }
             min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 1));
             min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 2));
-            // Places in the pool of the 32 pages from page0 on.
-            int page0 = u >> 1, id = -1;
-            auto look_up = [&]() {
-                id = -1;
-                if (page0 + lane < (end + 1) >> 1) {
-                    id = c.table[(size_t)b * c.width + page0 + lane];
-                    if (id < 0 || id >= c.pages) {
-                        atomicOr(c.err, VSA_DEVERR_INDEX);
-                        id = -1;
-                    }
-                }
-            };
-            look_up();
-            auto load = [&](int unit, KUnit<kD>& k) {
-                if ((unit >> 1) - page0 == 32) {
-                    page0 += 32;
-                    look_up();
-                }
-                const int page = __shfl_sync(0xffffffffu, id, (unit >> 1) - page0);
-                const unsigned char* base = c.pool + ((size_t)max(page, 0) * c.kv_heads + h) * L::kBytes;
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int tok = (unit & 1) * kUnit + 16 * m + 8 * half + g;
-                        const unsigned char* src = base + tok * L::kRow + t * (kWords * 4);
-                        const unsigned char* sc = base + L::kKScale + tok * L::kGroups + t * (kWords / 2);
-                        if constexpr (kWords == 4) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(src);
-                            k.codes[m][half][0] = x.x; k.codes[m][half][1] = x.y;
-                            k.codes[m][half][2] = x.z; k.codes[m][half][3] = x.w;
-                            k.scales[m][half] = *reinterpret_cast<const uint16_t*>(sc);
-                        } else {
-                            const uint2 x = *reinterpret_cast<const uint2*>(src);
-                            k.codes[m][half][0] = x.x; k.codes[m][half][1] = x.y;
-                            k.scales[m][half] = (uint32_t)*sc * 0x101u;
-                        }
-                    }
-                const int x = unit * kUnit + 16 * (t >> 1) + 8 * (t & 1) + g;
-                k.before = in ? in[x] : 0.f;
-                return page >= 0;
-            };
-            KUnit<kD> next;
-            bool next_there = load(u, next);
 #pragma unroll 1
             for (; u < end; ++u) {
-                const KUnit<kD> k = next;
-                const bool there = next_there;
-                if (u + 1 < end) next_there = load(u + 1, next);
+                const KUnit<kD> k = next[0];
+                const bool there = there_next[0];
+#pragma unroll
+                for (int a = 0; a + 1 < kAhead; ++a) {
+                    next[a] = next[a + 1];
+                    there_next[a] = there_next[a + 1];
+                }
+                if (u + kAhead < end) there_next[kAhead - 1] = load(u + kAhead, next[kAhead - 1]);
                 float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
                 if (there && rows > 0) {
                     float s[2][kNT][4];
