@@ -4,7 +4,7 @@
 // with the rows' log-sum-exp from the attention call.  Only K is read: 9/16 D bytes
 // a key and head, 2 D flops and an exponential for each row.
 //
-// Few rows a kv head (up to 16): HBM bound, K Q^T by mma.sync m16n8k16 (fp16 in,
+// Few rows a kv head (up to 24, or 32 of 64 channels): HBM bound, K Q^T by mma.sync m16n8k16 (fp16 in,
 // fp32 out) with tokens on the 16-row side, as in token_kernel (cache_attn.cu); a
 // weight is the sum over a token's row of the accumulator, so nothing is joined
 // across warps and each weight has one owner: same bits in every run.
@@ -26,7 +26,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int kWeighThreads = 512, kWeighWarps = kWeighThreads / 32;
 constexpr int kUnit = 32;  // tokens
 
 // Half pages of sequence b.
@@ -69,8 +68,8 @@ struct KUnit {
     float before;  // the weight of token 16 (t / 2) + 8 (t % 2) + g so far
 };
 
-template <int kD, int kNT>
-__global__ void __launch_bounds__(kWeighThreads, 1) weigh_kernel(WeighParams p) {
+template <int kD, int kNT, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
     using L = PageLayout<kD>;
     constexpr int kWords = kD / 32;
     early();
@@ -81,7 +80,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) weigh_kernel(WeighParams p) 
     if (blockIdx.x == 0 && warp == 0)  // lengths out of range are noted once
         for (int b = lane; b < c.B; b += 32) cache_len(c, b, true);
     const long long total = line_length(c);
-    const long long parts = (long long)gridDim.x * kWeighWarps, part = (long long)warp * gridDim.x + blockIdx.x;
+    const long long parts = (long long)gridDim.x * kWarps, part = (long long)warp * gridDim.x + blockIdx.x;
     long long left = total / parts + (part < total % parts ? 1 : 0);
     const size_t row_places = (size_t)c.width * kPageTokens;
     if (left > 0) {
@@ -289,11 +288,25 @@ cudaError_t launch_cache_weigh(const CacheView& c, int D, const void* q, const f
     p.causal = causal;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     const int rows = Sq * p.group;
-    if (rows > 16) return launch_weigh_chunk(p, D, num_sms, stream);
+    // weigh_kernel with as many row tiles of 8 as there are, or the chunk kernel.  Times
+    // in us of weigh_kernel | the chunk kernel, 8 kv heads (more rows than these: the
+    // registers for the queries leave too few warps):
+    //   rows of a kv head           20           32
+    //   D = 128,  1 x 32760     13.4 | 16.4  18.1 | 16.7
+    //             8 x 8000      19.5 | 26.0  28.2 | 26.0
+    //   D = 64,   1 x 32760     11.4 | 15.3  13.1 | 15.3
+    //             8 x 8000      15.7 | 24.4  18.7 | 24.4
+    if (rows > (D == 64 ? 32 : 24)) return launch_weigh_chunk(p, D, num_sms, stream);
     const dim3 grid((unsigned)num_sms);
-    auto kernel = D == 64 ? (rows <= 8 ? weigh_kernel<64, 1> : weigh_kernel<64, 2>)
-                          : (rows <= 8 ? weigh_kernel<128, 1> : weigh_kernel<128, 2>);
-    return launch_early(kernel, grid, kWeighThreads, 0, stream, p);
+    const auto few = [&](auto kernel, int warps) { return launch_early(kernel, grid, warps * 32, 0, stream, p); };
+    if (D == 64)
+        return rows <= 8    ? few(weigh_kernel<64, 1, 16>, 16)
+               : rows <= 16 ? few(weigh_kernel<64, 2, 16>, 16)
+               : rows <= 24 ? few(weigh_kernel<64, 3, 12>, 12)
+                            : few(weigh_kernel<64, 4, 12>, 12);
+    return rows <= 8    ? few(weigh_kernel<128, 1, 16>, 16)
+           : rows <= 16 ? few(weigh_kernel<128, 2, 16>, 16)
+                        : few(weigh_kernel<128, 3, 12>, 12);
 }
 
 }  // namespace vsa

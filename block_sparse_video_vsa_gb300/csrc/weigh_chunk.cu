@@ -363,6 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
     }
     if (threadIdx.x < kKeys) ms.sums[threadIdx.x] = 0.f;
+    // Rows of the query tiles that no load fills are zeros.
+    for (int i = threadIdx.x; i < S::kStages * S::kTile / 16; i += kThreads)
+        reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
     if (warp == 1) {
         tmem_alloc(smem_u32(&ms.tmem_base), 512);
         tmem_relinquish();
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t b0 = lo_q + ((st * S::kTile) >> 4);
-                issue_half<kD>(t_s + e0 * 64, a0, b0, hi, idesc_bf16_f32(128, (min(columns, p.half) + 15) & ~15, 0, 0),
+                issue_half<kD>(t_s + e0 * 64, a0, b0, hi, idesc_bf16_f32(128, (min(columns, p.half) + 31) & ~31, 0, 0),
                                smem_u32(&ms.s_full[s][e0]), halves == 1 ? q_empty : 0u);
                 if (e0)
                     ++used[1];
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++used[1];
                     tc_fence_after();
                     issue_half<kD>(t_s + 64, a0, b0 + (p.half * 128 >> 4), hi,
-                                   idesc_bf16_f32(128, (columns - p.half + 15) & ~15, 0, 0), smem_u32(&ms.s_full[s][1]), q_empty);
+                                   idesc_bf16_f32(128, (columns - p.half + 31) & ~31, 0, 0), smem_u32(&ms.s_full[s][1]), q_empty);
                 }
                 if (last) commit_one(k_empty);
             }
@@ -668,7 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const bool odd = *reinterpret_cast<volatile int*>(&ms.odd[place]);
-                const bool plain = !odd && end == c0 + p.half && !__any_sync(0xffffffffu, low > c0);
+                // (Columns past the last row are products with zeros where the queries end with
+                // the tensor, and weigh 2^-infinity; else they may be products with anything.)
+                const bool plain = !odd && (end == c0 + p.half || u.fresh == p.w.Sq) && !__any_sync(0xffffffffu, low > c0);
                 float2 a = make_float2(0.f, 0.f), b = make_float2(0.f, 0.f);
 #pragma unroll 1
                 for (int c1 = c0; c1 < end; c1 += 32) {
