@@ -24,7 +24,7 @@ namespace vsa {
 
 namespace {
 
-constexpr int kChooseThreads = 1024, kChooseWarps = kChooseThreads / 32, kMaxCluster = 8;
+constexpr int kMaxCluster = 8;
 constexpr int kDigits = 3;
 constexpr int kBins = 2048;
 constexpr int kCopies = 4;            // of a histogram: neighbouring lanes add to different ones
@@ -69,6 +69,15 @@ __device__ __forceinline__ uint2 load2_from_rank(const void* p, uint32_t rank) {
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at_rank(p, rank)) : "memory");
     return x;
 }
+__device__ __forceinline__ unsigned scan_warp32(unsigned x) {  // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned v = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += v;
+    }
+    return x;
+}
 
 // Bit patterns in the order of the numbers: NaN below all, -0 with 0.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -79,14 +88,16 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 
 struct ChooseSmem {
     unsigned int hist[kCopies][kBins];
-    alignas(8) unsigned int total[kDigits][kBins];  // of this block, for the others of the cluster
-    unsigned int warp_sum[kChooseWarps];
-    unsigned int counts[2][kChooseWarps];  // above T, at T: of a warp's stretch
+    alignas(16) unsigned int total[kDigits][kBins];  // of this block, for the others of the cluster
+    unsigned int warp_sum[32];
+    unsigned int counts[2][32];  // above T, at T: of a warp's stretch
     unsigned int totals[2];                // of the block
     unsigned int found, before, there, unused[3];
 };
 
+template <int kChooseThreads>
 __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p) {
+    constexpr int kChooseWarps = kChooseThreads / 32;
     extern __shared__ __align__(16) unsigned char choose_smem[];
     ChooseSmem& sm = *reinterpret_cast<ChooseSmem*>(choose_smem);
     uint32_t* keys = reinterpret_cast<uint32_t*>(choose_smem + sizeof(ChooseSmem));
@@ -138,6 +149,7 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
     // The digits of T; `left` of the places with T's digits so far are still to be found.
     uint32_t top = 0u, mask = 0u;
     unsigned left = (unsigned)want;
+    if (threadIdx.x == 0) sm.found = sm.before = sm.there = 0u;
 #pragma unroll 1
     for (int d = 0; d < kDigits; ++d) {
         const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? 1024 : 2048;
@@ -153,54 +165,62 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
                 if (i + j < size && (k[j] & mask) == top) atomicAdd(&hist[(k[j] >> shift) & (bins - 1)], 1u);
         }
         __syncthreads();
-        // Thread t: bins 2 x + 1 and 2 x, x = bins / 2 - 1 - t: from the top down.
-        const int x = bins / 2 - 1 - (int)threadIdx.x;
-        uint2 bin = make_uint2(0u, 0u);
-        if (x >= 0) {
+        // Thread t: the kPer bins from x on, x = bins - kPer (t + 1): from the top down.
+        constexpr int kPer = kBins / kChooseThreads;
+        const int x = bins - kPer * ((int)threadIdx.x + 1);
+        unsigned bin[kPer], sum = 0u;
 #pragma unroll
-            for (int k = 0; k < kCopies; ++k) {
-                const uint2 y = *reinterpret_cast<const uint2*>(&sm.hist[k][2 * x]);
-                bin.x += y.x;
-                bin.y += y.y;
+        for (int j = 0; j < kPer; j += 2) {
+            uint2 y = make_uint2(0u, 0u);
+            if (x >= 0) {
+#pragma unroll
+                for (int k = 0; k < kCopies; ++k) {
+                    const uint2 z = *reinterpret_cast<const uint2*>(&sm.hist[k][x + j]);
+                    y.x += z.x;
+                    y.y += z.y;
+                }
+                if (blocks > 1) *reinterpret_cast<uint2*>(&sm.total[d][x + j]) = y;
             }
+            bin[j] = y.x;
+            bin[j + 1] = y.y;
         }
         if (blocks > 1) {  // sums over the cluster
-            if (x >= 0) *reinterpret_cast<uint2*>(&sm.total[d][2 * x]) = bin;
             cluster_arrive();
             cluster_wait();
             if (x >= 0) {
-                bin = make_uint2(0u, 0u);
 #pragma unroll
-                for (int r = 0; r < kMaxCluster; ++r) {
-                    if (r >= blocks) break;
-                    const uint2 y = load2_from_rank(&sm.total[d][2 * x], (uint32_t)r);
-                    bin.x += y.x;
-                    bin.y += y.y;
+                for (int j = 0; j < kPer; j += 2) {
+                    uint2 y = make_uint2(0u, 0u);
+#pragma unroll
+                    for (int r = 0; r < kMaxCluster; ++r) {
+                        if (r >= blocks) break;
+                        const uint2 z = load2_from_rank(&sm.total[d][x + j], (uint32_t)r);
+                        y.x += z.x;
+                        y.y += z.y;
+                    }
+                    bin[j] = y.x;
+                    bin[j + 1] = y.y;
                 }
             }
         }
-        const unsigned sum = bin.x + bin.y;
-        unsigned incl = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
+        for (int j = 0; j < kPer; ++j) sum += bin[j];
+        const unsigned incl = scan_warp32(sum);
         if (lane == 31) sm.warp_sum[warp] = incl;
         __syncthreads();
-        const unsigned mine = sm.warp_sum[lane];
-        unsigned base = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned v = __shfl_up_sync(0xffffffffu, base, o);
-            if (lane >= o) base += v;
-        }
-        const unsigned before = __shfl_sync(0xffffffffu, base - mine, warp) + incl - sum;
+        const unsigned of_warp = lane < kChooseWarps ? sm.warp_sum[lane] : 0u;
+        const unsigned base = scan_warp32(of_warp) - of_warp;
+        unsigned before = __shfl_sync(0xffffffffu, base, warp) + incl - sum;
         if (before < left && before + sum >= left) {
-            const bool high = before + bin.y >= left;
-            sm.found = (unsigned)(2 * x + (high ? 1 : 0));
-            sm.before = before + (high ? 0u : bin.y);
-            sm.there = high ? bin.y : bin.x;
+#pragma unroll
+            for (int j = kPer - 1; j >= 0; --j) {
+                if (before < left && before + bin[j] >= left) {
+                    sm.found = (unsigned)(x + j);
+                    sm.before = before;
+                    sm.there = bin[j];
+                }
+                before += bin[j];
+            }
         }
         __syncthreads();
         top |= sm.found << shift;
@@ -229,19 +249,14 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
         sm.counts[1][warp] = same;
     }
     __syncthreads();
-    unsigned above_before = 0u, same_before = 0u;
-    for (int i = 0; i < kChooseWarps; ++i) {
-        if (i == warp) {
-            above = above_before;
-            same = same_before;
-        }
-        above_before += sm.counts[0][i];
-        same_before += sm.counts[1][i];
-    }
+    const unsigned above_of = lane < kChooseWarps ? sm.counts[0][lane] : 0u, same_of = lane < kChooseWarps ? sm.counts[1][lane] : 0u;
+    const unsigned above_to = scan_warp32(above_of), same_to = scan_warp32(same_of);
+    above = __shfl_sync(0xffffffffu, above_to - above_of, warp);
+    same = __shfl_sync(0xffffffffu, same_to - same_of, warp);
     if (blocks > 1) {
-        if (threadIdx.x == 0) {
-            sm.totals[0] = above_before;
-            sm.totals[1] = same_before;
+        if (threadIdx.x == 31) {
+            sm.totals[0] = above_to;
+            sm.totals[1] = same_to;
         }
         cluster_arrive();
         cluster_wait();
@@ -264,17 +279,13 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if ((unsigned)j < live) mine += k[j] > top ? 1u : k[j] == top ? 0x10000u : 0u;
-        unsigned incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
+        const unsigned incl = scan_warp32(mine);
         unsigned a = above + ((incl - mine) & 0xFFFFu), t = same + ((incl - mine) >> 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if ((unsigned)j < live && (k[j] > top || (k[j] == top && t < left))) {
-                kept[p.first + a + min(t, left)] = p.first + begin + i + j;
+                // (Inside the row's list even if somebody else writes the weights meanwhile.)
+                if (a + min(t, left) < (unsigned)want) kept[p.first + a + min(t, left)] = p.first + begin + i + j;
                 if (k[j] > top)
                     ++a;
                 else
@@ -297,10 +308,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictParams p) {
     begin_work();
     const int h = blockIdx.y, b = blockIdx.z, first = blockIdx.x * kPageTokens;
     const size_t row = (size_t)b * p.c.kv_heads + h;
-    const int n = min(cache_len(p.c, b, false), p.budget), size = min(kPageTokens, n - first);
+    const int held = cache_len(p.c, b, false), n = min(held, p.budget), size = min(kPageTokens, n - first);
     if (threadIdx.x < kPageTokens) {
         const int t = threadIdx.x;
-        const int s = t < size ? p.kept[row * p.budget + first + t] : -1;
+        int s = t < size ? p.kept[row * p.budget + first + t] : -1;
+        if (s >= held) s = -1;
         source[t] = s;
         p.moved[row * p.to_width * kPageTokens + first + t] =
             s >= 0 ? p.weights[row * p.c.width * kPageTokens + s] : 0.f;
@@ -332,8 +344,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_within_kernel(EvictParams p
     for (int first = rank * kPageTokens; first - rank * kPageTokens < p.budget; first += step, turn ^= 1) {
         const int size = min(kPageTokens, p.budget - first);
         if ((int)threadIdx.x < size) {
-            source[turn][threadIdx.x] = kept[first + threadIdx.x];
-            weight = w[source[turn][threadIdx.x]];
+            int s = kept[first + threadIdx.x];
+            if (s >= n) s = -1;
+            source[turn][threadIdx.x] = s;
+            weight = s >= 0 ? w[s] : 0.f;
         }
         __syncthreads();
         if (size > 0) take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source[turn], size, x);
@@ -394,13 +408,18 @@ cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, 
         cluster *= 2;
     const long long stretch = ((places + cluster - 1) / cluster + 127) / 128 * 128 + 128;
     p.keys = (int)std::min<long long>(stretch, kHeldKeys);
-    constexpr int kFixed = (int)sizeof(ChooseSmem);
+    // 512 threads where a thread has few keys: 300 places 4.7 us (1024 threads: 5.8), 4000
+    // 6.6 (7.0); 12000 in 192 rows 19.3 alone but 10 us more among other kernels.
+    constexpr int kFixed = (int)sizeof(ChooseSmem), kSmall = 4352;
     static_assert(kFixed % 16 == 0 && kFixed + kHeldKeys * 4 <= 232448, "shared memory of the choosing kernel");
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(choose_kernel, kFixed + kHeldKeys * 4, done);
+    cudaError_t e = allow_smem(choose_kernel<1024>, kFixed + kHeldKeys * 4, done);
     if (e != cudaSuccess) return e;
-    e = launch_clusters(choose_kernel, dim3((unsigned)(rows * cluster)), cluster, kChooseThreads, kFixed + p.keys * 4,
-                        stream, p);
+    static std::atomic<uint64_t> done_small{0};
+    e = allow_smem(choose_kernel<512>, kFixed + kSmall * 4, done_small);
+    if (e != cudaSuccess) return e;
+    e = launch_clusters(p.keys <= kSmall ? choose_kernel<512> : choose_kernel<1024>, dim3((unsigned)(rows * cluster)), cluster,
+                        p.keys <= kSmall ? 512 : 1024, kFixed + p.keys * 4, stream, p);
     if (e != cudaSuccess) return e;
     if (to_table) {
         const dim3 grid((unsigned)to_width, (unsigned)c.kv_heads, (unsigned)c.B);
