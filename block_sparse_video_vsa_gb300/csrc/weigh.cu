@@ -9,8 +9,8 @@
 // weight is the sum over a token's row of the accumulator, so nothing is joined
 // across warps and each weight has one owner: same bits in every run.
 //  * All warps take equal stretches of the line of half pages (32 tokens) of all
-//    sequences and heads; codes and scales come straight to registers, the next two
-//    half pages' while this one is worked on.
+//    sequences and heads; codes and scales come straight to registers, the next
+//    half page's while this one is worked on.
 //  * A key's 64 (or 32) code bytes are four lanes' loads; the order of channels
 //    within K Q^T is free, so a lane's 32 (16) channels need no shuffle.
 #include "weigh.cuh"
@@ -145,14 +145,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
                 return page >= 0;
             };
             // The first keys are on their way before the rows are looked at.
-            constexpr int kAhead = kNT == 1 ? 2 : 1;  // half pages on their way (two rows' registers leave room for one)
-            KUnit<kD> next[kAhead];
-            bool there_next[kAhead];
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                there_next[a] = false;
-                if (u + a < end) there_next[a] = load(u + a, next[a]);
-            }
+            KUnit<kD> ka, kb;  // this half page's and the next one's, in turns
+            bool there_a = load(u, ka), there_b = false;
             // The rows as the matrix instruction's columns.
             uint32_t qf[kNT][2 * kWords][2];
             float scale[kNT][2], off[kNT][2];  // logit = s scale - off (log2 units) of rows nt * 8 + 2 t + i
@@ -198,16 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
             }
             min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 1));
             min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 2));
-#pragma unroll 1
-            for (; u < end; ++u) {
-                const KUnit<kD> k = next[0];
-                const bool there = there_next[0];
-#pragma unroll
-                for (int a = 0; a + 1 < kAhead; ++a) {
-                    next[a] = next[a + 1];
-                    there_next[a] = there_next[a + 1];
-                }
-                if (u + kAhead < end) there_next[kAhead - 1] = load(u + kAhead, next[kAhead - 1]);
+            auto work = [&](const KUnit<kD>& k, bool there) {
                 float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
                 if (there && rows > 0) {
                     float s[2][kNT][4];
@@ -241,18 +226,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
                                             qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
                         }
                     const int key0 = u * kUnit;
-                    const bool masked = key0 + kUnit > min_lim;
+                    if (key0 + kUnit > min_lim) {  // keys past a row's limit
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (key0 + 16 * m + 8 * (i >> 1) + g >= lim[nt][i & 1]) s[m][nt][i] = -INFINITY;
+                    }
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int key = key0 + 16 * m + 8 * (i >> 1) + g;
-                                float x = ex2_approx(fmaf(s[m][nt][i], scale[nt][i & 1], -off[nt][i & 1]));
-                                if (masked && key >= lim[nt][i & 1]) x = 0.f;
-                                sum[m][i >> 1] += x;
-                            }
+                            for (int i = 0; i < 4; ++i)
+                                sum[m][i >> 1] += ex2_approx(fmaf(s[m][nt][i], scale[nt][i & 1], -off[nt][i & 1]));
                 }
                 // Sums over the four lanes of a token; lane t keeps that of (m, half) = (t / 2, t % 2).
                 const bool hi = t & 2, odd = t & 1;
@@ -263,6 +252,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
                 y += __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
                 const int x = u * kUnit + 16 * (t >> 1) + 8 * (t & 1) + g;
                 if (x < kv) out[x] = k.before + y;
+            };
+#pragma unroll 1
+            while (u < end) {
+                if (u + 1 < end) there_b = load(u + 1, kb);
+                work(ka, there_a);
+                if (++u >= end) break;
+                if (u + 1 < end) there_a = load(u + 1, ka);
+                work(kb, there_b);
+                ++u;
             }
             left -= n;
         }
@@ -305,7 +303,7 @@ cudaError_t launch_cache_weigh(const CacheView& c, int D, const void* q, const f
                : rows <= 24 ? few(weigh_kernel<64, 3, 12>, 12)
                             : few(weigh_kernel<64, 4, 12>, 12);
     return rows <= 8    ? few(weigh_kernel<128, 1, 16>, 16)
-           : rows <= 16 ? few(weigh_kernel<128, 2, 16>, 16)
+           : rows <= 16 ? few(weigh_kernel<128, 2, 12>, 12)
                         : few(weigh_kernel<128, 3, 12>, 12);
 }
 
