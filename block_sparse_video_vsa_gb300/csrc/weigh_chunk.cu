@@ -16,7 +16,9 @@
 //    of rows serves two tiles of keys, so that L2 gives 32 KB for some 1000 cycles.
 //  * Rows that fit one tile (a window of recent queries) stay in shared memory for
 //    all units of their head: the CTAs take runs of neighbouring units then, and
-//    pages are all that moves.  Else units are dealt to the CTAs in turn, which
+//    pages are all that moves.  Converting K is then most of the work, and 2.6
+//    instructions a pair to fp16 instead of 5.6 to bf16 pay for turning the rows into
+//    fp16 as well, once a head: a power of two a row, as everywhere (kHalf).  Else units are dealt to the CTAs in turn, which
 //    balances causal calls.  Where there are few units, the row tiles of one are
 //    dealt to the CTAs of a cluster and their sums added in rank order.
 //  * S^T is issued and summed in halves of a tile's columns, with a buffer and a
@@ -73,6 +75,7 @@ struct alignas(16) Unit {
 
 struct __align__(16) Misc {
     uint64_t q_full[3], q_empty[3];
+    uint64_t q_here[3];  // kHalf: the queries have landed
     uint64_t raw_full[kRaw][2], raw_empty[kRaw];  // [unit][key tile]
     uint64_t k_full[2][2], k_empty[2][2];  // [key tile][unit parity]
     uint64_t s_full[2][2], s_free[2][2];  // [key tile][buffer]
@@ -80,6 +83,7 @@ struct __align__(16) Misc {
     uint64_t part_full[2][2], part_empty[2][2];  // [key tile][unit parity]
     uint64_t drain[2];
     alignas(16) float nl[kNlStages][128];  // minus the log-sums (log2 units), read in 16 bytes
+    float cf[kNlStages][128];              // kHalf: logit (log2 units) of a product
     int odd[kNlStages];                    // a row of the tile weighs nothing: its logits may be anything
     float part[2][kKeys];                  // [unit parity]: the odd buffers' share of the sums
     float sums[kKeys];                     // of a cluster's CTA
@@ -87,7 +91,7 @@ struct __align__(16) Misc {
     uint32_t tmem_base;
     int abort_flag;
 };
-static_assert(offsetof(Misc, nl) % 16 == 0, "16-byte loads");
+static_assert(offsetof(Misc, nl) % 16 == 0 && offsetof(Misc, cf) % 16 == 0, "16-byte loads");
 
 template <int kD>
 constexpr int smem_bytes() {
@@ -284,6 +288,53 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
         : "memory");
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+    return x;
+}
+
+// One of two threads of a row of a query tile (`tile`: its first half's channels, the
+// second kHalf behind): bf16 to fp16, scaled by the power of two it returns; side 0
+// the first half of the channels, side 1 the other.  Pieces of 16 bytes are taken where
+// they lie (the swizzle keeps a row's together), each row from another one on, so that
+// 8 rows do not meet in a bank.
+template <int kD>
+__device__ __forceinline__ int half_row(uint32_t tile, int row, int side) {
+    constexpr int kPieces = kD / 16;  // of this thread
+    const uint32_t at = tile + row * 128 + (kD == 128 ? side * Sm<kD>::kHalf : 0);
+    const int first = kD == 128 ? 0 : side * kPieces;
+    uint32_t mx = 0u;
+#pragma unroll 1
+    for (int k = 0; k < kPieces; ++k) {
+        const uint4 x = lds128(at + (first + (k + row) % kPieces) * 16);
+        mx = __vimax3_u16x2(mx, x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu);
+        mx = __vimax3_u16x2(mx, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu);
+    }
+    uint32_t top = max(mx & 0xFFFFu, mx >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const int e = q_exponent(__uint_as_float(top << 16));
+    const float f = pow2i(e);
+#pragma unroll 1
+    for (int k = 0; k < kPieces; ++k) {
+        const uint32_t to = at + (first + (k + row) % kPieces) * 16;
+        const uint4 x = lds128(to);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = pack_f16x2(bf16_lo(w[j]) * f, bf16_hi(w[j]) * f);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                     : "memory");
+    }
+    return e;
+}
+
+// 128 keys by N rows, bf16 or fp16.
+__device__ __forceinline__ uint32_t idesc(bool half, int N) {
+    const uint32_t x = idesc_bf16_f32(128, N, 0, 0);
+    return half ? x & ~((1u << 7) | (1u << 10)) : x;
+}
+
 // cache_wait for a barrier and a phase of each lane's own, where it is `needed`.
 __device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, bool needed, volatile int* abort,
                                            unsigned int* err) {
@@ -313,13 +364,9 @@ __device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, bool n
 // uniform register then, as the products' operands have to be).
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-    uint4 x;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
-    return x;
-}
 
-template <int kD>
+// kHalf: K and the queries in fp16, each row's scale beside its log-sum (resident rows).
+template <int kD, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1)
     weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ ChunkParams p) {
     using L = PageLayout<kD>;
@@ -336,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tm_q);
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(smem_u32(&ms.q_full[s]), 2);  // queries, log-sums
+            mbar_init(smem_u32(&ms.q_full[s]), kHalf ? 1 + 8 : 2);  // log-sums; the converting warps, or the queries
+            mbar_init(smem_u32(&ms.q_here[s]), 1);
             mbar_init(smem_u32(&ms.q_empty[s]), 2);
         }
         for (int s = 0; s < (int)kRaw; ++s) {
@@ -430,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const TileRows x = tile_rows_of(p, u, t);
                 if (lane == 0) {
-                    const uint32_t bar = smem_u32(&ms.q_full[st]);
+                    const uint32_t bar = smem_u32(kHalf ? &ms.q_here[st] : &ms.q_full[st]);
                     mbar_arrive_expect_tx(bar, box_rows * kD * 2);
 #pragma unroll
                     for (int half = 0; half < kD / 64; ++half)
@@ -461,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The last load into each stage has landed before the CTA's shared memory is released.
         if (lane == 0)
             for (uint32_t s = 0; s < (uint32_t)S::kStages && s < i; ++s)
-                mbar_wait_drain_1(smem_u32(&ms.q_full[s]), ((i - 1 - s) / S::kStages) & 1, err, kCacheWaitNs);
+                mbar_wait_drain_1(smem_u32(kHalf ? &ms.q_here[s] : &ms.q_full[s]), ((i - 1 - s) / S::kStages) & 1, err,
+                                  kCacheWaitNs);
     } else if (warp == 1 || warp == 3) {
         // ================================ K Q^T: warp 1 of the first key tile, warp 3 of the other
         const int s = warp >> 1;
@@ -503,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t b0 = lo_q + ((st * S::kTile) >> 4);
-                issue_half<kD>(t_s + e0 * 64, a0, b0, hi, idesc_bf16_f32(128, (min(columns, p.half) + 31) & ~31, 0, 0),
+                issue_half<kD>(t_s + e0 * 64, a0, b0, hi, idesc(kHalf, (min(columns, p.half) + 31) & ~31),
                                smem_u32(&ms.s_full[s][e0]), halves == 1 ? q_empty : 0u);
                 if (e0)
                     ++used[1];
@@ -516,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++used[1];
                     tc_fence_after();
                     issue_half<kD>(t_s + 64, a0, b0 + (p.half * 128 >> 4), hi,
-                                   idesc_bf16_f32(128, (columns - p.half + 31) & ~31, 0, 0), smem_u32(&ms.s_full[s][1]), q_empty);
+                                   idesc(kHalf, (columns - p.half + 31) & ~31), smem_u32(&ms.s_full[s][1]), q_empty);
                 }
                 if (last) commit_one(k_empty);
             }
@@ -588,9 +637,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int page = 2 * s + (key >> 6), place = key & 63;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t slot = 0, turn = 0;
+        uint32_t i = 0;  // kHalf: row tiles so far
         bool ok = true;
         Unit u;
         for (uint32_t n = 0; take(n, ok, u); ++n) {
+            if (kHalf && u.fresh_rows) {
+                // The head's rows to fp16 in their places: two threads a row.
+                const int th = threadIdx.x - 128, row = th >> 1, side = th & 1;
+                const uint32_t st = i % S::kStages;
+                ok = cache_wait<kSleepShort>(smem_u32(&ms.q_here[st]), (i / S::kStages) & 1, abort_flag, err);
+                if (!ok) break;
+                const int e = half_row<kD>(sbase + st * S::kTile, row, side);
+                if (side == 0)
+                    ms.cf[i % kNlStages][row] = logit_scale(p.w.scale_log2, c.kv_scale ? c.kv_scale[u.h] : 1.f, e);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.q_full[st]));
+                ++i;
+            }
             const int par = n & 1;
             ok = cache_wait<kSleepShort>(smem_u32(&ms.raw_full[slot][s]), turn & 1, abort_flag, err);
             if (ok && n >= 2) ok = cache_wait<kSleepShort>(smem_u32(&ms.k_empty[s][par]), ((n >> 1) + 1) & 1, abort_flag, err);
@@ -614,7 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t y[4];
                     e2m1_to_f16(w[k], y);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) out[4 * k + j] = f16_to_bf16x2(mul_f16x2(y[j], k < 2 ? s0 : s1));
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t z = mul_f16x2(y[j], k < 2 ? s0 : s1);
+                        out[4 * k + j] = kHalf ? z : f16_to_bf16x2(z);
+                    }
                 }
                 tmem_st16(to + piece * 16, out);
             }
@@ -647,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (p.resident && u.fresh_rows) ++i;
                 continue;
             }
-            const float2 c2v = make_float2(u.c2, u.c2);
             float total = 0.f;
             if (p.resident && u.fresh_rows) ++i;
             const int c0 = p.one_half ? 0 : e * p.half;
@@ -681,6 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[32];
                     tmem_ld32(t_s + c1 - c0, v);
                     const float4* nl = reinterpret_cast<const float4*>(&ms.nl[place][c1]);
+                    const float4* cf = reinterpret_cast<const float4*>(&ms.cf[place][c1]);
                     tmem_wait_ld();
                     if (c1 + 32 >= end) {
                         // All of S is in registers: its columns may take the next tile's.
@@ -691,11 +758,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (plain) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
-                            const float4 l = nl[k / 4];
-                            const float2 e0 = __ffma2_rn(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2v,
-                                                         make_float2(l.x, l.y));
-                            const float2 e1 = __ffma2_rn(
-                                make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), c2v, make_float2(l.z, l.w));
+                            const float4 l = nl[k / 4], f = kHalf ? cf[k / 4] : make_float4(u.c2, u.c2, u.c2, u.c2);
+                            const float2 e0 = __ffma2_rn(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
+                                                         make_float2(f.x, f.y), make_float2(l.x, l.y));
+                            const float2 e1 = __ffma2_rn(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])),
+                                                         make_float2(f.z, f.w), make_float2(l.z, l.w));
                             a = __fadd2_rn(a, make_float2(ex2_approx(e0.x), ex2_approx(e0.y)));
                             b = __fadd2_rn(b, make_float2(ex2_approx(e1.x), ex2_approx(e1.y)));
                         }
@@ -708,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int q = 0; q < 4; ++q) {
                                 const int col = c1 + k + q;
                                 const bool sees = col >= low && col < columns && ls[q] > -INFINITY;
-                                const float y = ex2_approx(fmaf(__uint_as_float(v[k + q]), u.c2, ls[q]));
+                                const float y = ex2_approx(fmaf(__uint_as_float(v[k + q]), kHalf ? ms.cf[place][c1 + k + q] : u.c2, ls[q]));
                                 a.x += sees ? y : 0.f;
                             }
                         }
@@ -795,7 +862,7 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-template <int kD>
+template <int kD, bool kHalf>
 cudaError_t launch(const ChunkParams& p, int grid, cudaStream_t stream) {
     const WeighParams& w = p.w;
     EncodeTiledFn enc = encode_fn();
@@ -812,7 +879,7 @@ cudaError_t launch(const ChunkParams& p, int grid, cudaStream_t stream) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(weigh_chunk_kernel<kD>, smem_bytes<kD>(), done);
+    cudaError_t e = allow_smem(weigh_chunk_kernel<kD, kHalf>, smem_bytes<kD>(), done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -827,7 +894,7 @@ cudaError_t launch(const ChunkParams& p, int grid, cudaStream_t stream) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, weigh_chunk_kernel<kD>, map, p);
+    e = cudaLaunchKernelEx(&cfg, weigh_chunk_kernel<kD, kHalf>, map, p);
     note_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -849,7 +916,8 @@ cudaError_t launch_weigh_chunk(const WeighParams& w, int D, int num_sms, cudaStr
     p.half = 64;
     p.one_half = p.resident && w.Sq * w.group <= p.half;
     const int grid = p.cluster > 1 ? (int)most * p.cluster : (int)std::min<long long>(num_sms, most);
-    return D == 64 ? launch<64>(p, grid, stream) : launch<128>(p, grid, stream);
+    if (p.resident) return D == 64 ? launch<64, true>(p, grid, stream) : launch<128, true>(p, grid, stream);
+    return D == 64 ? launch<64, false>(p, grid, stream) : launch<128, false>(p, grid, stream);
 }
 
 }  // namespace vsa
