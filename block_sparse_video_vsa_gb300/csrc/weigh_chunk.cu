@@ -130,6 +130,9 @@ struct UnitWalk {
     long long left;  // units of a run
     bool any, moved;
     int known, fresh, tiles;  // the sequence whose queries are known, and they
+    int ids, ids_b, ids_from;  // lane i: the page number of page ids_from + i of sequence ids_b
+    int scale_h;               // the head whose scale is known
+    float c2;
 
     // The unit `at` places behind sequence b0's first; false: there is none.
     __device__ bool find(const ChunkParams& p, int b0, long long at) {
@@ -160,7 +163,7 @@ struct UnitWalk {
         rank = blockIdx.x % p.cluster;
         const int i = blockIdx.x / p.cluster, n = gridDim.x / p.cluster;
         moved = true;
-        known = -1;
+        known = ids_b = scale_h = -1;
         step = n;
         left = 1LL << 62;
         long long from = i;
@@ -176,8 +179,8 @@ struct UnitWalk {
         }
         any = left > 0 && find(p, 0, from);
     }
-    // The next unit with tiles, and the page numbers of its pages (lane i: page i).
-    __device__ bool next(const ChunkParams& p, Unit& u, int& id) {
+    // The next unit with tiles, and which lanes' `ids` are its page numbers, from `at` on.
+    __device__ bool next(const ChunkParams& p, Unit& u, int& at) {
         const CacheView& c = p.w.c;
         while (any) {
             if (b != known) {
@@ -210,11 +213,21 @@ struct UnitWalk {
                 if (h >= c.kv_heads) any = find(p, b + 1, (long long)(h - c.kv_heads) * blocks + block);
             }
             if (u.t0 >= u.tiles) continue;
-            const int lane = threadIdx.x & 31;
-            const int page = u.first / kPageTokens + lane;
-            id = -1;
-            if (lane < kPages && (long long)page * kPageTokens < u.kv) id = c.table[(size_t)u.b * c.width + page];
-            u.c2 = p.w.scale_log2 * (c.kv_scale ? c.kv_scale[u.h] : 1.f);
+            // Page numbers are looked up 32 at a time: a run of units needs the next eight
+            // units' with one wait for memory.
+            const int page = u.first / kPageTokens, lane = threadIdx.x & 31;
+            if (u.b != ids_b || page < ids_from || page + kPages > ids_from + 32) {
+                ids_b = u.b;
+                ids_from = page;
+                ids = -1;
+                if ((long long)(page + lane) * kPageTokens < u.kv) ids = c.table[(size_t)u.b * c.width + page + lane];
+            }
+            at = page - ids_from;
+            if (u.h != scale_h) {
+                scale_h = u.h;
+                c2 = p.w.scale_log2 * (c.kv_scale ? c.kv_scale[u.h] : 1.f);
+            }
+            u.c2 = c2;
             return true;
         }
         return false;
@@ -582,9 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t n = 0;  // units so far
         bool ok = true;
         Unit u;
-        int id = -1;
-        bool more = walk.next(p, u, id);
+        int at = 0;
+        bool more = walk.next(p, u, at);
         for (; ok && more; ++n) {
+            int id = __shfl_sync(0xffffffffu, walk.ids, at + lane % kPages);
             const bool there = lane < kPages && (long long)(u.first + lane * kPageTokens) < u.kv;
             if (there && (id < 0 || id >= c.pages)) {
                 atomicOr(err, VSA_DEVERR_INDEX);
@@ -600,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ms.unit[n % kUnits] = u;
                 mbar_arrive(smem_u32(&ms.unit_full[n % kUnits]));
             }
-            more = walk.next(p, u, id);  // (its page numbers are asked for before this unit's pages)
+            more = walk.next(p, u, at);  // (its page numbers are asked for before this unit's pages)
             if (n >= kRaw)
                 ok = cache_wait<kSleepShort>(smem_u32(&ms.raw_empty[raw]), (n / kRaw + 1) & 1, abort_flag, err);
             if (!ok) break;
@@ -821,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         walk.begin(p);
         walk.rank = 0;
         Unit u;
-        int id;
-        const bool has = walk.next(p, u, id);
+        int at_page;
+        const bool has = walk.next(p, u, at_page);
         const int rank = blockIdx.x % p.cluster;
         asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
         const int each = kKeys / p.cluster, key = rank * each + (int)threadIdx.x;
