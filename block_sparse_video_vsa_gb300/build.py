@@ -63,7 +63,7 @@ def _build_front(path: str) -> None:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{os.path.join(torch_dir, 'include')}",
            f"-I{sysconfig.get_paths()['include']}", f"-I{os.environ.get('CUDA_HOME', '/usr/local/cuda')}/include",
            f"-I{os.path.join(REPO_DIR, 'include')}", FRONT_SRC, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}",
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {FRONT_SRC}:\n{r.stdout}\n{r.stderr}")

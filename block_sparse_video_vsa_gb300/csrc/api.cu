@@ -510,7 +510,7 @@ vsa_status vsa_cache_evict(const vsa_cache* c, float* weights, int32_t budget, i
     if (to_table ? to_width <= 0 || !moved || moved == weights : to_width != 0 || moved) return VSA_ERR_INVALID_ARG;
     const int64_t most = std::min<int64_t>(budget, (int64_t)c->width * kPageTokens);
     if (to_table && (int64_t)to_width * kPageTokens < most) return VSA_ERR_INVALID_ARG;
-    if ((int64_t)c->B * c->kv_heads >= (1 << 27) || (int64_t)to_width * kPageTokens >= ((int64_t)1 << 31))
+    if (budget > (1 << 30) || (int64_t)c->B * c->kv_heads >= (1 << 27) || (int64_t)to_width * kPageTokens >= ((int64_t)1 << 31))
         return VSA_ERR_UNSUPPORTED;
     if (!aligned4(weights) || !aligned4(moved) || !aligned4(kept) || !aligned4(lens) || !aligned4(to_table))
         return VSA_ERR_ALIGNMENT;

@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_within_kernel(EvictParams p
         if (size > 0) put_tokens<kD>(p.c, p.c.table, p.c.width, b, h, first, size, x);
         if ((int)threadIdx.x < size) w[first + threadIdx.x] = weight;
     }
-    for (int i = p.budget + rank * kMoveThreads + threadIdx.x; i < n; i += blocks * kMoveThreads) w[i] = 0.f;
+    for (unsigned i = p.budget + rank * kMoveThreads + threadIdx.x; i < (unsigned)n; i += blocks * kMoveThreads) w[i] = 0.f;
 }
 
 // As launch_early, in clusters of `cluster` blocks along x.

@@ -2,7 +2,7 @@
 // tensors that it makes and the call itself, for calls on the current device
 // and stream.  A cache call's kernels take from 3 us; through ctypes, with its
 // arguments looked at one attribute at a time, a call took 18 to 24 us of the
-// host, here 2.4 with its tensors given and 5 to 7 with those it makes.  What
+// host, here 2.2 with its tensors given and 3 to 7 with those it makes.  What
 // this front does not take as it is (other types, another device, a shape that
 // does not fit) it leaves, by returning False, to the Python function, which
 // says what is wrong; a status of the library comes back as a number.
@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -94,7 +94,7 @@ bool vector(const at::Tensor* t, int64_t n) { return t->dim() == 1 && t->size(0)
 const at::Tensor* given_or_new(const at::Tensor* given, at::IntArrayRef sizes, at::ScalarType type, const Cache& x,
                                at::Tensor* made) {
     if (given) return given;
-    *made = at::empty(sizes, at::TensorOptions().dtype(type).device(x.device()));
+    *made = at::detail::empty_cuda(sizes, type, x.device(), std::nullopt);  // (past the dispatcher: 0.5 us less)
     return made;
 }
 PyObject* result(PyObject* given, const at::Tensor& made) {
@@ -337,7 +337,8 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (sizes[i] < 0 || sizes[i] > INT32_MAX) Py_RETURN_FALSE;
     }
     const int64_t places[3] = {x.c.B, x.c.kv_heads, (int64_t)x.c.width * 64}, chosen[3] = {x.c.B, x.c.kv_heads, sizes[0]};
-    if (sizes[0] == 0 || weights->sizes() != at::IntArrayRef(places, 3)) Py_RETURN_FALSE;
+    if (sizes[0] == 0 || sizes[1] + sizes[2] > sizes[0]) Py_RETURN_FALSE;
+    if (weights->sizes() != at::IntArrayRef(places, 3)) Py_RETURN_FALSE;
     if (to ? to->dim() != 2 || to->size(0) != x.c.B || to->size(1) == 0 : moved != nullptr) Py_RETURN_FALSE;
     const int64_t width = to ? to->size(1) : 0, after[3] = {x.c.B, x.c.kv_heads, width * 64};
     if ((kept && kept->sizes() != at::IntArrayRef(chosen, 3)) || (lens && !vector(lens, x.c.B)) ||

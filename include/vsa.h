@@ -651,7 +651,7 @@ vsa_status vsa_cache_weigh(const vsa_cache* c, const void* q, const float* lse, 
  *   moved    : with to_table fp32 [B, kv_heads, 64 * to_width] (written in full, zero
  *              from lens[b] on), else NULL
  * Keys keep the rotation they were stored with: append later tokens with their own
- * positions, which are no longer their places.  B * kv_heads < 2^27.
+ * positions, which are no longer their places.  budget <= 2^30, B * kv_heads < 2^27.
  */
 vsa_status vsa_cache_evict(const vsa_cache* c, float* weights, int32_t budget, int32_t first, int32_t recent,
                            const int32_t* to_table, int32_t to_width, int32_t* kept, int32_t* lens, float* moved,

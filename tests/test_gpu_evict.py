@@ -357,3 +357,125 @@ def test_weigh_and_evict_on_other_streams_through_both_paths_and_in_a_graph():
         assert torch.equal(x, y) and torch.equal(x, z)
     assert torch.equal(a_pool, b_pool) and torch.equal(a_pool, c_pool)
     assert vsa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("D,group,S,n,new", [(64, 5, 200, 300, 199), (128, 8, 150, 500, 150), (64, 300, 4, 200, 3)])
+def test_few_units_are_shared_by_clusters(D, group, S, n, new):
+    """One kv head, few keys and many tiles of rows: up to 8 blocks share a unit's rows."""
+    q, lse, pool, table, lens_t, call, before, want, lim = weigh_case(D, 1, group, S, [n], [new], True, True)
+    got = vsa.cache_weigh(q, lse, pool, table, lens_t, weights=dev(before), **call)
+    assert (np.abs(got.double().cpu().numpy() - want) <= lim).all()
+    assert torch.equal(got, vsa.cache_weigh(q, lse, pool, table, lens_t, weights=dev(before), **call))
+    assert vsa.device_error(reset=True) == 0
+
+
+def test_pages_beyond_four_gib():
+    """The same few tokens at the pool's start and at its end give the same weights, choice and moves."""
+    D, kv = 128, 40
+    r = np.random.default_rng(11)
+    pages = 2 ** 32 // (kv * 72 * D) + 60
+    lens = [500, 130]
+    small, table = filled(r, lens, 8, kv, D, np.ones((2, kv), np.float32))
+    pool = torch.zeros((pages, kv, 72 * D), dtype=torch.uint8, device="cuda")
+    shift = pages - small.shape[0]
+    pool[shift:] = dev(small)
+    far = np.where(table < small.shape[0], table + shift, table).astype(np.int32)
+    parents = i32(np.stack([np.arange(9) - 1, np.full(9, -1)]))
+    new = i32([9, 7])
+    mask, _ = vsa.cache_tree(parents, i32(lens), new)
+    results = []
+    for p, t in ((dev(small), table), (pool, far)):
+        t = dev(t)
+        for S in (1, 9):  # both kernels of each
+            q, _ = bf16(np.random.default_rng(S), 2, S, kv * 4, D)
+            m = new if S == 9 else None
+            out, lse = vsa.cache_attn(q, p, t, i32(lens), q_lens=m, tree=mask if S == 9 else None)
+            w = vsa.cache_weigh(q, lse, p, t, i32(lens), q_lens=m)
+            results.append((out, lse, w))
+        ends = vsa.cache_accept(p, t, i32(lens), new, i32([[0, 3, 4], [1, 2, -1]]), i32([3, 2]))
+        _, kept, moved = vsa.cache_evict(p, t, ends, w, 100, 2, 30)
+        results.append((ends, kept, moved, *vsa.cache_read(p, t, i32([100, 100]), 100)))
+    torch.cuda.synchronize()
+    assert vsa.device_error(reset=True) == 0
+    for a, b in zip(results[:3], results[3:]):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_refusals_say_what_is_wrong():
+    q, lse, pool, table, lens_t, call, _, _, _ = weigh_case(64, 2, 2, 3, [100, 40], [3, 2], True, False)
+    w = vsa.cache_weigh(q, lse, pool, table, lens_t, **call)
+    places = w.shape[2]
+    bad = [
+        lambda: vsa.cache_weigh(q.float(), lse, pool, table, lens_t),
+        lambda: vsa.cache_weigh(q, lse[:, :2], pool, table, lens_t),
+        lambda: vsa.cache_weigh(q, lse.transpose(1, 2), pool, table, lens_t),
+        lambda: vsa.cache_weigh(q[:, :, :3].contiguous(), lse, pool, table, lens_t),
+        lambda: vsa.cache_weigh(q, lse, pool, table, lens_t, q_lens=lens_t[:1]),
+        lambda: vsa.cache_weigh(q, lse, pool, table, lens_t, weights=w[..., :64]),
+        lambda: vsa.cache_weigh(q, lse, pool, table, lens_t, out=w.double()),
+        lambda: vsa.cache_evict(pool, table, lens_t, w, 0),
+        lambda: vsa.cache_evict(pool, table, lens_t, w, 10, 6, 5),
+        lambda: vsa.cache_evict(pool, table, lens_t, w, 10, -1, 0),
+        lambda: vsa.cache_evict(pool, table, lens_t, w[:, :1], 10),
+        lambda: vsa.cache_evict(pool, table, lens_t, w, 10, moved=w),
+        lambda: vsa.cache_evict(pool, table, lens_t, w, 10, to_table=table[:1]),
+        lambda: vsa.cache_evict(pool, table, lens_t, w, 10, to_table=table.float()),
+        lambda: vsa.cache_evict(pool, table, lens_t, w, 10, kept=torch.zeros((2, 2, 9), dtype=torch.int32, device="cuda")),
+        lambda: vsa.cache_tree(lens_t),
+        lambda: vsa.cache_tree(table, new_lens=lens_t[:1]),
+        lambda: vsa.cache_tree(table, mask=torch.zeros((2, 2, 1), dtype=torch.int64, device="cuda")),
+        lambda: vsa.cache_accept(pool, table, lens_t, None, table, lens_t),
+        lambda: vsa.cache_accept(pool, table, lens_t, lens_t, lens_t, lens_t),
+        lambda: vsa.cache_attn(q, pool, table, lens_t, tree=torch.zeros((2, 3, 2), dtype=torch.int64, device="cuda")),
+        lambda: vsa.cache_attn(q, pool, table, lens_t, tree=torch.zeros((2, 3, 1), dtype=torch.int32, device="cuda")),
+    ]
+    for call_ in bad:
+        with pytest.raises((ValueError, TypeError)):
+            call_()
+    for call_, status in ((lambda: vsa.cache_weigh(q, lse, pool, table, lens_t, sm_scale=float("nan")), 1),
+                          (lambda: vsa.cache_evict(pool, table, lens_t, w, 10, lens=lens_t), 1),
+                          (lambda: vsa.cache_evict(pool, table, lens_t, w, places, to_table=table[:, :1].contiguous()), 1),
+                          (lambda: vsa.cache_accept(pool, table, lens_t, lens_t, table, lens_t, lens=lens_t), 1)):
+        with pytest.raises(vsa.VsaError) as e:
+            call_()
+        assert e.value.status == status
+    torch.cuda.synchronize()
+    assert vsa.device_error(reset=True) == 0
+
+
+def test_four_host_threads_at_once():
+    """Each with its own stream and cache: the same answers as alone."""
+    import threading
+    cases = [weigh_case(128 if i % 2 else 64, 2, 3 + i, 1 + 9 * (i % 2), [700 + i, 90], None, True, False, seed=i)
+             for i in range(4)]
+
+    def steps(c):
+        q, lse, pool, table, lens_t, call = c[:6]
+        pool = pool.clone()
+        w = vsa.cache_weigh(q, lse, pool, table, lens_t, **call)
+        lens, kept, _ = vsa.cache_evict(pool, table, lens_t, w, 300, 2, 20)
+        return w, lens, kept, pool
+
+    alone = [steps(c) for c in cases]
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.default_stream())
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got[i] = steps(cases[i])
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for a, b in zip(alone, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)

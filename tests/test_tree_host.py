@@ -88,7 +88,7 @@ def test_evict_refusals(lib):
     assert evict(to=A) == INVALID and evict(to=A, tw=1) == INVALID and evict(tw=1) == INVALID
     assert evict(moved=B_) == INVALID and evict(to=A, tw=1, moved=A) == INVALID
     assert evict(to=A, tw=1, moved=B_, budget=65) == INVALID  # no room
-    assert evict(B=60000, kv_heads=3000) == UNSUPPORTED
+    assert evict(B=60000, kv_heads=3000) == UNSUPPORTED and evict(budget=(1 << 30) + 1) == UNSUPPORTED
     assert evict(to=A, tw=1 << 25, moved=B_) == UNSUPPORTED
     assert evict(w=MIS4) == ALIGNMENT and evict(to=MIS4, tw=1, moved=B_) == ALIGNMENT and evict(lens=B_ + 2) == ALIGNMENT
 
