@@ -49,6 +49,11 @@ constexpr int kKeys = 256, kPages = kKeys / kPageTokens;
 constexpr int kNlStages = 8;
 constexpr int kUnits = 16;                       // described at a time
 constexpr int kReaders = kThreads / 32 - 1;      // warps that read the descriptions
+// Registers, for rows that stream (which are summed more than converted: 452 us for a
+// frame's queries without, 436; a window's 50 and 53): 7 warpgroups launched with 72
+// each; the shares add up to 504.
+constexpr int kLaunchRegs = 72, kIssueRegs = 56, kConvertRegs = 48, kSumRegs = 88;
+static_assert(kIssueRegs + 2 * kConvertRegs + 4 * kSumRegs <= 7 * kLaunchRegs, "register split exceeds the launch");
 constexpr uint32_t kRaw = 6;     // units whose pages are on their way or being converted
 constexpr int kTmemS = 256;
 
@@ -449,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __any_sync(0xffffffffu, u.b >= 0) != 0;
     };
 
+    if (!kHalf && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0) {
         // =================================== queries (by TMA) and their log-sums
         // The log-sums are copied to their place asynchronously, and when the next tile
@@ -646,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait_drain_1(smem_u32(&ms.raw_full[s][lane]), ((asked - 1 - s) / kRaw) & 1, err, kCacheWaitNs);
     } else if (warp < 12) {
         // ============================ convert: warps 4..7 the first 128 keys, 8..11 the others
+        if (!kHalf) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
         const int s = (warp - 4) >> 2, quarter = warp & 3;
         const int key = quarter * 32 + lane;  // of the tile
         const int page = 2 * s + (key >> 6), place = key & 63;
@@ -712,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < 28) {
         // ============================ sums: a warpgroup for each key tile s and buffer e
+        if (!kHalf) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         const int s = (warp - 12) >> 3, e = ((warp - 12) >> 2) & 1, quarter = warp & 3;
         const int key = quarter * 32 + lane;
         const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemS + s * 128 + e * 64;
@@ -893,7 +901,14 @@ cudaError_t launch(const ChunkParams& p, int grid, cudaStream_t stream) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(weigh_chunk_kernel<kD, kHalf>, smem_bytes<kD>(), done);
+    static std::atomic<int> known{0};
+    // The register split draws on the launch's registers; with fewer, setmaxnreg
+    // would wait forever, so such a build is refused.
+    int regs = 0;
+    cudaError_t e = launch_registers(weigh_chunk_kernel<kD, kHalf>, known, &regs);
+    if (e != cudaSuccess) return e;
+    if (!kHalf && regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    e = allow_smem(weigh_chunk_kernel<kD, kHalf>, smem_bytes<kD>(), done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
