@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
         return k;
     };
     if (held) {
-        constexpr int kAhead = 8;
+        constexpr int kAhead = 16;
         for (int i0 = threadIdx.x; i0 < size; i0 += kAhead * kChooseThreads) {
             float x[kAhead];
 #pragma unroll
@@ -229,13 +229,20 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
         if (sm.there == left) break;  // all of them are kept: their other digits do not matter
         __syncthreads();              // (the next digit writes what was read here)
     }
-    // `left` of the places at T are kept, the lowest.  Where each warp's kept places go:
+    // `left` of the places at T are kept, the lowest.  (All of them as a rule: then every
+    // key from T on is one, and only those are counted.)  Where each warp's kept places go:
+    const bool ties = sm.there != left;  // (T is known to its last bit then)
     const int part = ((size - 1) / kChooseWarps / 128 + 1) * 128;  // of a warp (size > 0 or nothing to do)
     const int from = min(size, warp * part), to = min(size, from + part);
     unsigned above = 0u, same = 0u;
     for (int i = from + 4 * lane; i < to; i += 128) {
         const uint4 k4 = keys_at(i);
-        const uint32_t k[4] = {k4.x & mask, k4.y & mask, k4.z & mask, k4.w & mask};
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        if (!ties) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) above += i + j < to && k[j] >= top;
+            continue;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             above += i + j < to && k[j] > top;
@@ -266,33 +273,61 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
         }
         cluster_arrive();  // no block leaves while another reads from it
     }
+    if (!ties) {
+        unsigned j = above;  // (in the row's list whoever writes the weights meanwhile)
+        for (int i0 = from; i0 < to; i0 += 128) {
+            const int i = i0 + 4 * lane;
+            bool keep[4] = {false, false, false, false};
+            if (i < to) {
+                const uint4 k = keys_at(i);
+                keep[0] = k.x >= top;
+                keep[1] = i + 1 < to && k.y >= top;
+                keep[2] = i + 2 < to && k.z >= top;
+                keep[3] = i + 3 < to && k.w >= top;
+            }
+            const unsigned mine = keep[0] + keep[1] + keep[2] + keep[3], incl = scan_warp32(mine);
+            unsigned to_j = j + incl - mine;
+            int32_t* list = kept + p.first + to_j;
+            const int place = p.first + begin + i;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (keep[e] && to_j < (unsigned)want) *list = place + e;
+                list += keep[e];
+                to_j += keep[e];
+            }
+            j += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (blocks > 1) cluster_wait();
+        return;
+    }
     for (int i0 = from; i0 < to; i0 += 128) {
         const int i = i0 + 4 * lane;
-        uint32_t k[4] = {0u, 0u, 0u, 0u};
-        unsigned live = 0u;  // of this lane's four
+        bool over[4] = {false, false, false, false}, at_t[4] = {false, false, false, false};
         if (i < to) {
             const uint4 k4 = keys_at(i);
-            k[0] = k4.x & mask, k[1] = k4.y & mask, k[2] = k4.z & mask, k[3] = k4.w & mask;
-            live = (unsigned)min(4, to - i);
+            const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                over[e] = i + e < to && k[e] > top;
+                at_t[e] = i + e < to && k[e] == top;
+            }
         }
         unsigned mine = 0u;  // above T in the low half, at T in the high one
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if ((unsigned)j < live) mine += k[j] > top ? 1u : k[j] == top ? 0x10000u : 0u;
+        for (int e = 0; e < 4; ++e) mine += (over[e] ? 1u : 0u) + (at_t[e] ? 0x10000u : 0u);
         const unsigned incl = scan_warp32(mine);
-        unsigned a = above + ((incl - mine) & 0xFFFFu), t = same + ((incl - mine) >> 16);
+        unsigned t = same + ((incl - mine) >> 16);  // at T before this lane's
+        unsigned j = above + ((incl - mine) & 0xFFFFu) + min(t, left);
+        int32_t* list = kept + p.first + j;
+        const int place = p.first + begin + i;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if ((unsigned)j < live && (k[j] > top || (k[j] == top && t < left))) {
-                // (Inside the row's list even if somebody else writes the weights meanwhile.)
-                if (a + min(t, left) < (unsigned)want) kept[p.first + a + min(t, left)] = p.first + begin + i + j;
-                if (k[j] > top)
-                    ++a;
-                else
-                    ++t;
-            } else if ((unsigned)j < live && k[j] == top) {
-                ++t;
-            }
+        for (int e = 0; e < 4; ++e) {
+            const bool keep = over[e] || (at_t[e] && t < left);
+            if (keep && j < (unsigned)want) *list = place + e;
+            list += keep;
+            j += keep;
+            t += at_t[e];
+        }
         const unsigned all_of_them = __shfl_sync(0xffffffffu, incl, 31);
         above += all_of_them & 0xFFFFu;
         same += all_of_them >> 16;
