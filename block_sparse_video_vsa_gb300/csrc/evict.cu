@@ -433,18 +433,23 @@ cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, 
     p.recent = recent;
     p.to_width = to_width;
     // Blocks of a row: as many as its keys need shared memory of, and more while the
-    // rows leave SMs idle (32760 keys of 40 heads: 23 us with one, 17 with two, 34 with
-    // four, which share SMs).
+    // rows leave SMs idle and a block has keys enough to pay for the barriers.  The choice
+    // and a move of 1000 tokens, in us, with 1 / 2 / 4 / 8 blocks a row:
+    //    8 heads, 12000 keys    11.1 / 12.4 / 14.5 / 17.9
+    //    8 heads, 32760         17.6 / 16.2 / 14.0 / 20.6
+    //   40 heads, 32760         19.4 / 16.3 / 24.7 / 54.1 (blocks share SMs from four on)
+    //    8 heads, 115200           - /    - / 20.7 / 18.9
     const long long places = (long long)c.width * kPageTokens;
     const long long rows = (long long)c.B * c.kv_heads;
     int cluster = 1;
     while (cluster < kMaxCluster &&
-           (places > (long long)kHeldKeys * cluster || (2 * rows * cluster <= num_sms && places > 4096LL * cluster)))
+           (places > (long long)kHeldKeys * cluster || (2 * rows * cluster <= num_sms && places > 12288LL * cluster)))
         cluster *= 2;
     const long long stretch = ((places + cluster - 1) / cluster + 127) / 128 * 128 + 128;
     p.keys = (int)std::min<long long>(stretch, kHeldKeys);
-    // 512 threads where a thread has few keys: 300 places 4.7 us (1024 threads: 5.8), 4000
-    // 6.6 (7.0); 12000 in 192 rows 19.3 alone but 10 us more among other kernels.
+    // 512 threads where a thread has few keys: 300 keys of 2 heads 7.0 us as above (1024
+    // threads: 7.4), 2000 of 8 heads 7.7 (8.5), 4000 8.6 (8.8), 32760 20.6 (18.7); 12000 in 192
+    // rows 32.7 (29.5).
     constexpr int kFixed = (int)sizeof(ChooseSmem), kSmall = 4352;
     static_assert(kFixed % 16 == 0 && kFixed + kHeldKeys * 4 <= 232448, "shared memory of the choosing kernel");
     static std::atomic<uint64_t> done{0};

@@ -204,6 +204,14 @@ def test_evict_keeps_and_moves_what_the_definition_says(D, kv, lens, budget, fir
     assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "alike", "signed", "special"])
+@pytest.mark.parametrize("D,kv,lens,budget", [(64, 2, [13000, 300, 33000], 400), (64, 1, [16500, 8100], 8000),
+                                              (64, 40, [12400], 65)])
+def test_rows_shared_by_blocks_choose_the_same(D, kv, lens, budget, kind):
+    """Widths at which a row is a cluster's, with lengths that leave blocks of it few places or none."""
+    test_evict_keeps_and_moves_what_the_definition_says(D, kv, lens, budget, 2, 30, kind, False)
+
+
 def big_case(D, kv, n, budget, seed, B=1):
     gen = torch.Generator(device="cuda").manual_seed(seed)
     width = -(-n // 64)
