@@ -9,12 +9,16 @@
 // to 8, each a stretch of its places: keys go to shared memory once, histograms are
 // summed over the cluster by distributed shared memory (all blocks form the same
 // sums, one barrier a digit).  Counting is in integers: the same places in every run.
+// 40 rows of 32760 take 19 us for 5 MB from a cold cache (GB300): load, counting (0.58
+// instructions a scheduler and cycle), barriers and the ordered list follow one another.
 //
 // move_kernel and move_within_kernel bring the kept tokens' codes, scales and
 // weights to the places 0, 1, ...: 9/8 D + 4 bytes a token and head each way,
-// HBM bound.  To other pages a block takes a page of 64 places.  Within the
-// sequence's own pages a cluster takes a (sequence, kv head) and goes along the
-// places in order: kept[j] >= j and ascends, so once all its blocks have read the
+// by sectors of 32 bytes, of which a token's scales use 8: a move of every fourth
+// token reads twice the bytes it keeps (8190 of 32760 tokens, 40 heads of 128: 96 MB
+// read, 24 us from a cold cache, 4.4 TB/s; 65% of the copy rate).  To other pages a
+// block takes a page of 64 places.  Within the sequence's own pages a cluster takes
+// a (sequence, kv head) and goes along the places in order: kept[j] >= j and ascends, so once all its blocks have read the
 // places of a turn, no place that the turn writes is read again.
 #include <algorithm>
 

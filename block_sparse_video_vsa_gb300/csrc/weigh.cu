@@ -4,15 +4,20 @@
 // with the rows' log-sum-exp from the attention call.  Only K is read: 9/16 D bytes
 // a key and head, 2 D flops and an exponential for each row.
 //
-// Few rows a kv head (up to 24, or 32 of 64 channels): HBM bound, K Q^T by mma.sync m16n8k16 (fp16 in,
-// fp32 out) with tokens on the 16-row side, as in token_kernel (cache_attn.cu); a
-// weight is the sum over a token's row of the accumulator, so nothing is joined
+// Few rows a kv head (up to 24, or 32 of 64 channels): K Q^T by mma.sync m16n8k16
+// (fp16 in, fp32 out) with tokens on the 16-row side, as in token_kernel
+// (cache_attn.cu); a weight is the sum over a token's row of the accumulator, so nothing is joined
 // across warps and each weight has one owner: same bits in every run.
 //  * All warps take equal stretches of the line of half pages (32 tokens) of all
 //    sequences and heads; codes and scales come straight to registers, the next
 //    half page's while this one is worked on.
 //  * A key's 64 (or 32) code bytes are four lanes' loads; the order of channels
 //    within K Q^T is free, so a lane's 32 (16) channels need no shuffle.
+// Measured on a GB300, 4 rows a kv head, D = 128: 61 sequences of up to 12000 tokens,
+// 8 kv heads, 61 us = 4.1 TB/s read (61% of the measured copy rate): loads' latency and
+// issue, 0.47 instructions a scheduler and cycle with the 16 warps an SM that 124
+// registers leave.  One sequence of 32760: 9 us, the latency of lengths, page numbers,
+// rows and four half pages one after the other (its bytes take 3).
 #include "weigh.cuh"
 
 namespace vsa {
@@ -290,10 +295,13 @@ cudaError_t launch_cache_weigh(const CacheView& c, int D, const void* q, const f
     // in us of weigh_kernel | the chunk kernel, 8 kv heads (more rows than these: the
     // registers for the queries leave too few warps):
     //   rows of a kv head           20           32
-    //   D = 128,  1 x 32760     13.4 | 16.4  18.1 | 16.7
-    //             8 x 8000      19.5 | 26.0  28.2 | 26.0
-    //   D = 64,   1 x 32760     11.4 | 15.3  13.1 | 15.3
-    //             8 x 8000      15.7 | 24.4  18.7 | 24.4
+    //   D = 128,  1 x 32760     14.0 | 16.6  18.1 | 16.5
+    //             8 x 8000      20.2 | 24.9  28.2 | 24.8
+    //   D = 64,   1 x 32760     11.0 | 14.4  12.9 | 14.6
+    //             8 x 8000      14.9 | 22.1  17.8 | 22.2
+    // Warps of a block, one tile of 8 rows (61 sequences of up to 12000, D = 128): 60.8 us with
+    // 16, 68.6 with 12, 71.9 with 18, 67.1 with 20; two tiles (8 x 8000, 12 rows): 17.3 with 16,
+    // 16.1 with 12, 18.1 with 14.
     if (rows > (D == 64 ? 32 : 24)) return launch_weigh_chunk(p, D, num_sms, stream);
     const dim3 grid((unsigned)num_sms);
     const auto few = [&](auto kernel, int warps) { return launch_early(kernel, grid, warps * 32, 0, stream, p); };

@@ -16,10 +16,10 @@
 //    of rows serves two tiles of keys, so that L2 gives 32 KB for some 1000 cycles.
 //  * Rows that fit one tile (a window of recent queries) stay in shared memory for
 //    all units of their head: the CTAs take runs of neighbouring units then, and
-//    pages are all that moves.  Converting K is then most of the work, and 2.6
+//    pages are all that moves.  Converting K is then much of the work, and 2.6
 //    instructions a pair to fp16 instead of 5.6 to bf16 pay for turning the rows into
-//    fp16 as well, once a head: a power of two a row, as everywhere (kHalf).  Else units are dealt to the CTAs in turn, which
-//    balances causal calls.  Where there are few units, the row tiles of one are
+//    fp16 as well, once a head: a power of two a row, as everywhere (kHalf).  Else
+//    units are dealt to the CTAs in turn, which balances causal calls.  Where there are few units, the row tiles of one are
 //    dealt to the CTAs of a cluster and their sums added in rank order.
 //  * S^T is issued and summed in halves of a tile's columns, with a buffer and a
 //    warpgroup for each half and key tile: a half's products run while the others'
@@ -31,6 +31,12 @@
 //  * TMEM (512 columns): K of two units, two halves of S^T of the two key tiles.
 //  * Every wait is bounded; one that runs out raises the CTA's abort flag and the
 //    device error word, and each role winds down.
+// Measured on a GB300, D = 128, one sequence of 32760 tokens, 40 kv heads: 1560 rows
+// 435 us = 1.20 PFLOP/s (63% of the measured bf16 rate; tensor pipe 49% busy,
+// exponentials 51%, 0.69 instructions a scheduler and cycle: the loads from tensor memory and
+// waits around the exponentials); 64 rows 50 us = 1.9 TB/s of pages (28% of the copy
+// rate; 0.61 instructions: describing, converting and summing a unit of 256 keys takes
+// some 1760 a scheduler).
 #include <stddef.h>
 
 #include <algorithm>
