@@ -652,12 +652,90 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
 // x + gridDim.x, ...:
 //   m = max m_i, out = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i
 // The warps take the parts in turn and ask for eight at a time: a unit cut
-// into many parts is a matter of latency.  One of at most eight parts is joined a
-// row a warp, with the same sums in the same order (a tree of 60 on 32760 tokens:
-// 70.7 -> 67.4 us, 16 ragged trees 90.7 -> 83.0).
+// into many parts is a matter of latency.  Units of many rows (kRows) with at most
+// eight parts are joined a row a warp, with the same sums in the same order (a tree of 60
+// on 32760 tokens: 70.7 -> 67.4 us, 16 ragged trees 90.7 -> 83.4; single tokens of 61
+// sequences would go from 98.4 to 100.2), by code of its own for two parts, a third of the
+// instructions for what most cuts of a batch are (the ragged trees 83.4 -> 81.6; with code
+// for four as well, 82.5).
 constexpr int kJoinWarps = 4;
 
-template <int kD>
+// The rows of unit u (b, h, t) in the parts of CTAs c0 .. c1, at most kParts of them, a row a warp.
+template <int kD, int kParts>
+__device__ __forceinline__ void join_rows(const AttnParams& p, int4 u, int c0, int c1) {
+    constexpr int kPer = kD / 32, kWays = kParts < kJoinWarps ? kParts : kJoinWarps;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int live_rows = seq_lens(p, u.x).q * p.group;
+    const float v_head = p.c.kv_scale ? p.c.kv_scale[p.c.kv_heads + u.y] : 1.f;
+#pragma unroll 1
+    for (int r = blockIdx.x * kJoinWarps + warp; r < p.tile; r += gridDim.x * kJoinWarps) {
+        const int row = u.z * p.tile + r;
+        if (row >= p.Sq * p.group) return;
+        // (A row a block: parts w and w + 4 are warp w's.)
+        float2 ml[kParts];
+        float o[kParts][kPer];
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            const size_t at = (2 * (size_t)(c0 + k) + (k == 0)) * p.tile + r;
+            ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) o[k][i] = 0.f;
+            if (kParts > 2 && c0 + k > c1) continue;
+            ml[k] = p.part_ml[at];
+            const float* src = p.part_o + at * kD + lane * kPer;
+            if constexpr (kPer == 4)
+                *reinterpret_cast<float4*>(o[k]) = *reinterpret_cast<const float4*>(src);
+            else
+                *reinterpret_cast<float2*>(o[k]) = *reinterpret_cast<const float2*>(src);
+        }
+        float m_of[kWays], l_of[kWays], m = -INFINITY, l = 0.f, sum[kPer];
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) {
+            m_of[w] = ml[w].x;
+            if constexpr (kParts > kWays) m_of[w] = fmaxf(m_of[w], ml[w + kWays].x);
+            m = fmaxf(m, m_of[w]);
+            l_of[w] = 0.f;
+            float s[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) s[i] = 0.f;
+#pragma unroll
+            for (int k = w; k < kParts; k += kWays) {
+                if (ml[k].x == -INFINITY && ml[k].y == 0.f) continue;
+                const float a = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - m_of[w]);
+                l_of[w] = fmaf(a, ml[k].y, l_of[w]);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) s[i] = fmaf(a, o[k][i], s[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) o[w][i] = s[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sum[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) {
+            const float a = m_of[w] == -INFINITY ? 0.f : ex2_approx(m_of[w] - m);
+            l = fmaf(a, l_of[w], l);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) sum[i] = fmaf(a, o[w][i], sum[i]);
+        }
+        const int qi = row / p.group, head = u.y * p.group + row - qi * p.group;
+        const bool live = row < live_rows && l != 0.f;
+        const float inv = live ? v_head / l : 0.f;
+        uint32_t y[kPer / 2];
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) y[i / 2] = live ? pack_bf16x2(sum[i] * inv, sum[i + 1] * inv) : 0u;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)u.x * p.Sq + qi) * p.heads + head) * (kD / 8)) +
+                        lane * (kPer / 2);
+        if constexpr (kPer == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+        else
+            *dst = y[0];
+        if (lane == 0 && p.lse)
+            p.lse[((size_t)u.x * p.heads + head) * p.Sq + qi] = live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+}
+
+template <int kD, bool kRows>
 __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) {
     __shared__ float s_o[kJoinWarps][kD];
     __shared__ float2 s_ml[kJoinWarps];
@@ -681,75 +759,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) 
         if (more != 0xffffffffu) break;
     }
     constexpr int kPer = kD / 32, kAhead = 8;  // channels of a lane; parts asked for at a time
-    if (c1 - c0 < 2 * kJoinWarps) {
-        const int live_rows = seq_lens(p, u.x).q * p.group;
-        const float v_head = p.c.kv_scale ? p.c.kv_scale[p.c.kv_heads + u.y] : 1.f;
-#pragma unroll 1
-        for (int r = blockIdx.x * kJoinWarps + warp; r < p.tile; r += gridDim.x * kJoinWarps) {
-            const int row = u.z * p.tile + r;
-            if (row >= p.Sq * p.group) return;
-            // Parts w and w + 4 are warp w's below.
-            float2 ml[2 * kJoinWarps];
-            float o[2 * kJoinWarps][kPer];
-#pragma unroll
-            for (int k = 0; k < 2 * kJoinWarps; ++k) {
-                const size_t at = (2 * (size_t)(c0 + k) + (k == 0)) * p.tile + r;
-                ml[k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) o[k][i] = 0.f;
-                if (c0 + k > c1) continue;
-                ml[k] = p.part_ml[at];
-                const float* src = p.part_o + at * kD + lane * kPer;
-                if constexpr (kPer == 4)
-                    *reinterpret_cast<float4*>(o[k]) = *reinterpret_cast<const float4*>(src);
-                else
-                    *reinterpret_cast<float2*>(o[k]) = *reinterpret_cast<const float2*>(src);
-            }
-            float m_of[kJoinWarps], l_of[kJoinWarps], m = -INFINITY, l = 0.f, sum[kPer];
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) {
-                m_of[w] = fmaxf(ml[w].x, ml[w + kJoinWarps].x);
-                m = fmaxf(m, m_of[w]);
-                l_of[w] = 0.f;
-                float s[kPer];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) s[i] = 0.f;
-#pragma unroll
-                for (int k = w; k < 2 * kJoinWarps; k += kJoinWarps) {
-                    if (ml[k].x == -INFINITY && ml[k].y == 0.f) continue;
-                    const float a = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - m_of[w]);
-                    l_of[w] = fmaf(a, ml[k].y, l_of[w]);
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) s[i] = fmaf(a, o[k][i], s[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) o[w][i] = s[i];
-            }
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) sum[i] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) {
-                const float a = m_of[w] == -INFINITY ? 0.f : ex2_approx(m_of[w] - m);
-                l = fmaf(a, l_of[w], l);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) sum[i] = fmaf(a, o[w][i], sum[i]);
-            }
-            const int qi = row / p.group, head = u.y * p.group + row - qi * p.group;
-            const bool live = row < live_rows && l != 0.f;
-            const float inv = live ? v_head / l : 0.f;
-            uint32_t y[kPer / 2];
-#pragma unroll
-            for (int i = 0; i < kPer; i += 2) y[i / 2] = live ? pack_bf16x2(sum[i] * inv, sum[i + 1] * inv) : 0u;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (((size_t)u.x * p.Sq + qi) * p.heads + head) * (kD / 8)) +
-                            lane * (kPer / 2);
-            if constexpr (kPer == 4)
-                *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
-            else
-                *dst = y[0];
-            if (lane == 0 && p.lse)
-                p.lse[((size_t)u.x * p.heads + head) * p.Sq + qi] = live ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-        }
-        return;
+    if constexpr (kRows) {
+        if (c1 - c0 < 2) return join_rows<kD, 2>(p, u, c0, c1);
+        if (c1 - c0 < 2 * kJoinWarps) return join_rows<kD, 2 * kJoinWarps>(p, u, c0, c1);
     }
 #pragma unroll 1
     for (int r = blockIdx.x; r < p.tile; r += gridDim.x) {
@@ -934,7 +946,9 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
     if (e != cudaSuccess || p.whole) return e;
     if (p.grid < 2) return cudaSuccess;
     const dim3 grid((unsigned)std::min(p.tiles == 1 ? rows : p.tile, 32), (unsigned)(p.grid - 1));
-    return launch_early(D == 64 ? combine_kernel<64> : combine_kernel<128>, grid, kJoinWarps * 32, 0, stream, p);
+    const auto join = p.tile >= 128 ? (D == 64 ? combine_kernel<64, true> : combine_kernel<128, true>)
+                                    : (D == 64 ? combine_kernel<64, false> : combine_kernel<128, false>);
+    return launch_early(join, grid, kJoinWarps * 32, 0, stream, p);
 }
 
 }  // namespace vsa
