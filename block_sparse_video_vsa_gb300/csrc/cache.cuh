@@ -214,7 +214,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // is written by its CTA; the parts of a cut unit go to the workspace (two
 // slots a CTA: slot 0 for a unit begun by an earlier CTA, slot 1 for one it
 // begins itself and does not finish) and are joined by combine_kernel, a block
-// for each cut: there are fewer cuts than CTAs, whatever the batch.
+// or more for each cut unit: there are fewer of them than CTAs, whatever the batch.
 struct AttnParams {
     CacheView c;
     const int32_t* q_lens;    // [B], or null: Sq

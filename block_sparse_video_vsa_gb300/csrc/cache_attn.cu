@@ -34,6 +34,8 @@
 //    is issue: 1200 instructions a page at 0.55 a scheduler and cycle, 12 warps
 //    an SM (163 registers).  A producer warp with 7 consumers behind a barrier
 //    a unit took 127 us.  One token on one clip of 32760 tokens takes 22 us.
+#include <type_traits>
+
 #include "cache.cuh"
 
 namespace vsa {
@@ -647,9 +649,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) token_kernel(AttnParams p) {
             mbar_wait_drain_1(smem_u32(&sm.full[warp][j % kOwn]), (j / kOwn) & 1, p.c.err, kCacheWaitNs);
 }
 
-// Joins the parts of the units that were cut.  Block (x, y) looks at the cut
-// before CTA y + 1's part; if it is the unit's first, it joins the rows x,
-// x + gridDim.x, ...:
+// Joins the parts of the units that were cut.  Block (x, y) joins the rows x,
+// x + gridDim.x, ... of the one that begins in CTA y's part, or (kFind) of the y-th:
 //   m = max m_i, out = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i
 // The warps take the parts in turn and ask for eight at a time: a unit cut
 // into many parts is a matter of latency.  Units of many rows (kRows) with at most
@@ -735,21 +736,21 @@ __device__ __forceinline__ void join_rows(const AttnParams& p, int4 u, int c0, i
     }
 }
 
-template <int kD, bool kRows>
-__global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) {
-    __shared__ float s_o[kJoinWarps][kD];
-    __shared__ float2 s_ml[kJoinWarps];
-    early();
-    begin_work();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = blockIdx.y;  // the CTA that begins the unit, if this is its first cut
+// A unit (b, h, t) that is cut: it begins in CTA c0's part and ends in CTA c1's (c0 < 0: none).
+struct CutUnit {
+    int c0, c1;
+    int4 u;
+};
+// The one that begins in CTA blockIdx.y's part.
+__device__ __forceinline__ CutUnit cut_at(const AttnParams& p) {
+    const int lane = threadIdx.x & 31, c0 = blockIdx.y;
     // Lane i: where CTA c0 + i's part begins (b < 0: not inside a unit).
     int4 x = make_int4(-1, 0, 0, 0);
     if (c0 + lane < p.grid) x = p.places[c0 + lane];
     const int4 u = make_int4(__shfl_sync(0xffffffffu, x.x, 1), __shfl_sync(0xffffffffu, x.y, 1),
                              __shfl_sync(0xffffffffu, x.z, 1), 0);
     unsigned same = __ballot_sync(0xffffffffu, x.x == u.x && x.y == u.y && x.z == u.z);
-    if (u.x < 0 || (same & 1u)) return;
+    if (u.x < 0 || (same & 1u)) return {-1, 0, u};
     int c1 = c0 + __ffs(~(same >> 1)) - 1;  // the unit's last CTA
     for (int c = c0 + 32; same >> 31 && c < p.grid; c += 32) {  // (more than 31 parts)
         x = make_int4(-1, 0, 0, 0);
@@ -758,6 +759,73 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) 
         c1 = c - 1 + (more == 0xffffffffu ? 32 : __ffs(~more) - 1);
         if (more != 0xffffffffu) break;
     }
+    return {c0, c1, u};
+}
+// The blockIdx.y-th of all (for few units of many rows: most of 151 times 32 blocks would
+// find none; a tree of 60 67.5 -> 65.7 us, 36 rows on 11398 tokens of 5 heads 21.7 -> 20.4.  Finding
+// takes 1 us more, which single tokens, a few blocks a cut, would lose: 19.0 -> 20.2).
+__device__ __forceinline__ CutUnit find_cut(const AttnParams& p) {
+    constexpr int kWords = kMaxGrid / 32;
+    static_assert(kMaxGrid % 32 == 0, "a bit for each CTA");
+    // Bit i: CTA i + 1's part begins inside a unit which CTA i's part does not (first), does (same) begin inside of.
+    __shared__ unsigned s_first[kWords], s_same[kWords];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int w0 = 0; w0 < kWords; w0 += kJoinWarps) {
+        const int w = w0 + warp, i = w * 32 + lane;
+        int4 x = make_int4(-1, 0, 0, 0), y = x;  // (b < 0: not inside a unit)
+        if (w < kWords && i + 1 < p.grid) {
+            x = p.places[i];
+            y = p.places[i + 1];
+        }
+        const bool same = x.x == y.x && x.y == y.y && x.z == y.z;
+        const unsigned first_bits = __ballot_sync(0xffffffffu, y.x >= 0 && !same);
+        const unsigned same_bits = __ballot_sync(0xffffffffu, y.x >= 0 && same);
+        if (w < kWords && lane == 0) {
+            s_first[w] = first_bits;
+            s_same[w] = same_bits;
+        }
+    }
+    __syncthreads();
+    CutUnit cut = {-1, 0, make_int4(-1, 0, 0, 0)};
+    int before = blockIdx.y;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        const unsigned bits = s_first[w];
+        const int n = __popc(bits);
+        if (cut.c0 < 0 && before < n) {
+            const bool here = (bits >> lane & 1u) && __popc(bits & ((1u << lane) - 1u)) == before;
+            cut.c0 = w * 32 + __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        }
+        before -= n;
+    }
+    if (cut.c0 < 0) return cut;
+    cut.c1 = cut.c0 + 1;
+#pragma unroll 1
+    while (cut.c1 < kMaxGrid) {  // (the last CTA's bit is not set)
+        const int at = cut.c1 & 31, run = __ffs(~(s_same[cut.c1 >> 5] >> at)) - 1;  // (zeros come in from above, if at > 0)
+        cut.c1 += run < 0 ? 32 : run;
+        if (run >= 0 && at + run < 32) break;
+    }
+    cut.u = p.places[cut.c0 + 1];
+    return cut;
+}
+
+template <int kD, bool kRows, bool kFind>
+__global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(AttnParams p) {
+    __shared__ float s_o[kJoinWarps][kD];
+    __shared__ float2 s_ml[kJoinWarps];
+    early();
+    begin_work();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    CutUnit cut;
+    if constexpr (kFind)
+        cut = find_cut(p);
+    else
+        cut = cut_at(p);
+    if (cut.c0 < 0) return;
+    const int c0 = cut.c0, c1 = cut.c1;
+    const int4 u = cut.u;
     constexpr int kPer = kD / 32, kAhead = 8;  // channels of a lane; parts asked for at a time
     if constexpr (kRows) {
         if (c1 - c0 < 2) return join_rows<kD, 2>(p, u, c0, c1);
@@ -945,9 +1013,17 @@ cudaError_t launch_cache_attn(const CacheView& c, int D, const void* q, int Sq, 
         e = p.tile == 8 ? launch_token<128, 1, 12, 2>(p, stream) : launch_token<128, 2, 8, 3>(p, stream);
     if (e != cudaSuccess || p.whole) return e;
     if (p.grid < 2) return cudaSuccess;
-    const dim3 grid((unsigned)std::min(p.tiles == 1 ? rows : p.tile, 32), (unsigned)(p.grid - 1));
-    const auto join = p.tile >= 128 ? (D == 64 ? combine_kernel<64, true> : combine_kernel<128, true>)
-                                    : (D == 64 ? combine_kernel<64, false> : combine_kernel<128, false>);
+    const long long units = (long long)c.B * c.kv_heads * p.tiles;
+    const bool few = p.tile >= 128 && 2 * units <= p.grid;  // found by number
+    const dim3 grid((unsigned)std::min(p.tiles == 1 ? rows : p.tile, 32),
+                    (unsigned)(few ? units : p.grid - 1));
+    const auto of = [&](auto d) {
+        constexpr int kD = decltype(d)::value;
+        return few              ? combine_kernel<kD, true, true>
+               : p.tile >= 128 ? combine_kernel<kD, true, false>
+                               : combine_kernel<kD, false, false>;
+    };
+    const auto join = D == 64 ? of(std::integral_constant<int, 64>{}) : of(std::integral_constant<int, 128>{});
     return launch_early(join, grid, kJoinWarps * 32, 0, stream, p);
 }
 
