@@ -18,8 +18,10 @@
 // token reads twice the bytes it keeps (8190 of 32760 tokens, 40 heads of 128: 96 MB
 // read, 24 us from a cold cache, 4.4 TB/s; 65% of the copy rate).  To other pages a
 // block takes a page of 64 places.  Within the sequence's own pages a cluster takes
-// a (sequence, kv head) and goes along the places in order: kept[j] >= j and ascends, so once all its blocks have read the
-// places of a turn, no place that the turn writes is read again.
+// a (sequence, kv head) and goes along the places in order: kept[j] >= j and
+// ascends, so once all its blocks have read the places of a turn, no place that the
+// turn writes is read again.  evict_kernel is choice and move in one, for short rows
+// that keep up to 256 tokens.
 #include <algorithm>
 
 #include "move.cuh"
@@ -99,16 +101,15 @@ struct ChooseSmem {
     unsigned int found, before, there, unused[3];
 };
 
-template <int kChooseThreads>
-__global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p) {
+extern __shared__ __align__(16) unsigned char choose_smem[];
+
+template <int kChooseThreads, bool kClusters>
+__device__ __forceinline__ void choose(const EvictParams& p) {
     constexpr int kChooseWarps = kChooseThreads / 32;
-    extern __shared__ __align__(16) unsigned char choose_smem[];
     ChooseSmem& sm = *reinterpret_cast<ChooseSmem*>(choose_smem);
     uint32_t* keys = reinterpret_cast<uint32_t*>(choose_smem + sizeof(ChooseSmem));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    early();
-    begin_work();
-    const int blocks = (int)cluster_size(), rank = (int)cluster_rank();
+    const int blocks = kClusters ? (int)cluster_size() : 1, rank = kClusters ? (int)cluster_rank() : 0;
     const int row = blockIdx.x / blocks;  // of B * kv_heads
     const int b = row / p.c.kv_heads, h = row - b * p.c.kv_heads;
     const int n = cache_len(p.c, b, h == 0 && rank == 0 && threadIdx.x == 0);
@@ -339,6 +340,13 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
     if (blocks > 1) cluster_wait();
 }
 
+template <int kChooseThreads>
+__global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p) {
+    early();
+    begin_work();
+    choose<kChooseThreads, true>(p);
+}
+
 // To other pages: block (x, h, b) fills places 64 x .. 64 x + 63.
 template <int kD>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictParams p) {
@@ -359,8 +367,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictParams p) {
     if (size <= 0) return;
     __syncthreads();
     MovedToken<kD> x[MovedToken<kD>::kTurns];
-    take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source, size, x);
-    put_tokens<kD>(p.c, p.to_table, p.to_width, b, h, first, size, x);
+    take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source, size, threadIdx.x, x);
+    put_tokens<kD>(p.c, p.to_table, p.to_width, b, h, first, size, threadIdx.x, x);
 }
 
 // Within the sequence's pages: a cluster goes along the row, 64 places a block and turn.
@@ -389,13 +397,51 @@ __global__ void __launch_bounds__(kMoveThreads) move_within_kernel(EvictParams p
             weight = s >= 0 ? w[s] : 0.f;
         }
         __syncthreads();
-        if (size > 0) take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source[turn], size, x);
+        if (size > 0) take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source[turn], size, threadIdx.x, x);
         cluster_arrive();
         cluster_wait();
-        if (size > 0) put_tokens<kD>(p.c, p.c.table, p.c.width, b, h, first, size, x);
+        if (size > 0) put_tokens<kD>(p.c, p.c.table, p.c.width, b, h, first, size, threadIdx.x, x);
         if ((int)threadIdx.x < size) w[first + threadIdx.x] = weight;
     }
     for (unsigned i = p.budget + rank * kMoveThreads + threadIdx.x; i < (unsigned)n; i += blocks * kMoveThreads) w[i] = 0.f;
+}
+
+// Choice and move in one, for few tokens to keep: a block a row, 64 places for each 128 threads.
+constexpr int kFewThreads = 512, kFewBudget = kFewThreads / kMoveThreads * kPageTokens;
+template <int kD>
+__global__ void __launch_bounds__(kFewThreads, 1) evict_kernel(EvictParams p) {
+    __shared__ int source[kFewThreads / kMoveThreads][kPageTokens];
+    early();
+    begin_work();
+    choose<kFewThreads, false>(p);
+    __syncthreads();  // (the list is the block's own)
+    const size_t row = blockIdx.x;
+    const int b = (int)(row / p.c.kv_heads), h = (int)(row - (size_t)b * p.c.kv_heads);
+    const int n = cache_len(p.c, b, false);
+    const bool within = p.to_table == nullptr;
+    if (within && n <= p.budget) return;
+    const int32_t* table = within ? p.c.table : p.to_table;
+    const int width = within ? p.c.width : p.to_width;
+    const int32_t* kept = p.kept + row * p.budget;
+    const float* w = p.weights + row * p.c.width * kPageTokens;
+    float* moved = p.moved + row * width * kPageTokens;
+    const int group = threadIdx.x / kMoveThreads, thread = threadIdx.x % kMoveThreads, first = group * kPageTokens;
+    const int m = min(n, p.budget), size = min(kPageTokens, m - first);
+    float weight = 0.f;
+    if (thread < size) {
+        int s = kept[first + thread];
+        if (s >= n) s = -1;
+        source[group][thread] = s;
+        weight = s >= 0 ? w[s] : 0.f;
+    }
+    __syncthreads();
+    MovedToken<kD> x[MovedToken<kD>::kTurns];
+    if (size > 0) take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source[group], size, thread, x);
+    __syncthreads();  // all have read before any writes
+    if (size > 0) put_tokens<kD>(p.c, table, width, b, h, first, size, thread, x);
+    if (thread < size) moved[first + thread] = weight;
+    const unsigned end = within ? (unsigned)n : (unsigned)width * kPageTokens;
+    for (unsigned i = m + threadIdx.x; i < end; i += kFewThreads) moved[i] = 0.f;
 }
 
 // As launch_early, in clusters of `cluster` blocks along x.
@@ -462,6 +508,20 @@ cudaError_t launch_cache_evict(const CacheView& c, int D, const float* weights, 
     static std::atomic<uint64_t> done_small{0};
     e = allow_smem(choose_kernel<512>, kFixed + kSmall * 4, done_small);
     if (e != cudaSuccess) return e;
+    // Choice and move in one kernel where a block moves all that its row keeps at once.  In us, two
+    // kernels | one, D = 128, 4000 keys, to other pages and within their own (two turns of a
+    // block's threads for 512 tokens are as slow as they look):
+    //   budget 256,  1 sequence of 8 heads  9.6 |  8.9   8.5 |  7.4
+    //               61                     27.0 | 24.6  22.2 | 18.3
+    //   budget 512,  1                      9.6 | 10.8   8.5 |  9.1
+    //               61                     38.7 | 50.2  29.6 | 32.9
+    if (cluster == 1 && p.keys <= kSmall && budget <= kFewBudget) {
+        static std::atomic<uint64_t> done_few[2];
+        const auto kernel = D == 64 ? evict_kernel<64> : evict_kernel<128>;
+        e = allow_smem(kernel, kFixed + kSmall * 4, done_few[D == 64]);
+        if (e != cudaSuccess) return e;
+        return launch_early(kernel, dim3((unsigned)rows), kFewThreads, kFixed + p.keys * 4, stream, p);
+    }
     e = launch_clusters(p.keys <= kSmall ? choose_kernel<512> : choose_kernel<1024>, dim3((unsigned)(rows * cluster)), cluster,
                         p.keys <= kSmall ? 512 : 1024, kFixed + p.keys * 4, stream, p);
     if (e != cudaSuccess) return e;

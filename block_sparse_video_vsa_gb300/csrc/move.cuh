@@ -37,16 +37,17 @@ __device__ __forceinline__ unsigned char* token_page(const CacheView& c, const i
 }
 
 // Reads tokens source[0 .. size) (places in the sequence; -1: none) of kv head h
-// (all kMoveThreads threads call it; `source` is shared memory).
+// (kMoveThreads threads call it, `thread` is a thread's number among them; `source` is shared memory).
 template <int kD>
 __device__ __forceinline__ void take_tokens(const CacheView& c, const int32_t* table, int width, int b, int h,
-                                            const int* source, int size, MovedToken<kD> (&x)[MovedToken<kD>::kTurns]) {
+                                            const int* source, int size, int thread,
+                                            MovedToken<kD> (&x)[MovedToken<kD>::kTurns]) {
     using L = PageLayout<kD>;
     using M = MovedToken<kD>;
-    const int piece = threadIdx.x % M::kPieces;
+    const int piece = thread % M::kPieces;
 #pragma unroll
     for (int i = 0; i < M::kTurns; ++i) {
-        const int row = i * M::kRows + threadIdx.x / M::kPieces;  // K rows, then V rows
+        const int row = i * M::kRows + thread / M::kPieces;  // K rows, then V rows
         const int side = row / kPageTokens, t = row % kPageTokens;
         const int token = t < size ? source[t] : -1;
         const unsigned char* page = token >= 0 ? token_page<kD>(c, table, width, b, h, token) : nullptr;
@@ -64,13 +65,13 @@ __device__ __forceinline__ void take_tokens(const CacheView& c, const int32_t* t
 // Writes what take_tokens read to the places first .. first + size - 1 of a table's sequence.
 template <int kD>
 __device__ __forceinline__ void put_tokens(const CacheView& c, const int32_t* table, int width, int b, int h, int first,
-                                           int size, const MovedToken<kD> (&x)[MovedToken<kD>::kTurns]) {
+                                           int size, int thread, const MovedToken<kD> (&x)[MovedToken<kD>::kTurns]) {
     using L = PageLayout<kD>;
     using M = MovedToken<kD>;
-    const int piece = threadIdx.x % M::kPieces;
+    const int piece = thread % M::kPieces;
 #pragma unroll
     for (int i = 0; i < M::kTurns; ++i) {
-        const int row = i * M::kRows + threadIdx.x / M::kPieces;
+        const int row = i * M::kRows + thread / M::kPieces;
         const int side = row / kPageTokens, t = row % kPageTokens;
         if (t >= size || x[i].scales == 0xFFFFFFFFu) continue;
         unsigned char* page = token_page<kD>(c, table, width, b, h, first + t);

@@ -106,9 +106,9 @@ __global__ void __launch_bounds__(kMoveThreads) accept_kernel(AcceptParams p) {
         }
         __syncthreads();
         MovedToken<kD> moved[MovedToken<kD>::kTurns];
-        take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source, size, moved);
+        take_tokens<kD>(p.c, p.c.table, p.c.width, b, h, source, size, threadIdx.x, moved);
         __syncthreads();  // (and `source` is free again)
-        put_tokens<kD>(p.c, p.c.table, p.c.width, b, h, base + first, size, moved);
+        put_tokens<kD>(p.c, p.c.table, p.c.width, b, h, base + first, size, threadIdx.x, moved);
     }
 }
 
