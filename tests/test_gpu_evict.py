@@ -280,6 +280,41 @@ def test_evict_reports_bad_pages():
     assert lens.tolist() == [64] and np.array_equal(pool.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("budget", [200, 320])
+@pytest.mark.parametrize("inplace", [True, False])
+def test_bad_pages_among_those_moved(budget, inplace):
+    """Few tokens kept and more: those of a bad page leave their new places as they were."""
+    pool, table, to, w = big_case(128, 3, 700, 400, 5)
+    bad = table.clone()
+    bad[0, 7] = -1
+    w[..., 448:512] += 100
+    before, want = pool.cpu().numpy(), pool.cpu().numpy().copy()
+    weights = w[0].cpu().numpy().copy()
+    vsa.device_error(reset=True)
+    _, kept, _ = vsa.cache_evict(pool, bad, i32([700]), w, budget, 1, 9,
+                                 to_table=None if inplace else to[:, :-(-budget // 64)].contiguous())
+    torch.cuda.synchronize()
+    assert vsa.device_error(reset=True) == 2
+    for h in range(3):
+        at = tref.choose(weights[h], 700, budget, 1, 9)
+        assert kept[0, h].tolist() == at.tolist()
+        there = at // 64 != 7
+        assert (~there).sum() == 64
+        tref.move(before, want, table[0].cpu().numpy(), (table if inplace else to)[0].cpu().numpy(), at[there],
+                  np.arange(budget)[there], h, 128)
+    assert np.array_equal(pool.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("D,kv,lens,budget,first,recent", [
+    (128, 2, [4160, 256, 257, 0], 256, 0, 0), (64, 2, [4160, 255], 255, 3, 100), (64, 1, [4224, 100], 256, 0, 7),
+    (128, 1, [600, 258], 257, 1, 1), (128, 2, [300, 129, 64], 128, 64, 64), (64, 3, [193, 4000], 193, 0, 192)])
+@pytest.mark.parametrize("kind", ["spread", "ties", "special"])
+@pytest.mark.parametrize("inplace", [True, False])
+def test_few_kept_tokens_and_one_more(D, kv, lens, budget, first, recent, kind, inplace):
+    """Both sides of the lengths and budgets up to which choice and move are one kernel."""
+    test_evict_keeps_and_moves_what_the_definition_says(D, kv, lens, budget, first, recent, kind, inplace)
+
+
 # ----------------------------------------------------- together, as they are used
 def test_a_decoder_that_evicts():
     """A prompt, then tokens one by one with weights summed up and an eviction whenever the cache passes its
