@@ -102,6 +102,17 @@ def test_tree_attention(D, kv, group, S, lens, new):
     compare(out, lse, q_np, pool, table, lens, new, mask.cpu().numpy(), kv_scale, D ** -0.5)
 
 
+@pytest.mark.parametrize("D,kv,group,S,lens,new", [
+    (64, 1, 5, 12, [20000], [12]),                           # one unit in all CTAs
+    (128, 1, 4, 65, [9000], [65]),                           # three
+    (64, 3, 2, 70, [8000, 130, 0, 3000], [70, 33, 0, 5]),    # units of 40 parts, of two and of one
+    (128, 2, 1, 17, [1500, 90, 700, 2500, 64, 1000], [17, 17, 3, 16, 17, 0]),
+    (64, 4, 3, 40, [900] * 12, [40, 1] * 6),                 # as many units as CTAs, nearly
+])
+def test_units_cut_into_many_parts(D, kv, group, S, lens, new):
+    test_tree_attention(D, kv, group, S, lens, new)
+
+
 @pytest.mark.parametrize("D,group,S,lens,new", [
     (64, 1, 6, [6, 40, 70, 6], [6, 6, 6, 4]), (128, 3, 30, [30, 95, 64], [30, 30, 12]),
     (64, 2, 90, [90, 154, 60], [90, 90, 60])])
