@@ -14,9 +14,9 @@
 //
 // move_kernel and move_within_kernel bring the kept tokens' codes, scales and
 // weights to the places 0, 1, ...: 9/8 D + 4 bytes a token and head each way,
-// by sectors of 32 bytes, of which a token's scales use 8: a move of every fourth
-// token reads twice the bytes it keeps (8190 of 32760 tokens, 40 heads of 128: 96 MB
-// read, 24 us from a cold cache, 4.4 TB/s; 65% of the copy rate).  To other pages a
+// by sectors of 32 bytes, of which a token's scales use 8, and larger fetches: a move
+// of every fourth token reads twice the bytes it keeps (8190 of 32760 tokens, 40 heads
+// of 128: 96 MB read, 24 us from a cold cache, 4.4 TB/s; 65% of the copy rate).  To other pages a
 // block takes a page of 64 places.  Within the sequence's own pages a cluster takes
 // a (sequence, kv head) and goes along the places in order: kept[j] >= j and
 // ascends, so once all its blocks have read the places of a turn, no place that the
@@ -347,9 +347,11 @@ __global__ void __launch_bounds__(kChooseThreads, 1) choose_kernel(EvictParams p
     choose<kChooseThreads, true>(p);
 }
 
-// To other pages: block (x, h, b) fills places 64 x .. 64 x + 63.
+// To other pages: block (x, h, b) fills places 64 x .. 64 x + 63.  (All the blocks an SM holds, 32
+// registers a thread: what has to be waited for, one after the other, is most of a block's life.  40
+// heads of 8190 from 32760 tokens with a read 77.0 us at 40 registers, 75.8 so.)
 template <int kD>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 16) move_kernel(EvictParams p) {
     __shared__ int source[kPageTokens];
     early();
     begin_work();

@@ -40,7 +40,7 @@ __device__ __forceinline__ unsigned char* token_page(const CacheView& c, const i
 // (kMoveThreads threads call it, `thread` is a thread's number among them; `source` is shared memory).
 template <int kD>
 __device__ __forceinline__ void take_tokens(const CacheView& c, const int32_t* table, int width, int b, int h,
-                                            const int* source, int size, int thread,
+                                            const int* source, int size, unsigned thread,
                                             MovedToken<kD> (&x)[MovedToken<kD>::kTurns]) {
     using L = PageLayout<kD>;
     using M = MovedToken<kD>;
@@ -65,7 +65,7 @@ __device__ __forceinline__ void take_tokens(const CacheView& c, const int32_t* t
 // Writes what take_tokens read to the places first .. first + size - 1 of a table's sequence.
 template <int kD>
 __device__ __forceinline__ void put_tokens(const CacheView& c, const int32_t* table, int width, int b, int h, int first,
-                                           int size, int thread, const MovedToken<kD> (&x)[MovedToken<kD>::kTurns]) {
+                                           int size, unsigned thread, const MovedToken<kD> (&x)[MovedToken<kD>::kTurns]) {
     using L = PageLayout<kD>;
     using M = MovedToken<kD>;
     const int piece = thread % M::kPieces;
