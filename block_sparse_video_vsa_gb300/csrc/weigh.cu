@@ -9,15 +9,18 @@
 // (cache_attn.cu); a weight is the sum over a token's row of the accumulator, so nothing is joined
 // across warps and each weight has one owner: same bits in every run.
 //  * All warps take equal stretches of the line of half pages (32 tokens) of all
-//    sequences and heads; codes and scales come straight to registers, the next
-//    half page's while this one is worked on.
+//    sequences and heads; codes, scales and weights so far come to shared memory by
+//    asynchronous copies, three half pages ahead, each warp's for itself (61 sequences
+//    of up to 12000 tokens, 128 / 64 channels: 56.6 / 43.8 us; two half pages in
+//    registers in turns 60.7 / 54.8, four in shared memory 57.6 / 44.2; single calls are
+//    up to 0.2 us slower so).
 //  * A key's 64 (or 32) code bytes are four lanes' loads; the order of channels
 //    within K Q^T is free, so a lane's 32 (16) channels need no shuffle.
 // Measured on a GB300, 4 rows a kv head, D = 128: 61 sequences of up to 12000 tokens,
-// 8 kv heads, 61 us = 4.1 TB/s read (61% of the measured copy rate): loads' latency and
-// issue, 0.47 instructions a scheduler and cycle with the 16 warps an SM that 124
-// registers leave.  One sequence of 32760: 9 us, the latency of lengths, page numbers,
-// rows and four half pages one after the other (its bytes take 3).
+// 8 kv heads, 56.6 us = 4.4 TB/s read (65% of the measured copy rate): issue, some 340
+// instructions a half page and warp at 0.57 a scheduler and cycle.  One sequence of
+// 32760: 9 us, the latency of lengths, page numbers, rows and half pages one after the
+// other (its bytes take 3).
 #include "weigh.cuh"
 
 namespace vsa {
@@ -73,8 +76,19 @@ struct KUnit {
     float before;  // the weight of token 16 (t / 2) + 8 (t % 2) + g so far
 };
 
+// A half page's K and its tokens' weights so far, on their way to a warp.
+template <int kD>
+struct alignas(16) Piece {
+    static constexpr int kCodes = kUnit * PageLayout<kD>::kRow, kScales = kUnit * PageLayout<kD>::kGroups;
+    unsigned char codes[kCodes];
+    unsigned char scales[kScales];
+    float before[32];  // of the lane's token
+};
+constexpr int kStages = 3;  // pieces of a warp
+
 template <int kD, int kNT, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
+    extern __shared__ __align__(16) unsigned char weigh_smem[];
     using L = PageLayout<kD>;
     constexpr int kWords = kD / 32;
     early();
@@ -82,6 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const CacheView& c = p.c;
+    Piece<kD>* const pieces = reinterpret_cast<Piece<kD>*>(weigh_smem) + warp * kStages;
     if (blockIdx.x == 0 && warp == 0)  // lengths out of range are noted once
         for (int b = lane; b < c.B; b += 32) cache_len(c, b, true);
     const long long total = line_length(c);
@@ -120,20 +135,40 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
                 }
             };
             look_up();
-            auto load = [&](int unit, KUnit<kD>& k) {
-                if ((unit >> 1) - page0 == 32) {
-                    page0 += 32;
-                    look_up();
+            uint32_t there = 0;  // a bit for each stage: the page is one
+            auto ask = [&](int unit, int stage) {
+                if (unit < end) {
+                    if ((unit >> 1) - page0 == 32) {
+                        page0 += 32;
+                        look_up();
+                    }
+                    const int page = __shfl_sync(0xffffffffu, id, (unit >> 1) - page0);
+                    there = page >= 0 ? there | 1u << stage : there & ~(1u << stage);
+                    Piece<kD>& piece = pieces[stage];
+                    if (page >= 0) {
+                        using P = Piece<kD>;
+                        const unsigned char* base = c.pool + ((size_t)page * c.kv_heads + h) * L::kBytes;
+#pragma unroll
+                        for (int i = 0; i < P::kCodes / 512; ++i)
+                            cp_async16(smem_u32(piece.codes + i * 512 + lane * 16),
+                                       base + (unit & 1) * P::kCodes + i * 512 + lane * 16);
+                        if (lane < P::kScales / 16)
+                            cp_async16(smem_u32(piece.scales + lane * 16),
+                                       base + L::kKScale + (unit & 1) * P::kScales + lane * 16);
+                    }
+                    if (in) cp_async4(smem_u32(&piece.before[lane]), in + unit * kUnit + 16 * (t >> 1) + 8 * (t & 1) + g);
                 }
-                const int page = __shfl_sync(0xffffffffu, id, (unit >> 1) - page0);
-                const unsigned char* base = c.pool + ((size_t)max(page, 0) * c.kv_heads + h) * L::kBytes;
+                cp_async_commit();
+            };
+            auto take = [&](int stage, KUnit<kD>& k) {
+                const Piece<kD>& piece = pieces[stage];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const int tok = (unit & 1) * kUnit + 16 * m + 8 * half + g;
-                        const unsigned char* src = base + tok * L::kRow + t * (kWords * 4);
-                        const unsigned char* sc = base + L::kKScale + tok * L::kGroups + t * (kWords / 2);
+                        const int tok = 16 * m + 8 * half + g;
+                        const unsigned char* src = piece.codes + tok * L::kRow + t * (kWords * 4);
+                        const unsigned char* sc = piece.scales + tok * L::kGroups + t * (kWords / 2);
                         if constexpr (kWords == 4) {
                             const uint4 x = *reinterpret_cast<const uint4*>(src);
                             k.codes[m][half][0] = x.x; k.codes[m][half][1] = x.y;
@@ -145,13 +180,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
                             k.scales[m][half] = (uint32_t)*sc * 0x101u;
                         }
                     }
-                const int x = unit * kUnit + 16 * (t >> 1) + 8 * (t & 1) + g;
-                k.before = in ? in[x] : 0.f;
-                return page >= 0;
+                k.before = in ? piece.before[lane] : 0.f;
             };
             // The first keys are on their way before the rows are looked at.
-            KUnit<kD> ka, kb;  // this half page's and the next one's, in turns
-            bool there_a = load(u, ka), there_b = false;
+#pragma unroll
+            for (int i = 0; i < kStages; ++i) ask(u + i, i);
             // The rows as the matrix instruction's columns.
             uint32_t qf[kNT][2 * kWords][2];
             float scale[kNT][2], off[kNT][2];  // logit = s scale - off (log2 units) of rows nt * 8 + 2 t + i
@@ -197,9 +230,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
             }
             min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 1));
             min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 2));
-            auto work = [&](const KUnit<kD>& k, bool there) {
+            auto work = [&](const KUnit<kD>& k, bool held) {
                 float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-                if (there && rows > 0) {
+                if (held && rows > 0) {
                     float s[2][kNT][4];
                     uint32_t ks[2][2][kWords / 2];
 #pragma unroll
@@ -258,19 +291,34 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
                 const int x = u * kUnit + 16 * (t >> 1) + 8 * (t & 1) + g;
                 if (x < kv) out[x] = k.before + y;
             };
+            int stage = 0;
 #pragma unroll 1
-            while (u < end) {
-                if (u + 1 < end) there_b = load(u + 1, kb);
-                work(ka, there_a);
-                if (++u >= end) break;
-                if (u + 1 < end) there_a = load(u + 1, ka);
-                work(kb, there_b);
-                ++u;
+            for (; u < end; ++u) {
+                cp_async_wait<kStages - 1>();
+                __syncwarp();
+                KUnit<kD> k;
+                take(stage, k);
+                const bool held = there >> stage & 1u;
+                __syncwarp();  // all have what they need of the stage
+                ask(u + kStages, stage);
+                work(k, held);
+                stage = (stage + 1) % kStages;
             }
             left -= n;
         }
     }
     fill_rest(p, false);
+}
+
+template <int kD, int kNT, int kWarps>
+cudaError_t launch_few(const WeighParams& p, int num_sms, cudaStream_t stream) {
+    constexpr int smem = kWarps * kStages * (int)sizeof(Piece<kD>);
+    static_assert(smem <= 232448, "shared memory of the weighing kernel");
+    auto kernel = weigh_kernel<kD, kNT, kWarps>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(kernel, smem, done);
+    if (e != cudaSuccess) return e;
+    return launch_early(kernel, dim3((unsigned)num_sms), kWarps * 32, smem, stream, p);
 }
 
 }  // namespace
@@ -296,23 +344,20 @@ cudaError_t launch_cache_weigh(const CacheView& c, int D, const void* q, const f
     // registers for the queries leave too few warps):
     //   rows of a kv head           20           32
     //   D = 128,  1 x 32760     14.0 | 16.6  18.1 | 16.5
-    //             8 x 8000      20.2 | 24.9  28.2 | 24.8
+    //             8 x 8000      20.0 | 24.9  28.2 | 24.8
     //   D = 64,   1 x 32760     11.0 | 14.4  12.9 | 14.6
-    //             8 x 8000      14.9 | 22.1  17.8 | 22.2
-    // Warps of a block, one tile of 8 rows (61 sequences of up to 12000, D = 128): 60.8 us with
-    // 16, 68.6 with 12, 71.9 with 18, 67.1 with 20; two tiles (8 x 8000, 12 rows): 17.3 with 16,
-    // 16.1 with 12, 18.1 with 14.
+    //             8 x 8000      15.0 | 22.1  17.4 | 22.2
+    // Warps of a block, one tile of 8 rows (61 sequences of up to 12000, D = 128): 57.6 us with
+    // 16, 57.0 with 20, which makes single calls slower (9.1 and 9.8).
     if (rows > (D == 64 ? 32 : 24)) return launch_weigh_chunk(p, D, num_sms, stream);
-    const dim3 grid((unsigned)num_sms);
-    const auto few = [&](auto kernel, int warps) { return launch_early(kernel, grid, warps * 32, 0, stream, p); };
     if (D == 64)
-        return rows <= 8    ? few(weigh_kernel<64, 1, 16>, 16)
-               : rows <= 16 ? few(weigh_kernel<64, 2, 16>, 16)
-               : rows <= 24 ? few(weigh_kernel<64, 3, 12>, 12)
-                            : few(weigh_kernel<64, 4, 12>, 12);
-    return rows <= 8    ? few(weigh_kernel<128, 1, 16>, 16)
-           : rows <= 16 ? few(weigh_kernel<128, 2, 12>, 12)
-                        : few(weigh_kernel<128, 3, 12>, 12);
+        return rows <= 8    ? launch_few<64, 1, 16>(p, num_sms, stream)
+               : rows <= 16 ? launch_few<64, 2, 16>(p, num_sms, stream)
+               : rows <= 24 ? launch_few<64, 3, 12>(p, num_sms, stream)
+                            : launch_few<64, 4, 12>(p, num_sms, stream);
+    return rows <= 8    ? launch_few<128, 1, 16>(p, num_sms, stream)
+           : rows <= 16 ? launch_few<128, 2, 12>(p, num_sms, stream)
+                        : launch_few<128, 3, 12>(p, num_sms, stream);
 }
 
 }  // namespace vsa

@@ -18,6 +18,11 @@ struct WeighParams {
 
 #if defined(__CUDACC__)
 
+// 4-byte asynchronous global -> shared copy, tracked by commit groups.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Places from a sequence's length on: what `weights` has there, or zero
 // (nothing is to be done in place).  The blocks share the rows.
 __device__ __forceinline__ void fill_rest(const WeighParams& p, bool idle) {

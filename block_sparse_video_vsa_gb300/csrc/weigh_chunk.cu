@@ -259,11 +259,6 @@ __device__ __forceinline__ uint32_t f16_to_bf16x2(uint32_t h) {
     return pack_bf16x2(f.x, f.y);
 }
 
-// 4-byte asynchronous global -> shared copy, tracked by commit groups.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // The kD / 16 products of a half: d = a (kD / 2 columns of tensor memory) * b (shared
 // memory, 16 channels 32 bytes apart, 64 channels kHalf), and an arrival on `done` (and
 // on `also`, where that is not 0) once they and those before have completed.  All lanes call it; one issues, in one branch.
