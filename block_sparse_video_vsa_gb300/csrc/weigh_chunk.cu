@@ -761,9 +761,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const bool odd = *reinterpret_cast<volatile int*>(&ms.odd[place]);
-                // (Columns past the last row are products with zeros where the queries end with
-                // the tensor, and weigh 2^-infinity; else they may be products with anything.)
-                const bool plain = !odd && (end == c0 + p.half || u.fresh == p.w.Sq) && !__any_sync(0xffffffffu, low > c0);
+                // (Columns past the last row are products with zeros, and weigh 2^-infinity, where
+                // the tile ends with all of the tensor's queries; else they may be products with
+                // anything: with queries behind the sequence's, or, in the last tile of a group of
+                // more than 128 heads, with the next kv head's.)
+                const bool plain = !odd && (end == c0 + p.half || (p.splits == 1 && u.fresh == p.w.Sq)) &&
+                                   !__any_sync(0xffffffffu, low > c0);
                 float2 a = make_float2(0.f, 0.f), b = make_float2(0.f, 0.f);
 #pragma unroll 1
                 for (int c1 = c0; c1 < end; c1 += 32) {
