@@ -740,10 +740,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             float total = 0.f;
             if (p.resident && u.fresh_rows) ++i;
             const int c0 = p.one_half ? 0 : e * p.half;
-            // Columns from `low` on are rows that see the key; of the tile at hand.
-            const int step = p.per * p.w.group * p.cluster;
+            // Columns from `low` on are rows that see the key; of the tile at hand.  (A call's steps
+            // together are below 2^24 rows and a tile, whole tiles of a group of up to 128 heads; wider
+            // groups set `low` for each tile, or never.)
+            const int step = p.splits == 1 ? p.per * p.w.group * p.cluster : 0;
             int low = -0x40000000;
-            if (p.w.causal) low = (max(x - (u.kv - u.fresh), 0) - u.t0 * p.per) * p.w.group;
+            if (p.w.causal && p.splits == 1) low = (max(x - (u.kv - u.fresh), 0) - u.t0 * p.per) * p.w.group;
 #pragma unroll 1
             for (int t = u.t0; t < u.tiles; t += p.cluster, low -= step) {
                 const uint32_t place = (p.resident ? i - 1 : i++) % kNlStages;

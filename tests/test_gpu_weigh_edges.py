@@ -31,3 +31,38 @@ def test_more_heads_than_a_tile_has_rows_on_several_kv_heads(D, kv, group, S, le
     assert torch.equal(got_bad[:, 0], got[:, 0])
     assert torch.equal(got_bad, vsa.cache_weigh(q, no_lse, pool, table, lens_t, **call))
     assert vsa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_the_last_rows_of_the_widest_groups(causal):
+    """65408 heads (511 tiles of 128) of 64 queries on one kv head: only the last two queries' log-sums are
+    finite, and all their rows count.
+
+    A sum of the N rows' positive weights, a fp32 sum in any order, is N 2^-24 off; a weight by what the bound of
+    tree_ref.weigh says of logits."""
+    D, heads, S, n, live = 64, 511 * 128, 64, 130, 2
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    pool = vsa.cache_pool(3, 1, D)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    k = torch.randn((1, n, 1, D), generator=gen, device="cuda").bfloat16()
+    vsa.cache_append(pool, k, k, table, lens)
+    q = torch.randn((1, S, heads, D), generator=gen, device="cuda").bfloat16()
+    lse = torch.full((1, heads, S), float("inf"), device="cuda")
+    lse[:, :, S - live:] = 4 + torch.rand((1, heads, live), generator=gen, device="cuda")
+    got = vsa.cache_weigh(q, lse, pool, table, lens, causal=causal)
+    stored = vsa.cache_read(pool, table, lens, n)[0][0, :, 0].double()  # (exact in bf16: no head scale)
+    want, lim = torch.zeros(2, 192, dtype=torch.float64, device="cuda")
+    for i in range(S - live, S):
+        rows = q[0, i].double()
+        sums = lse[0, :, i].double()[:, None]
+        s = rows @ stored.T / 8
+        d = (D + 4) * 2.0 ** -24 * (rows.abs() @ stored.abs().T / 8) + 4 * 2.0 ** -24 * (s.abs() + sums.abs())
+        w = torch.exp(s - sums)
+        if causal:
+            w[:, n - S + i + 1:] = 0
+        want[:n] += w.sum(0)
+        lim[:n] += (w * (torch.expm1(d) + 2.0 ** -22 + (heads * live + 8) * 2.0 ** -24)).sum(0)
+    assert want[:n - 1].min() > heads / 100 and lim[:n].max() < 0.02 * want[:n].max()
+    assert ((got[0, 0].double() - want).abs() <= 1.01 * lim).all()
+    assert vsa.device_error(reset=True) == 0
