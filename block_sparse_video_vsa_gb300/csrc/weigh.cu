@@ -21,6 +21,8 @@
 // instructions a half page and warp at 0.57 a scheduler and cycle.  One sequence of
 // 32760: 9 us, the latency of lengths, page numbers, rows and half pages one after the
 // other (its bytes take 3).
+#include <float.h>
+
 #include "weigh.cuh"
 
 namespace vsa {
@@ -217,7 +219,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weigh_kernel(WeighParams p) {
                     qf[nt][i][0] = pack_f16x2(bf16_lo(w[2 * i]) * f, bf16_hi(w[2 * i]) * f);
                     qf[nt][i][1] = pack_f16x2(bf16_lo(w[2 * i + 1]) * f, bf16_hi(w[2 * i + 1]) * f);
                 }
-                const float mine = used ? lse * 1.4426950408889634f : INFINITY;
+                // (Finite below: a key that the row does not see has a logit of -infinity.)
+                const float mine = used ? fmaxf(lse * 1.4426950408889634f, -FLT_MAX) : INFINITY;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     scale[nt][i] = logit_scale(p.scale_log2, k_head, __shfl_sync(0xffffffffu, e, (2 * t + i) * 4));

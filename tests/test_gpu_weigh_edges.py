@@ -66,3 +66,14 @@ def test_the_last_rows_of_the_widest_groups(causal):
     assert want[:n - 1].min() > heads / 100 and lim[:n].max() < 0.02 * want[:n].max()
     assert ((got[0, 0].double() - want).abs() <= 1.01 * lim).all()
     assert vsa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("S,group", [(4, 4), (9, 1), (20, 1), (60, 2), (3, 130)])
+def test_rows_without_a_key_add_nothing_whatever_their_log_sum(S, group):
+    """Rows that see no key (more queries than tokens), their log-sums marked with the type's lowest value."""
+    q, lse, pool, table, lens_t, call, _, want, lim = weigh_case(64, 2, group, S, [2, 90], None, True, False)
+    marked = lse.clone()
+    marked[0, :, :S - 2] = torch.finfo(torch.float32).min
+    got = vsa.cache_weigh(q, marked, pool, table, lens_t, **call)
+    assert torch.equal(got, vsa.cache_weigh(q, lse, pool, table, lens_t, **call))
+    assert (abs(got.double().cpu().numpy() - want) <= lim).all()
