@@ -37,6 +37,7 @@
 // waits around the exponentials); 64 rows 50 us = 1.9 TB/s of pages (28% of the copy
 // rate; 0.61 instructions: describing, converting and summing a unit of 256 keys takes
 // some 1760 a scheduler).
+#include <float.h>
 #include <stddef.h>
 
 #include <algorithm>
@@ -460,8 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // =================================== queries (by TMA) and their log-sums
         // The log-sums are copied to their place asynchronously, and when the next tile
         // of the unit has been asked for turned into what the sums take there.  A
-        // column without a row is marked.
-        constexpr uint32_t kNoRow = 0x7FFFDEADu;
+        // column without a row gets the largest number: it becomes -infinity, as a row's
+        // log-sum does that is not finite, but is finite itself, so that no tile is marked for it.
+        constexpr float kNoRow = FLT_MAX;
         const int box_rows = p.splits == 1 ? p.per * p.w.group : 128;
         int off[4];  // of the lane's columns from the tile's first log-sum on
 #pragma unroll
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 128; k += 32) {
                 const float l = nl[k + lane];
                 const bool finite = fabsf(l) < INFINITY;
-                odd |= !finite && __float_as_uint(l) != kNoRow;
+                odd |= !finite;
                 nl[k + lane] = finite ? l * -1.4426950408889634f : -INFINITY;
             }
             odd = __any_sync(0xffffffffu, odd);
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (r < x.columns)
                         cp_async4(smem_u32(&nl[r]), lse + off[k]);
                     else
-                        nl[r] = __uint_as_float(kNoRow);
+                        nl[r] = kNoRow;
                 }
                 cp_async_commit();
                 if (pending) {

@@ -77,3 +77,18 @@ def test_rows_without_a_key_add_nothing_whatever_their_log_sum(S, group):
     got = vsa.cache_weigh(q, marked, pool, table, lens_t, **call)
     assert torch.equal(got, vsa.cache_weigh(q, lse, pool, table, lens_t, **call))
     assert (abs(got.double().cpu().numpy() - want) <= lim).all()
+
+
+@pytest.mark.parametrize("S,group", [(1, 3), (20, 2), (40, 5), (2, 130)])
+@pytest.mark.parametrize("bits", [0x7FFFDEAD, 0x7FC00000, 0x7F800001, -1])
+def test_no_bits_of_a_nan_log_sum_let_its_row_in(S, group, bits):
+    q, lse, pool, table, lens_t, call, _, _, _ = weigh_case(64, 2, group, S, [300, 90], None, False, False)
+    heads = 2 * group
+    bad_q, bad_lse, no_lse = q.clone(), lse.clone(), lse.clone()
+    for j in (0, group, heads - 1):
+        bad_q[:, S - 1, j] = float("nan")
+        bad_lse.view(torch.int32)[:, j, S - 1] = bits
+        no_lse[:, j, S - 1] = float("inf")
+    got = vsa.cache_weigh(bad_q, bad_lse, pool, table, lens_t, **call)
+    assert torch.isfinite(got).all()
+    assert torch.equal(got, vsa.cache_weigh(q, no_lse, pool, table, lens_t, **call))
