@@ -936,7 +936,11 @@ def cache_weigh(q, lse, pool, table, kv_lens, q_lens=None, causal: bool = True, 
     (vsa_cache_weigh).
 
     Added to weights (likewise shaped; None: zeros) in place, or to out where that is given; a new tensor
-    with neither.  Rows whose lse is not finite add nothing."""
+    with neither.  Rows whose lse is not finite add nothing.
+
+    The lse is that of attention over the same keys: all (or, causal, those up to the row), no selected
+    pages.  Of a tree, the rows and log-sums of the accepted path are passed, gathered, after cache_accept,
+    with its path_lens as q_lens."""
     if out is None:
         out = weights
     if stream is None and (_front_module or _front()):

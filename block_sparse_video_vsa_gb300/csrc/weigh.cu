@@ -17,8 +17,12 @@
 //  * A key's 64 (or 32) code bytes are four lanes' loads; the order of channels
 //    within K Q^T is free, so a lane's 32 (16) channels need no shuffle.
 // Measured on a GB300, 4 rows a kv head, D = 128: 61 sequences of up to 12000 tokens,
-// 8 kv heads, 56.6 us = 4.4 TB/s read (65% of the measured copy rate): issue, some 340
-// instructions a half page and warp at 0.57 a scheduler and cycle.  One sequence of
+// 8 kv heads, 56.9 us = 4.4 TB/s read (65% of the measured copy rate): some 340
+// instructions a half page and warp, and four warps a scheduler, which issue 0.57 a cycle.
+// A warp waits 6.8 cycles an instruction: 1.4 for the one before, 1.1 for memory,
+// 1.3 for the pipes and dispatch, 1.1 for its turn.  20 rows on 8 sequences of 8000, 19.8 us:
+// three warps a scheduler, 0.39 a cycle; 2.0 for the instruction before, 1.7 for memory, 1.1
+// for the pipes and dispatch.  One sequence of
 // 32760: 9 us, the latency of lengths, page numbers, rows and half pages one after the
 // other (its bytes take 3).
 #include <float.h>

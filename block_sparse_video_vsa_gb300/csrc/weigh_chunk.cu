@@ -7,8 +7,9 @@
 // lanes, up to 128 rows on its columns.  A thread owns a key, runs along the
 // columns and keeps the sum in a register over all tiles of rows: no maximum, no
 // exchange between threads, and the weights of a key have one owner (same bits in
-// every run).  Tensor and exponential bound for many rows (2 D flops and one
-// exponential a pair), HBM bound for few (9/16 D bytes a key).
+// every run).  The floor is that of products and exponentials for many rows (2 D flops
+// and one exponential a pair), of memory for few (9/16 D bytes a key); the kernel is bound
+// by waits of its roles for one another and by instructions (figures below).
 //  * A unit is 256 keys (four pages) of a kv head.  Its K is converted once, to
 //    bf16 (code * scale has at most 6 significant bits: exact), straight into
 //    tensor memory as the A operand, while the queries stream through shared
@@ -32,11 +33,12 @@
 //  * Every wait is bounded; one that runs out raises the CTA's abort flag and the
 //    device error word, and each role winds down.
 // Measured on a GB300, D = 128, one sequence of 32760 tokens, 40 kv heads: 1560 rows
-// 435 us = 1.20 PFLOP/s (63% of the measured bf16 rate; tensor pipe 49% busy,
-// exponentials 51%, 0.69 instructions a scheduler and cycle: the loads from tensor memory and
-// waits around the exponentials); 64 rows 50 us = 1.9 TB/s of pages (28% of the copy
-// rate; 0.61 instructions: describing, converting and summing a unit of 256 keys takes
-// some 1760 a scheduler).
+// 437 us = 1.20 PFLOP/s (63% of the measured bf16 rate; tensor pipe 49% busy,
+// exponentials 51%, in turns; 0.69 instructions a scheduler and cycle, and of the 10 cycles
+// that each of its seven warps takes an instruction 3.6 are waits for tensor memory and barriers);
+// 64 rows 51 us = 1.9 TB/s of pages (28% of the copy rate; 0.62 instructions, of 11 cycles 3.2 such
+// waits and 1.3 for shared memory; describing, converting and summing a unit of 256 keys takes some
+// 1760 instructions a scheduler).
 #include <float.h>
 #include <stddef.h>
 

@@ -614,7 +614,10 @@ vsa_status vsa_cache_accept(const vsa_cache* c, const int32_t* new_lens, const i
  *   out[b, h, x] = weights[b, h, x] + sum of exp(sm_scale * (q . k_x) - lse)
  * over the queries i < q_lens[b] that see x (all; with causal != 0 those with x <=
  * kv_lens[b] - q_lens[b] + i) and the heads that share h.  With the lse of
- * vsa_cache_attn on the same keys these are its softmax weights.  Rows whose lse is
+ * vsa_cache_attn on the same keys these are its softmax weights.  (With that of a call
+ * over selected pages they are not: every key would get a weight, also those that
+ * were not selected.  Rows of a tree: those of the accepted path, after
+ * vsa_cache_accept, with q_lens = path_lens and causal != 0.)  Rows whose lse is
  * not finite (no key, NaN) add nothing, whatever their q holds.
  *   q        : bf16 [B, Sq, heads, D], as vsa_cache_attn; rows from q_lens[b] on are
  *              not read
